@@ -20,6 +20,7 @@ STATUS_NAMES = {
     4: "BM_ERR_SLOT_FREE", 5: "BM_ERR_CUDA", 6: "BM_ERR_OOM", 7: "BM_ERR_NOT_READY",
     8: "BM_ERR_DEVICE_CHECK", 9: "BM_ERR_UNSUPPORTED",
 }
+KV8_E4M3, KV8_INT8 = 0, 1
 POLICY_AUTO, POLICY_SIMT, POLICY_TC, POLICY_MMA = 0, 1, 2, 3
 
 
@@ -49,6 +50,15 @@ class bm_layer_weights(ctypes.Structure):
 class bm_moe_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("experts", "top_k", "hidden", "ffn", "group", "renorm_topk")] + \
                [(n, _P) for n in ("wr", "wg", "wg_s", "wu", "wu_s", "wd", "wd_s")]
+
+
+class bm_kv8_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("format", "slots", "ctx_cap", "kv_heads", "head_dim")] + \
+               [(n, _P) for n in ("K", "V", "Ks", "Vs")]
+
+
+class bm_kv8_rope(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int), ("eps", ctypes.c_float)] + [(n, _P) for n in ("q_norm", "k_norm", "inv_freq")]
 
 
 class bm_kernel_profile(ctypes.Structure):
@@ -103,6 +113,12 @@ def lib():
             "decode_step": ([V, I, V, V, V, V, V], S),
             "kv_slot_prefill": ([V, I, I, V, V, V, V], S),
             "bm_engine_profile_step": ([V, I, V, V, V, ctypes.POINTER(bm_kernel_profile), I, PI, V], S),
+            "kv8_append": ([V, V, ctypes.c_int64, I, V, V, V, V, V, I, V], S),
+            "kv8_read": ([V, I, I, I, V, V, V], S),
+            "kv8_workspace_bytes": ([I, I, I, I, I, I], SZ),
+            "kv8_attend": ([V, V, V, V, I, ctypes.c_float, V, I, V, SZ, V], S),
+            "kv8_attend_prefix": ([V, V, I, I, V, V, V, I, ctypes.c_float, V, I, V, SZ, V], S),
+            "bm_sample": ([V, I, ctypes.c_int64, I, I, V, V, V, V, V, V, V, V], S),
             "bm_w4_quantize": ([V, I, I, I, V, V, V], S),
             "bm_engine_moe": ([V, I, V, V, V, V, I, V], S),
             "bm_probe_tcgen05_mma": ([I, I, I, I, I, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)], S),
@@ -361,6 +377,136 @@ def bm_probe_tcgen05_mma(n, a_in_tmem, swizzle128, iters, roundtrip=0):
 
 def bm_w4_quantize(W, N, K, g, packed, scales, stream=None):
     _check(lib().bm_w4_quantize(ptr(W), N, K, g, ptr(packed), ptr(scales), stream_handle(stream)))
+
+
+# --------------------------------------------------------------- 8-bit K/V cache, sampling
+# These calls take torch tensors and check what the C side cannot see: type,
+# shape, contiguity, and that the memory is on the current CUDA device.
+
+def _tensor(x, what, dtypes, shape=None, optional=False):
+    """Address of a contiguous CUDA tensor of the current device."""
+    if x is None:
+        if optional:
+            return None
+        raise BitMoeError(1, f"{what}: null tensor")
+    import torch
+    if x.dtype not in dtypes:
+        raise BitMoeError(1, f"{what}: dtype {x.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if shape is not None and x.shape != shape:
+        raise BitMoeError(1, f"{what}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if not x.is_contiguous():
+        raise BitMoeError(1, f"{what}: not contiguous")
+    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+        raise BitMoeError(1, f"{what}: on {x.device}, expected the current CUDA device")
+    return x.data_ptr()
+
+
+def _types():
+    import torch
+    return torch
+
+
+def kv8_cache(format, slots, ctx_cap, kv_heads, head_dim, K, V, Ks, Vs):
+    """The bm_kv8_cache of four tensors: codes uint8 [slots][kv_heads][ctx_cap][head_dim],
+    scales fp32 [slots][kv_heads][ctx_cap].  It keeps the tensors alive."""
+    t = _types()
+    rows = (slots, kv_heads, ctx_cap)
+    c = bm_kv8_cache(format, slots, ctx_cap, kv_heads, head_dim,
+                     *[_tensor(x, f"kv8_cache: {n}", (t.uint8,), rows + (head_dim,)) for n, x in (("K", K), ("V", V))],
+                     *[_tensor(x, f"kv8_cache: {n}", (t.float32,), rows) for n, x in (("Ks", Ks), ("Vs", Vs))])
+    c.tensors = (K, V, Ks, Vs)
+    return c
+
+
+def kv8_rope(norm=False, q_norm=None, k_norm=None, eps=1e-6, inv_freq=None):
+    """The bm_kv8_rope of its tensors (bf16 norm weights, fp32 inv_freq), which it keeps alive."""
+    t = _types()
+    r = bm_kv8_rope(int(norm), eps, _tensor(q_norm, "kv8_rope: q_norm", (t.bfloat16,), optional=True),
+                    _tensor(k_norm, "kv8_rope: k_norm", (t.bfloat16,), optional=True),
+                    _tensor(inv_freq, "kv8_rope: inv_freq", (t.float32,), optional=True))
+    r.tensors = (q_norm, k_norm, inv_freq)
+    return r
+
+
+def _cache_device(c, what):
+    t = _types()
+    if c.tensors[0].device.index != t.cuda.current_device():
+        raise BitMoeError(1, f"{what}: the cache is on {c.tensors[0].device}, expected the current CUDA device")
+
+
+def kv8_append(cache, qkv, rope, slots, index, Q, rope_pos=None, stream=None):
+    """qkv: bf16 [T][>= (q_heads + 2 kv_heads) * head_dim], rows may be strided; Q: bf16 [T][q_heads][head_dim]."""
+    t = _types()
+    _cache_device(cache, "kv8_append")
+    T, qh, d = Q.shape
+    if qkv.dim() != 2 or qkv.shape[0] != T or qkv.shape[1] < (qh + 2 * cache.kv_heads) * d or d != cache.head_dim:
+        raise BitMoeError(1, f"kv8_append: qkv {tuple(qkv.shape)} and Q {tuple(Q.shape)} do not fit the cache")
+    if qkv.dtype != t.bfloat16 or qkv.stride(1) != 1 or qkv.device != Q.device:
+        raise BitMoeError(1, "kv8_append: qkv must be bf16 rows of unit stride on Q's device")
+    for n, w, size in (("q_norm", rope.tensors[0], d), ("k_norm", rope.tensors[1], d), ("inv_freq", rope.tensors[2], d // 2)):
+        if w is not None and (w.numel() != size or w.device != Q.device):
+            raise BitMoeError(1, f"kv8_append: {n} must have {size} elements on Q's device")
+    i32 = (t.int32,)
+    ld = qkv.stride(0) if T > 1 else qkv.shape[1] + (-qkv.shape[1]) % 8
+    _check(lib().kv8_append(ctypes.addressof(cache), qkv.data_ptr(), ld, qh, ctypes.addressof(rope),
+                            _tensor(slots, "kv8_append: slots", i32, (T,)), _tensor(index, "kv8_append: index", i32, (T,)),
+                            _tensor(rope_pos, "kv8_append: rope_pos", i32, (T,), optional=True),
+                            _tensor(Q, "kv8_append: Q", (t.bfloat16,)), T, stream_handle(stream)))
+
+
+def kv8_read(cache, slot, first, count, K_out, V_out, stream=None):
+    """K_out, V_out: bf16 [kv_heads][count][head_dim]."""
+    t = _types()
+    _cache_device(cache, "kv8_read")
+    shape = (cache.kv_heads, count, cache.head_dim)
+    _check(lib().kv8_read(ctypes.addressof(cache), slot, first, count, _tensor(K_out, "kv8_read: K_out", (t.bfloat16,), shape),
+                          _tensor(V_out, "kv8_read: V_out", (t.bfloat16,), shape), stream_handle(stream)))
+
+
+def kv8_workspace_bytes(B, q_heads, kv_heads, head_dim, ctx_cap, prefix_len=0):
+    return lib().kv8_workspace_bytes(B, q_heads, kv_heads, head_dim, ctx_cap, prefix_len)
+
+
+def _attend_args(what, cache, Q, slots, lens, O, ws, scale):
+    t = _types()
+    _cache_device(cache, what)
+    B, qh, d = Q.shape
+    if d != cache.head_dim:
+        raise BitMoeError(1, f"{what}: Q of head_dim {d}, the cache of {cache.head_dim}")
+    return (_tensor(Q, f"{what}: Q", (t.bfloat16,)), _tensor(slots, f"{what}: slots", (t.int32,), (B,)),
+            _tensor(lens, f"{what}: lens", (t.int32,), (B,)), qh, d ** -0.5 if scale is None else scale,
+            _tensor(O, f"{what}: O", (t.bfloat16,), Q.shape), B, _tensor(ws, f"{what}: ws", (t.uint8,)), ws.numel())
+
+
+def kv8_attend(cache, Q, slots, lens, O, ws, scale=None, stream=None):
+    """Q, O: bf16 [B][q_heads][head_dim]; ws: uint8 tensor of kv8_workspace_bytes(...); scale: 1 / sqrt(head_dim) if None."""
+    args = _attend_args("kv8_attend", cache, Q, slots, lens, O, ws, scale)
+    _check(lib().kv8_attend(ctypes.addressof(cache), *args, stream_handle(stream)))
+
+
+def kv8_attend_prefix(cache, prefix, prefix_slot, prefix_len, Q, slots, lens, O, ws, scale=None, stream=None):
+    """kv8_attend behind positions 0..prefix_len-1 of slot prefix_slot of `prefix` (a kv8_cache, or `cache` itself)."""
+    _cache_device(prefix, "kv8_attend_prefix")
+    args = _attend_args("kv8_attend_prefix", cache, Q, slots, lens, O, ws, scale)
+    _check(lib().kv8_attend_prefix(ctypes.addressof(cache), ctypes.addressof(prefix), prefix_slot, prefix_len, *args,
+                                   stream_handle(stream)))
+
+
+def bm_sample(logits, temperature, top_k, top_p, min_p, u, ids, logprobs=None, stream=None):
+    """logits: fp32 or bf16 [B][V], rows may be strided; temperature, top_p, min_p (fp32) and top_k (int32) [B] or
+    None; u: fp32 [B]; ids: int32 [B]; logprobs: fp32 [B] or None."""
+    t = _types()
+    B, V = logits.shape
+    if logits.dtype not in (t.float32, t.bfloat16) or logits.stride(1) != 1 or logits.device != ids.device:
+        raise BitMoeError(1, "bm_sample: logits must be fp32 or bf16 rows of unit stride on ids' device")
+    f32, i32, n = (t.float32,), (t.int32,), (B,)
+    _check(lib().bm_sample(logits.data_ptr(), int(logits.dtype == t.bfloat16), logits.stride(0) if B > 1 else V, V, B,
+                           _tensor(temperature, "bm_sample: temperature", f32, n, optional=True),
+                           _tensor(top_k, "bm_sample: top_k", i32, n, optional=True),
+                           _tensor(top_p, "bm_sample: top_p", f32, n, optional=True),
+                           _tensor(min_p, "bm_sample: min_p", f32, n, optional=True),
+                           _tensor(u, "bm_sample: u", f32, n), _tensor(ids, "bm_sample: ids", i32, n),
+                           _tensor(logprobs, "bm_sample: logprobs", f32, n, optional=True), stream_handle(stream)))
 
 
 # --------------------------------------------------------------- host slot map

@@ -73,6 +73,12 @@ typedef enum bm_kernel_policy {
   BM_POLICY_MMA = 3
 } bm_kernel_policy;
 
+/* Codes of an 8-bit K/V cache: e4m3 floats (4 significant bits at any
+ * magnitude, largest 448) or signed integers in [-127, 127]. */
+typedef enum bm_kv8_format { BM_KV8_E4M3 = 0, BM_KV8_INT8 = 1 } bm_kv8_format;
+
+typedef enum bm_dtype { BM_F32 = 0, BM_BF16 = 1 } bm_dtype;
+
 /* Model geometry and engine limits. */
 typedef struct bm_config {
   int hidden;        /* H                                                     */
@@ -129,6 +135,29 @@ typedef struct bm_moe_weights {
   const uint8_t* wu; const uint16_t* wu_s;
   const uint8_t* wd; const uint16_t* wd_s;
 } bm_moe_weights;
+
+/* One layer of an 8-bit K/V cache, DEVICE pointers, caller-owned: codes
+ * [slots][kv_heads][ctx_cap][head_dim], one byte each (16-byte aligned), and
+ * fp32 scales [slots][kv_heads][ctx_cap]; a stored value is code * scale. */
+typedef struct bm_kv8_cache {
+  int format;        /* bm_kv8_format                                         */
+  int slots;         /* streams it holds                                      */
+  int ctx_cap;       /* positions per slot                                    */
+  int kv_heads;
+  int head_dim;      /* 64 or 128                                             */
+  uint8_t* K; uint8_t* V;
+  float* Ks; float* Vs;
+} bm_kv8_cache;
+
+/* What kv8_append does to the heads of q and k before it rounds them. */
+typedef struct bm_kv8_rope {
+  int norm;                 /* 1: RMSNorm of each q and k head before the rotation */
+  float eps;                /* its epsilon                                     */
+  const uint16_t* q_norm;   /* DEVICE bf16 [head_dim] or NULL (ones)           */
+  const uint16_t* k_norm;   /* DEVICE bf16 [head_dim] or NULL (ones)           */
+  const float* inv_freq;    /* DEVICE fp32 [head_dim / 2], radians per position,
+                               or NULL (no rotation)                           */
+} bm_kv8_rope;
 
 typedef struct bm_engine bm_engine;
 typedef struct bm_slot_map bm_slot_map;
@@ -426,6 +455,104 @@ bm_status kv_slot_prefill(bm_engine* e, int slot, int n_tokens, const int32_t* t
 bm_status bm_engine_profile_step(bm_engine* e, int B, const int32_t* slots, const int32_t* tokens,
                                  int32_t* next_tokens, bm_kernel_profile* out, int max_out, int* n_out,
                                  void* stream);
+
+/* ---------------------------------------------------------------- 8-bit K/V cache
+ * The slot arena of the engine holds K and V in bf16.  These calls work on a
+ * caller-owned arena of one layer that holds them in 8 bits, half the bytes
+ * that decode attention has to read.  No counterpart on the pages.  All of
+ * them only enqueue kernels (no allocation, no synchronisation), so they can
+ * be captured into a CUDA graph; slots, positions and lengths are read from
+ * DEVICE memory when the kernels run, so a replayed graph sees the values of
+ * that replay. */
+
+/* Write T rows of the QKV projection to the cache: per head RMSNorm of q and
+ * k (rope->norm), rotate-half RoPE of q and k (rope->inv_freq; angle =
+ * rope_pos[t] * inv_freq[i], reduced in 64 bits), then q rounded to bf16 into
+ * Q and k, v quantised at position index[t] of slot slots[t]: amax = largest
+ * |y| of the head, scale = amax / M, code = rn(y * (M / amax)), M = 448
+ * (e4m3) or 127 (int8), everything in fp32 up to that one rounding.  A head
+ * whose amax is below 2^-110 is stored as zeros; one that holds a NaN or an
+ * infinity gets the scale NaN, and reads back as NaN.
+ * qkv: DEVICE bf16 [T] rows of ld elements (q heads, then k, then v, as in
+ * bm_engine_attention; 16-byte aligned, ld % 8 == 0); slots, index: DEVICE
+ * int32 [T]; rope_pos: DEVICE int32 [T] or NULL (= index); Q: DEVICE bf16
+ * [T][q_heads][head_dim], 16-byte aligned, no overlap with qkv.  A row whose
+ * slot is outside [0, slots) or index outside [0, ctx_cap) is padding:
+ * neither the cache nor its row of Q is written.  Two rows of a call must not
+ * name the same position of the same slot (which row's codes and scale are
+ * left there is then undefined; nothing else is touched).
+ * Errors: BM_ERR_INVALID_ARG. */
+bm_status kv8_append(const bm_kv8_cache* c, const uint16_t* qkv, int64_t ld, int q_heads, const bm_kv8_rope* rope,
+                     const int32_t* slots, const int32_t* index, const int32_t* rope_pos, uint16_t* Q, int T,
+                     void* stream);
+
+/* Read positions [first, first + count) of a slot back as bf16(code * scale):
+ * K_out, V_out DEVICE bf16 [kv_heads][count][head_dim], 16-byte aligned.
+ * count == 0 does nothing.  Errors: BM_ERR_CTX_CAP (positions outside the
+ * slot), BM_ERR_INVALID_ARG. */
+bm_status kv8_read(const bm_kv8_cache* c, int slot, int first, int count, uint16_t* K_out, uint16_t* V_out, void* stream);
+
+/* Bytes of DEVICE workspace kv8_attend (prefix_len = 0) and
+ * kv8_attend_prefix need; 0 for sizes they reject. */
+size_t kv8_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int ctx_cap, int prefix_len);
+
+/* Decode attention of B streams over the cache: query head h of row b attends
+ * over positions 0..lens[b]-1 of slot slots[b], with KV head h / (q_heads /
+ * kv_heads), score factor `scale` (1 / sqrt(head_dim), usually); output
+ * rounded to bf16 once.  A row of length 0 has nothing to attend over and
+ * gets zeros.  A row whose slot is outside [0, slots) or length outside
+ * [0, ctx_cap] is padding: its row of O is left as it was.  A slot may occur
+ * in several rows.  Positions are split into chunks by the stream's own
+ * length and merged in ascending order, so a row's bytes do not depend on
+ * the other rows or on B.
+ * Q, O: DEVICE bf16 [B][q_heads][head_dim], 16-byte aligned; slots, lens:
+ * DEVICE int32 [B]; ws: DEVICE, 16-byte aligned, kv8_workspace_bytes(...)
+ * bytes, caller-owned, contents irrelevant before and after; calls that may
+ * overlap on the GPU need workspaces of their own.
+ * Errors: BM_ERR_INVALID_ARG (NULL, B outside [1, 1024], more than 8 query
+ * heads per kv head, scale not positive and finite, ws too small). */
+bm_status kv8_attend(const bm_kv8_cache* c, const uint16_t* Q, const int32_t* slots, const int32_t* lens, int q_heads,
+                     float scale, uint16_t* O, int B, void* ws, size_t ws_bytes, void* stream);
+
+/* kv8_attend for streams that share a prefix: every row attends over
+ * positions 0..prefix_len-1 of slot prefix_slot of `prefix` and then over its
+ * own.  The prefix is read once for all rows.  `prefix` has c's format,
+ * kv_heads and head_dim, and its own slots and ctx_cap; it may be c itself.
+ * A row with no positions of its own attends over the prefix alone.  The
+ * prefix's split depends on prefix_len alone, so a row's bytes do not depend
+ * on the other rows.  Errors: as kv8_attend, plus BM_ERR_CTX_CAP (prefix_len
+ * outside the slot). */
+bm_status kv8_attend_prefix(const bm_kv8_cache* c, const bm_kv8_cache* prefix, int prefix_slot, int prefix_len,
+                            const uint16_t* Q, const int32_t* slots, const int32_t* lens, int q_heads, float scale,
+                            uint16_t* O, int B, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- sampling */
+
+#define BM_SAMPLE_MAX_VOCAB 524288
+
+/* Draw one token per row of logits (for instance decode_step's), the random
+ * numbers given: the counterpart of decode_step's greedy argmax.  Per row b
+ * with temperature T > 0 the weights are w_i = exp((x_i - max x) / T),
+ * ordered by falling x and, among equal x, by rising index.  Kept are the
+ * first top_k of that order (top_k <= 0 or >= V: all); of these the smallest
+ * prefix holding at least top_p of their weight (top_p >= 1 or NaN: all); of
+ * these the ones with w >= min_p (min_p <= 0 or NaN: all; above 1 it counts
+ * as 1); the first is always kept.  The token is the lowest index whose
+ * cumulated kept weight exceeds u times the whole kept weight.  Any other T
+ * (0, negative, NaN) takes the argmax, lowest index first.
+ * NaN and -infinity are masked: never drawn.  Logits of +infinity share the
+ * row.  A row with nothing to draw gets the id -1 and the logprob -infinity.
+ * logits: DEVICE [B] rows of ld elements, dtype BM_F32 or BM_BF16;
+ * temperature, top_p, min_p: DEVICE fp32 [B] or NULL (1, 1, 0); top_k: DEVICE
+ * int32 [B] or NULL (all); u: DEVICE fp32 [B] in [0, 1) (below 0 or NaN counts
+ * as 0, above as the last kept token); ids: DEVICE int32 [B]; logprobs: DEVICE
+ * fp32 [B] or NULL, the log of the token's share of the kept weight (0 for an
+ * argmax).  A row's result does not depend on the other rows.
+ * Errors: BM_ERR_INVALID_ARG (NULL logits, u or ids; B outside [1, 65535], V
+ * outside [1, BM_SAMPLE_MAX_VOCAB], ld < V, misaligned logits). */
+bm_status bm_sample(const void* logits, int dtype, int64_t ld, int V, int B, const float* temperature,
+                    const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* ids,
+                    float* logprobs, void* stream);
 
 /* ---------------------------------------------------------------- layer ops of the step
  * The decode step's own kernels on one layer, with the engine's weights (in
