@@ -8,24 +8,76 @@
 //   top-p: of these, the smallest prefix whose weight is at least p times theirs;
 //   min-p: of these, the ones with w >= min_p * (the largest w = 1);
 // and always the first.  Every filter keeps a prefix of the order, so the kept
-// set is "x above a threshold, or equal to it and among the first r indices".
+// set is "x above a cut, or equal to it and among the first `ties` indices".
 // The draw walks the kept tokens by rising index: the first whose cumulated
 // weight exceeds u times the kept weight.
 //
-// One CTA per row; each threshold is a binary search over the ordered bit
-// patterns of x, one sweep of the row per bit.
+// A token on a border must fall where 64-bit arithmetic puts it, so a weight
+// is a 64-bit integer (2^44 for the largest), good to 2^-29 of itself: the
+// exponent in two fp32 words, 2^(j/128) from a table, the rest a cubic.  FP64
+// would do the same at a fortieth of the rate.  Integers also add up to the
+// same sum in any order, so histograms and sums may use atomics.
+//
+// A row belongs to a cluster of up to 16 CTAs that keep it in shared memory:
+// it is read from global memory once, and every later sweep is on chip.  A
+// warp owns a run of consecutive indices, so index order is warp order.  The
+// cut is found by histograms: first of counts over 1/32-wide steps of
+// log2(w); for top-p, a bin's weight is between its count times the bin's
+// borders, which leaves a few bins that may hold the cut, and only these get
+// exact sums, over ever finer ranges of the ordered bit patterns of x (ten
+// bits a sweep).  The CTAs add up their histograms through distributed shared
+// memory: each sums a share of the bins and writes it to all.
+#include <cooperative_groups.h>
+#include <float.h>
+#include <stddef.h>
+
+#include <mutex>
+#include <set>
+#include <type_traits>
+
 #include "common.cuh"
 #include "errors.h"
+
+namespace cg = cooperative_groups;
 
 namespace bm {
 namespace {
 
-constexpr int kThreads = 1024;
+using u64 = unsigned long long;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kTile = 128;            // indices a warp takes at once, four to a lane
+constexpr int kMaxTiles = 32;         // tiles of a warp
+constexpr int kMaxCluster = 16;
+constexpr int kBins = 1536;           // first histogram: three bins to a thread
+constexpr int kLastBin = 44 * 32;     // weights below 2^-44 are 0: one bin for all of them
+constexpr int kSub = 1024;            // finer histograms: two bins to a thread
+constexpr int kOne = 44;              // log2 of the largest weight
+
+// round(2^(30 + j/128))
+__device__ const uint32_t kExp2[128] = {
+    1073741824u, 1079572136u, 1085434106u, 1091327906u, 1097253708u, 1103211687u, 1109202018u, 1115224875u,
+    1121280436u, 1127368878u, 1133490379u, 1139645120u, 1145833280u, 1152055042u, 1158310587u, 1164600099u,
+    1170923762u, 1177281762u, 1183674286u, 1190101520u, 1196563654u, 1203060876u, 1209593378u, 1216161350u,
+    1222764986u, 1229404479u, 1236080024u, 1242791816u, 1249540052u, 1256324931u, 1263146652u, 1270005413u,
+    1276901417u, 1283834865u, 1290805962u, 1297814910u, 1304861917u, 1311947188u, 1319070932u, 1326233356u,
+    1333434672u, 1340675091u, 1347954824u, 1355274085u, 1362633090u, 1370032052u, 1377471191u, 1384950723u,
+    1392470869u, 1400031848u, 1407633882u, 1415277195u, 1422962010u, 1430688553u, 1438457051u, 1446267730u,
+    1454120821u, 1462016553u, 1469955159u, 1477936870u, 1485961921u, 1494030547u, 1502142985u, 1510299473u,
+    1518500250u, 1526745556u, 1535035634u, 1543370725u, 1551751076u, 1560176931u, 1568648537u, 1577166143u,
+    1585730000u, 1594340357u, 1602997467u, 1611701585u, 1620452965u, 1629251865u, 1638098541u, 1646993254u,
+    1655936265u, 1664927835u, 1673968228u, 1683057710u, 1692196547u, 1701385007u, 1710623359u, 1719911875u,
+    1729250827u, 1738640488u, 1748081133u, 1757573041u, 1767116489u, 1776711757u, 1786359126u, 1796058879u,
+    1805811301u, 1815616678u, 1825475297u, 1835387448u, 1845353420u, 1855373507u, 1865448001u, 1875577199u,
+    1885761398u, 1896000896u, 1906295993u, 1916646992u, 1927054196u, 1937517909u, 1948038440u, 1958616096u,
+    1969251188u, 1979944027u, 1990694927u, 2001504204u, 2012372174u, 2023299156u, 2034285470u, 2045331439u,
+    2056437387u, 2067603638u, 2078830522u, 2090118366u, 2101467502u, 2112878262u, 2124350982u, 2135885998u,
+};
 
 struct SampleArgs {
   const void* x;
   long long ld;
-  int V, B;
+  int V, B, tiles;                    // tiles: of a warp
   const float* temperature;
   const int32_t* top_k;
   const float* top_p;
@@ -35,170 +87,561 @@ struct SampleArgs {
   float* logp;
 };
 
-// Order-preserving bit pattern; NaN and -infinity are 0 (never drawn).
+// Order-preserving bit pattern of a logit without NaN and -0; -infinity is 0.
 __device__ __forceinline__ uint32_t key_of(float v) {
   const uint32_t b = __float_as_uint(v);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u || b == 0xFF800000u) return 0u;
-  if (b == 0x80000000u) return 0x80000000u;   // -0 equals +0
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return b == 0xFF800000u ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t k) {
-  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+  return k == 0 ? -INFINITY : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// NaN counts as -infinity, -0 as +0.
 template <typename T>
-__device__ __forceinline__ float load_logit(const void* x, long long i) {
-  if (sizeof(T) == 4) return static_cast<const float*>(x)[i];
-  return bf2f(static_cast<const bf16*>(x)[i]);
+__device__ __forceinline__ float clean(T v) {
+  const float f = (float)v + 0.0f;
+  return f != f ? -INFINITY : f;
 }
 
-template <typename T>
-__device__ T block_sum(T v, T* red) {
-  __syncthreads();
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  T s = 0;
-  for (int w = 0; w < kThreads / 32; ++w) s += red[w];
-  return s;
+struct Smem {
+  uint2 exp2[128];                    // kExp2 and its fp32 value
+  u64 best[kMaxCluster];              // by rank: largest key, lowest index
+  u64 sum[3][kMaxCluster];            // by rank: weight of the row, of its top-k set, above top-p's bins.  Each is
+                                      // told once: no CTA can overwrite what another still reads.
+  u64 kept[kMaxCluster];              // by rank: weight above the cut
+  uint32_t equal[kMaxCluster];        // by rank: logits equal to the cut
+  u64 warp64[kWarps];
+  uint32_t warp32[kWarps];
+  float warpf[2][kWarps];
+  u64 tile64[kMaxTiles];
+  uint32_t tile32[kMaxTiles];
+  u64 mine[kSub], all[kSub];          // a histogram of weights, the CTA's and the row's; counts as 32-bit words
+  int at[2];
+  u64 before;
+  float x[1];                         // [kWarps][tiles][kTile]
+};
+
+// Weights of a row: 2^((x - m) * c) with c = log2(e) / T in two words.
+struct Weights {
+  float m, ch, cl;
+  __device__ __forceinline__ u64 operator()(float x, const uint2* table) const {
+    // x - m exactly, as d + e
+    const float d = x - m, bb = d - x, e = (x - (d - bb)) + (-m - bb);
+    const float ph = d * ch, pl = fmaf(d, cl, fmaf(e, ch, fmaf(d, ch, -ph)));
+    // y = ph + pl = (128 n + j) / 128 + g
+    const float z = fmaf(ph, 128.f, 12582912.f), zf = z - 12582912.f;
+    const int N = __float_as_int(z) - 0x4B400000;
+    const float g = fmaf(zf, -1.f / 128, ph) + pl;
+    // 2^g - 1 for |g| <= 1/256: the next term of the series is below 2^-38
+    const float q = g * fmaf(g, fmaf(g, 0.05550411f, 0.24022651f), 0.69314718f);
+    const uint2 t = table[N & 127];
+    // t * 2^g, in steps of two: |t q| < 2^23
+    const float r = fmaf(__uint_as_float(t.y), q, 25165824.f);
+    const uint32_t w = t.x + 2u * (uint32_t)(__float_as_int(r) - 0x4BC00000);
+    const u64 v = ((u64)w << (kOne - 30)) >> min(63, -(N >> 7));
+    return ph > -45.f ? v : 0;
+  }
+  // step of 1/32 in log2 of the weight, from the top
+  __device__ __forceinline__ int bin(float x) const { return (int)fminf((m - x) * (32.f * ch), (float)kLastBin); }
+};
+
+__device__ __forceinline__ u64 warp_sum64(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
+// Sum over the lanes below this one and this one.
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T n = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v += n;
+  }
+  return v;
+}
+// Sum over the threads before this one; `tot` of all.  warp: kWarps words of shared memory.
+template <typename T>
+__device__ __forceinline__ T block_before(T v, T* warp, T* tot) {
+  const T inc = warp_scan(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 31) warp[threadIdx.x >> 5] = inc;
+  __syncthreads();
+  T b = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < (int)(threadIdx.x >> 5)) b += warp[w];
+    all += warp[w];
+  }
+  *tot = all;
+  return b + inc - v;
+}
+
+struct Row {
+  cg::cluster_group cl;
+  Smem& s;
+  int rank, n, tiles;
+  Weights w;
+  float4* tile;                       // this warp's tiles; lane's four logits of tile t at [32 t + lane]
+
+  __device__ void sync() const {
+    if (n == 1) __syncthreads();
+    else cl.sync();
+  }
+  // f(x) over this thread's logits
+  template <typename F>
+  __device__ __forceinline__ void sweep(F f) const {
+    for (int t = 0; t < tiles; ++t) {
+      const float4 v = tile[32 * t + (threadIdx.x & 31)];
+      f(v.x);
+      f(v.y);
+      f(v.z);
+      f(v.w);
+    }
+  }
+  // This CTA's value to slot[rank] of every CTA; read after the next sync().
+  template <typename T>
+  __device__ __forceinline__ void tell(T* slot, T v) const {
+    if ((int)threadIdx.x < n) cl.map_shared_rank(slot, threadIdx.x)[rank] = v;
+  }
+  template <typename T>
+  __device__ __forceinline__ T total(const T* slot) const {
+    T v = 0;
+    for (int r = 0; r < n; ++r) v += slot[r];
+    return v;
+  }
+  // all[0..count) = the CTAs' mine[] added up; mine[] is free again afterwards.
+  template <typename T>
+  __device__ void add_up(T* mine, T* all, int count) const {
+    sync();
+    const int share = (count + n - 1) / n;
+    for (int i = threadIdx.x; i < share; i += kThreads) {
+      const int b = rank * share + i;
+      if (b < count) {
+        T v = 0;
+#pragma unroll 8
+        for (int r = 0; r < n; ++r) v += cl.map_shared_rank(mine, r)[b];
+#pragma unroll 8
+        for (int r = 0; r < n; ++r) cl.map_shared_rank(all, r)[b] = v;
+      }
+    }
+    sync();
+  }
+  // Bounds of the keys whose bins are [b1, b2]; a little wider than they are.
+  __device__ void key_range(int b1, int b2, uint32_t& lo, uint32_t& hi) const {
+    const float step = 1.0f / (32.f * w.ch);
+    const float d1 = b1 * step, d2 = (b2 + 1) * step;
+    hi = key_of(w.m);
+    if (b1 > 0) hi = min(hi, key_of(w.m - d1 + 1e-5f * (fabsf(w.m) + d1)));
+    lo = 1;
+    if (b2 < kLastBin) {
+      const float v = w.m - d2 - 1e-5f * (fabsf(w.m) + d2);
+      if (v > -FLT_MAX) lo = max(lo, key_of(v));
+    }
+  }
+  // The key at which the weight (MASS) or the number of logits, taken from
+  // the largest key down, reaches `need`, among the keys of bins [b1, b2]
+  // that are at least `least`; *before is what the keys above it hold.  With
+  // MASS, the weight of the bins above b1 is summed on the way.
+  template <bool MASS>
+  __device__ uint32_t find(int b1, int b2, uint32_t least, u64 need, u64* before) const {
+    using Word = typename std::conditional<MASS, u64, uint32_t>::type;
+    Word* mine = reinterpret_cast<Word*>(s.mine);
+    Word* all = reinterpret_cast<Word*>(s.all);
+    uint32_t lo, hi;
+    key_range(b1, b2, lo, hi);
+    lo = max(lo, least);
+    hi = max(hi, lo);
+    u64 base = *before;
+    for (bool first = true;; first = false) {
+      const uint32_t width = hi - lo;
+      const int shift = max(0, 32 - __clz(width) - 10);
+      for (int i = threadIdx.x; i < kSub; i += kThreads) mine[i] = 0;
+      __syncthreads();
+      u64 above = 0;
+      sweep([&](float x) {
+        const int b = w.bin(x);
+        if (x == -INFINITY || b > b2) return;
+        if (b < b1) {
+          if (MASS && first) above += w(x, s.exp2);
+          return;
+        }
+        const uint32_t k = key_of(x);
+        if (k >= lo && k <= hi) atomicAdd(&mine[(hi - k) >> shift], MASS ? (Word)w(x, s.exp2) : (Word)1);
+      });
+      if (MASS && first) {
+        above = warp_sum64(above);
+        if ((threadIdx.x & 31) == 0) s.warp64[threadIdx.x >> 5] = above;
+        __syncthreads();
+        u64 t = 0;
+        for (int i = 0; i < kWarps; ++i) t += s.warp64[i];
+        tell(s.sum[2], t);
+      }
+      add_up(mine, all, kSub);
+      if (MASS && first) base += total(s.sum[2]);
+      // two bins to a thread
+      const u64 v0 = all[2 * threadIdx.x], v1 = all[2 * threadIdx.x + 1];
+      u64 tot;
+      const u64 b0 = base + block_before<u64>(v0 + v1, s.warp64, &tot);
+      if (threadIdx.x == 0) {
+        s.at[0] = (int)(width >> shift);   // should nothing reach `need`: the last bin
+        s.before = base;
+      }
+      __syncthreads();
+      if (b0 < need && b0 + v0 + v1 >= need) {
+        const bool second = b0 + v0 < need;
+        s.at[0] = 2 * threadIdx.x + second;
+        s.before = second ? b0 + v0 : b0;
+      }
+      __syncthreads();
+      const uint32_t sub = s.at[0];
+      base = s.before;
+      hi -= sub << shift;
+      const uint32_t span = (1u << shift) - 1;
+      lo = hi - lo > span ? hi - span : lo;
+      if (lo == hi) break;
+      __syncthreads();
+    }
+    *before = base;
+    return lo;
+  }
+};
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
-  __shared__ double red_d[32];
-  __shared__ int red_i[32];
-  __shared__ double part[kThreads];
-  const int b = blockIdx.x, V = a.V, t = threadIdx.x;
-  const long long row = b * a.ld;
-  auto key = [&](int i) { return key_of(load_logit<T>(a.x, row + i)); };
-  // thread t owns the indices [lo, hi): index order is thread order
-  const int lo = (int)((long long)V * t / kThreads), hi = (int)((long long)V * (t + 1) / kThreads);
-  const float T0 = a.temperature ? a.temperature[b] : 1.f;
-  const bool greedy = !(T0 > 0.f);
-  uint32_t best = 0;
-  for (int i = lo; i < hi; ++i) best = max(best, key(i));
-  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-  if ((t & 31) == 0) red_i[t >> 5] = (int)best;
+  extern __shared__ __align__(16) unsigned char raw[];
+  Smem& s = *reinterpret_cast<Smem*>(raw);
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = cl.block_rank(), n = cl.num_blocks(), b = blockIdx.x / n;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tiles = a.tiles, V = a.V;
+  float* xs = reinterpret_cast<float*>(raw + ((offsetof(Smem, x) + 15) & ~size_t(15)));
+  Row r{cl, s, rank, n, tiles, Weights{}, reinterpret_cast<float4*>(xs) + 32 * tiles * warp};
+
+  // Every CTA of the cluster has to have started before another writes to its shared memory.
+  if (n > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+
+  // ---- the row to shared memory, with its largest logit
+  const T* src = static_cast<const T*>(a.x) + b * a.ld;
+  const int first = (rank * kWarps + warp) * tiles * kTile;   // this warp's first index
+  const bool vec = (reinterpret_cast<uintptr_t>(src) & (4 * sizeof(T) - 1)) == 0;
+  u64 best = 0;
+#pragma unroll 4
+  for (int t = 0; t < tiles; ++t) {
+    const int i = first + t * kTile + 4 * lane;
+    float v[4];
+    if (vec && i + 3 < V) {
+      if (sizeof(T) == 4) {
+        const float4 f = __ldcs(reinterpret_cast<const float4*>(src + i));
+        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+      } else {
+        const uint2 f = __ldcs(reinterpret_cast<const uint2*>(src + i));
+        v[0] = bf_lo(f.x); v[1] = bf_hi(f.x); v[2] = bf_lo(f.y); v[3] = bf_hi(f.y);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = i + e < V ? (float)src[i + e] : -INFINITY;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = clean(v[e]);
+      const u64 k = ((u64)key_of(v[e]) << 32) | (uint32_t)~(i + e);
+      best = k > best ? k : best;
+    }
+    r.tile[32 * t + lane] = make_float4(v[0], v[1], v[2], v[3]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const u64 k = __shfl_xor_sync(0xffffffffu, best, o);
+    best = k > best ? k : best;
+  }
+  if (lane == 0) s.warp64[warp] = best;
+  if (tid < 128) s.exp2[tid] = make_uint2(kExp2[tid], __float_as_uint((float)kExp2[tid]));
+  if (n > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
-  for (int w = 0; w < 32; ++w) best = max(best, (uint32_t)red_i[w]);
-  __syncthreads();
-  if (best == 0) {
-    if (t == 0) {
-      a.ids[b] = -1;
-      if (a.logp) a.logp[b] = -INFINITY;
+  if (tid < n) {
+    for (int i = 0; i < kWarps; ++i) best = s.warp64[i] > best ? s.warp64[i] : best;
+    cl.map_shared_rank(s.best, tid)[rank] = best;
+  }
+  r.sync();
+  best = 0;
+  for (int i = 0; i < n; ++i) best = s.best[i] > best ? s.best[i] : best;
+  const uint32_t top = (uint32_t)(best >> 32);
+  const float temp = a.temperature ? a.temperature[b] : 1.f;
+  if (top == 0 || !(temp > 0.f)) {    // nothing to draw, or the argmax
+    if (rank == 0 && tid == 0) {
+      a.ids[b] = top == 0 ? -1 : (int32_t)~(uint32_t)best;
+      if (a.logp) a.logp[b] = top == 0 ? -INFINITY : 0.f;
     }
     return;
   }
-  const double top = value_of(best), invT = 1.0 / (double)(greedy ? 1.f : T0);
-  auto weight = [&](uint32_t k) -> double {
-    if (k == best) return 1.0;
-    return k == 0 ? 0.0 : exp(((double)value_of(k) - top) * invT);
-  };
-  // the kept set: key > cut, or key == cut and among the first `ties` indices
-  uint32_t cut = greedy ? best : 1;
-  long long ties = greedy ? 1 : V;
-  auto count_from = [&](uint32_t k) {
-    int n = 0;
-    for (int i = lo; i < hi; ++i) n += key(i) >= k;
-    return block_sum(n, red_i);
-  };
-  const int k = a.top_k && !greedy ? a.top_k[b] : 0;
-  if (k > 0 && k < V) {
-    uint32_t at = 0;   // the largest threshold that at least k keys reach
-    for (int bit = 31; bit >= 0; --bit)
-      if (count_from(at | (1u << bit)) >= k) at |= 1u << bit;
-    if (at > cut) {
-      cut = at;
-      ties = k - (at == 0xFFFFFFFFu ? 0 : count_from(at + 1));
+  r.w.m = value_of(top);
+  if (r.w.m == INFINITY) {            // the infinite logits share the row: they become 0, all others are masked
+    for (int t = 0; t < tiles; ++t) {
+      float4& v = r.tile[32 * t + lane];
+      v.x = v.x == INFINITY ? 0.f : -INFINITY;
+      v.y = v.y == INFINITY ? 0.f : -INFINITY;
+      v.z = v.z == INFINITY ? 0.f : -INFINITY;
+      v.w = v.w == INFINITY ? 0.f : -INFINITY;
     }
+    r.w.m = 0.f;
   }
-  // weight of the keys >= thr inside the top-k set
-  auto mass_from = [&](uint32_t thr) {
-    double s = 0;
-    for (int i = lo; i < hi; ++i) {
-      const uint32_t v = key(i);
-      if (v >= thr && v > cut) s += weight(v);
-    }
-    s = block_sum(s, red_d);
-    if (cut < thr) return s;
-    const long long equal = (long long)count_from(cut) - (cut == 0xFFFFFFFFu ? 0 : count_from(cut + 1));
-    return equal > 0 ? s + (double)min(ties, equal) * weight(cut) : s;
-  };
-  const float p = a.top_p && !greedy ? a.top_p[b] : 1.f;
-  if (p < 1.f) {
-    const double need = (double)p * mass_from(cut);
-    uint32_t at = 0;
-    for (int bit = 31; bit >= 0; --bit)
-      if (mass_from(at | (1u << bit)) >= need) at |= 1u << bit;
-    at = min(at, best);
-    const double above = at == 0xFFFFFFFFu ? 0.0 : mass_from(at + 1);
-    const double w = weight(at);
-    long long r = w > 0 ? (long long)ceil((need - above) / w) : 1;
-    r = max(r, 1LL);
-    if (at > cut || (at == cut && r < ties)) {
-      cut = at;
-      ties = r;
-    }
+  {
+    // below 2^-120 any two different logits of a model are infinitely far apart
+    const double c = 1.4426950408889634 / (double)fmaxf(temp, 7.5231638452626401e-37f);
+    r.w.ch = (float)c;
+    r.w.cl = (float)(c - (double)r.w.ch);
   }
-  const float mp = a.min_p && !greedy ? a.min_p[b] : 0.f;
-  if (mp > 0.f) {
-    uint32_t at = 0;   // the smallest key whose weight reaches min_p: weights rise with the key
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t cand = at | (1u << bit);
-      if (cand <= best && weight(cand - 1) < (double)fminf(mp, 1.f)) at = cand;
+  const Weights& w = r.w;
+
+  // ---- the cut: kept are the keys above it, and the first `ties` that equal it
+  uint32_t cut = 0, ties = 0;
+  const int k = a.top_k ? a.top_k[b] : 0;
+  const float p = a.top_p ? a.top_p[b] : 1.f, least = a.min_p ? a.min_p[b] : 0.f;
+  const bool use_k = k > 0 && k < V, use_p = p < 1.f;
+  if (use_k || use_p) {
+    uint32_t* mine = reinterpret_cast<uint32_t*>(s.mine);
+    uint32_t* hist = reinterpret_cast<uint32_t*>(s.all);
+    for (int i = tid; i < kBins; i += kThreads) mine[i] = 0;
+    __syncthreads();
+    u64 z = 0;
+    const bool with_sum = !use_k;
+    r.sweep([&](float x) {
+      if (x == -INFINITY) return;
+      atomicAdd(&mine[w.bin(x)], 1u);
+      if (with_sum) z += w(x, s.exp2);
+    });
+    if (with_sum) {
+      z = warp_sum64(z);
+      if (lane == 0) s.warp64[warp] = z;
+      __syncthreads();
+      z = 0;
+      for (int i = 0; i < kWarps; ++i) z += s.warp64[i];
+      r.tell(s.sum[0], z);
     }
-    if (at > cut) {
-      cut = at;
-      ties = V;
-    }
-  }
-  // equal keys before this thread's indices
-  int eq = 0;
-  for (int i = lo; i < hi; ++i) eq += key(i) == cut;
-  __syncthreads();
-  part[t] = eq;
-  __syncthreads();
-  long long before = 0;
-  for (int i = 0; i < t; ++i) before += (long long)part[i];
-  __syncthreads();
-  double s = 0;
-  long long seen = before;
-  for (int i = lo; i < hi; ++i) {
-    const uint32_t v = key(i);
-    if (v > cut || (v == cut && seen++ < ties)) s += weight(v);
-  }
-  part[t] = s;
-  __syncthreads();
-  if (t == 0) {
-    double total = 0;
-    for (int i = 0; i < kThreads; ++i) total += part[i];
-    const float u = a.u && a.u[b] > 0.f ? a.u[b] : 0.f;
-    const double target = (double)u * total;
-    double cum = 0;
-    int own = 0;
-    while (own < kThreads - 1 && cum + part[own] <= target) cum += part[own++];
-    // walk the owner's indices; a target past the last kept token takes that token
-    int id = -1;
-    double wid = 0;
-    for (int th = own; th >= 0 && id < 0; --th) {
-      const int l2 = (int)((long long)V * th / kThreads), h2 = (int)((long long)V * (th + 1) / kThreads);
-      long long eqs = 0;
-      for (int i = 0; i < l2; ++i) eqs += key(i) == cut;
-      for (int i = l2; i < h2; ++i) {
-        const uint32_t v = key(i);
-        if (v > cut || (v == cut && eqs++ < ties)) {
-          const double w = weight(v);
-          if (!(w > 0)) continue;
-          id = i;
-          wid = w;
-          cum += w;
-          if (th == own && cum > target) break;
+    r.add_up(mine, hist, kBins);
+    if (with_sum) z = r.total(s.sum[0]);
+    uint32_t c[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) c[i] = hist[3 * tid + i];
+    int k_bin = kLastBin;
+    if (use_k) {
+      uint32_t have;
+      const uint32_t b0 = block_before<uint32_t>(c[0] + c[1] + c[2], s.warp32, &have);
+      if (have > (uint32_t)k) {       // else the filter keeps all there are
+        uint32_t at = b0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          if (at < (uint32_t)k && at + c[i] >= (uint32_t)k) {
+            s.at[1] = 3 * tid + i;
+            s.before = at;
+          }
+          at += c[i];
         }
+        __syncthreads();
+        k_bin = s.at[1];
+        u64 before = s.before;
+        cut = r.find<false>(k_bin, k_bin, 1, (u64)k, &before);
+        ties = (uint32_t)(k - before);
+      }
+      if (use_p) {                    // the weight of what top-k keeps
+        const float cv = value_of(cut);
+        z = 0;
+        r.sweep([&](float x) {
+          if (x > cv) z += w(x, s.exp2);
+        });
+        z = warp_sum64(z);
+        __syncthreads();
+        if (lane == 0) s.warp64[warp] = z;
+        __syncthreads();
+        z = 0;
+        for (int i = 0; i < kWarps; ++i) z += s.warp64[i];
+        r.tell(s.sum[1], z);
+        r.sync();
+        z = r.total(s.sum[1]) + (ties ? ties * w(cv, s.exp2) : 0);
       }
     }
-    a.ids[b] = id;
-    if (a.logp) a.logp[b] = greedy ? 0.f : (float)log(wid / total);
+    if (use_p) {
+      const u64 need = max(1ull, (u64)ceil((double)fmaxf(p, 0.f) * (double)z));
+      // bins that may hold the cut: a bin's weights are within 2^(1/32) of each other.  fp32 sums of
+      // at most 1409 terms are good to 2^-13; the bounds are widened by 2^-12.
+      float lower = 0.f, upper = 0.f, lo3[3], up3[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int bin = 3 * tid + i;
+        const float edge = (float)c[i] * exp2f((float)kOne - (float)bin * (1.f / 32));
+        up3[i] = bin <= k_bin ? edge * (1.f + 1.f / 4096) + (float)c[i] : 0.f;
+        lo3[i] = bin < k_bin && bin < kLastBin ? edge * (0.97857206f * (1.f - 1.f / 4096)) : 0.f;
+        upper += up3[i];
+        lower += lo3[i];
+      }
+      float tot;
+      const float needf = (float)need;
+      float u0 = block_before<float>(upper, s.warpf[0], &tot), l0 = block_before<float>(lower, s.warpf[1], &tot);
+      if (tid == 0) {
+        s.at[0] = k_bin;
+        s.at[1] = k_bin;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        // the first bin that may reach `need`, and the first that surely does
+        if (c[i]) {
+          if ((u0 + up3[i]) * (1.f + 1.f / 4096) >= needf) atomicMin(&s.at[0], 3 * tid + i);
+          if ((l0 + lo3[i]) * (1.f - 1.f / 4096) >= needf) atomicMin(&s.at[1], 3 * tid + i);
+        }
+        u0 += up3[i];
+        l0 += lo3[i];
+      }
+      __syncthreads();
+      const int b1 = s.at[0], b2 = max(s.at[1], b1);
+      u64 before = 0;
+      const uint32_t k_cut = cut, k_ties = ties;
+      cut = r.find<true>(b1, b2, max(1u, k_cut), need, &before);
+      const u64 wc = w(value_of(cut), s.exp2);
+      const u64 want = wc ? (need - min(need, before) + wc - 1) / wc : 1;
+      ties = (uint32_t)min(want, (u64)V);
+      if (cut == k_cut) ties = min(ties, k_ties);
+    }
   }
+  const float cv = value_of(cut);
+  const u64 one = 1ull << kOne;
+  const u64 wmin = least > 0.f ? (u64)((double)fminf(least, 1.f) * (double)one) : 1;
+  const u64 wcut = ties ? w(cv, s.exp2) : 0;
+  if (wcut < wmin) ties = 0;
+
+  // ---- kept weight by warp, CTA and row
+  u64 mass = 0;
+  uint32_t eq = 0;
+  r.sweep([&](float x) {
+    if (x > cv) {
+      const u64 v = w(x, s.exp2);
+      mass += v >= wmin ? v : 0;
+    }
+    eq += x == cv;
+  });
+  mass = warp_sum64(mass);
+  eq = warp_sum(eq);
+  __syncthreads();
+  if (lane == 0) {
+    s.warp64[warp] = mass;
+    s.warp32[warp] = eq;
+  }
+  __syncthreads();
+  {
+    u64 m = 0;
+    uint32_t e = 0;
+    for (int i = 0; i < kWarps; ++i) {
+      m += s.warp64[i];
+      e += s.warp32[i];
+    }
+    r.tell(s.kept, m);
+    r.tell(s.equal, e);
+  }
+  r.sync();
+  const u64 kept = r.total(s.kept) + min((u64)ties, (u64)r.total(s.equal)) * wcut;
+  const float u = fmaxf(a.u[b], 0.f);  // NaN counts as 0
+  const double share = (double)u * (double)kept;
+  u64 target = share >= (double)kept ? kept - 1 : min((u64)share, kept - 1);
+  // the CTA, then the warp, then the tile that holds the target
+  int left = (int)ties, owner = -1;
+  for (int i = 0; i < n; ++i) {
+    const int e = min(left, (int)min(s.equal[i], 0x7FFFFFFFu));
+    const u64 v = s.kept[i] + e * wcut;
+    if (target < v) {
+      owner = i;
+      break;
+    }
+    target -= v;
+    left -= e;
+  }
+  if (owner != rank) return;
+  int own = 0;
+  for (; own < kWarps - 1; ++own) {
+    const int e = min(left, (int)s.warp32[own]);
+    const u64 v = s.warp64[own] + e * wcut;
+    if (target < v) break;
+    target -= v;
+    left -= e;
+  }
+  const float4* tile = reinterpret_cast<const float4*>(xs) + 32 * tiles * own;
+  auto four = [&](int t, u64 (&v)[4], uint32_t& same) {
+    const float4 x = tile[32 * t + lane];
+    const float xe[4] = {x.x, x.y, x.z, x.w};
+    same = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = 0;
+      if (xe[i] > cv) {
+        v[i] = w(xe[i], s.exp2);
+        if (v[i] < wmin) v[i] = 0;
+      }
+      same |= (uint32_t)(xe[i] == cv) << i;
+    }
+  };
+  u64 v[4];
+  uint32_t same;
+  for (int t = warp; t < tiles; t += kWarps) {
+    four(t, v, same);
+    const u64 m = warp_sum64(v[0] + v[1] + v[2] + v[3]);
+    const uint32_t e = warp_sum((uint32_t)__popc(same));
+    if (lane == 0) {
+      s.tile64[t] = m;
+      s.tile32[t] = e;
+    }
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  int at = 0;
+  for (; at < tiles - 1; ++at) {
+    const int e = min(left, (int)s.tile32[at]);
+    const u64 m = s.tile64[at] + e * wcut;
+    if (target < m) break;
+    target -= m;
+    left -= e;
+  }
+  four(at, v, same);
+  int e = left - ((int)warp_scan((uint32_t)__popc(same)) - __popc(same));   // ties left to this lane
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (same >> i & 1 && e-- > 0) v[i] = wcut;
+  const u64 sum = v[0] + v[1] + v[2] + v[3], upto = warp_scan(sum);
+  u64 cum = upto - sum;
+  if (!(cum <= target && target < upto)) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (cum <= target && target < cum + v[i]) {
+      a.ids[b] = (rank * kWarps + own) * tiles * kTile + at * kTile + 4 * lane + i;
+      if (a.logp) a.logp[b] = (float)log((double)v[i] / (double)kept);
+    }
+    cum += v[i];
+  }
+}
+
+std::mutex g_mu;
+std::set<int> g_devices;
+
+// Shared-memory and cluster attributes of both kernels on the current device.
+cudaError_t ensure_attributes() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_devices.count(dev)) return cudaSuccess;
+  const void* kernels[] = {(const void*)k_sample<float>, (const void*)k_sample<bf16>};
+  for (const void* f : kernels) {
+    if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+  }
+  g_devices.insert(dev);
+  return cudaSuccess;
+}
+
+// CTAs per row.
+int cluster_size(int B, int V) {
+  int n = 1;
+  while (n < 8 && n * 4096 < V) n *= 2;
+  if (V > 8 * kWarps * kTile * 20 || (n == 8 && B <= 4)) n = 16;
+  return n;
 }
 
 }  // namespace
@@ -214,11 +657,25 @@ extern "C" bm_status bm_sample(const void* logits, int dtype, int64_t ld, int V,
     return set_error(BM_ERR_INVALID_ARG, "bm_sample: need 1 <= B <= 65535 and 1 <= V <= " + std::to_string(BM_SAMPLE_MAX_VOCAB));
   if (ld < V) return set_error(BM_ERR_INVALID_ARG, "bm_sample: ld must be at least V");
   if ((uintptr_t)logits & (dtype == BM_F32 ? 3 : 1)) return set_error(BM_ERR_INVALID_ARG, "bm_sample: misaligned logits");
-  SampleArgs a{logits, ld, V, B, temperature, top_k, top_p, min_p, u, ids, logprobs};
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == BM_F32) k_sample<float><<<B, kThreads, 0, s>>>(a);
-  else k_sample<bf16><<<B, kThreads, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = ensure_attributes();
+  if (e == cudaSuccess) {
+    const int n = cluster_size(B, V);
+    const int tiles = (V + n * kWarps * kTile - 1) / (n * kWarps * kTile);
+    const SampleArgs a{logits, ld, V, B, tiles, temperature, top_k, top_p, min_p, u, ids, logprobs};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)B * n);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Smem) + 16 + (size_t)kWarps * tiles * kTile * sizeof(float);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = dtype == BM_F32 ? cudaLaunchKernelEx(&cfg, k_sample<float>, a) : cudaLaunchKernelEx(&cfg, k_sample<bf16>, a);
+  }
   if (e != cudaSuccess) return set_error(BM_ERR_CUDA, std::string("bm_sample: ") + cudaGetErrorString(e));
   return ok();
 }
