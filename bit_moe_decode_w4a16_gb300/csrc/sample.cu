@@ -20,13 +20,18 @@
 //
 // A row belongs to a cluster of up to 16 CTAs that keep it in shared memory:
 // it is read from global memory once, and every later sweep is on chip.  A
-// warp owns a run of consecutive indices, so index order is warp order.  The
-// cut is found by histograms: first of counts over 1/32-wide steps of
-// log2(w); for top-p, a bin's weight is between its count times the bin's
-// borders, which leaves a few bins that may hold the cut, and only these get
-// exact sums, over ever finer ranges of the ordered bit patterns of x (ten
-// bits a sweep).  The CTAs add up their histograms through distributed shared
-// memory: each sums a share of the bins and writes it to all.
+// warp owns a run of consecutive indices, so index order is warp order.  A
+// cut is found in two steps: a histogram over 1/23-wide steps of log2(w), of
+// counts for top-k and of weights for top-p, names the step that holds it;
+// the logits of that step, a few hundred as a rule, are gathered by every
+// CTA and searched there.  (A step that holds more than 2048, as in a row of
+// equal logits, is searched where it lies, by histograms over ten bits of the
+// logits' ordered bit patterns at a time.)  The CTAs add up histograms
+// through distributed shared memory: each sums a share of the bins and writes
+// it to all.
+//
+// What bounds it is instructions: about 45 for a weight, one weight a logit
+// without filters.
 #include <cooperative_groups.h>
 #include <float.h>
 #include <stddef.h>
@@ -49,9 +54,10 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kTile = 128;            // indices a warp takes at once, four to a lane
 constexpr int kMaxTiles = 32;         // tiles of a warp
 constexpr int kMaxCluster = 16;
-constexpr int kBins = 1536;           // first histogram: three bins to a thread
-constexpr int kLastBin = 44 * 32;     // weights below 2^-44 are 0: one bin for all of them
-constexpr int kSub = 1024;            // finer histograms: two bins to a thread
+constexpr int kBins = 1024;           // bins of a histogram: two to a thread
+constexpr int kSteps = 23;            // steps to a factor of two of the weight
+constexpr int kLastStep = 44 * kSteps;   // weights below 2^-44 are 0: one step for all of them
+constexpr int kList = 2 * kBins;      // logits a gathered step may have
 constexpr int kOne = 44;              // log2 of the largest weight
 
 // round(2^(30 + j/128))
@@ -103,22 +109,32 @@ __device__ __forceinline__ float clean(T v) {
   return f != f ? -INFINITY : f;
 }
 
+constexpr uint32_t kLowest = 0x00800000u;   // key of the lowest finite value
+
 struct Smem {
   uint2 exp2[128];                    // kExp2 and its fp32 value
-  u64 best[kMaxCluster];              // by rank: largest key, lowest index
-  u64 sum[3][kMaxCluster];            // by rank: weight of the row, of its top-k set, above top-p's bins.  Each is
-                                      // told once: no CTA can overwrite what another still reads.
-  u64 kept[kMaxCluster];              // by rank: weight above the cut
-  uint32_t equal[kMaxCluster];        // by rank: logits equal to the cut
+  // by rank; each is told once, so no CTA overwrites what another still reads
+  float top[kMaxCluster];             // largest logit
+  uint32_t listed[2][kMaxCluster];    // logits of the step that holds the cut: top-k's, top-p's
+  u64 kept[kMaxCluster];              // weight above the cut
+  uint32_t equal[kMaxCluster];        // logits equal to the cut
   u64 warp64[kWarps];
   uint32_t warp32[kWarps];
-  float warpf[2][kWarps];
+  float warpf[kWarps];
   u64 tile64[kMaxTiles];
   uint32_t tile32[kMaxTiles];
-  u64 mine[kSub], all[kSub];          // a histogram of weights, the CTA's and the row's; counts as 32-bit words
-  int at[2];
+  u64 mine[kBins], all[kBins];        // a histogram, the CTA's and the row's; counts in 32-bit words.  mine: also the CTA's list
+  float list[kList];                  // the row's list
+  int at;
+  uint32_t count;
   u64 before;
   float x[1];                         // [kWarps][tiles][kTile]
+};
+
+// The first step of a search, from its histogram: what the bins above it hold.
+struct Found {
+  int bin;
+  u64 before;
 };
 
 // Weights of a row: 2^((x - m) * c) with c = log2(e) / T in two words.
@@ -141,14 +157,22 @@ struct Weights {
     const u64 v = ((u64)w << (kOne - 30)) >> min(63, -(N >> 7));
     return ph > -45.f ? v : 0;
   }
-  // step of 1/32 in log2 of the weight, from the top
-  __device__ __forceinline__ int bin(float x) const { return (int)fminf((m - x) * (32.f * ch), (float)kLastBin); }
+  // ln(v / kept), v <= kept
+  __device__ float log_share(u64 v, u64 kept, const uint2*) const { return (float)log((double)v / (double)kept); }
+  // step of 1/kSteps in log2 of the weight, from the top
+  __device__ __forceinline__ int bin(float x) const { return (int)fminf((m - x) * (kSteps * ch), (float)kLastStep); }
 };
 
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+// 64-bit sum in shared memory from two 32-bit atomics: the low word's old value tells the carry.
+__device__ __forceinline__ void add64(u64* at, u64 v) {
+  uint32_t* p = reinterpret_cast<uint32_t*>(at);
+  const uint32_t lo = (uint32_t)v, old = atomicAdd(p, lo), hi = (uint32_t)(v >> 32) + (old + lo < old);
+  if (hi) atomicAdd(p + 1, hi);
 }
 // Sum over the lanes below this one and this one.
 template <typename T>
@@ -227,80 +251,103 @@ struct Row {
     }
     sync();
   }
-  // Bounds of the keys whose bins are [b1, b2]; a little wider than they are.
-  __device__ void key_range(int b1, int b2, uint32_t& lo, uint32_t& hi) const {
-    const float step = 1.0f / (32.f * w.ch);
-    const float d1 = b1 * step, d2 = (b2 + 1) * step;
-    hi = key_of(w.m);
-    if (b1 > 0) hi = min(hi, key_of(w.m - d1 + 1e-5f * (fabsf(w.m) + d1)));
-    lo = 1;
-    if (b2 < kLastBin) {
-      const float v = w.m - d2 - 1e-5f * (fabsf(w.m) + d2);
-      if (v > -FLT_MAX) lo = max(lo, key_of(v));
+  // The bin at which the histogram all[] reaches `need`, counted on from
+  // `base`; the last one that holds anything, should it not.  Also the sum.
+  template <typename Word>
+  __device__ Found reach(const Word* all, u64 base, u64 need, u64* sum) const {
+    const u64 v0 = all[2 * threadIdx.x], v1 = all[2 * threadIdx.x + 1];
+    const u64 b0 = base + block_before<u64>(v0 + v1, s.warp64, sum);
+    if (threadIdx.x == 0) {
+      s.at = 0;
+      s.before = base;
     }
+    __syncthreads();
+    const u64 end = base + *sum;
+    need = min(need, end);
+    if (b0 < need && b0 + v0 + v1 >= need) {
+      const bool second = b0 + v0 < need;
+      s.at = 2 * threadIdx.x + second;
+      s.before = second ? b0 + v0 : b0;
+    }
+    __syncthreads();
+    const Found f{s.at, s.before};
+    __syncthreads();
+    return f;
   }
-  // The key at which the weight (MASS) or the number of logits, taken from
-  // the largest key down, reaches `need`, among the keys of bins [b1, b2]
-  // that are at least `least`; *before is what the keys above it hold.  With
-  // MASS, the weight of the bins above b1 is summed on the way.
+  // Bounds of the keys of a step; a little wider than they are.
+  __device__ void key_range(int bin, uint32_t& lo, uint32_t& hi) const {
+    const float step = 1.0f / (kSteps * w.ch);
+    const float d1 = bin * step, d2 = (bin + 1) * step;
+    hi = key_of(w.m);
+    if (bin > 0) hi = min(hi, key_of(w.m - d1 + 1e-5f * (fabsf(w.m) + d1)));
+    lo = kLowest;
+    const float v = w.m - d2 - 1e-5f * (fabsf(w.m) + d2);
+    if (bin < kLastStep && v > -FLT_MAX) lo = key_of(v);
+  }
+  // The key at which the weight (MASS) or the number of the logits of step
+  // f.bin that are at least `least` reaches `need`, from the largest down,
+  // counted on from f.before; *before is what the keys above it hold.
   template <bool MASS>
-  __device__ uint32_t find(int b1, int b2, uint32_t least, u64 need, u64* before) const {
+  __device__ uint32_t find(Found f, uint32_t least, u64 need, uint32_t* listed, u64* before) const {
     using Word = typename std::conditional<MASS, u64, uint32_t>::type;
-    Word* mine = reinterpret_cast<Word*>(s.mine);
-    Word* all = reinterpret_cast<Word*>(s.all);
     uint32_t lo, hi;
-    key_range(b1, b2, lo, hi);
+    key_range(f.bin, lo, hi);
     lo = max(lo, least);
     hi = max(hi, lo);
-    u64 base = *before;
-    for (bool first = true;; first = false) {
-      const uint32_t width = hi - lo;
-      const int shift = max(0, 32 - __clz(width) - 10);
-      for (int i = threadIdx.x; i < kSub; i += kThreads) mine[i] = 0;
+    const float vlo = value_of(lo), vhi = value_of(hi);
+    // every CTA's logits of the step to every CTA
+    float* own = reinterpret_cast<float*>(s.mine);
+    if (threadIdx.x == 0) s.count = 0;
+    __syncthreads();
+    sweep([&](float x) {
+      if (x >= vlo && x <= vhi && w.bin(x) == f.bin) {
+        const uint32_t i = atomicAdd(&s.count, 1u);
+        if (i < kList) own[i] = x;
+      }
+    });
+    __syncthreads();
+    tell(listed, s.count);
+    sync();
+    const uint32_t count = total(listed);
+    const bool gathered = count <= kList;
+    if (gathered) {
+      uint32_t off = 0;
+      for (int i = 0; i < n; ++i) {
+        const float* theirs = cl.map_shared_rank(own, i);
+        for (uint32_t j = threadIdx.x; j < listed[i]; j += kThreads) s.list[off + j] = theirs[j];
+        off += listed[i];
+      }
+    }
+    Word* mine = reinterpret_cast<Word*>(gathered ? s.all : s.mine);
+    Word* all = reinterpret_cast<Word*>(s.all);
+    u64 base = f.before;
+    for (;;) {
+      const int shift = max(0, 32 - __clz(hi - lo) - 10);
+      for (int i = threadIdx.x; i < kBins; i += kThreads) mine[i] = 0;
       __syncthreads();
-      u64 above = 0;
-      sweep([&](float x) {
-        const int b = w.bin(x);
-        if (x == -INFINITY || b > b2) return;
-        if (b < b1) {
-          if (MASS && first) above += w(x, s.exp2);
-          return;
-        }
+      auto put = [&](float x) {
         const uint32_t k = key_of(x);
-        if (k >= lo && k <= hi) atomicAdd(&mine[(hi - k) >> shift], MASS ? (Word)w(x, s.exp2) : (Word)1);
-      });
-      if (MASS && first) {
-        above = warp_sum64(above);
-        if ((threadIdx.x & 31) == 0) s.warp64[threadIdx.x >> 5] = above;
+        if (k >= lo && k <= hi) {
+          if (MASS) add64(reinterpret_cast<u64*>(&mine[(hi - k) >> shift]), w(x, s.exp2));
+          else atomicAdd(reinterpret_cast<uint32_t*>(&mine[(hi - k) >> shift]), 1u);
+        }
+      };
+      if (gathered) {
+        for (uint32_t i = threadIdx.x; i < count; i += kThreads) put(s.list[i]);
         __syncthreads();
-        u64 t = 0;
-        for (int i = 0; i < kWarps; ++i) t += s.warp64[i];
-        tell(s.sum[2], t);
+      } else {
+        sweep([&](float x) {
+          if (x >= vlo && x <= vhi && w.bin(x) == f.bin) put(x);
+        });
+        add_up(mine, all, kBins);
       }
-      add_up(mine, all, kSub);
-      if (MASS && first) base += total(s.sum[2]);
-      // two bins to a thread
-      const u64 v0 = all[2 * threadIdx.x], v1 = all[2 * threadIdx.x + 1];
-      u64 tot;
-      const u64 b0 = base + block_before<u64>(v0 + v1, s.warp64, &tot);
-      if (threadIdx.x == 0) {
-        s.at[0] = (int)(width >> shift);   // should nothing reach `need`: the last bin
-        s.before = base;
-      }
-      __syncthreads();
-      if (b0 < need && b0 + v0 + v1 >= need) {
-        const bool second = b0 + v0 < need;
-        s.at[0] = 2 * threadIdx.x + second;
-        s.before = second ? b0 + v0 : b0;
-      }
-      __syncthreads();
-      const uint32_t sub = s.at[0];
-      base = s.before;
-      hi -= sub << shift;
+      u64 sum;
+      const Found g = reach(all, base, need, &sum);
+      base = g.before;
+      hi -= (uint32_t)g.bin << shift;
       const uint32_t span = (1u << shift) - 1;
       lo = hi - lo > span ? hi - span : lo;
       if (lo == hi) break;
-      __syncthreads();
     }
     *before = base;
     return lo;
@@ -324,8 +371,12 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
   const T* src = static_cast<const T*>(a.x) + b * a.ld;
   const int first = (rank * kWarps + warp) * tiles * kTile;   // this warp's first index
   const bool vec = (reinterpret_cast<uintptr_t>(src) & (4 * sizeof(T) - 1)) == 0;
-  u64 best = 0;
-#pragma unroll 4
+  // the row's settings, and log2(e) / T in two words, while the row is on its way
+  const float temp = a.temperature ? a.temperature[b] : 1.f;
+  const int k = a.top_k ? a.top_k[b] : 0;
+  const float p = a.top_p ? a.top_p[b] : 1.f, least = a.min_p ? a.min_p[b] : 0.f, u = fmaxf(a.u[b], 0.f);   // NaN u: 0
+  float best = -INFINITY;
+#pragma unroll 5
   for (int t = 0; t < tiles; ++t) {
     const int i = first + t * kTile + 4 * lane;
     float v[4];
@@ -344,38 +395,33 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       v[e] = clean(v[e]);
-      const u64 k = ((u64)key_of(v[e]) << 32) | (uint32_t)~(i + e);
-      best = k > best ? k : best;
+      best = fmaxf(best, v[e]);
     }
     r.tile[32 * t + lane] = make_float4(v[0], v[1], v[2], v[3]);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const u64 k = __shfl_xor_sync(0xffffffffu, best, o);
-    best = k > best ? k : best;
-  }
-  if (lane == 0) s.warp64[warp] = best;
+  best = warp_max(best);
+  if (lane == 0) s.warpf[warp] = best;
   if (tid < 128) s.exp2[tid] = make_uint2(kExp2[tid], __float_as_uint((float)kExp2[tid]));
+  {
+    // below 2^-120 any two different logits of a model are infinitely far apart
+    const float t = fmaxf(temp, 7.5231638452626401e-37f);
+    r.w.ch = 1.44269502f / t;
+    r.w.cl = t < INFINITY ? (fmaf(-r.w.ch, t, 1.44269502f) + 1.92596303e-08f) / t : 0.f;
+  }
   if (n > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
-  if (tid < n) {
-    for (int i = 0; i < kWarps; ++i) best = s.warp64[i] > best ? s.warp64[i] : best;
-    cl.map_shared_rank(s.best, tid)[rank] = best;
-  }
+  for (int i = 0; i < kWarps; ++i) best = fmaxf(best, s.warpf[i]);
+  r.tell(s.top, best);
   r.sync();
-  best = 0;
-  for (int i = 0; i < n; ++i) best = s.best[i] > best ? s.best[i] : best;
-  const uint32_t top = (uint32_t)(best >> 32);
-  const float temp = a.temperature ? a.temperature[b] : 1.f;
-  if (top == 0 || !(temp > 0.f)) {    // nothing to draw, or the argmax
+  for (int i = 0; i < n; ++i) best = fmaxf(best, s.top[i]);
+  if (best == -INFINITY) {            // nothing to draw
     if (rank == 0 && tid == 0) {
-      a.ids[b] = top == 0 ? -1 : (int32_t)~(uint32_t)best;
-      if (a.logp) a.logp[b] = top == 0 ? -INFINITY : 0.f;
+      a.ids[b] = -1;
+      if (a.logp) a.logp[b] = -INFINITY;
     }
     return;
   }
-  r.w.m = value_of(top);
-  if (r.w.m == INFINITY) {            // the infinite logits share the row: they become 0, all others are masked
+  if (best == INFINITY) {             // the infinite logits share the row: they become 0, all others are masked
     for (int t = 0; t < tiles; ++t) {
       float4& v = r.tile[32 * t + lane];
       v.x = v.x == INFINITY ? 0.f : -INFINITY;
@@ -383,120 +429,53 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
       v.z = v.z == INFINITY ? 0.f : -INFINITY;
       v.w = v.w == INFINITY ? 0.f : -INFINITY;
     }
-    r.w.m = 0.f;
+    best = 0.f;
   }
-  {
-    // below 2^-120 any two different logits of a model are infinitely far apart
-    const double c = 1.4426950408889634 / (double)fmaxf(temp, 7.5231638452626401e-37f);
-    r.w.ch = (float)c;
-    r.w.cl = (float)(c - (double)r.w.ch);
-  }
+  r.w.m = best;
   const Weights& w = r.w;
 
   // ---- the cut: kept are the keys above it, and the first `ties` that equal it
   uint32_t cut = 0, ties = 0;
-  const int k = a.top_k ? a.top_k[b] : 0;
-  const float p = a.top_p ? a.top_p[b] : 1.f, least = a.min_p ? a.min_p[b] : 0.f;
-  const bool use_k = k > 0 && k < V, use_p = p < 1.f;
-  if (use_k || use_p) {
-    uint32_t* mine = reinterpret_cast<uint32_t*>(s.mine);
-    uint32_t* hist = reinterpret_cast<uint32_t*>(s.all);
-    for (int i = tid; i < kBins; i += kThreads) mine[i] = 0;
-    __syncthreads();
-    u64 z = 0;
-    const bool with_sum = !use_k;
-    r.sweep([&](float x) {
-      if (x == -INFINITY) return;
-      atomicAdd(&mine[w.bin(x)], 1u);
-      if (with_sum) z += w(x, s.exp2);
-    });
-    if (with_sum) {
-      z = warp_sum64(z);
-      if (lane == 0) s.warp64[warp] = z;
+  if (!(temp > 0.f)) {                // the argmax, lowest index first
+    cut = key_of(best);
+    ties = 1;
+  } else {
+    if (k > 0 && k < V) {
+      uint32_t* mine = reinterpret_cast<uint32_t*>(s.mine);
+      uint32_t* all = reinterpret_cast<uint32_t*>(s.all);
+      for (int i = tid; i < kBins; i += kThreads) mine[i] = 0;
       __syncthreads();
-      z = 0;
-      for (int i = 0; i < kWarps; ++i) z += s.warp64[i];
-      r.tell(s.sum[0], z);
-    }
-    r.add_up(mine, hist, kBins);
-    if (with_sum) z = r.total(s.sum[0]);
-    uint32_t c[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) c[i] = hist[3 * tid + i];
-    int k_bin = kLastBin;
-    if (use_k) {
-      uint32_t have;
-      const uint32_t b0 = block_before<uint32_t>(c[0] + c[1] + c[2], s.warp32, &have);
-      if (have > (uint32_t)k) {       // else the filter keeps all there are
-        uint32_t at = b0;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          if (at < (uint32_t)k && at + c[i] >= (uint32_t)k) {
-            s.at[1] = 3 * tid + i;
-            s.before = at;
-          }
-          at += c[i];
-        }
-        __syncthreads();
-        k_bin = s.at[1];
-        u64 before = s.before;
-        cut = r.find<false>(k_bin, k_bin, 1, (u64)k, &before);
+      r.sweep([&](float x) {
+        if (x > -INFINITY) atomicAdd(&mine[w.bin(x)], 1u);
+      });
+      r.add_up(mine, all, kBins);
+      u64 have;
+      const Found f = r.reach(all, 0, (u64)k, &have);
+      if (have > (u64)k) {            // else there are no more than k
+        u64 before;
+        cut = r.template find<false>(f, 1, (u64)k, s.listed[0], &before);
         ties = (uint32_t)(k - before);
-      }
-      if (use_p) {                    // the weight of what top-k keeps
-        const float cv = value_of(cut);
-        z = 0;
-        r.sweep([&](float x) {
-          if (x > cv) z += w(x, s.exp2);
-        });
-        z = warp_sum64(z);
-        __syncthreads();
-        if (lane == 0) s.warp64[warp] = z;
-        __syncthreads();
-        z = 0;
-        for (int i = 0; i < kWarps; ++i) z += s.warp64[i];
-        r.tell(s.sum[1], z);
-        r.sync();
-        z = r.total(s.sum[1]) + (ties ? ties * w(cv, s.exp2) : 0);
+        if (p < 1.f) r.sync();        // every CTA has read the lists
       }
     }
-    if (use_p) {
+    if (p < 1.f) {
+      const float kv = value_of(cut);
+      const u64 tied = ties ? w(kv, s.exp2) : 0;
+      for (int i = tid; i < kBins; i += kThreads) s.mine[i] = 0;
+      __syncthreads();
+      r.sweep([&](float x) {
+        if (x > kv) add64(&s.mine[w.bin(x)], w(x, s.exp2));
+      });
+      if (rank == 0 && tid == 0 && ties) add64(&s.mine[w.bin(kv)], ties * tied);
+      r.add_up(s.mine, s.all, kBins);
+      u64 z = 0;
+      for (int i = lane; i < kBins; i += 32) z += s.all[i];
+      z = warp_sum64(z);
       const u64 need = max(1ull, (u64)ceil((double)fmaxf(p, 0.f) * (double)z));
-      // bins that may hold the cut: a bin's weights are within 2^(1/32) of each other.  fp32 sums of
-      // at most 1409 terms are good to 2^-13; the bounds are widened by 2^-12.
-      float lower = 0.f, upper = 0.f, lo3[3], up3[3];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int bin = 3 * tid + i;
-        const float edge = (float)c[i] * exp2f((float)kOne - (float)bin * (1.f / 32));
-        up3[i] = bin <= k_bin ? edge * (1.f + 1.f / 4096) + (float)c[i] : 0.f;
-        lo3[i] = bin < k_bin && bin < kLastBin ? edge * (0.97857206f * (1.f - 1.f / 4096)) : 0.f;
-        upper += up3[i];
-        lower += lo3[i];
-      }
-      float tot;
-      const float needf = (float)need;
-      float u0 = block_before<float>(upper, s.warpf[0], &tot), l0 = block_before<float>(lower, s.warpf[1], &tot);
-      if (tid == 0) {
-        s.at[0] = k_bin;
-        s.at[1] = k_bin;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        // the first bin that may reach `need`, and the first that surely does
-        if (c[i]) {
-          if ((u0 + up3[i]) * (1.f + 1.f / 4096) >= needf) atomicMin(&s.at[0], 3 * tid + i);
-          if ((l0 + lo3[i]) * (1.f - 1.f / 4096) >= needf) atomicMin(&s.at[1], 3 * tid + i);
-        }
-        u0 += up3[i];
-        l0 += lo3[i];
-      }
-      __syncthreads();
-      const int b1 = s.at[0], b2 = max(s.at[1], b1);
-      u64 before = 0;
+      const Found f = r.reach(s.all, 0, need, &z);
       const uint32_t k_cut = cut, k_ties = ties;
-      cut = r.find<true>(b1, b2, max(1u, k_cut), need, &before);
+      u64 before;
+      cut = r.template find<true>(f, max(1u, k_cut), need, s.listed[1], &before);
       const u64 wc = w(value_of(cut), s.exp2);
       const u64 want = wc ? (need - min(need, before) + wc - 1) / wc : 1;
       ties = (uint32_t)min(want, (u64)V);
@@ -505,7 +484,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
   }
   const float cv = value_of(cut);
   const u64 one = 1ull << kOne;
-  const u64 wmin = least > 0.f ? (u64)((double)fminf(least, 1.f) * (double)one) : 1;
+  const u64 wmin = least > 0.f && temp > 0.f ? (u64)((double)fminf(least, 1.f) * (double)one) : 1;
   const u64 wcut = ties ? w(cv, s.exp2) : 0;
   if (wcut < wmin) ties = 0;
 
@@ -539,7 +518,6 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
   }
   r.sync();
   const u64 kept = r.total(s.kept) + min((u64)ties, (u64)r.total(s.equal)) * wcut;
-  const float u = fmaxf(a.u[b], 0.f);  // NaN counts as 0
   const double share = (double)u * (double)kept;
   u64 target = share >= (double)kept ? kept - 1 : min((u64)share, kept - 1);
   // the CTA, then the warp, then the tile that holds the target
@@ -611,7 +589,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
   for (int i = 0; i < 4; ++i) {
     if (cum <= target && target < cum + v[i]) {
       a.ids[b] = (rank * kWarps + own) * tiles * kTile + at * kTile + 4 * lane + i;
-      if (a.logp) a.logp[b] = (float)log((double)v[i] / (double)kept);
+      if (a.logp) a.logp[b] = temp > 0.f ? w.log_share(v[i], kept, s.exp2) : 0.f;
     }
     cum += v[i];
   }
