@@ -21,7 +21,7 @@
 // A row belongs to a cluster of up to 16 CTAs that keep it in shared memory:
 // it is read from global memory once, and every later sweep is on chip.  A
 // warp owns a run of consecutive indices, so index order is warp order.  A
-// cut is found in two steps: a histogram over 1/23-wide steps of log2(w), of
+// cut is found in two steps: a histogram over 1/32-wide steps of log2(w), of
 // counts for top-k and of weights for top-p, names the step that holds it;
 // the logits of that step, a few hundred as a rule, are gathered by every
 // CTA and searched there.  (A step that holds more than 2048, as in a row of
@@ -55,8 +55,8 @@ constexpr int kTile = 128;            // indices a warp takes at once, four to a
 constexpr int kMaxTiles = 32;         // tiles of a warp
 constexpr int kMaxCluster = 16;
 constexpr int kBins = 1024;           // bins of a histogram: two to a thread
-constexpr int kSteps = 23;            // steps to a factor of two of the weight
-constexpr int kLastStep = 44 * kSteps;   // weights below 2^-44 are 0: one step for all of them
+constexpr int kSteps = 32;            // steps to a factor of two of the weight
+constexpr int kLastStep = kBins - 1;  // one step for all weights below 2^-31.97
 constexpr int kList = 2 * kBins;      // logits a gathered step may have
 constexpr int kOne = 44;              // log2 of the largest weight
 
@@ -137,37 +137,95 @@ struct Found {
   u64 before;
 };
 
+// 2^y for y = hi + lo <= 0: 2^30 * 2^(j/128 + g) in w, and the power of two it is to be divided by.
+__device__ __forceinline__ uint32_t exp2_parts(float hi, float lo, const uint2* table, int& down) {
+  hi = fmaxf(hi, -60.f);
+  // hi = (128 n + j) / 128 + g; the bits of z hold 128 n + j
+  const float z = fmaf(hi, 128.f, 12582912.f);
+  const float g = fmaf(z - 12582912.f, -1.f / 128, hi) + lo;
+  const int N = __float_as_int(z) - 0x4B400000;
+  down = -(N >> 7);
+  // 2^g - 1 for |g| <= 1/256: the next term of the series is below 2^-38
+  const float q = g * fmaf(g, fmaf(g, 0.05550411f, 0.24022651f), 0.69314718f);
+  const uint2 t = table[N & 127];
+  // t * 2^g, in steps of two: |t q| < 2^23
+  return t.x + 2u * (uint32_t)(__float_as_int(fmaf(__uint_as_float(t.y), q, 25165824.f)) - 0x4BC00000);
+}
+
 // Weights of a row: 2^((x - m) * c) with c = log2(e) / T in two words.
 struct Weights {
   float m, ch, cl;
-  __device__ __forceinline__ u64 operator()(float x, const uint2* table) const {
-    // x - m exactly, as d + e
-    const float d = x - m, bb = d - x, e = (x - (d - bb)) + (-m - bb);
-    const float ph = d * ch, pl = fmaf(d, cl, fmaf(e, ch, fmaf(d, ch, -ph)));
-    // y = ph + pl = (128 n + j) / 128 + g
-    const float z = fmaf(ph, 128.f, 12582912.f), zf = z - 12582912.f;
-    const int N = __float_as_int(z) - 0x4B400000;
-    const float g = fmaf(zf, -1.f / 128, ph) + pl;
-    // 2^g - 1 for |g| <= 1/256: the next term of the series is below 2^-38
-    const float q = g * fmaf(g, fmaf(g, 0.05550411f, 0.24022651f), 0.69314718f);
-    const uint2 t = table[N & 127];
-    // t * 2^g, in steps of two: |t q| < 2^23
-    const float r = fmaf(__uint_as_float(t.y), q, 25165824.f);
-    const uint32_t w = t.x + 2u * (uint32_t)(__float_as_int(r) - 0x4BC00000);
-    const u64 v = ((u64)w << (kOne - 30)) >> min(63, -(N >> 7));
-    return ph > -45.f ? v : 0;
+  // log2 of x's weight as hi + lo
+  __device__ __forceinline__ float exponent(float x, float& lo) const {
+    const float d = x - m, bb = d - x, e = (x - (d - bb)) + (-m - bb);   // x - m = d + e
+    const float hi = d * ch;
+    lo = fmaf(d, cl, fmaf(e, ch, fmaf(d, ch, -hi)));
+    return hi;
   }
-  // ln(v / kept), v <= kept
-  __device__ float log_share(u64 v, u64 kept, const uint2*) const { return (float)log((double)v / (double)kept); }
+  // sum + (take ? the weight of x : 0).  The weight is 2^30..2^31 in 32 bits, multiplied up or, where it is
+  // below 2^-14 of the largest, shifted down and rounded: one wide multiply-add, and no 64-bit shift.
+  __device__ __forceinline__ u64 add(u64 sum, float x, const uint2* table, bool take = true) const {
+    float lo;
+    int down;
+    const float hi = exponent(x, lo);
+    const uint32_t w = exp2_parts(hi, lo, table, down);
+    const int up = kOne - 30 - down;
+    const uint32_t v = (__funnelshift_rc(2 * w, 0u, max(0, -up)) + (up < 0)) >> 1;
+    return (u64)v * (take ? 1u << max(0, up) : 0u) + sum;
+  }
+  __device__ __forceinline__ u64 operator()(float x, const uint2* table) const { return add(0, x, table); }
+  // The weight of x, of step `bin`, in units of 2^(kOne - 31 - octave): below 2^32, for all of a step the same unit.
+  __device__ __forceinline__ uint32_t in_step(float x, int bin, const uint2* table) const {
+    float lo;
+    int down;
+    const float hi = exponent(x, lo);
+    const uint32_t w = exp2_parts(hi, lo, table, down);
+    const int up = bin / kSteps + 1 - down;              // 0 or 1, but for the last step
+    return up >= 0 ? w << up : __funnelshift_rc(w, 0u, -up);
+  }
+  static __device__ __forceinline__ u64 from_step(u64 sum, int bin) {
+    const int up = kOne - 31 - bin / kSteps;
+    return up >= 0 ? sum << up : (sum + (1ull << (-up - 1))) >> -up;
+  }
   // step of 1/kSteps in log2 of the weight, from the top
   __device__ __forceinline__ int bin(float x) const { return (int)fminf((m - x) * (kSteps * ch), (float)kLastStep); }
 };
+
+// ln(v / total), 0 < v <= total, to fp32: an fp32 logarithm of the quotient's mantissa, corrected once
+// by its exponential in integers.
+__device__ float log_share(u64 v, u64 total, const uint2* table) {
+  const int zv = __clzll(v), zt = __clzll(total);
+  const u64 a = v << zv, b = total << zt;                  // v / total = a / b * 2^(zt - zv)
+  const u64 small = a < b ? a : b, large = a < b ? b : a;
+  const float y = fminf(log2f((float)small / (float)large), 0.f);
+  int down;
+  const uint32_t w = exp2_parts(y, 0.f, table, down);
+  const u64 back = __umul64hi(large, (u64)w << (33 - down)) << 1;   // large * 2^y
+  const float off = (float)(long long)(small - back) / (float)small * 1.44269502f;
+  // log2(v / total) = hi + lo
+  const float e = (float)(zt - zv), l = a < b ? y : -y;
+  const float hi = e + l, lo = (l - (hi - e)) + (a < b ? off : -off);
+  const float r = hi * 0.693147182f;
+  return r + fmaf(lo, 0.693147182f, fmaf(hi, 0.693147182f, -r) + hi * -1.90465421e-09f);
+}
 
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// A histogram's sums of 32-bit weights: 16 bits to a word, as a CTA has fewer than 2^16 logits (no carry,
+// so nothing waits for an atomic's old value).
+struct Halves {
+  uint32_t lo, hi;
+  __device__ __forceinline__ void add(uint32_t v) {
+    atomicAdd(&lo, v & 0xFFFFu);
+    atomicAdd(&hi, v >> 16);
+  }
+  __device__ __forceinline__ u64 sum() const { return lo + ((u64)hi << 16); }
+};
+static_assert(kWarps * kMaxTiles * kTile <= 1 << 16, "a word of Halves holds a CTA's sum");
+
 // 64-bit sum in shared memory from two 32-bit atomics: the low word's old value tells the carry.
 __device__ __forceinline__ void add64(u64* at, u64 v) {
   uint32_t* p = reinterpret_cast<uint32_t*>(at);
@@ -212,16 +270,46 @@ struct Row {
     if (n == 1) __syncthreads();
     else cl.sync();
   }
-  // f(x) over this thread's logits
+  // f(four logits) over this thread's
+  template <typename F>
+  __device__ __forceinline__ void sweep4(F f) const {
+    for (int t = 0; t < tiles; ++t) f(tile[32 * t + (threadIdx.x & 31)]);
+  }
   template <typename F>
   __device__ __forceinline__ void sweep(F f) const {
-    for (int t = 0; t < tiles; ++t) {
-      const float4 v = tile[32 * t + (threadIdx.x & 31)];
+    sweep4([&](const float4 v) {
       f(v.x);
       f(v.y);
       f(v.z);
       f(v.w);
-    }
+    });
+  }
+  // f(x, x > cut) over the logits, where any of four is above it: with a branch
+  // to each, their latencies would add up
+  template <typename F>
+  __device__ __forceinline__ void sweep_above(float cut, F f) const {
+    sweep4([&](const float4 v) {
+      const bool a = v.x > cut, b = v.y > cut, c = v.z > cut, d = v.w > cut;
+      if (a || b || c || d) {
+        f(v.x, a);
+        f(v.y, b);
+        f(v.z, c);
+        f(v.w, d);
+      }
+    });
+  }
+  // f(x) over the logits in [lo, hi], which are few
+  template <typename F>
+  __device__ __forceinline__ void sweep_range(float lo, float hi, F f) const {
+    sweep4([&](const float4 v) {
+      const bool a = v.x >= lo && v.x <= hi, b = v.y >= lo && v.y <= hi, c = v.z >= lo && v.z <= hi, d = v.w >= lo && v.w <= hi;
+      if (a || b || c || d) {
+        if (a) f(v.x);
+        if (b) f(v.y);
+        if (c) f(v.z);
+        if (d) f(v.w);
+      }
+    });
   }
   // This CTA's value to slot[rank] of every CTA; read after the next sync().
   template <typename T>
@@ -234,45 +322,45 @@ struct Row {
     for (int r = 0; r < n; ++r) v += slot[r];
     return v;
   }
-  // all[0..count) = the CTAs' mine[] added up; mine[] is free again afterwards.
-  template <typename T>
-  __device__ void add_up(T* mine, T* all, int count) const {
+  // all[] = the CTAs' mine[] added up; mine[] is free again afterwards.  A CTA
+  // sums kBins / n of the bins, n / 2 lanes to a bin, and tells all CTAs.
+  template <typename M, typename T>
+  __device__ void add_up(M* mine, T* all) const {
     sync();
-    const int share = (count + n - 1) / n;
-    for (int i = threadIdx.x; i < share; i += kThreads) {
-      const int b = rank * share + i;
-      if (b < count) {
-        T v = 0;
-#pragma unroll 8
-        for (int r = 0; r < n; ++r) v += cl.map_shared_rank(mine, r)[b];
-#pragma unroll 8
-        for (int r = 0; r < n; ++r) cl.map_shared_rank(all, r)[b] = v;
-      }
+    if (n == 1) {
+      for (int b = threadIdx.x; b < kBins; b += kThreads) all[b] = whole(mine[b], b);
+    } else {
+      const int per = n / 2, b = rank * (kBins / n) + threadIdx.x / per, q = threadIdx.x & (per - 1);
+      const M v0 = cl.map_shared_rank(mine, q)[b], v1 = cl.map_shared_rank(mine, q + per)[b];
+      T v = whole(v0, b) + whole(v1, b);
+      for (int o = per / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      cl.map_shared_rank(all, q)[b] = v;
+      cl.map_shared_rank(all, q + per)[b] = v;
     }
     sync();
   }
-  // The bin at which the histogram all[] reaches `need`, counted on from
-  // `base`; the last one that holds anything, should it not.  Also the sum.
-  template <typename Word>
-  __device__ Found reach(const Word* all, u64 base, u64 need, u64* sum) const {
-    const u64 v0 = all[2 * threadIdx.x], v1 = all[2 * threadIdx.x + 1];
-    const u64 b0 = base + block_before<u64>(v0 + v1, s.warp64, sum);
+  static __device__ __forceinline__ uint32_t whole(uint32_t v, int) { return v; }
+  static __device__ __forceinline__ u64 whole(u64 v, int) { return v; }
+  static __device__ __forceinline__ u64 whole(Halves v, int bin) { return Weights::from_step(v.sum(), bin); }
+  // The bin at which the histogram all[], of sum s, reaches need(s), counted
+  // on from `base`; the last one that holds anything, should it not.
+  // Between two calls there is a barrier.
+  template <typename Word, typename F>
+  __device__ Found reach(const Word* all, u64 base, F need_of) const {
     if (threadIdx.x == 0) {
       s.at = 0;
       s.before = base;
     }
-    __syncthreads();
-    const u64 end = base + *sum;
-    need = min(need, end);
+    const u64 v0 = all[2 * threadIdx.x], v1 = all[2 * threadIdx.x + 1];
+    u64 sum;
+    const u64 b0 = base + block_before<u64>(v0 + v1, s.warp64, &sum), need = min((u64)need_of(sum), base + sum);
     if (b0 < need && b0 + v0 + v1 >= need) {
       const bool second = b0 + v0 < need;
       s.at = 2 * threadIdx.x + second;
       s.before = second ? b0 + v0 : b0;
     }
     __syncthreads();
-    const Found f{s.at, s.before};
-    __syncthreads();
-    return f;
+    return Found{s.at, s.before};
   }
   // Bounds of the keys of a step; a little wider than they are.
   __device__ void key_range(int bin, uint32_t& lo, uint32_t& hi) const {
@@ -299,11 +387,10 @@ struct Row {
     float* own = reinterpret_cast<float*>(s.mine);
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
-    sweep([&](float x) {
-      if (x >= vlo && x <= vhi && w.bin(x) == f.bin) {
-        const uint32_t i = atomicAdd(&s.count, 1u);
-        if (i < kList) own[i] = x;
-      }
+    sweep_range(vlo, vhi, [&](float x) {
+      if (w.bin(x) != f.bin) return;
+      const uint32_t i = atomicAdd(&s.count, 1u);
+      if (i < kList) own[i] = x;
     });
     __syncthreads();
     tell(listed, s.count);
@@ -311,11 +398,12 @@ struct Row {
     const uint32_t count = total(listed);
     const bool gathered = count <= kList;
     if (gathered) {
-      uint32_t off = 0;
-      for (int i = 0; i < n; ++i) {
+      const int i = threadIdx.x >> 5;   // warp i takes the list of CTA i
+      if (i < n) {
+        uint32_t off = 0;
+        for (int j = 0; j < i; ++j) off += listed[j];
         const float* theirs = cl.map_shared_rank(own, i);
-        for (uint32_t j = threadIdx.x; j < listed[i]; j += kThreads) s.list[off + j] = theirs[j];
-        off += listed[i];
+        for (uint32_t j = threadIdx.x & 31; j < listed[i]; j += 32) s.list[off + j] = theirs[j];
       }
     }
     Word* mine = reinterpret_cast<Word*>(gathered ? s.all : s.mine);
@@ -336,13 +424,12 @@ struct Row {
         for (uint32_t i = threadIdx.x; i < count; i += kThreads) put(s.list[i]);
         __syncthreads();
       } else {
-        sweep([&](float x) {
-          if (x >= vlo && x <= vhi && w.bin(x) == f.bin) put(x);
+        sweep_range(vlo, vhi, [&](float x) {
+          if (w.bin(x) == f.bin) put(x);
         });
-        add_up(mine, all, kBins);
+        add_up(mine, all);
       }
-      u64 sum;
-      const Found g = reach(all, base, need, &sum);
+      const Found g = reach(all, base, [&](u64) { return need; });
       base = g.before;
       hi -= (uint32_t)g.bin << shift;
       const uint32_t span = (1u << shift) - 1;
@@ -448,9 +535,12 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
       r.sweep([&](float x) {
         if (x > -INFINITY) atomicAdd(&mine[w.bin(x)], 1u);
       });
-      r.add_up(mine, all, kBins);
-      u64 have;
-      const Found f = r.reach(all, 0, (u64)k, &have);
+      r.add_up(mine, all);
+      u64 have = 0;
+      const Found f = r.reach(all, 0, [&](u64 sum) {
+        have = sum;
+        return (u64)k;
+      });
       if (have > (u64)k) {            // else there are no more than k
         u64 before;
         cut = r.template find<false>(f, 1, (u64)k, s.listed[0], &before);
@@ -460,44 +550,53 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
     }
     if (p < 1.f) {
       const float kv = value_of(cut);
-      const u64 tied = ties ? w(kv, s.exp2) : 0;
+      Halves* mine = reinterpret_cast<Halves*>(s.mine);
       for (int i = tid; i < kBins; i += kThreads) s.mine[i] = 0;
       __syncthreads();
-      r.sweep([&](float x) {
-        if (x > kv) add64(&s.mine[w.bin(x)], w(x, s.exp2));
+      r.sweep_above(kv, [&](float x, bool above) {
+        const int bin = w.bin(x);
+        const uint32_t v = w.in_step(x, bin, s.exp2);
+        if (above) mine[bin].add(v);
       });
-      if (rank == 0 && tid == 0 && ties) add64(&s.mine[w.bin(kv)], ties * tied);
-      r.add_up(s.mine, s.all, kBins);
-      u64 z = 0;
-      for (int i = lane; i < kBins; i += 32) z += s.all[i];
-      z = warp_sum64(z);
-      const u64 need = max(1ull, (u64)ceil((double)fmaxf(p, 0.f) * (double)z));
-      const Found f = r.reach(s.all, 0, need, &z);
+      r.add_up(mine, s.all);
+      if (ties) {                     // the logits that top-k's cut shares, by count
+        if (tid == 0) s.all[w.bin(kv)] += ties * w(kv, s.exp2);
+        __syncthreads();
+      }
+      const u64 p64 = __float2ull_rz(fmaxf(p, 0.f) * 18446744073709551616.f);   // p < 1 in 64 binary places
+      u64 need = 0;
+      const Found f = r.reach(s.all, 0, [&](u64 sum) { return need = max(1ull, __umul64hi(sum, p64) + (sum * p64 != 0)); });
       const uint32_t k_cut = cut, k_ties = ties;
       u64 before;
       cut = r.template find<true>(f, max(1u, k_cut), need, s.listed[1], &before);
       const u64 wc = w(value_of(cut), s.exp2);
-      const u64 want = wc ? (need - min(need, before) + wc - 1) / wc : 1;
+      const u64 rest = need - min(need, before), want = rest <= wc ? 1 : wc ? (rest + wc - 1) / wc : 1;
       ties = (uint32_t)min(want, (u64)V);
       if (cut == k_cut) ties = min(ties, k_ties);
     }
   }
   const float cv = value_of(cut);
   const u64 one = 1ull << kOne;
-  const u64 wmin = least > 0.f && temp > 0.f ? (u64)((double)fminf(least, 1.f) * (double)one) : 1;
+  const u64 wmin = least > 0.f && temp > 0.f ? __float2ull_rz(fminf(least, 1.f) * (float)one) : 0;
   const u64 wcut = ties ? w(cv, s.exp2) : 0;
   if (wcut < wmin) ties = 0;
 
   // ---- kept weight by warp, CTA and row
   u64 mass = 0;
   uint32_t eq = 0;
-  r.sweep([&](float x) {
-    if (x > cv) {
-      const u64 v = w(x, s.exp2);
-      mass += v >= wmin ? v : 0;
+  if (cut == 0 && wmin == 0) {
+    r.sweep([&](float x) { mass = w.add(mass, x, s.exp2); });
+  } else {
+    if (wmin) {
+      r.sweep_above(cv, [&](float x, bool above) {
+        const u64 v = w(x, s.exp2);
+        mass += above && v >= wmin ? v : 0;
+      });
+    } else {
+      r.sweep_above(cv, [&](float x, bool above) { mass = w.add(mass, x, s.exp2, above); });
     }
-    eq += x == cv;
-  });
+    if (ties) r.sweep([&](float x) { eq += x == cv; });
+  }
   mass = warp_sum64(mass);
   eq = warp_sum(eq);
   __syncthreads();
@@ -518,8 +617,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
   }
   r.sync();
   const u64 kept = r.total(s.kept) + min((u64)ties, (u64)r.total(s.equal)) * wcut;
-  const double share = (double)u * (double)kept;
-  u64 target = share >= (double)kept ? kept - 1 : min((u64)share, kept - 1);
+  u64 target = u >= 1.f ? kept - 1 : __umul64hi(kept, __float2ull_rz(u * 18446744073709551616.f));
   // the CTA, then the warp, then the tile that holds the target
   int left = (int)ties, owner = -1;
   for (int i = 0; i < n; ++i) {
@@ -589,7 +687,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
   for (int i = 0; i < 4; ++i) {
     if (cum <= target && target < cum + v[i]) {
       a.ids[b] = (rank * kWarps + own) * tiles * kTile + at * kTile + 4 * lane + i;
-      if (a.logp) a.logp[b] = temp > 0.f ? w.log_share(v[i], kept, s.exp2) : 0.f;
+      if (a.logp) a.logp[b] = temp > 0.f ? log_share(v[i], kept, s.exp2) : 0.f;
     }
     cum += v[i];
   }
