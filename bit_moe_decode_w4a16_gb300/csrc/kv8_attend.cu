@@ -11,6 +11,9 @@
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "kv8.cuh"
 
@@ -19,7 +22,9 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kMaxGroup = 8;
+constexpr int kMaxGroup = 8, kMaxBatch = 1024;
+constexpr int kMaxRecords = 128;      // of a stream: 64 chunks of the prefix, 64 of its own
+constexpr int kSms = 152;
 
 struct AttendArgs {
   Cache c, p;            // the streams' cache, the prefix's
@@ -42,118 +47,452 @@ struct AttendArgs {
   }
 };
 
-// One chunk of one (stream, kv head): a warp takes every eighth position,
-// a lane d / 32 of its elements.
+// ---------------------------------------------------------------- one pass over a chunk
+//
+// A work item is a chunk of positions and up to 8 query rows of one kv head:
+// the group of a stream over its own positions, or 8 of the batch's rows over
+// the prefix.  The item's four warps take 16 positions each of every stage
+// of 64; each keeps a running maximum, sum and output of its own, and the
+// four are merged at the end of the item.  A warp streams its positions
+// through a ring of its own in shared memory (cp.async, two stages ahead,
+// across items), so the loop has no barrier between warps.
+//
+// On the tensor cores (mma.sync m16n8k16, fp16, fp32 sums), with g = lane / 4
+// and t = lane % 4:
+//   S = Q K^T: rows are heads (8 to 15 are zero), columns positions.  The
+//     reduction over d is permuted: lane t takes the 16-byte pieces of a K
+//     row that it reads whole, and q in the same order.  Codes become fp16
+//     exactly; the score is multiplied by the position's scale in fp32.
+//   O^T = V^T P^T: rows are elements of d, columns heads.  S's layout is
+//     P^T's: no exchange.  Row g of tile j is element 16g + 2j, row g + 8 the
+//     next one, so that lane (g, t) reads 16 bytes of each of its four
+//     positions and interleaves them by byte.
+// A weight enters as fp16(p * vs).  Its reference is the running maximum of
+// s + log2(vs), not of s: the product stays in fp16's range whatever V's
+// magnitude, and what is rounded away is small against the largest term of
+// the sum.  The reference moves only when it is passed by 2^8 (an fp16 holds
+// that), so the output is seldom rescaled.
+constexpr int kWarpsPerItem = 4, kStage = 64, kRing = 3;
+
+template <int D>
+struct Ring {
+  uint8_t k[16 * D], v[16 * D];
+  float ks[16], vs[16];
+};
+
+template <int D>
+struct ChunkSmem {
+  Ring<D> ring[kWarpsPerItem][kRing];
+  float o[kWarpsPerItem][8][D + 8];
+  float m[kWarpsPerItem][8], l[kWarpsPerItem][8];
+  int table[1];                       // [B] slots, [B] lengths, [B + 1] own items before each stream's
+};
+
+// 16-byte piece c of a position's codes in the ring: swizzled so that both products read without bank conflicts.
+template <int D>
+__device__ __forceinline__ int piece(int token, int c) {
+  return token * D + 16 * (D == 128 ? c ^ (token & 7) : c ^ (token >> 1 & 3));
+}
+
+// Two codes in the low half of w -> fp16 pair (exact).
+template <int FMT>
+__device__ __forceinline__ uint32_t codes2(uint32_t w) {
+  uint32_t r;
+  if (FMT == BM_KV8_E4M3) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(r) : "r"(w));
+  } else {
+    // 0x64 in front of u = code + 128 is the fp16 1024 + u
+    const uint32_t u = __byte_perm(w ^ 0x8080u, 0x64646464u, 0x4140);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1152.f));
+    r = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return r;
+}
+template <int FMT>
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  lo = codes2<FMT>(w);
+  hi = codes2<FMT>(w >> 16);
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool live) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool live) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+struct Item {
+  const uint8_t *K, *V;
+  const float *Ks, *Vs;
+  int n, kh, b, row0, rec;            // positions; kv head; stream, or -1 with the first of 8 rows; record
+};
+
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) k_kv8_chunk(AttendArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float so[8][kMaxGroup][D], sm[8][kMaxGroup], sl[8][kMaxGroup];
-  const int b = blockIdx.z, kh = blockIdx.y, r = blockIdx.x;
-  int slot, len;
-  if (!a.live(b, slot, len)) return;
-  const bool pre = r < a.p_chunks;
-  const int size = pre ? a.p_chunk : chunk_of(len), j0 = (pre ? r : r - a.p_chunks) * size;
-  const int n = min(size, (pre ? a.p_len : len) - j0);
-  if (n <= 0) return;
-  const Cache& c = pre ? a.p : a.c;
-  const size_t row0 = c.row(pre ? a.p_slot : slot, kh, j0);
-  const int G = a.qh / a.c.kvh, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float q[kMaxGroup][E], o[kMaxGroup][E], m[kMaxGroup], l[kMaxGroup];
+__global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs a) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  ChunkSmem<D>& sm = *reinterpret_cast<ChunkSmem<D>*>(raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int kvh = a.c.kvh, G = a.qh / kvh, rows = a.B * G;
+  int *slots = sm.table, *lens = slots + a.B, *first = lens + a.B;
+
+  // ---- the items: the prefix's, then each stream's own
+  const int row_blocks = (rows + 7) / 8, pre_items = kvh * a.p_chunks * row_blocks;
+  if (warp == 0) {
+    int sum = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int slot, len, c = 0;
+      if (b0 + lane < a.B) {
+        if (a.live(b0 + lane, slot, len)) c = chunks_of(len) * kvh;
+        slots[b0 + lane] = slot;
+        lens[b0 + lane] = len;
+      }
+      int inc = c;
 #pragma unroll
-  for (int g = 0; g < kMaxGroup; ++g) {
-    m[g] = -FLT_MAX;
-    l[g] = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      o[g][e] = 0.f;
-      q[g][e] = g < G ? bf2f(a.Q[((size_t)b * a.qh + kh * G + g) * D + lane * E + e]) : 0.f;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (b0 + lane < a.B) first[b0 + lane] = sum + inc - c;
+      sum += __shfl_sync(0xffffffffu, inc, 31);
     }
-  }
-  for (int j = warp; j < n; j += 8) {
-    float k[4], v[4];
-    uint32_t kw, vw;
-    if (E == 4) {
-      kw = reinterpret_cast<const uint32_t*>(c.K + (row0 + j) * D)[lane];
-      vw = reinterpret_cast<const uint32_t*>(c.V + (row0 + j) * D)[lane];
-    } else {
-      kw = reinterpret_cast<const uint16_t*>(c.K + (row0 + j) * D)[lane];
-      vw = reinterpret_cast<const uint16_t*>(c.V + (row0 + j) * D)[lane];
-    }
-    decode4<FMT>(kw, k);
-    decode4<FMT>(vw, v);
-    const float ks = c.Ks[row0 + j], vs = c.Vs[row0 + j];
-#pragma unroll
-    for (int g = 0; g < kMaxGroup; ++g) {
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(q[g][e], k[e], s);
-      s = warp_sum(s) * ks * a.scale_log2;
-      const float mn = fmaxf(m[g], s), f = exp2f(m[g] - mn), p = exp2f(s - mn);
-      m[g] = mn;
-      l[g] = l[g] * f + p;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[g][e] = o[g][e] * f + p * vs * v[e];
-    }
-  }
-#pragma unroll
-  for (int g = 0; g < kMaxGroup; ++g) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][g][lane * E + e] = o[g][e];
-    if (lane == 0) {
-      sm[warp][g] = m[g];
-      sl[warp][g] = l[g];
-    }
+    if (lane == 0) first[a.B] = sum;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < G * D; i += 256) {
-    const int g = i / D, d = i - g * D;
-    float mx = -FLT_MAX, den = 0.f, acc = 0.f;
-    for (int w = 0; w < 8; ++w) mx = fmaxf(mx, sm[w][g]);
-    for (int w = 0; w < 8; ++w) {
-      const float f = exp2f(sm[w][g] - mx);
-      den += sl[w][g] * f;
-      acc += so[w][g][d] * f;
+  const int items = pre_items + first[a.B];
+  auto item_of = [&](int it) {
+    Item i;
+    const Cache* c;
+    int slot, j0, size, len;
+    if (it < pre_items) {
+      i.kh = it / (a.p_chunks * row_blocks);
+      const int r = it - i.kh * a.p_chunks * row_blocks, ch = r / row_blocks;
+      i.b = -1;
+      i.row0 = (r - ch * row_blocks) * 8;
+      i.rec = ch;
+      c = &a.p;
+      slot = a.p_slot;
+      size = a.p_chunk;
+      len = a.p_len;
+      j0 = ch * size;
+    } else {
+      it -= pre_items;
+      int lo = 0, hi = a.B;           // the last stream with first <= it
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (first[mid] <= it) lo = mid;
+        else hi = mid;
+      }
+      const int r = it - first[lo];
+      i.b = lo;
+      i.row0 = 0;
+      i.kh = r % kvh;
+      c = &a.c;
+      slot = slots[lo];
+      len = lens[lo];
+      size = chunk_of(len);
+      j0 = r / kvh * size;
+      i.rec = a.p_chunks + r / kvh;
     }
-    float* rec = a.record(b, kh * G + g, r, D);
-    rec[d] = acc;
-    if (d == 0) {
-      rec[D] = mx;
-      rec[D + 1] = den;
+    const size_t row = c->row(slot, i.kh, j0);
+    i.K = c->K + row * D;
+    i.V = c->V + row * D;
+    i.Ks = c->Ks + row;
+    i.Vs = c->Vs + row;
+    i.n = min(size, len - j0);
+    return i;
+  };
+
+  // ---- loads run two stages ahead of the arithmetic, into the next item too
+  int load_it = blockIdx.x, load_j = 0, load_slot = 0;
+  Item li{};
+  if (load_it < items) li = item_of(load_it);
+  auto load = [&]() {
+    if (load_it < items) {
+      Ring<D>& s = sm.ring[warp][load_slot];
+      const int j = load_j + 16 * warp;
+      constexpr int kPieces = D / 16;
+#pragma unroll
+      for (int i = 0; i < kPieces / 2; ++i) {
+        const int c = lane + 32 * i, token = c / kPieces, p = c % kPieces;
+        const bool live = j + token < li.n;
+        const size_t off = live ? (size_t)(j + token) * D + 16 * p : 0;
+        copy16(s.k + piece<D>(token, p), li.K + off, live);
+        copy16(s.v + piece<D>(token, p), li.V + off, live);
+      }
+      const int token = lane & 15;
+      const bool live = j + token < li.n;
+      const float* src = (lane < 16 ? li.Ks : li.Vs) + (live ? j + token : 0);
+      copy4((lane < 16 ? s.ks : s.vs) + token, src, live);
+      load_slot = load_slot + 1 == kRing ? 0 : load_slot + 1;
+      load_j += kStage;
+      if (load_j >= li.n) {
+        load_it += gridDim.x;
+        load_j = 0;
+        if (load_it < items) li = item_of(load_it);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) load();
+
+  int slot = 0;
+  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    const Item i = item_of(it);
+    // ---- this lane's query row (head g), as fp16 of about its own magnitude
+    constexpr int kPer = D / 64;      // 16-byte pieces of a K row per lane
+    uint32_t q[kPer][4][2];
+    float qf = a.scale_log2;
+    {
+      const int r = i.row0 + g, b = i.b < 0 ? r / G : i.b, h = i.kh * G + (i.b < 0 ? r - b * G : r);
+      const bool live = i.b < 0 ? r < rows : r < G;
+      uint4 x[kPer][2];
+      float mx = 0.f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          x[j][u] = make_uint4(0, 0, 0, 0);
+          if (live) x[j][u] = *reinterpret_cast<const uint4*>(a.Q + ((size_t)b * a.qh + h) * D + 16 * (kPer * t + j) + 8 * u);
+          const uint32_t w[4] = {x[j][u].x, x[j][u].y, x[j][u].z, x[j][u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w[e])), fabsf(bf_hi(w[e]))));
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // a power of two: exact, and undone on the scores
+      float down = 1.f;
+      if (mx >= 1e-30f && mx <= 1e30f) {
+        const uint32_t e = __float_as_uint(mx) >> 23;
+        down = __uint_as_float((254u - e) << 23);
+        qf *= __uint_as_float(e << 23);
+      }
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t w[4] = {x[j][u].x, x[j][u].y, x[j][u].z, x[j][u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 v = __floats2half2_rn(bf_lo(w[e]) * down, bf_hi(w[e]) * down);
+            q[j][2 * u + e / 2][e & 1] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+        }
+    }
+    constexpr int kTiles = D / 16;
+    float o[kTiles][4], m = -1e30f, l = 0.f;
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+
+    for (int j0 = 0; j0 < i.n; j0 += kStage) {
+      load();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      __syncwarp();
+      const Ring<D>& s = sm.ring[warp][slot];
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+      const int left = i.n - j0 - 16 * warp;   // positions of this warp's 16
+      if (left > 0) {
+        float c[2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const uint4 k = *reinterpret_cast<const uint4*>(s.k + piece<D>(8 * nt + g, kPer * t + j));
+            const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t b0, b1;
+              codes4<FMT>(w[e], b0, b1);
+              mma16816(c[nt], q[j][e][0], 0u, q[j][e][1], 0u, b0, b1);
+            }
+          }
+        }
+        // head g, positions 8 nt + 2 t + e
+        float p[2][2], vs[2][2], mx = -1e30f;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const float2 kf = *reinterpret_cast<const float2*>(&s.ks[8 * nt + 2 * t]);
+          const float2 vf = *reinterpret_cast<const float2*>(&s.vs[8 * nt + 2 * t]);
+          vs[nt][0] = vf.x;
+          vs[nt][1] = vf.y;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float sc = c[nt][e] * ((e ? kf.y : kf.x) * qf);
+            p[nt][e] = 8 * nt + 2 * t + e < left ? sc : -INFINITY;
+            mx = fmaxf(mx, p[nt][e] + fmaxf(__log2f(vs[nt][e]), -100.f));
+          }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+          const float mn = fmaxf(m, mx), f = exp2_fast(m - mn);
+          m = mn;
+          l *= f;
+          const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j) {
+            o[j][0] *= f0;
+            o[j][1] *= f1;
+            o[j][2] *= f0;
+            o[j][3] *= f1;
+          }
+        }
+        uint32_t pb[2];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const float p0 = exp2_fast(p[nt][0] - m), p1 = exp2_fast(p[nt][1] - m);
+          l += p0 + p1;
+          const __half2 w = __floats2half2_rn(p0 * vs[nt][0], p1 * vs[nt][1]);
+          pb[nt] = *reinterpret_cast<const uint32_t*>(&w);
+        }
+        uint32_t v[4][D / 32];        // this lane's D / 8 codes of positions 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int token = 2 * t + (r & 1) + 8 * (r >> 1);
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(s.v + piece<D>(token, g));
+            v[r][0] = x.x; v[r][1] = x.y; v[r][D / 32 - 2] = x.z; v[r][D / 32 - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(s.v + piece<D>(token, g >> 1) + 8 * (g & 1));
+            v[r][0] = x.x; v[r][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
+          uint32_t a0, a1, a2, a3;
+          codes4<FMT>(__byte_perm(v[0][j / 2], v[1][j / 2], sel), a0, a1);
+          codes4<FMT>(__byte_perm(v[2][j / 2], v[3][j / 2], sel), a2, a3);
+          mma16816(o[j], a0, a1, a2, a3, pb[0], pb[1]);
+        }
+      }
+      __syncwarp();                   // every lane has read the slot before it is loaded again
+    }
+
+    // ---- the item's record from the four warps'
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    __syncthreads();
+    if (t == 0) {
+      sm.m[warp][g] = m;
+      sm.l[warp][g] = l;
+    }
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      const int d = D / 8 * g + 2 * j;
+      *reinterpret_cast<float2*>(&sm.o[warp][2 * t][d]) = make_float2(o[j][0], o[j][2]);
+      *reinterpret_cast<float2*>(&sm.o[warp][2 * t + 1][d]) = make_float2(o[j][1], o[j][3]);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int r = warp; r < 8; r += kWarpsPerItem) {
+      const int row = i.row0 + r, b = i.b < 0 ? row / G : i.b, h = i.kh * G + (i.b < 0 ? row - b * G : row);
+      if (i.b < 0 ? row >= rows : row >= G) break;
+      float f[kWarpsPerItem], mx = sm.m[0][r], den = 0.f;
+#pragma unroll
+      for (int w = 1; w < kWarpsPerItem; ++w) mx = fmaxf(mx, sm.m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kWarpsPerItem; ++w) {
+        f[w] = exp2_fast(sm.m[w][r] - mx);
+        den += sm.l[w][r] * f[w];
+      }
+      float* rec = a.record(b, h, i.rec, D);
+#pragma unroll
+      for (int d = 2 * lane; d < D; d += 64) {
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarpsPerItem; ++w) {
+          const float2 v = *reinterpret_cast<const float2*>(&sm.o[w][r][d]);
+          acc.x = fmaf(v.x, f[w], acc.x);
+          acc.y = fmaf(v.y, f[w], acc.y);
+        }
+        *reinterpret_cast<float2*>(rec + d) = acc;
+      }
+      if (lane == 0) *reinterpret_cast<float2*>(rec + D) = make_float2(mx, den);
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // One head of one stream: its records in ascending order.
 template <int D>
 __global__ void __launch_bounds__(D) k_kv8_merge(AttendArgs a) {
+  __shared__ float f[kMaxRecords];
+  __shared__ float red[2];
   const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+  pdl_wait();
   int slot, len;
   if (!a.live(b, slot, len)) return;
   const int n = a.p_chunks + chunks_of(len);
-  float mx = -FLT_MAX, den = 0.f, acc = 0.f;
-  for (int r = 0; r < n; ++r) mx = fmaxf(mx, a.record(b, h, r, D)[D]);
-  for (int r = 0; r < n; ++r) {
-    const float* rec = a.record(b, h, r, D);
-    const float f = exp2f(rec[D] - mx);
-    den += rec[D + 1] * f;
-    acc += rec[d] * f;
+  const float* rec = a.record(b, h, 0, D);
+  if (d < 32) {
+    float mx = -FLT_MAX, den = 0.f;
+    for (int r = d; r < n; r += 32) mx = fmaxf(mx, rec[r * (D + 2) + D]);
+    mx = warp_max(mx);
+    for (int r = d; r < n; r += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(rec + r * (D + 2) + D);
+      f[r] = exp2f(ml.x - mx);
+      den += ml.y * f[r];
+    }
+    den = warp_sum(den);
+    if (d == 0) red[0] = den;
   }
-  a.O[((size_t)b * a.qh + h) * D + d] = f2bf(n == 0 ? 0.f : acc / den);   // no positions: zeros
+  __syncthreads();
+  float acc = 0.f;
+#pragma unroll 8
+  for (int r = 0; r < n; ++r) acc = fmaf(rec[r * (D + 2) + d], f[r], acc);
+  a.O[((size_t)b * a.qh + h) * D + d] = f2bf(n == 0 ? 0.f : acc / red[0]);   // no positions: zeros
+}
+
+// Shared-memory attribute of a kernel on the current device, set once.
+std::mutex g_mu;
+std::set<std::pair<int, const void*>> g_set;
+
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_set.count({dev, kernel})) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) g_set.insert({dev, kernel});
+  return e;
 }
 
 template <int D, int FMT>
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
-  const int per_stream = a.p_chunks + a.own_chunks;
-  if (per_stream > 0) k_kv8_chunk<D, FMT><<<dim3(per_stream, a.c.kvh, a.B), 256, 0, s>>>(a);
-  k_kv8_merge<D><<<dim3(a.qh, a.B), D, 0, s>>>(a);
-  return cudaGetLastError();
+  const int kvh = a.c.kvh;
+  const size_t pre = (size_t)kvh * a.p_chunks * ((a.B * (a.qh / kvh) + 7) / 8);
+  const size_t items = pre + (size_t)a.B * kvh * a.own_chunks;
+  const size_t most = sizeof(ChunkSmem<D>) + (3 * kMaxBatch + 1) * sizeof(int);
+  cudaError_t e = allow_smem((const void*)k_kv8_chunk<D, FMT>, most);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min<size_t>(items, kSms * 3);
+  e = launch_k(false, k_kv8_chunk<D, FMT>, dim3(grid), dim3(kWarpsPerItem * 32), sizeof(ChunkSmem<D>) + 3 * a.B * sizeof(int), s, a);
+  if (e != cudaSuccess) return e;
+  return launch_k(true, k_kv8_merge<D>, dim3(a.qh, a.B), dim3(D), 0, s, a);
 }
 
 // Positions per chunk of the shared prefix; a function of its length only.
 int prefix_chunk(int len) { return chunk_of(len); }
 
 bool shapes_ok(int B, int qh, int kvh, int d) {
-  return B >= 1 && B <= 1024 && kvh >= 1 && qh >= 1 && qh % kvh == 0 && qh / kvh <= kMaxGroup && qh <= 1024 &&
+  return B >= 1 && B <= kMaxBatch && kvh >= 1 && qh >= 1 && qh % kvh == 0 && qh / kvh <= kMaxGroup && qh <= 1024 &&
          (d == 64 || d == 128);
 }
 

@@ -60,6 +60,9 @@ def attend(cache, Q, slots, lens, scale, prefix=None):
     A weight's own error: it is rounded to 16 bits (2^-11) on the way to the tensor cores, and its score,
     a sum of d products in fp32, may be off by (d + 8) * 2^-24 * scale * sum|q||k| absolute, which moves
     the weight, and in the same way the normalising sum, by that factor; e^x and the sums add 2^-18.
+    What is rounded to 16 bits is p_j * (V's scale) in units of at most its largest value of the row.  fp16's
+    smallest step is 2^-24, so a weight far below the largest is also off by up to 2^-25 of that largest one:
+    2^-25 * max_j (p_j vs_j) * sum_j |code_j| of the output.
     Rows of slot < 0 are None."""
     B, qh, d = Q.shape
     kvh = cache["kv_heads"]
@@ -74,6 +77,8 @@ def attend(cache, Q, slots, lens, scale, prefix=None):
         parts = [(cache, slot, n)]
         if prefix is not None:
             parts.insert(0, prefix)
+        codes = torch.cat([decode(c["V"][s, :, :j], c["format"]) for c, s, j in parts], 1).abs().sum(1)
+        vs = torch.cat([c["Vs"][s, :, :j].double() for c, s, j in parts], 1)
         k, v = (torch.cat([decode(c[m][s, :, :j], c["format"]) * c[m + "s"][s, :, :j].double().unsqueeze(-1)
                            for c, s, j in parts], 1) for m in ("K", "V"))
         q = Q[b].double().view(kvh, G, d)
@@ -84,7 +89,8 @@ def attend(cache, Q, slots, lens, scale, prefix=None):
         p = torch.softmax(torch.einsum("hgd,hnd->hgn", q, k) * scale, -1)
         off = torch.einsum("hgd,hnd->hgn", q.abs(), k.abs()).amax(-1, keepdim=True) * scale * (d + 8) * 2.0 ** -24
         out.append(torch.einsum("hgn,hnd->hgd", p, v).reshape(qh, d))
-        bound.append((torch.einsum("hgn,hnd->hgd", p, v.abs()) * (2.0 ** -11 + 2.0 ** -18 + 2 * off)).reshape(qh, d))
+        small = 2.0 ** -25 * (p * vs[:, None]).amax(-1, keepdim=True) * codes[:, None]
+        bound.append((torch.einsum("hgn,hnd->hgd", p, v.abs()) * (2.0 ** -11 + 2.0 ** -18 + 2 * off) + small).reshape(qh, d))
     return out, bound
 
 
