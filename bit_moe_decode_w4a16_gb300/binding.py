@@ -381,132 +381,160 @@ def bm_w4_quantize(W, N, K, g, packed, scales, stream=None):
 
 # --------------------------------------------------------------- 8-bit K/V cache, sampling
 # These calls take torch tensors and check what the C side cannot see: type,
-# shape, contiguity, and that the memory is on the current CUDA device.
+# shape, contiguity, and that the memory is on the current CUDA device.  A
+# decode step makes several of them, so the checks take the short way through
+# and only a failing one works out what is wrong.
 
-def _tensor(x, what, dtypes, shape=None, optional=False):
-    """Address of a contiguous CUDA tensor of the current device."""
+_torch = None
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+        if torch.cuda.is_available():
+            torch.cuda.init()
+        _torch = torch
+    return _torch
+
+
+def _here():
+    """Index of the current CUDA device; -2 without one (a CPU tensor's is -1)."""
+    t = _t()
+    return t._C._cuda_getDevice() if t.cuda.is_initialized() else -2
+
+
+def _stream(s, dev):
+    return _t()._C._cuda_getCurrentRawStream(dev) if s is None else s if isinstance(s, int) else s.cuda_stream
+
+
+def _tensor(x, what, dtype, shape, dev):
+    """Address of a contiguous tensor of that type and shape (None: any) on device dev."""
+    if x is None or x.dtype is not dtype or x.get_device() != dev or not x.is_contiguous() or (shape is not None and x.shape != shape):
+        _refuse(x, what, dtype, shape)
+    return x.data_ptr()
+
+
+def _optional(x, what, dtype, shape, dev):
+    return None if x is None else _tensor(x, what, dtype, shape, dev)
+
+
+def _refuse(x, what, dtype, shape):
     if x is None:
-        if optional:
-            return None
         raise BitMoeError(1, f"{what}: null tensor")
-    import torch
-    if x.dtype not in dtypes:
-        raise BitMoeError(1, f"{what}: dtype {x.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if x.dtype is not dtype:
+        raise BitMoeError(1, f"{what}: dtype {x.dtype}, expected {dtype}")
     if shape is not None and x.shape != shape:
         raise BitMoeError(1, f"{what}: shape {tuple(x.shape)}, expected {tuple(shape)}")
     if not x.is_contiguous():
         raise BitMoeError(1, f"{what}: not contiguous")
-    if not x.is_cuda or x.device.index != torch.cuda.current_device():
-        raise BitMoeError(1, f"{what}: on {x.device}, expected the current CUDA device")
-    return x.data_ptr()
-
-
-def _types():
-    import torch
-    return torch
+    raise BitMoeError(1, f"{what}: on {x.device}, expected the current CUDA device")
 
 
 def kv8_cache(format, slots, ctx_cap, kv_heads, head_dim, K, V, Ks, Vs):
     """The bm_kv8_cache of four tensors: codes uint8 [slots][kv_heads][ctx_cap][head_dim],
     scales fp32 [slots][kv_heads][ctx_cap].  It keeps the tensors alive."""
-    t = _types()
-    rows = (slots, kv_heads, ctx_cap)
+    t, dev, rows = _t(), _here(), (slots, kv_heads, ctx_cap)
     c = bm_kv8_cache(format, slots, ctx_cap, kv_heads, head_dim,
-                     *[_tensor(x, f"kv8_cache: {n}", (t.uint8,), rows + (head_dim,)) for n, x in (("K", K), ("V", V))],
-                     *[_tensor(x, f"kv8_cache: {n}", (t.float32,), rows) for n, x in (("Ks", Ks), ("Vs", Vs))])
-    c.tensors = (K, V, Ks, Vs)
+                     *[_tensor(x, f"kv8_cache: {n}", t.uint8, rows + (head_dim,), dev) for n, x in (("K", K), ("V", V))],
+                     *[_tensor(x, f"kv8_cache: {n}", t.float32, rows, dev) for n, x in (("Ks", Ks), ("Vs", Vs))])
+    c.tensors, c.device, c.address = (K, V, Ks, Vs), dev, ctypes.addressof(c)
     return c
 
 
 def kv8_rope(norm=False, q_norm=None, k_norm=None, eps=1e-6, inv_freq=None):
-    """The bm_kv8_rope of its tensors (bf16 norm weights, fp32 inv_freq), which it keeps alive."""
-    t = _types()
-    r = bm_kv8_rope(int(norm), eps, _tensor(q_norm, "kv8_rope: q_norm", (t.bfloat16,), optional=True),
-                    _tensor(k_norm, "kv8_rope: k_norm", (t.bfloat16,), optional=True),
-                    _tensor(inv_freq, "kv8_rope: inv_freq", (t.float32,), optional=True))
-    r.tensors = (q_norm, k_norm, inv_freq)
+    """The bm_kv8_rope of its tensors (bf16 norm weights [head_dim], fp32 inv_freq [head_dim / 2]), which it keeps alive."""
+    t, dev = _t(), _here()
+    r = bm_kv8_rope(int(norm), eps, _optional(q_norm, "kv8_rope: q_norm", t.bfloat16, None, dev),
+                    _optional(k_norm, "kv8_rope: k_norm", t.bfloat16, None, dev),
+                    _optional(inv_freq, "kv8_rope: inv_freq", t.float32, None, dev))
+    r.tensors, r.device, r.address = (q_norm, k_norm, inv_freq), dev, ctypes.addressof(r)
+    # the head_dim each tensor fits
+    r.fits = {x.numel() * f for x, f in ((q_norm, 1), (k_norm, 1), (inv_freq, 2)) if x is not None}
     return r
 
 
-def _cache_device(c, what):
-    t = _types()
-    if c.tensors[0].device.index != t.cuda.current_device():
-        raise BitMoeError(1, f"{what}: the cache is on {c.tensors[0].device}, expected the current CUDA device")
+def _on_device(c, what, dev):
+    if c.device != dev:
+        raise BitMoeError(1, f"{what}: its tensors are on cuda:{c.device}, expected the current CUDA device")
 
 
 def kv8_append(cache, qkv, rope, slots, index, Q, rope_pos=None, stream=None):
     """qkv: bf16 [T][>= (q_heads + 2 kv_heads) * head_dim], rows may be strided; Q: bf16 [T][q_heads][head_dim]."""
-    t = _types()
-    _cache_device(cache, "kv8_append")
+    t, dev = _t(), _here()
+    _on_device(cache, "kv8_append: cache", dev)
+    _on_device(rope, "kv8_append: rope", dev)
     T, qh, d = Q.shape
     if qkv.dim() != 2 or qkv.shape[0] != T or qkv.shape[1] < (qh + 2 * cache.kv_heads) * d or d != cache.head_dim:
         raise BitMoeError(1, f"kv8_append: qkv {tuple(qkv.shape)} and Q {tuple(Q.shape)} do not fit the cache")
-    if qkv.dtype != t.bfloat16 or qkv.stride(1) != 1 or qkv.device != Q.device:
-        raise BitMoeError(1, "kv8_append: qkv must be bf16 rows of unit stride on Q's device")
-    for n, w, size in (("q_norm", rope.tensors[0], d), ("k_norm", rope.tensors[1], d), ("inv_freq", rope.tensors[2], d // 2)):
-        if w is not None and (w.numel() != size or w.device != Q.device):
-            raise BitMoeError(1, f"kv8_append: {n} must have {size} elements on Q's device")
-    i32 = (t.int32,)
+    if qkv.dtype is not t.bfloat16 or qkv.stride(1) != 1 or qkv.get_device() != dev:
+        raise BitMoeError(1, "kv8_append: qkv must be bf16 rows of unit stride on the current CUDA device")
+    if rope.fits and rope.fits != {d}:
+        raise BitMoeError(1, f"kv8_append: q_norm and k_norm need {d} elements, inv_freq {d // 2}")
     ld = qkv.stride(0) if T > 1 else qkv.shape[1] + (-qkv.shape[1]) % 8
-    _check(lib().kv8_append(ctypes.addressof(cache), qkv.data_ptr(), ld, qh, ctypes.addressof(rope),
-                            _tensor(slots, "kv8_append: slots", i32, (T,)), _tensor(index, "kv8_append: index", i32, (T,)),
-                            _tensor(rope_pos, "kv8_append: rope_pos", i32, (T,), optional=True),
-                            _tensor(Q, "kv8_append: Q", (t.bfloat16,)), T, stream_handle(stream)))
+    i32, n = t.int32, (T,)
+    _check(lib().kv8_append(cache.address, qkv.data_ptr(), ld, qh, rope.address, _tensor(slots, "kv8_append: slots", i32, n, dev),
+                            _tensor(index, "kv8_append: index", i32, n, dev),
+                            _optional(rope_pos, "kv8_append: rope_pos", i32, n, dev),
+                            _tensor(Q, "kv8_append: Q", t.bfloat16, None, dev), T, _stream(stream, dev)))
 
 
 def kv8_read(cache, slot, first, count, K_out, V_out, stream=None):
     """K_out, V_out: bf16 [kv_heads][count][head_dim]."""
-    t = _types()
-    _cache_device(cache, "kv8_read")
+    t, dev = _t(), _here()
+    _on_device(cache, "kv8_read: cache", dev)
     shape = (cache.kv_heads, count, cache.head_dim)
-    _check(lib().kv8_read(ctypes.addressof(cache), slot, first, count, _tensor(K_out, "kv8_read: K_out", (t.bfloat16,), shape),
-                          _tensor(V_out, "kv8_read: V_out", (t.bfloat16,), shape), stream_handle(stream)))
+    _check(lib().kv8_read(cache.address, slot, first, count, _tensor(K_out, "kv8_read: K_out", t.bfloat16, shape, dev),
+                          _tensor(V_out, "kv8_read: V_out", t.bfloat16, shape, dev), _stream(stream, dev)))
 
 
 def kv8_workspace_bytes(B, q_heads, kv_heads, head_dim, ctx_cap, prefix_len=0):
     return lib().kv8_workspace_bytes(B, q_heads, kv_heads, head_dim, ctx_cap, prefix_len)
 
 
-def _attend_args(what, cache, Q, slots, lens, O, ws, scale):
-    t = _types()
-    _cache_device(cache, what)
-    B, qh, d = Q.shape
+def _attend_args(what, cache, Q, slots, lens, O, ws, scale, dev):
+    t = _t()
+    _on_device(cache, what, dev)
+    shape = Q.shape
+    B, qh, d = shape
     if d != cache.head_dim:
         raise BitMoeError(1, f"{what}: Q of head_dim {d}, the cache of {cache.head_dim}")
-    return (_tensor(Q, f"{what}: Q", (t.bfloat16,)), _tensor(slots, f"{what}: slots", (t.int32,), (B,)),
-            _tensor(lens, f"{what}: lens", (t.int32,), (B,)), qh, d ** -0.5 if scale is None else scale,
-            _tensor(O, f"{what}: O", (t.bfloat16,), Q.shape), B, _tensor(ws, f"{what}: ws", (t.uint8,)), ws.numel())
+    return (_tensor(Q, f"{what}: Q", t.bfloat16, None, dev), _tensor(slots, f"{what}: slots", t.int32, (B,), dev),
+            _tensor(lens, f"{what}: lens", t.int32, (B,), dev), qh, d ** -0.5 if scale is None else scale,
+            _tensor(O, f"{what}: O", t.bfloat16, shape, dev), B, _tensor(ws, f"{what}: ws", t.uint8, None, dev), ws.numel())
 
 
 def kv8_attend(cache, Q, slots, lens, O, ws, scale=None, stream=None):
     """Q, O: bf16 [B][q_heads][head_dim]; ws: uint8 tensor of kv8_workspace_bytes(...); scale: 1 / sqrt(head_dim) if None."""
-    args = _attend_args("kv8_attend", cache, Q, slots, lens, O, ws, scale)
-    _check(lib().kv8_attend(ctypes.addressof(cache), *args, stream_handle(stream)))
+    dev = _here()
+    args = _attend_args("kv8_attend", cache, Q, slots, lens, O, ws, scale, dev)
+    _check(lib().kv8_attend(cache.address, *args, _stream(stream, dev)))
 
 
 def kv8_attend_prefix(cache, prefix, prefix_slot, prefix_len, Q, slots, lens, O, ws, scale=None, stream=None):
     """kv8_attend behind positions 0..prefix_len-1 of slot prefix_slot of `prefix` (a kv8_cache, or `cache` itself)."""
-    _cache_device(prefix, "kv8_attend_prefix")
-    args = _attend_args("kv8_attend_prefix", cache, Q, slots, lens, O, ws, scale)
-    _check(lib().kv8_attend_prefix(ctypes.addressof(cache), ctypes.addressof(prefix), prefix_slot, prefix_len, *args,
-                                   stream_handle(stream)))
+    dev = _here()
+    _on_device(prefix, "kv8_attend_prefix: prefix", dev)
+    args = _attend_args("kv8_attend_prefix", cache, Q, slots, lens, O, ws, scale, dev)
+    _check(lib().kv8_attend_prefix(cache.address, prefix.address, prefix_slot, prefix_len, *args, _stream(stream, dev)))
 
 
 def bm_sample(logits, temperature, top_k, top_p, min_p, u, ids, logprobs=None, stream=None):
     """logits: fp32 or bf16 [B][V], rows may be strided; temperature, top_p, min_p (fp32) and top_k (int32) [B] or
     None; u: fp32 [B]; ids: int32 [B]; logprobs: fp32 [B] or None."""
-    t = _types()
+    t, dev = _t(), _here()
     B, V = logits.shape
-    if logits.dtype not in (t.float32, t.bfloat16) or logits.stride(1) != 1 or logits.device != ids.device:
-        raise BitMoeError(1, "bm_sample: logits must be fp32 or bf16 rows of unit stride on ids' device")
-    f32, i32, n = (t.float32,), (t.int32,), (B,)
-    _check(lib().bm_sample(logits.data_ptr(), int(logits.dtype == t.bfloat16), logits.stride(0) if B > 1 else V, V, B,
-                           _tensor(temperature, "bm_sample: temperature", f32, n, optional=True),
-                           _tensor(top_k, "bm_sample: top_k", i32, n, optional=True),
-                           _tensor(top_p, "bm_sample: top_p", f32, n, optional=True),
-                           _tensor(min_p, "bm_sample: min_p", f32, n, optional=True),
-                           _tensor(u, "bm_sample: u", f32, n), _tensor(ids, "bm_sample: ids", i32, n),
-                           _tensor(logprobs, "bm_sample: logprobs", f32, n, optional=True), stream_handle(stream)))
+    half = logits.dtype is t.bfloat16
+    if not (half or logits.dtype is t.float32) or logits.stride(1) != 1 or logits.get_device() != dev:
+        raise BitMoeError(1, "bm_sample: logits must be fp32 or bf16 rows of unit stride on the current CUDA device")
+    f32, n = t.float32, (B,)
+    _check(lib().bm_sample(logits.data_ptr(), int(half), logits.stride(0) if B > 1 else V, V, B,
+                           _optional(temperature, "bm_sample: temperature", f32, n, dev),
+                           _optional(top_k, "bm_sample: top_k", t.int32, n, dev),
+                           _optional(top_p, "bm_sample: top_p", f32, n, dev),
+                           _optional(min_p, "bm_sample: min_p", f32, n, dev), _tensor(u, "bm_sample: u", f32, n, dev),
+                           _tensor(ids, "bm_sample: ids", t.int32, n, dev),
+                           _optional(logprobs, "bm_sample: logprobs", f32, n, dev), _stream(stream, dev)))
 
 
 # --------------------------------------------------------------- host slot map
