@@ -67,17 +67,34 @@ __device__ __forceinline__ uint32_t encode4(const float* f) {
   return w;
 }
 
-// Positions per chunk of a stream of `len` positions: 256, doubled until the
-// stream has at most 64 chunks.  It depends on the stream's own length only,
-// so a stream's result does not depend on the batch it is attended in.
+// Positions per chunk of a stream of `len` positions: 256, doubled each time
+// the length passes four times the last border (2048, 8192, 32768, ...), and
+// beyond 131072 kept so large that there are at most kMaxChunks.  A chunk has
+// a fixed cost, a record to merge among it, and a lone stream needs chunks to
+// spread over the GPU: half as many of each as the length grows fourfold.  It
+// depends on the stream's own length only, so a stream's result does not
+// depend on the batch it is attended in.
+constexpr int kMaxChunks = 64;
 __host__ __device__ inline int chunk_of(int len) {
   int c = 256;
-  while ((size_t)c * 64 < (size_t)len) c *= 2;
+  for (long long border = 2048; len > border; border *= border < 131072 ? 4 : 2) c *= 2;
   return c;
 }
 __host__ __device__ inline int chunks_of(int len) {
   const int c = chunk_of(len);
-  return (len + c - 1) / c;
+  return len > 0 ? (len - 1) / c + 1 : 0;
+}
+// The most chunks a stream of up to `cap` positions can have.
+__host__ __device__ inline int most_chunks(int cap) {
+  int most = 0;
+  for (long long border = 2048, n = 8;; border *= border < 131072 ? 4 : 2) {
+    if (cap <= border) {
+      const int c = chunks_of(cap);
+      return most > c ? most : c;
+    }
+    most = (int)n;
+    if (border < 131072) n *= 2;
+  }
 }
 
 // Checks a caller's cache descriptor (kv8_append.cu); `who` opens the message.

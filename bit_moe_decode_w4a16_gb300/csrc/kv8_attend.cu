@@ -23,7 +23,7 @@ namespace {
 using namespace kv8;
 
 constexpr int kMaxGroup = 8, kMaxBatch = 1024;
-constexpr int kMaxRecords = 128;      // of a stream: 64 chunks of the prefix, 64 of its own
+constexpr int kMaxRecords = 2 * kMaxChunks;   // of a stream: the prefix's chunks and its own
 constexpr int kSms = 152;
 
 struct AttendArgs {
@@ -51,10 +51,10 @@ struct AttendArgs {
 //
 // A work item is a chunk of positions and up to 8 query rows of one kv head:
 // the group of a stream over its own positions, or 8 of the batch's rows over
-// the prefix.  The item's four warps take 16 positions each of every stage
-// of 64; each keeps a running maximum, sum and output of its own, and the
+// the prefix.  The item's four warps take 32 positions each of every stage
+// of 128; each keeps a running maximum, sum and output of its own, and the
 // four are merged at the end of the item.  A warp streams its positions
-// through a ring of its own in shared memory (cp.async, two stages ahead,
+// through a ring of its own in shared memory (cp.async, a stage ahead,
 // across items), so the loop has no barrier between warps.
 //
 // On the tensor cores (mma.sync m16n8k16, fp16, fp32 sums), with g = lane / 4
@@ -72,18 +72,21 @@ struct AttendArgs {
 // magnitude, and what is rounded away is small against the largest term of
 // the sum.  The reference moves only when it is passed by 2^8 (an fp16 holds
 // that), so the output is seldom rescaled.
-constexpr int kWarpsPerItem = 4, kStage = 64, kRing = 3;
+constexpr int kWarpsPerItem = 4, kTake = 32, kStage = kWarpsPerItem * kTake, kRing = 2;
 
 template <int D>
-struct Ring {
-  uint8_t k[16 * D], v[16 * D];
-  float ks[16], vs[16];
+struct alignas(16) Ring {
+  uint8_t k[kTake * D], v[kTake * D];
+  float ks[kTake], vs[kTake];
 };
 
 template <int D>
+using WarpOut = float[8][D + 8];
+
+template <int D>
 struct ChunkSmem {
-  Ring<D> ring[kWarpsPerItem][kRing];
-  float o[kWarpsPerItem][8][D + 8];
+  static_assert(sizeof(WarpOut<D>) <= sizeof(Ring<D>), "a warp's output fits a slot");
+  Ring<D> ring[kWarpsPerItem][kRing];   // at an item's end a warp's output lies in the slot it has just used
   float m[kWarpsPerItem][8], l[kWarpsPerItem][8];
   int table[1];                       // [B] slots, [B] lengths, [B + 1] own items before each stream's
 };
@@ -115,23 +118,32 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool live) {
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(live ? 16 : 0) : "memory");
+__device__ __forceinline__ uint32_t shared_address(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared_address(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy4(void* dst, const void* src, bool live) {
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(live ? 4 : 0) : "memory");
+__device__ __forceinline__ void copy4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_address(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(shared_address(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4_or_zero(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(shared_address(dst)), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -147,6 +159,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
   ChunkSmem<D>& sm = *reinterpret_cast<ChunkSmem<D>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int kvh = a.c.kvh, G = a.qh / kvh, rows = a.B * G;
+  pdl_trigger();   // the whole grid is resident: the merge may take the free slots
   int *slots = sm.table, *lens = slots + a.B, *first = lens + a.B;
 
   // ---- the items: the prefix's, then each stream's own
@@ -173,15 +186,17 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
   }
   __syncthreads();
   const int items = pre_items + first[a.B];
+  // a CTA takes a run of items: the chunks of a query row one after the other
+  const int begin = (int)((long long)items * blockIdx.x / gridDim.x), end = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
   auto item_of = [&](int it) {
     Item i;
     const Cache* c;
     int slot, j0, size, len;
     if (it < pre_items) {
-      i.kh = it / (a.p_chunks * row_blocks);
-      const int r = it - i.kh * a.p_chunks * row_blocks, ch = r / row_blocks;
+      const int line = it / a.p_chunks, ch = it - line * a.p_chunks;
+      i.kh = line / row_blocks;
       i.b = -1;
-      i.row0 = (r - ch * row_blocks) * 8;
+      i.row0 = (line - i.kh * row_blocks) * 8;
       i.rec = ch;
       c = &a.p;
       slot = a.p_slot;
@@ -196,16 +211,17 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
         if (first[mid] <= it) lo = mid;
         else hi = mid;
       }
-      const int r = it - first[lo];
       i.b = lo;
       i.row0 = 0;
-      i.kh = r % kvh;
       c = &a.c;
       slot = slots[lo];
       len = lens[lo];
       size = chunk_of(len);
-      j0 = r / kvh * size;
-      i.rec = a.p_chunks + r / kvh;
+      const int r = it - first[lo], chunks = (first[lo + 1] - first[lo]) / kvh;
+      i.kh = r / chunks;
+      const int ch = r - i.kh * chunks;
+      j0 = ch * size;
+      i.rec = a.p_chunks + ch;
     }
     const size_t row = c->row(slot, i.kh, j0);
     i.K = c->K + row * D;
@@ -216,33 +232,46 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
     return i;
   };
 
-  // ---- loads run two stages ahead of the arithmetic, into the next item too
-  int load_it = blockIdx.x, load_j = 0, load_slot = 0;
+  // ---- loads run a stage ahead of the arithmetic, into the next item too
+  constexpr int kPieces = D / 16, kRows = 32 / kPieces, kCopies = kTake / kRows;   // a lane copies a piece of every kRows-th position
+  const int my_row = lane / kPieces, my_piece = lane % kPieces;
+  int load_it = begin, load_j = kTake * warp, load_slot = 0;
   Item li{};
-  if (load_it < items) li = item_of(load_it);
+  if (load_it < end) li = item_of(load_it);
   auto load = [&]() {
-    if (load_it < items) {
+    if (load_it < end) {
       Ring<D>& s = sm.ring[warp][load_slot];
-      const int j = load_j + 16 * warp;
-      constexpr int kPieces = D / 16;
+      const int left = li.n - load_j;
+      const size_t off = (size_t)(load_j + my_row) * D + 16 * my_piece;
+      const uint8_t *pk = li.K + off, *pv = li.V + off;
+      const float *ps = li.Ks + load_j + lane, *pz = li.Vs + load_j + lane;
+      if (left >= kTake) {
 #pragma unroll
-      for (int i = 0; i < kPieces / 2; ++i) {
-        const int c = lane + 32 * i, token = c / kPieces, p = c % kPieces;
-        const bool live = j + token < li.n;
-        const size_t off = live ? (size_t)(j + token) * D + 16 * p : 0;
-        copy16(s.k + piece<D>(token, p), li.K + off, live);
-        copy16(s.v + piece<D>(token, p), li.V + off, live);
+        for (int i = 0; i < kCopies; ++i) {
+          const int at = piece<D>(my_row + kRows * i, my_piece);
+          copy16(s.k + at, pk + kRows * D * i);
+          copy16(s.v + at, pv + kRows * D * i);
+        }
+        copy4(s.ks + lane, ps);
+        copy4(s.vs + lane, pz);
+      } else {                        // the stream's last positions, then zeros
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int at = piece<D>(my_row + kRows * i, my_piece);
+          const bool live = my_row + kRows * i < left;
+          copy16_or_zero(s.k + at, live ? pk + kRows * D * i : li.K, live);
+          copy16_or_zero(s.v + at, live ? pv + kRows * D * i : li.V, live);
+        }
+        const bool live = lane < left;
+        copy4_or_zero(s.ks + lane, live ? ps : li.Ks, live);
+        copy4_or_zero(s.vs + lane, live ? pz : li.Vs, live);
       }
-      const int token = lane & 15;
-      const bool live = j + token < li.n;
-      const float* src = (lane < 16 ? li.Ks : li.Vs) + (live ? j + token : 0);
-      copy4((lane < 16 ? s.ks : s.vs) + token, src, live);
       load_slot = load_slot + 1 == kRing ? 0 : load_slot + 1;
       load_j += kStage;
-      if (load_j >= li.n) {
-        load_it += gridDim.x;
-        load_j = 0;
-        if (load_it < items) li = item_of(load_it);
+      if (load_j - kTake * warp >= li.n) {
+        ++load_it;
+        load_j = kTake * warp;
+        if (load_it < end) li = item_of(load_it);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -251,13 +280,18 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
   for (int i = 0; i < kRing - 1; ++i) load();
 
   int slot = 0;
-  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+  constexpr int kPer = D / 64;        // 16-byte pieces of a K row per lane
+  uint32_t q[kPer][4][2];
+  float qf = 0.f;
+  int q_b = -2, q_kh = 0, q_row0 = 0;
+  for (int it = begin; it < end; ++it) {
     const Item i = item_of(it);
-    // ---- this lane's query row (head g), as fp16 of about its own magnitude
-    constexpr int kPer = D / 64;      // 16-byte pieces of a K row per lane
-    uint32_t q[kPer][4][2];
-    float qf = a.scale_log2;
-    {
+    if (i.b != q_b || i.kh != q_kh || i.row0 != q_row0) {
+      // ---- this lane's query row (head g), as fp16 of about its own magnitude
+      q_b = i.b;
+      q_kh = i.kh;
+      q_row0 = i.row0;
+      qf = a.scale_log2;
       const int r = i.row0 + g, b = i.b < 0 ? r / G : i.b, h = i.kh * G + (i.b < 0 ? r - b * G : r);
       const bool live = i.b < 0 ? r < rows : r < G;
       uint4 x[kPer][2];
@@ -304,39 +338,51 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
       __syncwarp();
       const Ring<D>& s = sm.ring[warp][slot];
       slot = slot + 1 == kRing ? 0 : slot + 1;
-      const int left = i.n - j0 - 16 * warp;   // positions of this warp's 16
+      const int left = i.n - j0 - kTake * warp;   // positions of this warp's
       if (left > 0) {
-        float c[2][4];
+        constexpr int kN = kTake / 8;
+        float c[kN][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+        for (int nt = 0; nt < kN; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) {
+        for (int j = 0; j < kPer; ++j) {
+          uint32_t w[kN][4];
+#pragma unroll
+          for (int nt = 0; nt < kN; ++nt) {
             const uint4 k = *reinterpret_cast<const uint4*>(s.k + piece<D>(8 * nt + g, kPer * t + j));
-            const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+            w[nt][0] = k.x; w[nt][1] = k.y; w[nt][2] = k.z; w[nt][3] = k.w;
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int nt = 0; nt < kN; ++nt) {
               uint32_t b0, b1;
-              codes4<FMT>(w[e], b0, b1);
+              codes4<FMT>(w[nt][e], b0, b1);
               mma16816(c[nt], q[j][e][0], 0u, q[j][e][1], 0u, b0, b1);
             }
-          }
         }
         // head g, positions 8 nt + 2 t + e
-        float p[2][2], vs[2][2], mx = -1e30f;
+        float p[kN][2], vs[kN][2], mx = -1e30f;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < kN; ++nt) {
           const float2 kf = *reinterpret_cast<const float2*>(&s.ks[8 * nt + 2 * t]);
           const float2 vf = *reinterpret_cast<const float2*>(&s.vs[8 * nt + 2 * t]);
           vs[nt][0] = vf.x;
           vs[nt][1] = vf.y;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float sc = c[nt][e] * ((e ? kf.y : kf.x) * qf);
-            p[nt][e] = 8 * nt + 2 * t + e < left ? sc : -INFINITY;
-            mx = fmaxf(mx, p[nt][e] + fmaxf(__log2f(vs[nt][e]), -100.f));
-          }
+          p[nt][0] = c[nt][0] * (kf.x * qf);
+          p[nt][1] = c[nt][1] * (kf.y * qf);
         }
+        if (left < kTake) {
+#pragma unroll
+          for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (8 * nt + 2 * t + e >= left) p[nt][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mx = fmaxf(mx, p[nt][e] + fmaxf(log2_fast(vs[nt][e]), -100.f));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         if (__any_sync(0xffffffffu, mx > m + 8.f)) {
@@ -352,33 +398,36 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
             o[j][3] *= f1;
           }
         }
-        uint32_t pb[2];
+        uint32_t pb[kN];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < kN; ++nt) {
           const float p0 = exp2_fast(p[nt][0] - m), p1 = exp2_fast(p[nt][1] - m);
           l += p0 + p1;
           const __half2 w = __floats2half2_rn(p0 * vs[nt][0], p1 * vs[nt][1]);
           pb[nt] = *reinterpret_cast<const uint32_t*>(&w);
         }
-        uint32_t v[4][D / 32];        // this lane's D / 8 codes of positions 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int token = 2 * t + (r & 1) + 8 * (r >> 1);
-          if (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(s.v + piece<D>(token, g));
-            v[r][0] = x.x; v[r][1] = x.y; v[r][D / 32 - 2] = x.z; v[r][D / 32 - 1] = x.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(s.v + piece<D>(token, g >> 1) + 8 * (g & 1));
-            v[r][0] = x.x; v[r][1] = x.y;
+        for (int u = 0; u < kTake / 16; ++u) {
+          uint32_t v[4][D / 32];      // this lane's D / 8 codes of positions 16u + 2t, + 1, + 8, + 9
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int token = 16 * u + 2 * t + (r & 1) + 8 * (r >> 1);
+            if (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(s.v + piece<D>(token, g));
+              v[r][0] = x.x; v[r][1] = x.y; v[r][D / 32 - 2] = x.z; v[r][D / 32 - 1] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(s.v + piece<D>(token, g >> 1) + 8 * (g & 1));
+              v[r][0] = x.x; v[r][1] = x.y;
+            }
           }
-        }
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-          const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
-          uint32_t a0, a1, a2, a3;
-          codes4<FMT>(__byte_perm(v[0][j / 2], v[1][j / 2], sel), a0, a1);
-          codes4<FMT>(__byte_perm(v[2][j / 2], v[3][j / 2], sel), a2, a3);
-          mma16816(o[j], a0, a1, a2, a3, pb[0], pb[1]);
+          for (int j = 0; j < kTiles; ++j) {
+            const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
+            uint32_t a0, a1, a2, a3;
+            codes4<FMT>(__byte_perm(v[0][j / 2], v[1][j / 2], sel), a0, a1);
+            codes4<FMT>(__byte_perm(v[2][j / 2], v[3][j / 2], sel), a2, a3);
+            mma16816(o[j], a0, a1, a2, a3, pb[2 * u], pb[2 * u + 1]);
+          }
         }
       }
       __syncwarp();                   // every lane has read the slot before it is loaded again
@@ -387,7 +436,8 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
     // ---- the item's record from the four warps'
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    __syncthreads();
+    const int used = slot == 0 ? kRing - 1 : slot - 1;
+    WarpOut<D>& out = *reinterpret_cast<WarpOut<D>*>(&sm.ring[warp][used]);
     if (t == 0) {
       sm.m[warp][g] = m;
       sm.l[warp][g] = l;
@@ -395,8 +445,8 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) {
       const int d = D / 8 * g + 2 * j;
-      *reinterpret_cast<float2*>(&sm.o[warp][2 * t][d]) = make_float2(o[j][0], o[j][2]);
-      *reinterpret_cast<float2*>(&sm.o[warp][2 * t + 1][d]) = make_float2(o[j][1], o[j][3]);
+      *reinterpret_cast<float2*>(&out[2 * t][d]) = make_float2(o[j][0], o[j][2]);
+      *reinterpret_cast<float2*>(&out[2 * t + 1][d]) = make_float2(o[j][1], o[j][3]);
     }
     __syncthreads();
 #pragma unroll 1
@@ -417,7 +467,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
         float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarpsPerItem; ++w) {
-          const float2 v = *reinterpret_cast<const float2*>(&sm.o[w][r][d]);
+          const float2 v = *reinterpret_cast<const float2*>(&(*reinterpret_cast<const WarpOut<D>*>(&sm.ring[w][used]))[r][d]);
           acc.x = fmaf(v.x, f[w], acc.x);
           acc.y = fmaf(v.y, f[w], acc.y);
         }
@@ -425,6 +475,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
       }
       if (lane == 0) *reinterpret_cast<float2*>(rec + D) = make_float2(mx, den);
     }
+    __syncthreads();                  // the slots are loaded again
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -435,9 +486,10 @@ __global__ void __launch_bounds__(D) k_kv8_merge(AttendArgs a) {
   __shared__ float f[kMaxRecords];
   __shared__ float red[2];
   const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
-  pdl_wait();
   int slot, len;
-  if (!a.live(b, slot, len)) return;
+  const bool live = a.live(b, slot, len);   // inputs of the call: not written by the kernel before
+  pdl_wait();
+  if (!live) return;
   const int n = a.p_chunks + chunks_of(len);
   const float* rec = a.record(b, h, 0, D);
   if (d < 32) {
@@ -498,7 +550,7 @@ bool shapes_ok(int B, int qh, int kvh, int d) {
 
 size_t records(int ctx_cap, int prefix_len) {
   const int pc = prefix_len > 0 ? (prefix_len + prefix_chunk(prefix_len) - 1) / prefix_chunk(prefix_len) : 0;
-  return (size_t)pc + std::min(64, (ctx_cap + 255) / 256);
+  return (size_t)pc + most_chunks(ctx_cap);
 }
 
 bm_status attend(const char* who, const bm_kv8_cache* c, const bm_kv8_cache* p, int p_slot, int p_len, const uint16_t* Q,
@@ -535,7 +587,7 @@ bm_status attend(const char* who, const bm_kv8_cache* c, const bm_kv8_cache* p, 
   a.rec = static_cast<float*>(ws);
   a.B = B;
   a.qh = q_heads;
-  a.own_chunks = std::min(64, (c->ctx_cap + 255) / 256);
+  a.own_chunks = most_chunks(c->ctx_cap);
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4 = c->format == BM_KV8_E4M3, d128 = c->head_dim == 128;
