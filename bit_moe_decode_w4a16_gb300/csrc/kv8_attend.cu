@@ -15,43 +15,17 @@
 #include <set>
 #include <utility>
 
-#include "kv8.cuh"
+#include "kv8_attend.cuh"
 
 namespace bm {
 namespace {
 
 using namespace kv8;
 
-constexpr int kMaxGroup = 8, kMaxBatch = 1024;
-constexpr int kMaxRecords = 2 * kMaxChunks;   // of a stream: the prefix's chunks and its own
-constexpr int kSms = 152;
-
-struct AttendArgs {
-  Cache c, p;            // the streams' cache, the prefix's
-  int p_slot, p_len, p_chunk, p_chunks;
-  const bf16* Q;
-  const int32_t* slots;
-  const int32_t* lens;
-  bf16* O;
-  float* rec;            // [B][q_heads][p_chunks + own chunks] records of d + 2 floats: o, m, l
-  int B, qh, own_chunks;
-  float scale_log2;      // scale * log2(e): the scores are powers of two
-  __device__ float* record(int b, int h, int r, int d) const {
-    return rec + (((size_t)b * qh + h) * (p_chunks + own_chunks) + r) * (size_t)(d + 2);
-  }
-  // A stream that takes part: padding and out-of-range rows are skipped.
-  __device__ bool live(int b, int& slot, int& len) const {
-    slot = slots[b];
-    len = lens[b];
-    return slot >= 0 && slot < c.slots && len >= 0 && len <= c.cap;
-  }
-};
-
 // ---------------------------------------------------------------- one pass over a chunk
 //
-// A work item is a chunk of positions and up to 8 query rows of one kv head:
-// the group of a stream over its own positions, or 8 of the batch's rows over
-// the prefix.  The item's four warps take 32 positions each of every stage
+// A work item is a chunk of a stream's positions and the query rows of one
+// of its kv heads.  The item's four warps take 32 positions each of every stage
 // of 128; each keeps a running maximum, sum and output of its own, and the
 // four are merged at the end of the item.  A warp streams its positions
 // through a ring of its own in shared memory (cp.async, a stage ahead,
@@ -97,26 +71,6 @@ __device__ __forceinline__ int piece(int token, int c) {
   return token * D + 16 * (D == 128 ? c ^ (token & 7) : c ^ (token >> 1 & 3));
 }
 
-// Two codes in the low half of w -> fp16 pair (exact).
-template <int FMT>
-__device__ __forceinline__ uint32_t codes2(uint32_t w) {
-  uint32_t r;
-  if (FMT == BM_KV8_E4M3) {
-    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(r) : "r"(w));
-  } else {
-    // 0x64 in front of u = code + 128 is the fp16 1024 + u
-    const uint32_t u = __byte_perm(w ^ 0x8080u, 0x64646464u, 0x4140);
-    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1152.f));
-    r = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  return r;
-}
-template <int FMT>
-__device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  lo = codes2<FMT>(w);
-  hi = codes2<FMT>(w >> 16);
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -136,21 +90,10 @@ __device__ __forceinline__ void copy16_or_zero(void* dst, const void* src, bool 
 __device__ __forceinline__ void copy4_or_zero(void* dst, const void* src, bool live) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(shared_address(dst)), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float log2_fast(float x) {
-  float r;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 struct Item {
   const uint8_t *K, *V;
   const float *Ks, *Vs;
-  int n, kh, b, row0, rec;            // positions; kv head; stream, or -1 with the first of 8 rows; record
+  int n, kh, b, rec;                  // positions; kv head; stream; chunk of the stream
 };
 
 template <int D, int FMT>
@@ -158,12 +101,11 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
   extern __shared__ __align__(16) unsigned char raw[];
   ChunkSmem<D>& sm = *reinterpret_cast<ChunkSmem<D>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int kvh = a.c.kvh, G = a.qh / kvh, rows = a.B * G;
+  const int kvh = a.c.kvh, G = a.qh / kvh;
   pdl_trigger();   // the whole grid is resident: the merge may take the free slots
   int *slots = sm.table, *lens = slots + a.B, *first = lens + a.B;
 
-  // ---- the items: the prefix's, then each stream's own
-  const int row_blocks = (rows + 7) / 8, pre_items = kvh * a.p_chunks * row_blocks;
+  // ---- the items: every live stream's kv heads and chunks
   if (warp == 0) {
     int sum = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -185,50 +127,27 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
     if (lane == 0) first[a.B] = sum;
   }
   __syncthreads();
-  const int items = pre_items + first[a.B];
+  const int items = first[a.B];
   // a CTA takes a run of items: the chunks of a query row one after the other
   const int begin = (int)((long long)items * blockIdx.x / gridDim.x), end = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
   auto item_of = [&](int it) {
-    Item i;
-    const Cache* c;
-    int slot, j0, size, len;
-    if (it < pre_items) {
-      const int line = it / a.p_chunks, ch = it - line * a.p_chunks;
-      i.kh = line / row_blocks;
-      i.b = -1;
-      i.row0 = (line - i.kh * row_blocks) * 8;
-      i.rec = ch;
-      c = &a.p;
-      slot = a.p_slot;
-      size = a.p_chunk;
-      len = a.p_len;
-      j0 = ch * size;
-    } else {
-      it -= pre_items;
-      int lo = 0, hi = a.B;           // the last stream with first <= it
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (first[mid] <= it) lo = mid;
-        else hi = mid;
-      }
-      i.b = lo;
-      i.row0 = 0;
-      c = &a.c;
-      slot = slots[lo];
-      len = lens[lo];
-      size = chunk_of(len);
-      const int r = it - first[lo], chunks = (first[lo + 1] - first[lo]) / kvh;
-      i.kh = r / chunks;
-      const int ch = r - i.kh * chunks;
-      j0 = ch * size;
-      i.rec = a.p_chunks + ch;
+    int lo = 0, hi = a.B;             // the last stream with first <= it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (first[mid] <= it) lo = mid;
+      else hi = mid;
     }
-    const size_t row = c->row(slot, i.kh, j0);
-    i.K = c->K + row * D;
-    i.V = c->V + row * D;
-    i.Ks = c->Ks + row;
-    i.Vs = c->Vs + row;
-    i.n = min(size, len - j0);
+    Item i;
+    const int r = it - first[lo], chunks = (first[lo + 1] - first[lo]) / kvh, size = chunk_of(lens[lo]);
+    i.b = lo;
+    i.kh = r / chunks;
+    i.rec = r - i.kh * chunks;
+    const size_t row = a.c.row(slots[lo], i.kh, i.rec * size);
+    i.K = a.c.K + row * D;
+    i.V = a.c.V + row * D;
+    i.Ks = a.c.Ks + row;
+    i.Vs = a.c.Vs + row;
+    i.n = min(size, lens[lo] - i.rec * size);
     return i;
   };
 
@@ -283,17 +202,14 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
   constexpr int kPer = D / 64;        // 16-byte pieces of a K row per lane
   uint32_t q[kPer][4][2];
   float qf = 0.f;
-  int q_b = -2, q_kh = 0, q_row0 = 0;
+  int q_b = -1, q_kh = 0;
   for (int it = begin; it < end; ++it) {
     const Item i = item_of(it);
-    if (i.b != q_b || i.kh != q_kh || i.row0 != q_row0) {
+    if (i.b != q_b || i.kh != q_kh) {
       // ---- this lane's query row (head g), as fp16 of about its own magnitude
       q_b = i.b;
       q_kh = i.kh;
-      q_row0 = i.row0;
       qf = a.scale_log2;
-      const int r = i.row0 + g, b = i.b < 0 ? r / G : i.b, h = i.kh * G + (i.b < 0 ? r - b * G : r);
-      const bool live = i.b < 0 ? r < rows : r < G;
       uint4 x[kPer][2];
       float mx = 0.f;
 #pragma unroll
@@ -301,20 +217,16 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           x[j][u] = make_uint4(0, 0, 0, 0);
-          if (live) x[j][u] = *reinterpret_cast<const uint4*>(a.Q + ((size_t)b * a.qh + h) * D + 16 * (kPer * t + j) + 8 * u);
+          if (g < G) x[j][u] = *reinterpret_cast<const uint4*>(a.Q + ((size_t)i.b * a.qh + i.kh * G + g) * D + 16 * (kPer * t + j) + 8 * u);
           const uint32_t w[4] = {x[j][u].x, x[j][u].y, x[j][u].z, x[j][u].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w[e])), fabsf(bf_hi(w[e]))));
         }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // a power of two: exact, and undone on the scores
-      float down = 1.f;
-      if (mx >= 1e-30f && mx <= 1e30f) {
-        const uint32_t e = __float_as_uint(mx) >> 23;
-        down = __uint_as_float((254u - e) << 23);
-        qf *= __uint_as_float(e << 23);
-      }
+      float down, up;
+      row_scale(mx, down, up);
+      qf *= up;
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
 #pragma unroll
@@ -450,9 +362,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
     }
     __syncthreads();
 #pragma unroll 1
-    for (int r = warp; r < 8; r += kWarpsPerItem) {
-      const int row = i.row0 + r, b = i.b < 0 ? row / G : i.b, h = i.kh * G + (i.b < 0 ? row - b * G : row);
-      if (i.b < 0 ? row >= rows : row >= G) break;
+    for (int r = warp; r < G; r += kWarpsPerItem) {
       float f[kWarpsPerItem], mx = sm.m[0][r], den = 0.f;
 #pragma unroll
       for (int w = 1; w < kWarpsPerItem; ++w) mx = fmaxf(mx, sm.m[w][r]);
@@ -461,7 +371,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
         f[w] = exp2_fast(sm.m[w][r] - mx);
         den += sm.l[w][r] * f[w];
       }
-      float* rec = a.record(b, h, i.rec, D);
+      float* rec = a.record(i.b, i.kh * G + r, a.p_chunks + i.rec, D);
 #pragma unroll
       for (int d = 2 * lane; d < D; d += 64) {
         float2 acc = make_float2(0.f, 0.f);
@@ -478,6 +388,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
     __syncthreads();                  // the slots are loaded again
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  pdl_wait();                         // done means done: the prefix's records are there too
 }
 
 // One head of one stream: its records in ascending order.
@@ -528,30 +439,22 @@ cudaError_t allow_smem(const void* kernel, size_t bytes) {
 
 template <int D, int FMT>
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
-  const int kvh = a.c.kvh;
-  const size_t pre = (size_t)kvh * a.p_chunks * ((a.B * (a.qh / kvh) + 7) / 8);
-  const size_t items = pre + (size_t)a.B * kvh * a.own_chunks;
-  const size_t most = sizeof(ChunkSmem<D>) + (3 * kMaxBatch + 1) * sizeof(int);
+  const size_t most = sizeof(ChunkSmem<D>) + 3 * kMaxBatch * sizeof(int), items = (size_t)a.B * a.c.kvh * a.own_chunks;
   cudaError_t e = allow_smem((const void*)k_kv8_chunk<D, FMT>, most);
+  if (e == cudaSuccess && a.p_chunks > 0) e = launch_kv8_prefix(a, FMT, D, s);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<size_t>(items, kSms * 3);
-  e = launch_k(false, k_kv8_chunk<D, FMT>, dim3(grid), dim3(kWarpsPerItem * 32), sizeof(ChunkSmem<D>) + 3 * a.B * sizeof(int), s, a);
+  e = launch_k(a.p_chunks > 0, k_kv8_chunk<D, FMT>, dim3(grid), dim3(kWarpsPerItem * 32), sizeof(ChunkSmem<D>) + 3 * a.B * sizeof(int), s, a);
   if (e != cudaSuccess) return e;
   return launch_k(true, k_kv8_merge<D>, dim3(a.qh, a.B), dim3(D), 0, s, a);
 }
-
-// Positions per chunk of the shared prefix; a function of its length only.
-int prefix_chunk(int len) { return chunk_of(len); }
 
 bool shapes_ok(int B, int qh, int kvh, int d) {
   return B >= 1 && B <= kMaxBatch && kvh >= 1 && qh >= 1 && qh % kvh == 0 && qh / kvh <= kMaxGroup && qh <= 1024 &&
          (d == 64 || d == 128);
 }
 
-size_t records(int ctx_cap, int prefix_len) {
-  const int pc = prefix_len > 0 ? (prefix_len + prefix_chunk(prefix_len) - 1) / prefix_chunk(prefix_len) : 0;
-  return (size_t)pc + most_chunks(ctx_cap);
-}
+size_t records(int ctx_cap, int prefix_len, int kvh) { return (size_t)prefix_chunks(prefix_len, kvh) + most_chunks(ctx_cap); }
 
 bm_status attend(const char* who, const bm_kv8_cache* c, const bm_kv8_cache* p, int p_slot, int p_len, const uint16_t* Q,
                  const int32_t* slots, const int32_t* lens, int q_heads, float scale, uint16_t* O, int B, void* ws,
@@ -578,8 +481,8 @@ bm_status attend(const char* who, const bm_kv8_cache* c, const bm_kv8_cache* p, 
     return set_error(BM_ERR_INVALID_ARG, w + ": workspace of " + std::to_string(ws_bytes) + " bytes, " + std::to_string(need) + " needed");
   a.p_slot = p_slot;
   a.p_len = p_len;
-  a.p_chunk = prefix_chunk(p_len);
-  a.p_chunks = p_len > 0 ? (p_len + a.p_chunk - 1) / a.p_chunk : 0;
+  a.p_chunk = prefix_chunk(p_len, c->kv_heads);
+  a.p_chunks = prefix_chunks(p_len, c->kv_heads);
   a.Q = reinterpret_cast<const bf16*>(Q);
   a.slots = slots;
   a.lens = lens;
@@ -605,7 +508,7 @@ extern "C" {
 size_t kv8_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int ctx_cap, int prefix_len) {
   using namespace bm;
   if (!shapes_ok(B, q_heads, kv_heads, head_dim) || ctx_cap < 1 || prefix_len < 0) return 0;
-  return (size_t)B * q_heads * records(ctx_cap, prefix_len) * (head_dim + 2) * sizeof(float);
+  return (size_t)B * q_heads * records(ctx_cap, prefix_len, kv_heads) * (head_dim + 2) * sizeof(float);
 }
 
 bm_status kv8_attend(const bm_kv8_cache* c, const uint16_t* Q, const int32_t* slots, const int32_t* lens, int q_heads,

@@ -1,0 +1,88 @@
+// What the kernels of attention over the 8-bit cache share.
+#pragma once
+
+#include "kv8.cuh"
+
+namespace bm {
+namespace kv8 {
+
+constexpr int kMaxGroup = 8, kMaxBatch = 1024;
+constexpr int kSms = 152;
+constexpr int kMaxRecords = kSms + kMaxChunks;   // of a stream: the prefix's chunks and its own
+
+struct AttendArgs {
+  Cache c, p;            // the streams' cache, the prefix's
+  int p_slot, p_len, p_chunk, p_chunks;
+  const bf16* Q;
+  const int32_t* slots;
+  const int32_t* lens;
+  bf16* O;
+  float* rec;            // [B][q_heads][p_chunks + own chunks] records of d + 2 floats: o, m, l
+  int B, qh, own_chunks;
+  float scale_log2;      // scale * log2(e): the scores are powers of two
+  __device__ float* record(int b, int h, int r, int d) const {
+    return rec + (((size_t)b * qh + h) * (p_chunks + own_chunks) + r) * (size_t)(d + 2);
+  }
+  // A stream that takes part: padding and out-of-range rows are skipped.
+  __device__ bool live(int b, int& slot, int& len) const {
+    slot = slots[b];
+    len = lens[b];
+    return slot >= 0 && slot < c.slots && len >= 0 && len <= c.cap;
+  }
+};
+
+// Four codes -> two fp16 pairs (exact).
+template <int FMT>
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == BM_KV8_E4M3) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    // 0x64 in front of u = code + 128 is the fp16 1024 + u
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __float2half2_rn(1152.f);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), k), y = __hsub2(*reinterpret_cast<const __half2*>(&b), k);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A power of two that brings a query row of largest magnitude `amax` into fp16's range; exact, and undone
+// on the scores by its inverse.
+__device__ __forceinline__ void row_scale(float amax, float& down, float& up) {
+  down = up = 1.f;
+  if (amax >= 1e-30f && amax <= 1e30f) {
+    const uint32_t e = __float_as_uint(amax) >> 23;
+    down = __uint_as_float((254u - e) << 23);
+    up = __uint_as_float(e << 23);
+  }
+}
+
+// Positions per chunk of the shared prefix, and the chunks: at most as many as fill the GPU, one CTA an SM,
+// for one tile of query rows.
+inline int prefix_chunk(int len, int kvh) {
+  const int most = kSms / kvh > 1 ? kSms / kvh : 1, tiles = len > 0 ? (len - 1) / 128 + 1 : 1;
+  return (tiles + most - 1) / most * 128;
+}
+inline int prefix_chunks(int len, int kvh) {
+  return len > 0 ? (len - 1) / prefix_chunk(len, kvh) + 1 : 0;
+}
+
+// The prefix's records (kv8_prefix.cu).
+cudaError_t launch_kv8_prefix(const AttendArgs& a, int format, int d, cudaStream_t s);
+
+}  // namespace kv8
+}  // namespace bm
