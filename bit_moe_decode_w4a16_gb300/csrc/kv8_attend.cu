@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-          const float mn = fmaxf(m, mx), f = exp2_fast(m - mn);
+          const float mn = mx > m + 8.f ? mx : m, f = exp2_fast(m - mn);
           m = mn;
           l *= f;
           const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
