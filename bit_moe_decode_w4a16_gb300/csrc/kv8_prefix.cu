@@ -7,32 +7,33 @@
 // takes 128 rows and one chunk of the prefix and leaves one record (o, m, l)
 // per row; the records are merged with those of the streams' own positions.
 //
-// Per tile of 64 positions, on the 5th-generation tensor cores (fp16
+// Per tile of 128 positions, on the 5th-generation tensor cores (fp16
 // operands, fp32 sums in tensor memory):
-//   S[row][position] = Q K^T, MMAs of 128 x 64 x 16, both operands in shared
+//   S[row][position] = Q K^T, MMAs of 128 x 128 x 16, both operands in shared
 //     memory (K-major, 128-byte swizzle);
-//   p and the weights p * vs as in kv8_attend.cu, a thread to a row, two
-//     positions to an instruction (f32x2); the weights go back over S as the
-//     fp16 A operand;
+//   p and the weights p * vs as in kv8_attend.cu, in two sweeps of S, two
+//     positions to an instruction (f32x2); the weights go to tensor memory as
+//     the fp16 A operand.  S is read in the fragment layout (4 rows x 16
+//     positions to a thread): with a row to a thread, every thread reads every
+//     position's scales, and those reads alone took 2000 cycles a tile;
 //   O[row][element] += P V, MMAs of 128 x d x 16, A in tensor memory, B = V^T
 //     in shared memory, positions contiguous (K-major).
-// Four warps do the softmax; four convert codes to fp16 (V is transposed on
+// Eight warps do the softmax; eight convert codes to fp16 (V is transposed on
 // the way, 8 positions x 4 bytes to a thread; its elements are stored at row
 // d / 4 (e % 4) + e / 4 of B so that a warp's stores meet no bank conflict,
-// and O's columns come out in that order), and a lane of theirs issues the
-// MMAs.  K, V and S have two buffers each: a commit is seen about 2000 cycles
-// after its MMAs were issued, so the next tile's scores are on their way
-// while this one's softmax runs, and O is waited for only to rescale it.  Two
-// CTAs share an SM (256 of its 512 tensor memory columns and about 100 KB of
-// shared memory each).
+// and O's columns come out in that order); one lane issues the MMAs.
+// K, V and S have two buffers each, so the next tile's scores are made
+// while this one's softmax runs, and O is waited for only to rescale it.
 //
-// What bounds it is the issue of the softmax's instructions, about 6 per
-// score, and the conversions'.
+// An MMA takes about 100 cycles whether N is 16 or 128, so the tile is as
+// wide as tensor memory allows (two S of 128 columns and O; 64-position tiles
+// at two CTAs an SM measured 55 us where these take @@).
 //
 // Every wait is bounded.  A wait that gives up leaves NaN in its CTA's
 // records, and so in the output rows.
 #include <mutex>
 #include <set>
+#include <type_traits>
 #include <utility>
 
 #include "kv8_attend.cuh"
@@ -43,17 +44,19 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kRows = 128, kTokens = 64;           // a tile
-constexpr int kSoftmax = 128, kConvert = 128, kThreads = kSoftmax + kConvert;   // 8 warps: 128 registers at two CTAs an SM
-constexpr uint32_t kTmemCols = 256;                // S (then P) of even tiles, of odd tiles, O
+constexpr int kRows = 128, kTokens = 128, kHalf = kTokens / 2;   // a tile; the positions of a softmax thread
+constexpr int kSoftmax = 256, kConvert = 256, kThreads = kSoftmax + kConvert + 32;
+constexpr uint32_t kTmemCols = 512;                // S of even and of odd tiles, O, P of even and of odd tiles
 constexpr uint32_t kWaitLimit = 1u << 18;          // polls of ~3.7 us: a wait gives up after about a second
 
 template <int D>
 struct PrefixSmem {
   uint8_t q[kRows * D * 2];                        // [d / 64][row][64] fp16, swizzled
   uint8_t k[2][kTokens * D * 2];                   // [d / 64][position][64]
-  uint8_t v[2][kTokens * D * 2];                   // [element][64 positions]
+  uint8_t v[2][kTokens * D * 2];                   // [position / 64][element][64]
   float ks[2][kTokens], vs[2][kTokens], lg[2][kTokens];   // scales, log2 of V's
+  float most[2][2][kRows];                         // a tile's largest of each half row
+  float l[2][kRows], up[kRows];
   // by the tile's parity; their phase is the tile's half
   uint64_t k_full[2], v_full[2], s_ready[2], p_ready[2], o_ready[2], drained;
   uint32_t tmem;
@@ -94,7 +97,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 2) k_kv8_prefix(AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
   extern __shared__ unsigned char raw[];
   const uint32_t raw_at = tc::smem_u32(raw);
   PrefixSmem<D>& sm = *reinterpret_cast<PrefixSmem<D>*>(raw + ((1024u - (raw_at & 1023u)) & 1023u));
@@ -102,10 +105,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv8_prefix(AttendArgs a) {
   const int chunk = blockIdx.x, row0 = blockIdx.y * kRows, kh = blockIdx.z;
   const int kvh = a.c.kvh, G = a.qh / kvh, rows = a.B * G;
   const int j0 = chunk * a.p_chunk, n = min(a.p_chunk, a.p_len - j0), tiles = (n + kTokens - 1) / kTokens;
+  const float inv_g = 1.f / G;
+  auto stream_of = [&](int r) { return (int)((r + 0.5f) * inv_g); };   // r / G, exact below 2^20
   const size_t at = a.p.row(a.p_slot, kh, j0);
   pdl_trigger();                                   // the streams' own chunks do not depend on this
 
-  if (warp == 4) {
+  if (warp == kSoftmax / 32) {
     tc::tmem_alloc(tc::smem_u32(&sm.tmem), kTmemCols);
     tc::tmem_relinquish();
   }
@@ -121,57 +126,88 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv8_prefix(AttendArgs a) {
     tc::fence_mbar_init();
     sm.gave_up = 0;
   }
-  float up = 1.f;
-  if (tid < kSoftmax) {
-    // ---- this thread's query row, as fp16 of about its own magnitude
-    const int r = row0 + tid, b = r / G, h = kh * G + r - b * G;
-    uint4 x[D / 8];
-    float mx = 0.f;
+  // ---- the query rows as fp16 of about their own magnitude, d / 8 lanes to a row
+  constexpr int kPieces = D / 8;
+  if (tid < kSoftmax + kConvert)
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      x[c] = make_uint4(0, 0, 0, 0);
-      if (r < rows) x[c] = *reinterpret_cast<const uint4*>(a.Q + ((size_t)b * a.qh + h) * D + 8 * c);
-      const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+  for (int u = tid; u < kRows * kPieces; u += kSoftmax + kConvert) {
+    const int at_row = u / kPieces, c = u % kPieces, r = row0 + at_row, b = stream_of(r), h = kh * G + r - b * G;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < rows) x = *reinterpret_cast<const uint4*>(a.Q + ((size_t)b * a.qh + h) * D + 8 * c);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float mx = 0.f, down, up;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w[e])), fabsf(bf_hi(w[e]))));
-    }
-    float down;
+    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w[e])), fabsf(bf_hi(w[e]))));
+#pragma unroll
+    for (int o = kPieces / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     row_scale(mx, down, up);
+    uint32_t f[4];
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-      uint32_t f[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __half2 v = __floats2half2_rn(bf_lo(w[e]) * down, bf_hi(w[e]) * down);
-        f[e] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-      *reinterpret_cast<uint4*>(sm.q + piece(kRows, tid, c)) = make_uint4(f[0], f[1], f[2], f[3]);
+    for (int e = 0; e < 4; ++e) {
+      const __half2 v = __floats2half2_rn(bf_lo(w[e]) * down, bf_hi(w[e]) * down);
+      f[e] = *reinterpret_cast<const uint32_t*>(&v);
     }
-    tc::fence_proxy_async_smem();
+    *reinterpret_cast<uint4*>(sm.q + piece(kRows, at_row, c)) = make_uint4(f[0], f[1], f[2], f[3]);
+    if (c == 0) sm.up[at_row] = up;
   }
+  tc::fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t s_cols = sm.tmem, o_cols = s_cols + 2 * kTokens;
+  const uint32_t s_cols = sm.tmem, o_cols = s_cols + 2 * kTokens, p_cols = o_cols + 128;
   // tile i's phase of a pair of barriers.  No thread can miss one: a tile's barrier completes again only after
   // every thread that waits for it has arrived at another barrier of that tile.
-  auto wait = [](uint64_t* bars, int i) { return tc::mbar_wait_spin(tc::smem_u32(&bars[i & 1]), i >> 1 & 1, kWaitLimit); };
+  // try_wait suspends the thread: sixteen polling warps would take the issue slots of the one that works.
+  auto wait = [](uint64_t* bars, int i) { return tc::mbar_wait(tc::smem_u32(&bars[i & 1]), i >> 1 & 1, kWaitLimit); };
   bool ok = true;
-  float m = -1e30f, l = 0.f;
 
-  if (warp >= 4) {
+  if (warp == (kSoftmax + kConvert) / 32) {
+    // ---------------- MMAs: issuing one takes as long as running it, so a lane does nothing else
+    if (lane == 0) {
+      const uint32_t qk = tc::idesc_f16_f32(kRows, kTokens), pv = tc::idesc_f16_f32(kRows, D);
+      const uint32_t q_at = tc::smem_u32(sm.q);
+      // tile i's scores, once its K is there
+      auto issue_scores = [&](int i) {
+        if (!wait(sm.k_full, i)) return false;
+        tc::fence_after_sync();
+        const uint32_t k_at = tc::smem_u32(sm.k[i & 1]);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_f16_ss(s_cols + (i & 1) * kTokens, operand(q_at, kRows, k), operand(k_at, kTokens, k), qk, k > 0);
+        tc::mma_commit(tc::smem_u32(&sm.s_ready[i & 1]));
+        return true;
+      };
+      // tile i's part of O, once its weights and its V are there
+      auto issue_output = [&](int i) {
+        if (!wait(sm.v_full, i) || !wait(sm.p_ready, i)) return false;
+        tc::fence_after_sync();
+        const uint32_t v_at = tc::smem_u32(sm.v[i & 1]);
+#pragma unroll
+        for (int k = 0; k < kTokens / 16; ++k)
+          tc::mma_f16_tmem_a(o_cols, p_cols + (i & 1) * (kTokens / 2) + 8 * k, operand(v_at, D, k), pv, i > 0 || k > 0);
+        tc::mma_commit(tc::smem_u32(&sm.o_ready[i & 1]));
+        return true;
+      };
+      ok = issue_scores(0) && (tiles < 2 || issue_scores(1));
+      // scores go where those of two tiles before were, which that tile's weights say have been read
+      for (int i = 0; ok && i < tiles; ++i) ok = issue_output(i) && (i + 2 >= tiles || issue_scores(i + 2));
+      // nothing of this CTA's is in flight when it ends
+      tc::mma_commit(tc::smem_u32(&sm.drained));
+      if (!tc::mbar_wait(tc::smem_u32(&sm.drained), 0, kWaitLimit)) ok = false;
+    }
+    __syncwarp();
+  } else if (warp >= kSoftmax / 32) {
     // ---------------- conversion: warp w takes positions 16 w .. of a tile
-    const int cw = warp - 4, ct = tid - kSoftmax;
+    const int cw = warp - kSoftmax / 32, ct = tid - kSoftmax;
     constexpr int kRowsAt = D == 128 ? 4 : 8;      // K rows to a warp's load
-    constexpr int kK = kTokens / 4 / kRowsAt;      // loads of 16 codes
+    constexpr int kK = 16 / kRowsAt;      // loads of 16 codes
     constexpr int kG = D == 128 ? 2 : 1;           // groups of 8 positions to a thread
     const int k_row = lane / (32 / kRowsAt), k_piece = lane % (32 / kRowsAt);
     const int v_word = D == 128 ? lane : lane & 15, v_half = D == 128 ? 0 : lane >> 4;
     const uint8_t *K = a.p.K + at * D, *V = a.p.V + at * D;
     uint4 kr[kK];
     uint32_t vr[kG][8];
-    float scale;                                   // K's in threads 0 .. 63, V's in the others
+    float scale;                                   // K's in the first half of the threads, V's in the others
     auto load = [&](int i) {
       const int t0 = i * kTokens + 16 * cw;        // positions of the chunk
       const bool whole = t0 + 16 <= n;
@@ -187,38 +223,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv8_prefix(AttendArgs a) {
           const int p = t0 + (D == 128 ? 8 * q : 8 * v_half) + r;
           vr[q][r] = whole || p < n ? __ldg(reinterpret_cast<const uint32_t*>(V + (size_t)p * D) + v_word) : 0u;
         }
-      const int p = i * kTokens + (ct & 63);
-      scale = p < n ? __ldg((ct < 64 ? a.p.Ks : a.p.Vs) + at + p) : 0.f;
-    };
-    const bool issuer = ct == 0;
-    const uint32_t qk = tc::idesc_f16_f32(kRows, kTokens), pv = tc::idesc_f16_f32(kRows, D);
-    const uint32_t q_at = tc::smem_u32(sm.q);
-    // tile i's scores, once its K is there
-    auto issue_scores = [&](int i) {
-      if (!wait(sm.k_full, i)) return false;
-      tc::fence_after_sync();
-      const uint32_t k_at = tc::smem_u32(sm.k[i & 1]);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        tc::mma_f16_ss(s_cols + (i & 1) * kTokens, operand(q_at, kRows, k), operand(k_at, kTokens, k), qk, k > 0);
-      tc::mma_commit(tc::smem_u32(&sm.s_ready[i & 1]));
-      return true;
-    };
-    // tile i's part of O, once its weights and its V are there
-    auto issue_output = [&](int i) {
-      if (!wait(sm.v_full, i) || !wait(sm.p_ready, i)) return false;
-      tc::fence_after_sync();
-      const uint32_t v_at = tc::smem_u32(sm.v[i & 1]);
-#pragma unroll
-      for (int k = 0; k < kTokens / 16; ++k)
-        tc::mma_f16_tmem_a(o_cols, s_cols + (i & 1) * kTokens + 8 * k, operand(v_at, D, k), pv, i > 0 || k > 0);
-      tc::mma_commit(tc::smem_u32(&sm.o_ready[i & 1]));
-      return true;
+      const int p = i * kTokens + (ct & (kTokens - 1));
+      scale = p < n ? __ldg((ct < kTokens ? a.p.Ks : a.p.Vs) + at + p) : 0.f;
     };
     load(0);
     for (int i = 0; i < tiles; ++i) {
       // the K buffer is free once tile i - 2 has its scores
-      if (i > 1 && !(ok = wait(sm.s_ready, i - 2))) break;
+      if (i > 1) {
+        if (lane == 0) ok = wait(sm.s_ready, i - 2);
+        if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
+      }
       uint8_t *k_to = sm.k[i & 1], *v_to = sm.v[i & 1];
 #pragma unroll
       for (int r = 0; r < kK; ++r) {
@@ -237,17 +251,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv8_prefix(AttendArgs a) {
       }
       tc::fence_proxy_async_smem();
       tc::mbar_arrive(tc::smem_u32(&sm.k_full[i & 1]));
-      // these scores go where tile i - 2's weights are: after its output's MMAs
-      if (issuer) ok = (i < 2 || issue_output(i - 2)) && issue_scores(i);
-      __syncwarp();
       // V, and the scales that tile i - 2's softmax has read
-      if (i > 1) ok = ok && wait(sm.o_ready, i - 2);
-      if (!ok) break;
-      if (ct < 64) {
+      if (i > 1) {
+        if (lane == 0) ok = wait(sm.o_ready, i - 2);
+        if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
+      }
+      if (ct < kTokens) {
         sm.ks[i & 1][ct] = scale;
       } else {
-        sm.vs[i & 1][ct - 64] = scale;
-        sm.lg[i & 1][ct - 64] = fmaxf(log2_fast(scale), -100.f);
+        sm.vs[i & 1][ct - kTokens] = scale;
+        sm.lg[i & 1][ct - kTokens] = fmaxf(log2_fast(scale), -100.f);
       }
 #pragma unroll
       for (int q = 0; q < kG; ++q) {
@@ -266,109 +279,156 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv8_prefix(AttendArgs a) {
       tc::mbar_arrive(tc::smem_u32(&sm.v_full[i & 1]));
       if (i + 1 < tiles) load(i + 1);
     }
-    if (issuer) {
-      if (ok && tiles > 1) ok = issue_output(tiles - 2);
-      if (ok) ok = issue_output(tiles - 1);
-      // nothing of this CTA's is in flight when it ends
-      tc::mma_commit(tc::smem_u32(&sm.drained));
-      if (!tc::mbar_wait(tc::smem_u32(&sm.drained), 0, kWaitLimit)) ok = false;
-    }
-    __syncwarp();
   } else {
-    // ---------------- softmax: a thread to a row
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    const float qf = a.scale_log2 * up;
-    const uint64_t qf2 = pack2(qf, qf);
+    // ---------------- softmax.  Two warps share 32 rows, 64 positions each; thread (g, t) of a warp has rows
+    // g + 8 r of them, r = 0 .. 3, and positions 8 j + 2 t and the next, j = 0 .. 7.
+    const int quarter = warp & 3, half = warp >> 2, g = lane >> 2, t = lane & 3;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    float qf[4], m[4], l[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      qf[r] = a.scale_log2 * sm.up[32 * quarter + g + 8 * r];
+      m[r] = -1e30f;
+      l[r] = 0.f;
+    }
     for (int i = 0; i < tiles; ++i) {
-      ok = wait(sm.v_full, i) && wait(sm.s_ready, i) && (i < 2 || wait(sm.o_ready, i - 2));
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
+      if (lane == 0) ok = ok && wait(sm.v_full, i) && wait(sm.s_ready, i) && (i < 2 || wait(sm.o_ready, i - 2));
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {                                   // the row's other half is not left waiting
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+        tc::mbar_arrive(tc::smem_u32(&sm.p_ready[i & 1]));
+        continue;
       }
       tc::fence_after_sync();
-      const int left = n - i * kTokens;
-      const ulonglong2 *ks = reinterpret_cast<const ulonglong2*>(sm.ks[i & 1]), *vs = reinterpret_cast<const ulonglong2*>(sm.vs[i & 1]),
-                       *lg = reinterpret_cast<const ulonglong2*>(sm.lg[i & 1]);
-      const uint32_t cols = s_cols + lanes + (i & 1) * kTokens;
-      uint32_t v[2][32];
-      tc::tmem_ld32(cols, v[0]);
-      tc::tmem_ld32(cols + 32, v[1]);
-      tc::tmem_wait_ld();
-      uint64_t t[kTokens / 2];                     // q . k * ks, two positions each
-      float mx = -1e30f, my = -1e30f;
+      const int here = n - i * kTokens - half * kHalf, left = here - 2 * t, b = i & 1;   // positions of the chunk from here on
+      const uint32_t s_at = s_cols + lanes + b * kTokens + half * kHalf, p_at = p_cols + lanes + b * (kTokens / 2) + half * (kHalf / 2);
+      float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
+      auto largest = [&](auto whole) {             // a branch per score would cost more than the score
 #pragma unroll
-      for (int k = 0; k < kTokens / 4; ++k) {
-        const ulonglong2 kk = ks[k], gg = lg[k];
-        const uint32_t* x = &v[k / 8][4 * (k % 8)];
-        t[2 * k] = mul2((uint64_t)x[0] | (uint64_t)x[1] << 32, kk.x);
-        t[2 * k + 1] = mul2((uint64_t)x[2] | (uint64_t)x[3] << 32, kk.y);
-        const uint64_t x0 = fma2(t[2 * k], qf2, gg.x), x1 = fma2(t[2 * k + 1], qf2, gg.y);
-        if (left >= kTokens) {
-          mx = fmaxf(mx, fmaxf(first(x0), second(x0)));
-          my = fmaxf(my, fmaxf(first(x1), second(x1)));
-        } else {
-          if (4 * k < left) mx = fmaxf(mx, first(x0));
-          if (4 * k + 1 < left) mx = fmaxf(mx, second(x0));
-          if (4 * k + 2 < left) mx = fmaxf(mx, first(x1));
-          if (4 * k + 3 < left) mx = fmaxf(mx, second(x1));
-        }
-      }
-      mx = fmaxf(mx, my);
-      if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-        const float mn = mx > m + 8.f ? mx : m, f = exp2_fast(m - mn);   // each row by itself: its neighbours are other streams'
-        m = mn;
-        l *= f;
-        if (i > 0) {                               // O holds the tiles before
-          ok = wait(sm.o_ready, i - 1);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
+        for (int c = 0; c < kHalf; c += 32) {
+          uint64_t ks[4], lg[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            ks[j] = *reinterpret_cast<const uint64_t*>(&sm.ks[b][half * kHalf + c + 8 * j + 2 * t]);
+            lg[j] = *reinterpret_cast<const uint64_t*>(&sm.lg[b][half * kHalf + c + 8 * j + 2 * t]);
           }
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t v[16];
+            tc::tmem_ld_frag32(s_at + c + ((uint32_t)(16 * hh) << 16), v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const float q = qf[2 * hh + r];
+                const uint64_t x = fma2(mul2((uint64_t)v[4 * j + 2 * r] | (uint64_t)v[4 * j + 2 * r + 1] << 32, ks[j]), pack2(q, q), lg[j]);
+                float& most = mx[2 * hh + r];
+                if (decltype(whole)::value) {
+                  most = fmaxf(most, fmaxf(first(x), second(x)));
+                } else {
+                  if (c + 8 * j < left) most = fmaxf(most, first(x));
+                  if (c + 8 * j + 1 < left) most = fmaxf(most, second(x));
+                }
+              }
+          }
+        }
+      };
+      if (here >= kHalf) largest(std::true_type());
+      else largest(std::false_type());
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        if (t == 0) sm.most[b][half][32 * quarter + g + 8 * r] = mx[r];
+      }
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+      bool moves = false;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        mx[r] = fmaxf(mx[r], sm.most[b][half ^ 1][32 * quarter + g + 8 * r]);
+        moves |= mx[r] > m[r] + 8.f;
+      }
+      if (__any_sync(0xffffffffu, moves)) {
+        // each row by itself: its neighbours are other streams'
+        float f[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float mn = mx[r] > m[r] + 8.f ? mx[r] : m[r];
+          f[r] = exp2_fast(m[r] - mn);
+          m[r] = mn;
+          l[r] *= f[r];
+        }
+        if (i > 0) {                               // O holds the tiles before
+          if (lane == 0) ok = wait(sm.o_ready, i - 1);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
           tc::fence_after_sync();
+          // a row to a lane here: lane 8 r + g has f[r] of the threads (g, t)
+          float mine = 1.f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float other = __shfl_sync(0xffffffffu, f[r], 4 * (lane & 7));
+            if (lane >> 3 == r) mine = other;
+          }
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
+          for (int c = half * D / 2; c < (half + 1) * D / 2; c += 16) {
             uint32_t o[16];
             tc::tmem_ld16(o_cols + lanes + c, o);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * mine);
             tc::tmem_st16(o_cols + lanes + c, o);
           }
         }
       }
-      const uint64_t m2 = pack2(-m, -m);
-      uint64_t sum0 = 0, sum1 = 0;
-      uint32_t w[kTokens / 2];
+      auto weights = [&](auto whole) {
 #pragma unroll
-      for (int k = 0; k < kTokens / 4; ++k) {
-        const ulonglong2 vv = vs[k];
-        const uint64_t x0 = fma2(t[2 * k], qf2, m2), x1 = fma2(t[2 * k + 1], qf2, m2);
-        uint64_t p0 = pack2(exp2_fast(first(x0)), exp2_fast(second(x0))), p1 = pack2(exp2_fast(first(x1)), exp2_fast(second(x1)));
-        if (left < kTokens) {
-          p0 = pack2(4 * k < left ? first(p0) : 0.f, 4 * k + 1 < left ? second(p0) : 0.f);
-          p1 = pack2(4 * k + 2 < left ? first(p1) : 0.f, 4 * k + 3 < left ? second(p1) : 0.f);
+        for (int c = 0; c < kHalf; c += 32) {
+          uint64_t ks[4], vs[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            ks[j] = *reinterpret_cast<const uint64_t*>(&sm.ks[b][half * kHalf + c + 8 * j + 2 * t]);
+            vs[j] = *reinterpret_cast<const uint64_t*>(&sm.vs[b][half * kHalf + c + 8 * j + 2 * t]);
+          }
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t v[16], w[8];
+            tc::tmem_ld_frag32(s_at + c + ((uint32_t)(16 * hh) << 16), v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float mr = m[2 * hh + r], q = qf[2 * hh + r];
+              uint64_t sum = 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint64_t x = fma2(mul2((uint64_t)v[4 * j + 2 * r] | (uint64_t)v[4 * j + 2 * r + 1] << 32, ks[j]), pack2(q, q), pack2(-mr, -mr));
+                uint64_t p = pack2(exp2_fast(first(x)), exp2_fast(second(x)));
+                if (!decltype(whole)::value) p = pack2(c + 8 * j < left ? first(p) : 0.f, c + 8 * j + 1 < left ? second(p) : 0.f);
+                sum = add2(sum, p);
+                const uint64_t x2 = mul2(p, vs[j]);
+                const __half2 h2 = __floats2half2_rn(first(x2), second(x2));
+                w[2 * j + r] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              l[2 * hh + r] += first(sum) + second(sum);
+            }
+            tc::tmem_st_frag16(p_at + c / 2 + ((uint32_t)(16 * hh) << 16), w);
+          }
         }
-        sum0 = add2(sum0, p0);
-        sum1 = add2(sum1, p1);
-        const uint64_t w0 = mul2(p0, vv.x), w1 = mul2(p1, vv.y);
-        const __half2 h0 = __floats2half2_rn(first(w0), second(w0)), h1 = __floats2half2_rn(first(w1), second(w1));
-        w[2 * k] = *reinterpret_cast<const uint32_t*>(&h0);
-        w[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-      }
-      tc::tmem_st32(cols, w);
-      sum0 = add2(sum0, sum1);
-      l += first(sum0) + second(sum0);
+      };
+      if (here >= kHalf) weights(std::true_type());
+      else weights(std::false_type());
       tc::tmem_wait_st();
       tc::fence_before_sync();
       tc::mbar_arrive(tc::smem_u32(&sm.p_ready[i & 1]));
     }
-    if (ok) ok = (tiles < 2 || wait(sm.o_ready, tiles - 2)) && wait(sm.o_ready, tiles - 1);
+    if (lane == 0 && ok) ok = (tiles < 2 || wait(sm.o_ready, tiles - 2)) && wait(sm.o_ready, tiles - 1);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
     tc::fence_after_sync();
-    if (__all_sync(0xffffffffu, ok)) {
-      // every MMA is done: O goes out over the operands, a row to a thread
-      float* out = reinterpret_cast<float*>(&sm) + tid * (D == 128 ? kOutStride : 65);
+    if (ok) {
+      // every MMA is done: O goes out over the operands, a row to a lane
+      float* out = reinterpret_cast<float*>(&sm) + (32 * quarter + lane) * (D == 128 ? kOutStride : 65);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = half * D / 2; c < (half + 1) * D / 2; c += 32) {
         uint32_t o[32];
         tc::tmem_ld32(o_cols + lanes + c, o);
         tc::tmem_wait_ld();
@@ -380,24 +440,37 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv8_prefix(AttendArgs a) {
       }
     }
     tc::fence_before_sync();
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");   // both halves are done with `most`
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int at_row = 32 * quarter + g + 8 * r;
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (t == 0) {
+        sm.l[half][at_row] = l[r];
+        sm.most[0][0][at_row] = m[r];
+      }
+    }
   }
   if (!ok) sm.gave_up = 1;
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 4) tc::tmem_dealloc(s_cols, kTmemCols);
+  if (warp == kSoftmax / 32) tc::tmem_dealloc(s_cols, kTmemCols);
   const bool bad = sm.gave_up != 0;
   // ---- records, a row to a warp at a time
   const float* out = reinterpret_cast<const float*>(&sm);
-  for (int r = warp; r < kRows && row0 + r < rows; r += kThreads / 32) {
-    const int b = (row0 + r) / G, h = kh * G + row0 + r - b * G;
+  constexpr int kOutWarps = (kSoftmax + kConvert) / 32;
+#pragma unroll 4
+  for (int k = 0; k < kRows / kOutWarps; ++k) {
+    const int at_row = warp + k * kOutWarps, r = row0 + at_row, b = stream_of(r), h = kh * G + r - b * G;
+    if (warp >= kOutWarps || r >= rows) continue;
     float* rec = a.record(b, h, chunk, D);
 #pragma unroll
-    for (int d = lane; d < D; d += 32) rec[d] = out[r * (D == 128 ? kOutStride : 65) + d];
-  }
-  if (tid < kSoftmax && row0 + tid < rows) {
-    const int b = (row0 + tid) / G, h = kh * G + row0 + tid - b * G;
-    float* rec = a.record(b, h, chunk, D);
-    *reinterpret_cast<float2*>(rec + D) = make_float2(bad ? 0.f : m, bad ? __uint_as_float(0x7FC00000u) : l);
+    for (int d = lane; d < D; d += 32) rec[d] = out[at_row * (D == 128 ? kOutStride : 65) + d];
+    if (lane == 0) {
+      *reinterpret_cast<float2*>(rec + D) =
+          make_float2(bad ? 0.f : sm.most[0][0][at_row], bad ? __uint_as_float(0x7FC00000u) : sm.l[0][at_row] + sm.l[1][at_row]);
+    }
   }
 }
 
