@@ -9,11 +9,13 @@
 // rounded from fp32, with no bf16 step between the norm and the rotation.
 //
 // It is bound by the bytes of the rows (each read once and written once).  A
-// head belongs to d / 8 lanes of 16 bytes each: a head's sums and maxima are
-// 3 or 4 shuffles, the other half of a rotated pair is one shuffle away
-// (lane ^ d / 16), and no head touches shared memory.  A CTA holds a row's
-// heads; its first d / 2 threads turn the position into the row's cosines
-// and sines.
+// head belongs to d / 8 lanes, 4 elements and their 4 partners of the rotation
+// each: a head's sums and maxima are 3 or 4 shuffles, a rotation none.  A thread keeps its
+// place in the row and walks over rows, so norm weights and frequencies are
+// read once; two rows are on their way while one is worked on, and a CTA's
+// first d / 2 threads make the next row's cosines and sines meanwhile.
+#include <algorithm>
+
 #include "kv8.cuh"
 
 namespace bm {
@@ -35,16 +37,20 @@ struct AppendArgs {
   const int32_t* index;
   const int32_t* pos;
   bf16* Q;
-  int heads_per_cta;
+  int heads_per_cta, T;
 };
 
-// Cosine and sine of pos * f.  The angle is reduced in 64 bits, in turns:
-// at position 2^17 an fp32 product would be off by 2^-7 of a radian.
-__device__ __forceinline__ float2 rotation(int pos, float f) {
-  const double turns = (double)pos * (double)f * 0.15915494309189533577;   // / (2 pi)
-  const float frac = (float)(turns - rint(turns));
+// f / (2 pi) in 2^-64 turns.  A product with a position wraps around at whole
+// turns, so the angle's fraction of a turn is exact to 2^-47 at position 2^17;
+// an fp32 product would be off by 2^-7 of a radian there.
+__device__ __forceinline__ unsigned long long turns64(float f) {
+  const double t = (double)f * 0.15915494309189533577;
+  return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+}
+__device__ __forceinline__ float2 rotation(int pos, unsigned long long turns) {
+  const int frac = (int)(((unsigned long long)(long long)pos * turns) >> 32);   // of a turn, in [-1/2, 1/2)
   float s, c;
-  sincospif(2.0f * frac, &s, &c);
+  sincospif((float)frac * 4.656612873077393e-10f, &s, &c);   // * 2^-31: half turns
   return make_float2(c, s);
 }
 
@@ -53,80 +59,122 @@ __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
   x[4] = bf_lo(r.z); x[5] = bf_hi(r.z); x[6] = bf_lo(r.w); x[7] = bf_hi(r.w);
 }
 
+constexpr int kMaxThreads = 512;
+
+struct AppendRow {
+  uint4 raw;
+  int slot, idx, pos;
+};
+
 template <int D, int FMT>
-__global__ void __launch_bounds__(1024) k_kv8_append(AppendArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) k_kv8_append(AppendArgs a) {
   constexpr int kLanes = D / 8;   // lanes of a head
-  __shared__ float2 cs[D / 2];
-  const int t = blockIdx.x;
-  const int slot = a.slots[t], idx = a.index[t];
-  if (slot < 0 || slot >= a.c.slots || idx < 0 || idx >= a.c.cap) return;   // padding: nothing of the row is written
+  __shared__ __align__(16) float2 cs[2][D / 2];
   const int l = threadIdx.x % kLanes, h = blockIdx.y * a.heads_per_cta + threadIdx.x / kLanes;
   const int kvh = a.c.kvh, heads = a.qh + 2 * kvh;
   const bool live = h < heads && (int)(threadIdx.x / kLanes) < a.heads_per_cta;
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (live) raw = *reinterpret_cast<const uint4*>(a.qkv + t * a.ld + (size_t)h * D + 8 * l);
-  const bool rotated = a.inv_freq != nullptr;
-  if (rotated) {
-    if (threadIdx.x < D / 2) cs[threadIdx.x] = rotation(a.pos ? a.pos[t] : idx, a.inv_freq[threadIdx.x]);
-    __syncthreads();
-  }
-  float x[8];
-  unpack8(raw, x);
-  const bool is_v = h >= a.qh + kvh, is_q = h < a.qh;
-  if (a.norm) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-    ss = group_sum<kLanes>(ss);
-    const float inv = 1.0f / sqrtf(ss / (float)D + a.eps);
-    const bf16* nw = is_q ? a.q_norm : a.k_norm;
-    if (!is_v) {
-      float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-      if (nw) unpack8(*reinterpret_cast<const uint4*>(nw + 8 * l), w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+  const bool is_v = h >= a.qh + kvh, is_q = h < a.qh, all_v = __all_sync(0xffffffffu, is_v), any_kv = __any_sync(0xffffffffu, live && !is_q);
+  const bool rotated = a.inv_freq != nullptr, turns_here = rotated && threadIdx.x < D / 2;
+  // Rows outside the cache are padding: nothing of theirs is written.
+  auto valid = [&](const AppendRow& r) { return r.slot >= 0 && r.slot < a.c.slots && r.idx >= 0 && r.idx < a.c.cap; };
+  // elements 4l .. 4l + 3 and their partners of the rotation, d / 2 further on
+  auto both_halves = [&](const bf16* head) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(head + 4 * l)), y = __ldg(reinterpret_cast<const uint2*>(head + D / 2 + 4 * l));
+    return make_uint4(x.x, x.y, y.x, y.y);
+  };
+  auto load = [&](int t) {
+    AppendRow r{make_uint4(0, 0, 0, 0), -1, -1, 0};
+    if (t < a.T) {
+      r.slot = __ldg(a.slots + t);
+      r.idx = __ldg(a.index + t);
+      if (turns_here) r.pos = a.pos ? __ldg(a.pos + t) : r.idx;
+      if (live) r.raw = both_halves(a.qkv + t * a.ld + (size_t)h * D);
     }
-  }
-  if (rotated) {
-    const bool second = l >= kLanes / 2;
+    return r;
+  };
+  const int step = gridDim.x;
+  AppendRow now = load(blockIdx.x), next = load(blockIdx.x + step);
+  const unsigned long long turns = turns_here ? turns64(a.inv_freq[threadIdx.x]) : 0;
+  const bf16* nw = is_q ? a.q_norm : a.k_norm;
+  uint4 w8 = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // ones
+  if (a.norm && !is_v && nw) w8 = both_halves(nw);
+  if (turns_here) cs[0][threadIdx.x] = rotation(now.pos, turns);
+  if (rotated) __syncthreads();
+  int b = 0;
+  for (int t = blockIdx.x; t < a.T; t += step) {
+    const AppendRow after = load(t + 2 * step);
+    if (turns_here && t + step < a.T) cs[b ^ 1][threadIdx.x] = rotation(next.pos, turns);
+    if (valid(now)) {
+      float x[8];
+      unpack8(now.raw, x);
+      if (a.norm && !all_v) {
+        float ss = 0.f, w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_xor_sync(0xffffffffu, x[i], kLanes / 2);
-      const float2 r = cs[(8 * l + i) % (D / 2)];
-      if (!is_v) x[i] = fmaf(x[i], r.x, second ? other * r.y : -(other * r.y));
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        ss = group_sum<kLanes>(ss);
+        const float inv = is_v ? 1.f : rsqrtf(fmaf(ss, 1.0f / D, a.eps));
+        unpack8(w8, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= inv * w[i];
+      }
+      if (rotated && !all_v) {
+        const float4* at = reinterpret_cast<const float4*>(&cs[b][4 * l]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 r = at[i];   // two pairs' cosine and sine
+          if (!is_v) {
+            const float p = x[2 * i], q = x[2 * i + 1];
+            x[2 * i] = fmaf(p, r.x, -(x[2 * i + 4] * r.y));
+            x[2 * i + 1] = fmaf(q, r.z, -(x[2 * i + 5] * r.w));
+            x[2 * i + 4] = fmaf(x[2 * i + 4], r.x, p * r.y);
+            x[2 * i + 5] = fmaf(x[2 * i + 5], r.z, q * r.w);
+          }
+        }
+      }
+      if (is_q) {
+        if (live) {
+          uint32_t p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            p[i] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          bf16* q = a.Q + ((size_t)t * a.qh + h) * D + 4 * l;
+          *reinterpret_cast<uint2*>(q) = make_uint2(p[0], p[1]);
+          *reinterpret_cast<uint2*>(q + D / 2) = make_uint2(p[2], p[3]);
+        }
+      }
+      // the largest magnitude, on the bit patterns: NaN > infinity > any number
+      if (any_kv) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (live && !is_q) {
+          const float amax = __uint_as_float(mx);
+          float inv = 0.f, scale = 0.f;
+          if (mx >= 0x7F800000u) {
+            scale = __uint_as_float(0x7FC00000u);   // a head with infinity or NaN reads back as NaN
+          } else if (amax >= kTinyHead) {
+            inv = code_max<FMT>() / amax;
+            scale = amax / code_max<FMT>();
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = scale == scale ? x[i] * inv : 0.f;
+          const size_t row = a.c.row(now.slot, is_v ? h - a.qh - kvh : h - a.qh, now.idx);
+          uint8_t* codes = is_v ? a.c.V : a.c.K;
+          *reinterpret_cast<uint32_t*>(codes + row * D + 4 * l) = encode4<FMT>(x);
+          *reinterpret_cast<uint32_t*>(codes + row * D + D / 2 + 4 * l) = encode4<FMT>(x + 4);
+          if (l == 0) (is_v ? a.c.Vs : a.c.Ks)[row] = scale;
+        }
+      }
     }
+    now = next;
+    next = after;
+    b ^= 1;
+    if (rotated) __syncthreads();
   }
-  // the largest magnitude, on the bit patterns: NaN > infinity > any number
-  uint32_t mx = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (!live) return;
-  if (is_q) {
-    uint32_t p[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      p[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    *reinterpret_cast<uint4*>(a.Q + ((size_t)t * a.qh + h) * D + 8 * l) = make_uint4(p[0], p[1], p[2], p[3]);
-    return;
-  }
-  const float amax = __uint_as_float(mx);
-  float inv = 0.f, scale = 0.f;
-  if (mx >= 0x7F800000u) {
-    scale = __uint_as_float(0x7FC00000u);   // a head with infinity or NaN reads back as NaN
-  } else if (amax >= kTinyHead) {
-    inv = code_max<FMT>() / amax;
-    scale = amax / code_max<FMT>();
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = inv == 0.f ? 0.f : x[i] * inv;
-  const size_t row = a.c.row(slot, is_v ? h - a.qh - kvh : h - a.qh, idx);
-  uint8_t* codes = is_v ? a.c.V : a.c.K;
-  *reinterpret_cast<uint2*>(codes + row * D + 8 * l) = make_uint2(encode4<FMT>(x), encode4<FMT>(x + 4));
-  if (l == 0) (is_v ? a.c.Vs : a.c.Ks)[row] = scale;
 }
 
 // bf16(code * scale), 16 codes to a thread; K in blockIdx.z = 0, V in 1.
@@ -160,11 +208,14 @@ __global__ void __launch_bounds__(256) k_kv8_read(Cache c, int slot, int first, 
 template <int D, int FMT>
 cudaError_t launch_append(const AppendArgs& args, int T, cudaStream_t s) {
   AppendArgs a = args;
-  const int heads = a.qh + 2 * a.c.kvh, per = 1024 / (D / 8);
+  const int heads = a.qh + 2 * a.c.kvh, per = kMaxThreads / (D / 8);
   const int ny = (heads + per - 1) / per;
   a.heads_per_cta = (heads + ny - 1) / ny;
   const int threads = ((max(a.heads_per_cta * (D / 8), D / 2) + 31) / 32) * 32;
-  k_kv8_append<D, FMT><<<dim3(T, ny), threads, 0, s>>>(a);
+  a.T = T;
+  // as many CTAs as an SM's threads hold, on every SM
+  const int ctas = std::max(1, 152 * (1024 / threads) / ny);
+  k_kv8_append<D, FMT><<<dim3(std::min(T, ctas), ny), threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
