@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <mutex>
 #include <set>
+#include <type_traits>
 #include <utility>
 
 #include "kv8_attend.cuh"
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
         f[w] = exp2_fast(sm.m[w][r] - mx);
         den += sm.l[w][r] * f[w];
       }
-      float* rec = a.record(i.b, i.kh * G + r, a.p_chunks + i.rec, D);
+      const size_t rec = a.record(i.b, i.kh * G + r, a.p_chunks + i.rec);
 #pragma unroll
       for (int d = 2 * lane; d < D; d += 64) {
         float2 acc = make_float2(0.f, 0.f);
@@ -381,9 +382,9 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
           acc.x = fmaf(v.x, f[w], acc.x);
           acc.y = fmaf(v.y, f[w], acc.y);
         }
-        *reinterpret_cast<float2*>(rec + d) = acc;
+        *reinterpret_cast<float2*>(a.rec_o + rec * D + d) = acc;
       }
-      if (lane == 0) *reinterpret_cast<float2*>(rec + D) = make_float2(mx, den);
+      if (lane == 0) a.rec_ml[rec] = make_float2(mx, den);
     }
     __syncthreads();                  // the slots are loaded again
   }
@@ -391,35 +392,65 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
   pdl_wait();                         // done means done: the prefix's records are there too
 }
 
-// One head of one stream: its records in ascending order.
+// One head of one stream to a warp: its records in ascending order, a lane
+// d / 32 elements.  The kernel is a chain of latencies, so everything is
+// asked for at once: the maxima and sums (a record to a lane), and the first
+// outputs before their weights are known.
+constexpr int kMergeWarps = 4, kMergeAhead = 8;
+
 template <int D>
-__global__ void __launch_bounds__(D) k_kv8_merge(AttendArgs a) {
-  __shared__ float f[kMaxRecords];
-  __shared__ float red[2];
-  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+__global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_merge(AttendArgs a) {
+  constexpr int E = D / 32;
+  using Part = typename std::conditional<E == 4, float4, float2>::type;
+  const int at = blockIdx.x * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (at >= a.B * a.qh) return;
+  const int b = at / a.qh, h = at - b * a.qh;
   int slot, len;
-  const bool live = a.live(b, slot, len);   // inputs of the call: not written by the kernel before
+  const bool live = a.live(b, slot, len);   // inputs of the call: not written by the kernels before
   pdl_wait();
   if (!live) return;
   const int n = a.p_chunks + chunks_of(len);
-  const float* rec = a.record(b, h, 0, D);
-  if (d < 32) {
-    float mx = -FLT_MAX, den = 0.f;
-    for (int r = d; r < n; r += 32) mx = fmaxf(mx, rec[r * (D + 2) + D]);
-    mx = warp_max(mx);
-    for (int r = d; r < n; r += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(rec + r * (D + 2) + D);
-      f[r] = exp2f(ml.x - mx);
-      den += ml.y * f[r];
+  const Part* o = reinterpret_cast<const Part*>(a.rec_o + a.record(b, h, 0) * D) + lane;
+  const float2* ml = a.rec_ml + a.record(b, h, 0);
+  float2 mine = lane < n ? ml[lane] : make_float2(-FLT_MAX, 0.f);
+  Part part[kMergeAhead];
+#pragma unroll
+  for (int k = 0; k < kMergeAhead; ++k)
+    if (k < n) part[k] = o[k * 32];
+  float mx = mine.x;
+  for (int r = lane + 32; r < n; r += 32) mx = fmaxf(mx, ml[r].x);
+  mx = warp_max(mx);
+  float den = 0.f, acc[E] = {};
+  for (int r0 = 0; r0 < n; r0 += 32) {
+    if (r0) mine = r0 + lane < n ? ml[r0 + lane] : make_float2(-FLT_MAX, 0.f);
+    const float f = exp2f(mine.x - mx);
+    den += mine.y * f;
+    for (int k0 = 0; k0 < 32 && r0 + k0 < n; k0 += kMergeAhead) {
+      Part next[kMergeAhead];
+      const int ahead = r0 + k0 + kMergeAhead;
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k)
+        if (ahead + k < n) next[k] = o[(ahead + k) * 32];
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k0 + k);
+        if (r0 + k0 + k < n) {
+          const float* p = reinterpret_cast<const float*>(&part[k]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(p[e], fk, acc[e]);
+        }
+        part[k] = next[k];
+      }
     }
-    den = warp_sum(den);
-    if (d == 0) red[0] = den;
   }
-  __syncthreads();
-  float acc = 0.f;
-#pragma unroll 8
-  for (int r = 0; r < n; ++r) acc = fmaf(rec[r * (D + 2) + d], f[r], acc);
-  a.O[((size_t)b * a.qh + h) * D + d] = f2bf(n == 0 ? 0.f : acc / red[0]);   // no positions: zeros
+  den = warp_sum(den);
+  const float inv = n == 0 ? 0.f : 1.f / den;   // no positions: zeros
+  __nv_bfloat162 out[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) out[e] = __floats2bfloat162_rn(n == 0 ? 0.f : acc[2 * e] * inv, n == 0 ? 0.f : acc[2 * e + 1] * inv);
+  bf16* to = a.O + ((size_t)b * a.qh + h) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) *reinterpret_cast<__nv_bfloat162*>(to + 2 * e) = out[e];
 }
 
 // Shared-memory attribute of a kernel on the current device, set once.
@@ -446,7 +477,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
   const unsigned grid = (unsigned)std::min<size_t>(items, kSms * 3);
   e = launch_k(a.p_chunks > 0, k_kv8_chunk<D, FMT>, dim3(grid), dim3(kWarpsPerItem * 32), sizeof(ChunkSmem<D>) + 3 * a.B * sizeof(int), s, a);
   if (e != cudaSuccess) return e;
-  return launch_k(true, k_kv8_merge<D>, dim3(a.qh, a.B), dim3(D), 0, s, a);
+  return launch_k(true, k_kv8_merge<D>, dim3((a.B * a.qh + kMergeWarps - 1) / kMergeWarps), dim3(kMergeWarps * 32), 0, s, a);
 }
 
 bool shapes_ok(int B, int qh, int kvh, int d) {
@@ -487,10 +518,11 @@ bm_status attend(const char* who, const bm_kv8_cache* c, const bm_kv8_cache* p, 
   a.slots = slots;
   a.lens = lens;
   a.O = reinterpret_cast<bf16*>(O);
-  a.rec = static_cast<float*>(ws);
   a.B = B;
   a.qh = q_heads;
   a.own_chunks = most_chunks(c->ctx_cap);
+  a.rec_o = static_cast<float*>(ws);
+  a.rec_ml = reinterpret_cast<float2*>(a.rec_o + a.record(B, 0, 0) * c->head_dim);
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4 = c->format == BM_KV8_E4M3, d128 = c->head_dim == 128;

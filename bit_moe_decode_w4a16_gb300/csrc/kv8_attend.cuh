@@ -8,7 +8,6 @@ namespace kv8 {
 
 constexpr int kMaxGroup = 8, kMaxBatch = 1024;
 constexpr int kSms = 152;
-constexpr int kMaxRecords = kSms + kMaxChunks;   // of a stream: the prefix's chunks and its own
 
 struct AttendArgs {
   Cache c, p;            // the streams' cache, the prefix's
@@ -17,12 +16,11 @@ struct AttendArgs {
   const int32_t* slots;
   const int32_t* lens;
   bf16* O;
-  float* rec;            // [B][q_heads][p_chunks + own chunks] records of d + 2 floats: o, m, l
+  float* rec_o;          // records [B][q_heads][p_chunks + own chunks]: unnormalised output [d]
+  float2* rec_ml;        // and its maximum and sum
   int B, qh, own_chunks;
   float scale_log2;      // scale * log2(e): the scores are powers of two
-  __device__ float* record(int b, int h, int r, int d) const {
-    return rec + (((size_t)b * qh + h) * (p_chunks + own_chunks) + r) * (size_t)(d + 2);
-  }
+  __host__ __device__ size_t record(int b, int h, int r) const { return ((size_t)b * qh + h) * (p_chunks + own_chunks) + r; }
   // A stream that takes part: padding and out-of-range rows are skipped.
   __device__ bool live(int b, int& slot, int& len) const {
     slot = slots[b];

@@ -464,11 +464,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
   for (int k = 0; k < kRows / kOutWarps; ++k) {
     const int at_row = warp + k * kOutWarps, r = row0 + at_row, b = stream_of(r), h = kh * G + r - b * G;
     if (warp >= kOutWarps || r >= rows) continue;
-    float* rec = a.record(b, h, chunk, D);
+    const size_t rec = a.record(b, h, chunk);
 #pragma unroll
-    for (int d = lane; d < D; d += 32) rec[d] = out[at_row * (D == 128 ? kOutStride : 65) + d];
+    for (int d = lane; d < D; d += 32) a.rec_o[rec * D + d] = out[at_row * (D == 128 ? kOutStride : 65) + d];
     if (lane == 0) {
-      *reinterpret_cast<float2*>(rec + D) =
+      a.rec_ml[rec] =
           make_float2(bad ? 0.f : sm.most[0][0][at_row], bad ? __uint_as_float(0x7FC00000u) : sm.l[0][at_row] + sm.l[1][at_row]);
     }
   }
