@@ -68,8 +68,8 @@ __device__ __forceinline__ uint32_t encode4(const float* f) {
 }
 
 // Positions per chunk of a stream of `len` positions: 256, doubled each time
-// the length passes four times the last border (2048, 8192, 32768, ...), and
-// beyond 131072 kept so large that there are at most kMaxChunks.  A chunk has
+// the length passes four times the last border (4096, 16384, 65536), and
+// beyond that kept so large that there are at most kMaxChunks.  A chunk has
 // a fixed cost, a record to merge among it, and a lone stream needs chunks to
 // spread over the GPU: half as many of each as the length grows fourfold.  It
 // depends on the stream's own length only, so a stream's result does not
@@ -77,7 +77,7 @@ __device__ __forceinline__ uint32_t encode4(const float* f) {
 constexpr int kMaxChunks = 64;
 __host__ __device__ inline int chunk_of(int len) {
   int c = 256;
-  for (long long border = 2048; len > border; border *= border < 131072 ? 4 : 2) c *= 2;
+  for (long long border = 4096; len > border; border *= border < 65536 ? 4 : 2) c *= 2;
   return c;
 }
 __host__ __device__ inline int chunks_of(int len) {
@@ -87,13 +87,13 @@ __host__ __device__ inline int chunks_of(int len) {
 // The most chunks a stream of up to `cap` positions can have.
 __host__ __device__ inline int most_chunks(int cap) {
   int most = 0;
-  for (long long border = 2048, n = 8;; border *= border < 131072 ? 4 : 2) {
+  for (long long border = 4096, n = 16;; border *= border < 65536 ? 4 : 2) {
     if (cap <= border) {
       const int c = chunks_of(cap);
       return most > c ? most : c;
     }
     most = (int)n;
-    if (border < 131072) n *= 2;
+    if (border < 65536) n *= 2;
   }
 }
 
