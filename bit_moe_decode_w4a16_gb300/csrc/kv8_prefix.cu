@@ -13,7 +13,7 @@
 //     memory (K-major, 128-byte swizzle);
 //   p and the weights p * vs as in kv8_attend.cu, in two sweeps of S, two
 //     positions to an instruction (f32x2); the weights go to tensor memory as
-//     the fp16 A operand.  S is read in the fragment layout (4 rows x 16
+//     the fp16 A operand.  S is read in the fragment layout (2 rows x 32
 //     positions to a thread): with a row to a thread, every thread reads every
 //     position's scales, and those reads alone took 2000 cycles a tile;
 //   O[row][element] += P V, MMAs of 128 x d x 16, A in tensor memory, B = V^T
@@ -44,7 +44,7 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kRows = 128, kTokens = 128, kHalf = kTokens / 2;   // a tile; the positions of a softmax thread
+constexpr int kRows = 128, kTokens = 128;          // a tile
 constexpr int kSoftmax = 256, kConvert = 256, kThreads = kSoftmax + kConvert + 32;
 constexpr uint32_t kTmemCols = 512;                // S of even and of odd tiles, O, P of even and of odd tiles
 constexpr uint32_t kWaitLimit = 1u << 18;          // polls of ~3.7 us: a wait gives up after about a second
@@ -54,9 +54,9 @@ struct PrefixSmem {
   uint8_t q[kRows * D * 2];                        // [d / 64][row][64] fp16, swizzled
   uint8_t k[2][kTokens * D * 2];                   // [d / 64][position][64]
   uint8_t v[2][kTokens * D * 2];                   // [position / 64][element][64]
-  float ks[2][kTokens], vs[2][kTokens], lg[2][kTokens];   // scales, log2 of V's
-  float most[2][2][kRows];                         // a tile's largest of each half row
-  float l[2][kRows], up[kRows];
+  // scales and log2 of V's, of four tiles: they are written with a tile's K, when the softmax may be two tiles back
+  float ks[4][kTokens], vs[4][kTokens], lg[4][kTokens];
+  float m[kRows], l[kRows], up[kRows];
   // by the tile's parity; their phase is the tile's half
   uint64_t k_full[2], v_full[2], s_ready[2], p_ready[2], o_ready[2], drained;
   uint32_t tmem;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
       tc::mbar_init(tc::smem_u32(&sm.k_full[b]), kConvert);
       tc::mbar_init(tc::smem_u32(&sm.v_full[b]), kConvert);
       tc::mbar_init(tc::smem_u32(&sm.p_ready[b]), kSoftmax);
-      tc::mbar_init(tc::smem_u32(&sm.s_ready[b]), 1);
+      tc::mbar_init(tc::smem_u32(&sm.s_ready[b]), 2);
       tc::mbar_init(tc::smem_u32(&sm.o_ready[b]), 1);
     }
     tc::mbar_init(tc::smem_u32(&sm.drained), 1);
@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
         for (int k = 0; k < D / 16; ++k)
           tc::mma_f16_ss(s_cols + (i & 1) * kTokens, operand(q_at, kRows, k), operand(k_at, kTokens, k), qk, k > 0);
         tc::mma_commit(tc::smem_u32(&sm.s_ready[i & 1]));
+        tc::mbar_arrive(tc::smem_u32(&sm.s_ready[i & 1]));   // a release by this thread: it passes the scales on
         return true;
       };
       // tile i's part of O, once its weights and its V are there
@@ -234,6 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
         if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
       }
       uint8_t *k_to = sm.k[i & 1], *v_to = sm.v[i & 1];
+      if (ct < kTokens) {
+        sm.ks[i & 3][ct] = scale;
+      } else {
+        sm.vs[i & 3][ct - kTokens] = scale;
+        sm.lg[i & 3][ct - kTokens] = fmaxf(log2_fast(scale), -100.f);
+      }
 #pragma unroll
       for (int r = 0; r < kK; ++r) {
         const int row = 16 * cw + kRowsAt * r + k_row;
@@ -251,16 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
       }
       tc::fence_proxy_async_smem();
       tc::mbar_arrive(tc::smem_u32(&sm.k_full[i & 1]));
-      // V, and the scales that tile i - 2's softmax has read
       if (i > 1) {
         if (lane == 0) ok = wait(sm.o_ready, i - 2);
         if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
-      }
-      if (ct < kTokens) {
-        sm.ks[i & 1][ct] = scale;
-      } else {
-        sm.vs[i & 1][ct - kTokens] = scale;
-        sm.lg[i & 1][ct - kTokens] = fmaxf(log2_fast(scale), -100.f);
       }
 #pragma unroll
       for (int q = 0; q < kG; ++q) {
@@ -280,80 +280,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
       if (i + 1 < tiles) load(i + 1);
     }
   } else {
-    // ---------------- softmax.  Two warps share 32 rows, 64 positions each; thread (g, t) of a warp has rows
-    // g + 8 r of them, r = 0 .. 3, and positions 8 j + 2 t and the next, j = 0 .. 7.
-    const int quarter = warp & 3, half = warp >> 2, g = lane >> 2, t = lane & 3;
-    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    float qf[4], m[4], l[4];
+    // ---------------- softmax: 16 rows to a warp.  Thread (g, t) has rows g and g + 8 of them and positions
+    // 8 j + 2 t and the next, j = 0 .. 15.
+    const int row = 32 * (warp & 3) + 16 * (warp >> 2), g = lane >> 2, t = lane & 3;
+    const uint32_t lanes = (uint32_t)row << 16;
+    float qf[2], m[2], l[2];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      qf[r] = a.scale_log2 * sm.up[32 * quarter + g + 8 * r];
+    for (int r = 0; r < 2; ++r) {
+      qf[r] = a.scale_log2 * sm.up[row + g + 8 * r];
       m[r] = -1e30f;
       l[r] = 0.f;
     }
     for (int i = 0; i < tiles; ++i) {
-      if (lane == 0) ok = ok && wait(sm.v_full, i) && wait(sm.s_ready, i) && (i < 2 || wait(sm.o_ready, i - 2));
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) {                                   // the row's other half is not left waiting
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-        tc::mbar_arrive(tc::smem_u32(&sm.p_ready[i & 1]));
-        continue;
-      }
+      // tile i's scores, and tile i - 2's output, which read the weights that these will overwrite
+      if (lane == 0) ok = wait(sm.s_ready, i) && (i < 2 || wait(sm.o_ready, i - 2));
+      if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
       tc::fence_after_sync();
-      const int here = n - i * kTokens - half * kHalf, left = here - 2 * t, b = i & 1;   // positions of the chunk from here on
-      const uint32_t s_at = s_cols + lanes + b * kTokens + half * kHalf, p_at = p_cols + lanes + b * (kTokens / 2) + half * (kHalf / 2);
-      float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
+      const int here = n - i * kTokens, left = here - 2 * t, b = i & 3;   // positions of the chunk from here on
+      const uint32_t s_at = s_cols + lanes + (i & 1) * kTokens, p_at = p_cols + lanes + (i & 1) * (kTokens / 2);
+      auto pair = [&](const float* of, int at) { return *reinterpret_cast<const uint64_t*>(of + at + 2 * t); };
+      float mx[2] = {-1e30f, -1e30f};
       auto largest = [&](auto whole) {             // a branch per score would cost more than the score
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 32) {
-          uint64_t ks[4], lg[4];
+        for (int c = 0; c < kTokens; c += 32) {
+          uint32_t v[16];
+          tc::tmem_ld_frag32(s_at + c, v);
+          tc::tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            ks[j] = *reinterpret_cast<const uint64_t*>(&sm.ks[b][half * kHalf + c + 8 * j + 2 * t]);
-            lg[j] = *reinterpret_cast<const uint64_t*>(&sm.lg[b][half * kHalf + c + 8 * j + 2 * t]);
-          }
+            const uint64_t ks = pair(sm.ks[b], c + 8 * j), lg = pair(sm.lg[b], c + 8 * j);
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t v[16];
-            tc::tmem_ld_frag32(s_at + c + ((uint32_t)(16 * hh) << 16), v);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const float q = qf[2 * hh + r];
-                const uint64_t x = fma2(mul2((uint64_t)v[4 * j + 2 * r] | (uint64_t)v[4 * j + 2 * r + 1] << 32, ks[j]), pack2(q, q), lg[j]);
-                float& most = mx[2 * hh + r];
-                if (decltype(whole)::value) {
-                  most = fmaxf(most, fmaxf(first(x), second(x)));
-                } else {
-                  if (c + 8 * j < left) most = fmaxf(most, first(x));
-                  if (c + 8 * j + 1 < left) most = fmaxf(most, second(x));
-                }
+            for (int r = 0; r < 2; ++r) {
+              const uint64_t x = fma2(mul2((uint64_t)v[4 * j + 2 * r] | (uint64_t)v[4 * j + 2 * r + 1] << 32, ks), pack2(qf[r], qf[r]), lg);
+              if (decltype(whole)::value) {
+                mx[r] = fmaxf(mx[r], fmaxf(first(x), second(x)));
+              } else {
+                if (c + 8 * j < left) mx[r] = fmaxf(mx[r], first(x));
+                if (c + 8 * j + 1 < left) mx[r] = fmaxf(mx[r], second(x));
               }
+            }
           }
         }
       };
-      if (here >= kHalf) largest(std::true_type());
+      if (here >= kTokens) largest(std::true_type());
       else largest(std::false_type());
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < 2; ++r) {
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        if (t == 0) sm.most[b][half][32 * quarter + g + 8 * r] = mx[r];
       }
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-      bool moves = false;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        mx[r] = fmaxf(mx[r], sm.most[b][half ^ 1][32 * quarter + g + 8 * r]);
-        moves |= mx[r] > m[r] + 8.f;
-      }
-      if (__any_sync(0xffffffffu, moves)) {
+      if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
         // each row by itself: its neighbours are other streams'
-        float f[4];
+        float f[2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < 2; ++r) {
           const float mn = mx[r] > m[r] + 8.f ? mx[r] : m[r];
           f[r] = exp2_fast(m[r] - mn);
           m[r] = mn;
@@ -361,76 +341,61 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
         }
         if (i > 0) {                               // O holds the tiles before
           if (lane == 0) ok = wait(sm.o_ready, i - 1);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
           tc::fence_after_sync();
-          // a row to a lane here: lane 8 r + g has f[r] of the threads (g, t)
-          float mine = 1.f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float other = __shfl_sync(0xffffffffu, f[r], 4 * (lane & 7));
-            if (lane >> 3 == r) mine = other;
-          }
 #pragma unroll 1
-          for (int c = half * D / 2; c < (half + 1) * D / 2; c += 16) {
+          for (int c = 0; c < D; c += 32) {
             uint32_t o[16];
-            tc::tmem_ld16(o_cols + lanes + c, o);
+            tc::tmem_ld_frag32(o_cols + lanes + c, o);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * mine);
-            tc::tmem_st16(o_cols + lanes + c, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[k >> 1 & 1]);
+            tc::tmem_st_frag32(o_cols + lanes + c, o);
           }
         }
       }
       auto weights = [&](auto whole) {
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 32) {
-          uint64_t ks[4], vs[4];
+        for (int c = 0; c < kTokens; c += 32) {
+          uint32_t v[16], w[8];
+          tc::tmem_ld_frag32(s_at + c, v);
+          tc::tmem_wait_ld();
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            ks[j] = *reinterpret_cast<const uint64_t*>(&sm.ks[b][half * kHalf + c + 8 * j + 2 * t]);
-            vs[j] = *reinterpret_cast<const uint64_t*>(&sm.vs[b][half * kHalf + c + 8 * j + 2 * t]);
-          }
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t v[16], w[8];
-            tc::tmem_ld_frag32(s_at + c + ((uint32_t)(16 * hh) << 16), v);
-            tc::tmem_wait_ld();
+            const uint64_t ks = pair(sm.ks[b], c + 8 * j), vs = pair(sm.vs[b], c + 8 * j);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const float mr = m[2 * hh + r], q = qf[2 * hh + r];
-              uint64_t sum = 0;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint64_t x = fma2(mul2((uint64_t)v[4 * j + 2 * r] | (uint64_t)v[4 * j + 2 * r + 1] << 32, ks[j]), pack2(q, q), pack2(-mr, -mr));
-                uint64_t p = pack2(exp2_fast(first(x)), exp2_fast(second(x)));
-                if (!decltype(whole)::value) p = pack2(c + 8 * j < left ? first(p) : 0.f, c + 8 * j + 1 < left ? second(p) : 0.f);
-                sum = add2(sum, p);
-                const uint64_t x2 = mul2(p, vs[j]);
-                const __half2 h2 = __floats2half2_rn(first(x2), second(x2));
-                w[2 * j + r] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-              l[2 * hh + r] += first(sum) + second(sum);
+              const uint64_t x = fma2(mul2((uint64_t)v[4 * j + 2 * r] | (uint64_t)v[4 * j + 2 * r + 1] << 32, ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
+              uint64_t p = pack2(exp2_fast(first(x)), exp2_fast(second(x)));
+              if (!decltype(whole)::value) p = pack2(c + 8 * j < left ? first(p) : 0.f, c + 8 * j + 1 < left ? second(p) : 0.f);
+              sum[r] = add2(sum[r], p);
+              const uint64_t x2 = mul2(p, vs);
+              const __half2 h2 = __floats2half2_rn(first(x2), second(x2));
+              w[2 * j + r] = *reinterpret_cast<const uint32_t*>(&h2);
             }
-            tc::tmem_st_frag16(p_at + c / 2 + ((uint32_t)(16 * hh) << 16), w);
           }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) l[r] += first(sum[r]) + second(sum[r]);
+          tc::tmem_st_frag16(p_at + c / 2, w);
         }
       };
-      if (here >= kHalf) weights(std::true_type());
+      if (here >= kTokens) weights(std::true_type());
       else weights(std::false_type());
       tc::tmem_wait_st();
       tc::fence_before_sync();
       tc::mbar_arrive(tc::smem_u32(&sm.p_ready[i & 1]));
     }
-    if (lane == 0 && ok) ok = (tiles < 2 || wait(sm.o_ready, tiles - 2)) && wait(sm.o_ready, tiles - 1);
+    if (lane == 0 && ok) ok = wait(sm.o_ready, tiles - 1);
     ok = __shfl_sync(0xffffffffu, ok, 0);
     tc::fence_after_sync();
     if (ok) {
-      // every MMA is done: O goes out over the operands, a row to a lane
-      float* out = reinterpret_cast<float*>(&sm) + (32 * quarter + lane) * (D == 128 ? kOutStride : 65);
+      // every MMA is done: O goes out over the operands, a row to a lane, half of the elements to a warp
+      float* out = reinterpret_cast<float*>(&sm) + (32 * (warp & 3) + lane) * (D == 128 ? kOutStride : 65);
 #pragma unroll 1
-      for (int c = half * D / 2; c < (half + 1) * D / 2; c += 32) {
+      for (int c = (warp >> 2) * D / 2; c < ((warp >> 2) + 1) * D / 2; c += 32) {
         uint32_t o[32];
-        tc::tmem_ld32(o_cols + lanes + c, o);
+        tc::tmem_ld32(o_cols + ((uint32_t)(32 * (warp & 3)) << 16) + c, o);
         tc::tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
@@ -440,15 +405,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
       }
     }
     tc::fence_before_sync();
-    asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");   // both halves are done with `most`
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int at_row = 32 * quarter + g + 8 * r;
+    for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       if (t == 0) {
-        sm.l[half][at_row] = l[r];
-        sm.most[0][0][at_row] = m[r];
+        sm.l[row + g + 8 * r] = l[r];
+        sm.m[row + g + 8 * r] = m[r];
       }
     }
   }
@@ -469,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
     for (int d = lane; d < D; d += 32) a.rec_o[rec * D + d] = out[at_row * (D == 128 ? kOutStride : 65) + d];
     if (lane == 0) {
       a.rec_ml[rec] =
-          make_float2(bad ? 0.f : sm.most[0][0][at_row], bad ? __uint_as_float(0x7FC00000u) : sm.l[0][at_row] + sm.l[1][at_row]);
+          make_float2(bad ? 0.f : sm.m[at_row], bad ? __uint_as_float(0x7FC00000u) : sm.l[at_row]);
     }
   }
 }

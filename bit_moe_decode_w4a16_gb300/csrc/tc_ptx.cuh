@@ -107,6 +107,16 @@ __device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, uint32_t (&v)[16]
       : "r"(taddr)
       : "memory");
 }
+// Its counterpart: store 32 columns.
+__device__ __forceinline__ void tmem_st_frag32(uint32_t taddr, const uint32_t (&v)[16]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 // Store 16 columns of the same 16 lanes: registers 2j and 2j + 1 are column 4j + t of lanes g and g + 8.
 __device__ __forceinline__ void tmem_st_frag16(uint32_t taddr, const uint32_t (&v)[8]) {
   __syncwarp();
