@@ -295,7 +295,8 @@ def test_offsets_past_32_bits(bm):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("B,P,qh,kvh,d", [(1, 1, 8, 2, 64), (3, 1000, 8, 2, 64), (5, 129, 32, 4, 128), (17, 2049, 32, 4, 128),
-                                          (40, 300, 12, 4, 128), (33, 128, 4, 4, 64), (9, 5000, 16, 2, 128), (2, 640, 7, 1, 64)])
+                                          (40, 300, 12, 4, 128), (33, 128, 4, 4, 64), (9, 5000, 16, 2, 128), (2, 640, 7, 1, 64),
+                                          (130, 5000, 32, 4, 128), (97, 20000, 8, 1, 64), (100, 40, 8, 1, 128)])
 def test_prefix(bm, fmt, B, P, qh, kvh, d):
     prefix = ref.random_cache(fmt, 2, P + 3, kvh, d, 31)
     _spoil(prefix, 1, P)
