@@ -408,15 +408,15 @@ def _stream(s, dev):
     return _t()._C._cuda_getCurrentRawStream(dev) if s is None else s if isinstance(s, int) else s.cuda_stream
 
 
-def _tensor(x, what, dtype, shape, dev):
+def _tensor(x, call, name, dtype, shape, dev):
     """Address of a contiguous tensor of that type and shape (None: any) on device dev."""
     if x is None or x.dtype is not dtype or x.get_device() != dev or not x.is_contiguous() or (shape is not None and x.shape != shape):
-        _refuse(x, what, dtype, shape)
+        _refuse(x, f"{call}: {name}", dtype, shape)
     return x.data_ptr()
 
 
-def _optional(x, what, dtype, shape, dev):
-    return None if x is None else _tensor(x, what, dtype, shape, dev)
+def _optional(x, call, name, dtype, shape, dev):
+    return None if x is None else _tensor(x, call, name, dtype, shape, dev)
 
 
 def _refuse(x, what, dtype, shape):
@@ -436,8 +436,8 @@ def kv8_cache(format, slots, ctx_cap, kv_heads, head_dim, K, V, Ks, Vs):
     scales fp32 [slots][kv_heads][ctx_cap].  It keeps the tensors alive."""
     t, dev, rows = _t(), _here(), (slots, kv_heads, ctx_cap)
     c = bm_kv8_cache(format, slots, ctx_cap, kv_heads, head_dim,
-                     *[_tensor(x, f"kv8_cache: {n}", t.uint8, rows + (head_dim,), dev) for n, x in (("K", K), ("V", V))],
-                     *[_tensor(x, f"kv8_cache: {n}", t.float32, rows, dev) for n, x in (("Ks", Ks), ("Vs", Vs))])
+                     *[_tensor(x, "kv8_cache", n, t.uint8, rows + (head_dim,), dev) for n, x in (("K", K), ("V", V))],
+                     *[_tensor(x, "kv8_cache", n, t.float32, rows, dev) for n, x in (("Ks", Ks), ("Vs", Vs))])
     c.tensors, c.device, c.address = (K, V, Ks, Vs), dev, ctypes.addressof(c)
     return c
 
@@ -445,9 +445,9 @@ def kv8_cache(format, slots, ctx_cap, kv_heads, head_dim, K, V, Ks, Vs):
 def kv8_rope(norm=False, q_norm=None, k_norm=None, eps=1e-6, inv_freq=None):
     """The bm_kv8_rope of its tensors (bf16 norm weights [head_dim], fp32 inv_freq [head_dim / 2]), which it keeps alive."""
     t, dev = _t(), _here()
-    r = bm_kv8_rope(int(norm), eps, _optional(q_norm, "kv8_rope: q_norm", t.bfloat16, None, dev),
-                    _optional(k_norm, "kv8_rope: k_norm", t.bfloat16, None, dev),
-                    _optional(inv_freq, "kv8_rope: inv_freq", t.float32, None, dev))
+    r = bm_kv8_rope(int(norm), eps, _optional(q_norm, "kv8_rope", "q_norm", t.bfloat16, None, dev),
+                    _optional(k_norm, "kv8_rope", "k_norm", t.bfloat16, None, dev),
+                    _optional(inv_freq, "kv8_rope", "inv_freq", t.float32, None, dev))
     r.tensors, r.device, r.address = (q_norm, k_norm, inv_freq), dev, ctypes.addressof(r)
     # the head_dim each tensor fits
     r.fits = {x.numel() * f for x, f in ((q_norm, 1), (k_norm, 1), (inv_freq, 2)) if x is not None}
@@ -473,10 +473,10 @@ def kv8_append(cache, qkv, rope, slots, index, Q, rope_pos=None, stream=None):
         raise BitMoeError(1, f"kv8_append: q_norm and k_norm need {d} elements, inv_freq {d // 2}")
     ld = qkv.stride(0) if T > 1 else qkv.shape[1] + (-qkv.shape[1]) % 8
     i32, n = t.int32, (T,)
-    _check(lib().kv8_append(cache.address, qkv.data_ptr(), ld, qh, rope.address, _tensor(slots, "kv8_append: slots", i32, n, dev),
-                            _tensor(index, "kv8_append: index", i32, n, dev),
-                            _optional(rope_pos, "kv8_append: rope_pos", i32, n, dev),
-                            _tensor(Q, "kv8_append: Q", t.bfloat16, None, dev), T, _stream(stream, dev)))
+    _check(lib().kv8_append(cache.address, qkv.data_ptr(), ld, qh, rope.address, _tensor(slots, "kv8_append", "slots", i32, n, dev),
+                            _tensor(index, "kv8_append", "index", i32, n, dev),
+                            _optional(rope_pos, "kv8_append", "rope_pos", i32, n, dev),
+                            _tensor(Q, "kv8_append", "Q", t.bfloat16, None, dev), T, _stream(stream, dev)))
 
 
 def kv8_read(cache, slot, first, count, K_out, V_out, stream=None):
@@ -484,8 +484,8 @@ def kv8_read(cache, slot, first, count, K_out, V_out, stream=None):
     t, dev = _t(), _here()
     _on_device(cache, "kv8_read: cache", dev)
     shape = (cache.kv_heads, count, cache.head_dim)
-    _check(lib().kv8_read(cache.address, slot, first, count, _tensor(K_out, "kv8_read: K_out", t.bfloat16, shape, dev),
-                          _tensor(V_out, "kv8_read: V_out", t.bfloat16, shape, dev), _stream(stream, dev)))
+    _check(lib().kv8_read(cache.address, slot, first, count, _tensor(K_out, "kv8_read", "K_out", t.bfloat16, shape, dev),
+                          _tensor(V_out, "kv8_read", "V_out", t.bfloat16, shape, dev), _stream(stream, dev)))
 
 
 def kv8_workspace_bytes(B, q_heads, kv_heads, head_dim, ctx_cap, prefix_len=0):
@@ -499,9 +499,9 @@ def _attend_args(what, cache, Q, slots, lens, O, ws, scale, dev):
     B, qh, d = shape
     if d != cache.head_dim:
         raise BitMoeError(1, f"{what}: Q of head_dim {d}, the cache of {cache.head_dim}")
-    return (_tensor(Q, f"{what}: Q", t.bfloat16, None, dev), _tensor(slots, f"{what}: slots", t.int32, (B,), dev),
-            _tensor(lens, f"{what}: lens", t.int32, (B,), dev), qh, d ** -0.5 if scale is None else scale,
-            _tensor(O, f"{what}: O", t.bfloat16, shape, dev), B, _tensor(ws, f"{what}: ws", t.uint8, None, dev), ws.numel())
+    return (_tensor(Q, what, "Q", t.bfloat16, None, dev), _tensor(slots, what, "slots", t.int32, (B,), dev),
+            _tensor(lens, what, "lens", t.int32, (B,), dev), qh, d ** -0.5 if scale is None else scale,
+            _tensor(O, what, "O", t.bfloat16, shape, dev), B, _tensor(ws, what, "ws", t.uint8, None, dev), ws.numel())
 
 
 def kv8_attend(cache, Q, slots, lens, O, ws, scale=None, stream=None):
@@ -529,12 +529,12 @@ def bm_sample(logits, temperature, top_k, top_p, min_p, u, ids, logprobs=None, s
         raise BitMoeError(1, "bm_sample: logits must be fp32 or bf16 rows of unit stride on the current CUDA device")
     f32, n = t.float32, (B,)
     _check(lib().bm_sample(logits.data_ptr(), int(half), logits.stride(0) if B > 1 else V, V, B,
-                           _optional(temperature, "bm_sample: temperature", f32, n, dev),
-                           _optional(top_k, "bm_sample: top_k", t.int32, n, dev),
-                           _optional(top_p, "bm_sample: top_p", f32, n, dev),
-                           _optional(min_p, "bm_sample: min_p", f32, n, dev), _tensor(u, "bm_sample: u", f32, n, dev),
-                           _tensor(ids, "bm_sample: ids", t.int32, n, dev),
-                           _optional(logprobs, "bm_sample: logprobs", f32, n, dev), _stream(stream, dev)))
+                           _optional(temperature, "bm_sample", "temperature", f32, n, dev),
+                           _optional(top_k, "bm_sample", "top_k", t.int32, n, dev),
+                           _optional(top_p, "bm_sample", "top_p", f32, n, dev),
+                           _optional(min_p, "bm_sample", "min_p", f32, n, dev), _tensor(u, "bm_sample", "u", f32, n, dev),
+                           _tensor(ids, "bm_sample", "ids", t.int32, n, dev),
+                           _optional(logprobs, "bm_sample", "logprobs", f32, n, dev), _stream(stream, dev)))
 
 
 # --------------------------------------------------------------- host slot map

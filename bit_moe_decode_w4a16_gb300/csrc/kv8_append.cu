@@ -225,16 +225,16 @@ namespace kv8 {
 
 // The cache descriptor's own checks; `who` opens the message.
 bm_status check_cache(const bm_kv8_cache* c, const char* who, Cache* out) {
-  const std::string w(who);
-  if (!c) return set_error(BM_ERR_INVALID_ARG, w + ": null cache");
+  auto refuse = [&](const std::string& what) { return set_error(BM_ERR_INVALID_ARG, std::string(who) + ": " + what); };
+  if (!c) return refuse("null cache");
   if (c->format != BM_KV8_E4M3 && c->format != BM_KV8_INT8)
-    return set_error(BM_ERR_INVALID_ARG, w + ": unknown cache format " + std::to_string(c->format));
-  if (c->head_dim != 64 && c->head_dim != 128) return set_error(BM_ERR_INVALID_ARG, w + ": head_dim must be 64 or 128");
+    return refuse("unknown cache format " + std::to_string(c->format));
+  if (c->head_dim != 64 && c->head_dim != 128) return refuse("head_dim must be 64 or 128");
   if (c->slots < 1 || c->ctx_cap < 1 || c->kv_heads < 1 || c->kv_heads > 1024)
-    return set_error(BM_ERR_INVALID_ARG, w + ": slots and ctx_cap must be >= 1, kv_heads in [1, 1024]");
-  if (!c->K || !c->V || !c->Ks || !c->Vs) return set_error(BM_ERR_INVALID_ARG, w + ": null cache pointer");
+    return refuse("slots and ctx_cap must be >= 1, kv_heads in [1, 1024]");
+  if (!c->K || !c->V || !c->Ks || !c->Vs) return refuse("null cache pointer");
   if (((uintptr_t)c->K | (uintptr_t)c->V) & 15 || ((uintptr_t)c->Ks | (uintptr_t)c->Vs) & 3)
-    return set_error(BM_ERR_INVALID_ARG, w + ": codes must be 16-byte aligned and scales 4-byte aligned");
+    return refuse("codes must be 16-byte aligned and scales 4-byte aligned");
   *out = Cache{c->slots, c->ctx_cap, c->kv_heads, c->K, c->V, c->Ks, c->Vs};
   return BM_OK;
 }

@@ -11,10 +11,7 @@
 #include <math.h>
 
 #include <algorithm>
-#include <mutex>
-#include <set>
 #include <type_traits>
-#include <utility>
 
 #include "kv8_attend.cuh"
 
@@ -453,25 +450,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_merge(AttendArgs a) {
   for (int e = 0; e < E / 2; ++e) *reinterpret_cast<__nv_bfloat162*>(to + 2 * e) = out[e];
 }
 
-// Shared-memory attribute of a kernel on the current device, set once.
-std::mutex g_mu;
-std::set<std::pair<int, const void*>> g_set;
-
-cudaError_t allow_smem(const void* kernel, size_t bytes) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (g_set.count({dev, kernel})) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) g_set.insert({dev, kernel});
-  return e;
-}
-
 template <int D, int FMT>
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
   const size_t most = sizeof(ChunkSmem<D>) + 3 * kMaxBatch * sizeof(int), items = (size_t)a.B * a.c.kvh * a.own_chunks;
-  cudaError_t e = allow_smem((const void*)k_kv8_chunk<D, FMT>, most);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = once_per_device(
+      done, [&] { return cudaFuncSetAttribute(k_kv8_chunk<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most); });
   if (e == cudaSuccess && a.p_chunks > 0) e = launch_kv8_prefix(a, FMT, D, s);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<size_t>(items, kSms * 3);
@@ -490,26 +474,26 @@ size_t records(int ctx_cap, int prefix_len, int kvh) { return (size_t)prefix_chu
 bm_status attend(const char* who, const bm_kv8_cache* c, const bm_kv8_cache* p, int p_slot, int p_len, const uint16_t* Q,
                  const int32_t* slots, const int32_t* lens, int q_heads, float scale, uint16_t* O, int B, void* ws,
                  size_t ws_bytes, void* stream) {
-  const std::string w(who);
+  auto refuse = [&](bm_status st, const std::string& what) { return set_error(st, std::string(who) + ": " + what); };
   AttendArgs a{};
   bm_status st = check_cache(c, who, &a.c);
   if (st != BM_OK) return st;
   if (p) {
     if ((st = check_cache(p, who, &a.p)) != BM_OK) return st;
     if (p->format != c->format || p->kv_heads != c->kv_heads || p->head_dim != c->head_dim)
-      return set_error(BM_ERR_INVALID_ARG, w + ": the prefix's cache must have the streams' format, kv_heads and head_dim");
-    if (p_slot < 0 || p_slot >= p->slots) return set_error(BM_ERR_INVALID_ARG, w + ": prefix_slot out of range");
-    if (p_len < 0 || p_len > p->ctx_cap) return set_error(BM_ERR_CTX_CAP, w + ": prefix_len outside the slot");
+      return refuse(BM_ERR_INVALID_ARG, "the prefix's cache must have the streams' format, kv_heads and head_dim");
+    if (p_slot < 0 || p_slot >= p->slots) return refuse(BM_ERR_INVALID_ARG, "prefix_slot out of range");
+    if (p_len < 0 || p_len > p->ctx_cap) return refuse(BM_ERR_CTX_CAP, "prefix_len outside the slot");
   }
-  if (!Q || !slots || !lens || !O || !ws) return set_error(BM_ERR_INVALID_ARG, w + ": null pointer");
+  if (!Q || !slots || !lens || !O || !ws) return refuse(BM_ERR_INVALID_ARG, "null pointer");
   if (((uintptr_t)Q | (uintptr_t)O | (uintptr_t)ws) & 15)
-    return set_error(BM_ERR_INVALID_ARG, w + ": Q, O and the workspace must be 16-byte aligned");
+    return refuse(BM_ERR_INVALID_ARG, "Q, O and the workspace must be 16-byte aligned");
   if (!shapes_ok(B, q_heads, c->kv_heads, c->head_dim))
-    return set_error(BM_ERR_INVALID_ARG, w + ": need 1 <= B <= 1024, q_heads <= 1024 and a multiple of kv_heads, at most 8 query heads per kv head");
-  if (!(scale > 0.f) || !(scale < INFINITY)) return set_error(BM_ERR_INVALID_ARG, w + ": scale must be positive and finite");
+    return refuse(BM_ERR_INVALID_ARG, "need 1 <= B <= 1024, q_heads <= 1024 and a multiple of kv_heads, at most 8 query heads per kv head");
+  if (!(scale > 0.f) || !(scale < INFINITY)) return refuse(BM_ERR_INVALID_ARG, "scale must be positive and finite");
   const size_t need = kv8_workspace_bytes(B, q_heads, c->kv_heads, c->head_dim, c->ctx_cap, p_len);
   if (ws_bytes < need)
-    return set_error(BM_ERR_INVALID_ARG, w + ": workspace of " + std::to_string(ws_bytes) + " bytes, " + std::to_string(need) + " needed");
+    return refuse(BM_ERR_INVALID_ARG, "workspace of " + std::to_string(ws_bytes) + " bytes, " + std::to_string(need) + " needed");
   a.p_slot = p_slot;
   a.p_len = p_len;
   a.p_chunk = prefix_chunk(p_len, c->kv_heads);
@@ -528,7 +512,7 @@ bm_status attend(const char* who, const bm_kv8_cache* c, const bm_kv8_cache* p, 
   const bool e4 = c->format == BM_KV8_E4M3, d128 = c->head_dim == 128;
   const cudaError_t e = d128 ? (e4 ? launch_attend<128, BM_KV8_E4M3>(a, s) : launch_attend<128, BM_KV8_INT8>(a, s))
                              : (e4 ? launch_attend<64, BM_KV8_E4M3>(a, s) : launch_attend<64, BM_KV8_INT8>(a, s));
-  if (e != cudaSuccess) return set_error(BM_ERR_CUDA, w + ": " + cudaGetErrorString(e));
+  if (e != cudaSuccess) return refuse(BM_ERR_CUDA, cudaGetErrorString(e));
   return ok();
 }
 

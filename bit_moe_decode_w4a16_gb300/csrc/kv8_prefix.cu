@@ -31,10 +31,7 @@
 //
 // Every wait is bounded.  A wait that gives up leaves NaN in its CTA's
 // records, and so in the output rows.
-#include <mutex>
-#include <set>
 #include <type_traits>
-#include <utility>
 
 #include "kv8_attend.cuh"
 #include "tc_ptx.cuh"
@@ -437,23 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
   }
 }
 
-std::mutex g_mu;
-std::set<std::pair<int, const void*>> g_set;
-
 template <int D, int FMT>
 cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
   const size_t smem = sizeof(PrefixSmem<D>) + 1024;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = once_per_device(
+      done, [&] { return cudaFuncSetAttribute(k_kv8_prefix<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
   if (e != cudaSuccess) return e;
-  {
-    std::lock_guard<std::mutex> lk(g_mu);
-    const void* f = (const void*)k_kv8_prefix<D, FMT>;
-    if (!g_set.count({dev, f})) {
-      if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-      g_set.insert({dev, f});
-    }
-  }
   const int rows = a.B * (a.qh / a.c.kvh);
   return launch_k(false, k_kv8_prefix<D, FMT>, dim3(a.p_chunks, (rows + kRows - 1) / kRows, a.c.kvh), dim3(kThreads), smem, s, a);
 }

@@ -36,8 +36,6 @@
 #include <float.h>
 #include <stddef.h>
 
-#include <mutex>
-#include <set>
 #include <type_traits>
 
 #include "common.cuh"
@@ -693,23 +691,18 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
   }
 }
 
-std::mutex g_mu;
-std::set<int> g_devices;
-
 // Shared-memory and cluster attributes of both kernels on the current device.
 cudaError_t ensure_attributes() {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (g_devices.count(dev)) return cudaSuccess;
-  const void* kernels[] = {(const void*)k_sample<float>, (const void*)k_sample<bf16>};
-  for (const void* f : kernels) {
-    if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-  }
-  g_devices.insert(dev);
-  return cudaSuccess;
+  static std::atomic<unsigned long long> done{0};
+  return once_per_device(done, [] {
+    const void* kernels[] = {(const void*)k_sample<float>, (const void*)k_sample<bf16>};
+    cudaError_t e = cudaSuccess;
+    for (const void* f : kernels) {
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    }
+    return e;
+  });
 }
 
 // CTAs per row.
