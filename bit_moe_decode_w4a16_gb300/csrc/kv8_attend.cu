@@ -60,7 +60,8 @@ struct ChunkSmem {
   static_assert(sizeof(WarpOut<D>) <= sizeof(Ring<D>), "a warp's output fits a slot");
   Ring<D> ring[kWarpsPerItem][kRing];   // at an item's end a warp's output lies in the slot it has just used
   float m[kWarpsPerItem][8], l[kWarpsPerItem][8];
-  int table[1];                       // [B] slots, [B] lengths, [B + 1] own items before each stream's
+  int streams;                        // live ones of some length
+  int table[1];                       // [B] slots, [B] lengths, [B] the live streams in item order, [2 B + 1] items before each entry's
 };
 
 // 16-byte piece c of a position's codes in the ring: swizzled so that both products read without bank conflicts.
@@ -101,62 +102,95 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int kvh = a.c.kvh, G = a.qh / kvh;
   pdl_trigger();   // the whole grid is resident: the merge may take the free slots
-  int *slots = sm.table, *lens = slots + a.B, *first = lens + a.B;
+  int *slots = sm.table, *lens = slots + a.B, *order = lens + a.B, *first = order + a.B;
 
-  // ---- the items: every live stream's kv heads and chunks
+  // ---- the items: the streams' whole chunks, streams of the largest chunks first, then their last, shorter ones.
+  // CTA i takes item i of every even block of gridDim items and the opposite one of every odd block, which
+  // evens out their sizes.
+  int streams = 0;
   if (warp == 0) {
-    int sum = 0;
+    int top = 0, low = 1 << 30, sum = 0;   // chunk sizes there are
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      int slot, len, c = 0;
-      if (b0 + lane < a.B) {
-        if (a.live(b0 + lane, slot, len)) c = chunks_of(len) * kvh;
-        slots[b0 + lane] = slot;
-        lens[b0 + lane] = len;
+      const int b = b0 + lane;
+      if (b < a.B) {
+        int slot, len;
+        if (!a.live(b, slot, len)) len = 0;
+        slots[b] = slot;
+        lens[b] = len;
+        if (len > 0) {
+          top = max(top, chunk_of(len));
+          low = min(low, chunk_of(len));
+        }
       }
-      int inc = c;
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    low = __reduce_min_sync(0xffffffffu, low);
+    // an entry's items before it, the lanes' entries in their order
+    auto enter = [&](bool has, int count, int at) {
+      int inc = has ? count : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
-      if (b0 + lane < a.B) first[b0 + lane] = sum + inc - c;
+      if (has) first[at] = sum + inc - count;
       sum += __shfl_sync(0xffffffffu, inc, 31);
+    };
+    for (int size = top; size >= low; size /= 2)
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane, len = b < a.B ? lens[b] : 0;
+        const bool has = len > 0 && chunk_of(len) == size;
+        const unsigned votes = __ballot_sync(0xffffffffu, has);
+        const int at = streams + __popc(votes & ((1u << lane) - 1));
+        if (has) order[at] = b;
+        enter(has, len / size * kvh, at);
+        streams += __popc(votes);
+      }
+    __syncwarp();
+    for (int e0 = 0; e0 < streams; e0 += 32) {
+      const int e = e0 + lane, len = e < streams ? lens[order[e]] : 0;
+      enter(e < streams, len > 0 && len % chunk_of(len) ? kvh : 0, streams + e);
     }
-    if (lane == 0) first[a.B] = sum;
+    if (lane == 0) {
+      first[2 * streams] = sum;
+      sm.streams = streams;
+    }
   }
   __syncthreads();
-  const int items = first[a.B];
-  // a CTA takes a run of items: the chunks of a query row one after the other
-  const int begin = (int)((long long)items * blockIdx.x / gridDim.x), end = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
+  streams = sm.streams;
+  const int items = first[2 * streams], step = gridDim.x;
+  const float inv_kvh = 1.f / kvh;
+  auto take = [&](int round) { return round * step + (round & 1 ? step - 1 - (int)blockIdx.x : (int)blockIdx.x); };
   auto item_of = [&](int it) {
-    int lo = 0, hi = a.B;             // the last stream with first <= it
+    int lo = 0, hi = 2 * streams;     // the last entry with first <= it
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (first[mid] <= it) lo = mid;
       else hi = mid;
     }
     Item i;
-    const int r = it - first[lo], chunks = (first[lo + 1] - first[lo]) / kvh, size = chunk_of(lens[lo]);
-    i.b = lo;
-    i.kh = r / chunks;
-    i.rec = r - i.kh * chunks;
-    const size_t row = a.c.row(slots[lo], i.kh, i.rec * size);
+    i.b = order[lo < streams ? lo : lo - streams];
+    const int r = it - first[lo], len = lens[i.b], size = chunk_of(len);
+    const int c = (int)((r + 0.5f) * inv_kvh);   // r / kvh, exact below 2^17
+    i.kh = r - c * kvh;
+    i.rec = lo < streams ? c : len / size;
+    const size_t row = a.c.row(slots[i.b], i.kh, i.rec * size);
     i.K = a.c.K + row * D;
     i.V = a.c.V + row * D;
     i.Ks = a.c.Ks + row;
     i.Vs = a.c.Vs + row;
-    i.n = min(size, lens[lo] - i.rec * size);
+    i.n = min(size, len - i.rec * size);
     return i;
   };
 
   // ---- loads run a stage ahead of the arithmetic, into the next item too
   constexpr int kPieces = D / 16, kRows = 32 / kPieces, kCopies = kTake / kRows;   // a lane copies a piece of every kRows-th position
   const int my_row = lane / kPieces, my_piece = lane % kPieces;
-  int load_it = begin, load_j = kTake * warp, load_slot = 0;
+  int load_round = 0, load_it = take(0), load_j = kTake * warp, load_slot = 0;
   Item li{};
-  if (load_it < end) li = item_of(load_it);
+  if (load_it < items) li = item_of(load_it);
   auto load = [&]() {
-    if (load_it < end) {
+    if (load_it < items) {
       Ring<D>& s = sm.ring[warp][load_slot];
       const int left = li.n - load_j;
       const size_t off = (size_t)(load_j + my_row) * D + 16 * my_piece;
@@ -186,9 +220,9 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
       load_slot = load_slot + 1 == kRing ? 0 : load_slot + 1;
       load_j += kStage;
       if (load_j - kTake * warp >= li.n) {
-        ++load_it;
+        load_it = take(++load_round);
         load_j = kTake * warp;
-        if (load_it < end) li = item_of(load_it);
+        if (load_it < items) li = item_of(load_it);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -200,31 +234,38 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
   constexpr int kPer = D / 64;        // 16-byte pieces of a K row per lane
   uint32_t q[kPer][4][2];
   float qf = 0.f;
-  int q_b = -1, q_kh = 0;
-  for (int it = begin; it < end; ++it) {
-    const Item i = item_of(it);
-    if (i.b != q_b || i.kh != q_kh) {
-      // ---- this lane's query row (head g), as fp16 of about its own magnitude
-      q_b = i.b;
-      q_kh = i.kh;
-      qf = a.scale_log2;
-      uint4 x[kPer][2];
-      float mx = 0.f;
+  // this lane's query row (head g), read while the item before is merged
+  uint4 x[kPer][2];
+  auto ask = [&](const Item& i) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        x[j][u] = make_uint4(0, 0, 0, 0);
+        if (g < G) x[j][u] = *reinterpret_cast<const uint4*>(a.Q + ((size_t)i.b * a.qh + i.kh * G + g) * D + 16 * (kPer * t + j) + 8 * u);
+      }
+  };
+  Item i{};
+  if (take(0) < items) {
+    i = item_of(take(0));
+    ask(i);
+  }
+  for (int round = 0; take(round) < items; ++round) {
+    // ---- as fp16 of about its own magnitude
+    {
+      float mx = 0.f, down, up;
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          x[j][u] = make_uint4(0, 0, 0, 0);
-          if (g < G) x[j][u] = *reinterpret_cast<const uint4*>(a.Q + ((size_t)i.b * a.qh + i.kh * G + g) * D + 16 * (kPer * t + j) + 8 * u);
           const uint32_t w[4] = {x[j][u].x, x[j][u].y, x[j][u].z, x[j][u].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w[e])), fabsf(bf_hi(w[e]))));
         }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      float down, up;
       row_scale(mx, down, up);
-      qf *= up;
+      qf = a.scale_log2 * up;
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
 #pragma unroll
@@ -358,6 +399,11 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
       *reinterpret_cast<float2*>(&out[2 * t][d]) = make_float2(o[j][0], o[j][2]);
       *reinterpret_cast<float2*>(&out[2 * t + 1][d]) = make_float2(o[j][1], o[j][3]);
     }
+    const Item done = i;
+    if (take(round + 1) < items) {
+      i = item_of(take(round + 1));
+      ask(i);
+    }
     __syncthreads();
 #pragma unroll 1
     for (int r = warp; r < G; r += kWarpsPerItem) {
@@ -369,7 +415,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
         f[w] = exp2_fast(sm.m[w][r] - mx);
         den += sm.l[w][r] * f[w];
       }
-      const size_t rec = a.record(i.b, i.kh * G + r, a.p_chunks + i.rec);
+      const size_t rec = a.record(done.b, done.kh * G + r, a.p_chunks + done.rec);
 #pragma unroll
       for (int d = 2 * lane; d < D; d += 64) {
         float2 acc = make_float2(0.f, 0.f);
@@ -452,14 +498,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_merge(AttendArgs a) {
 
 template <int D, int FMT>
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
-  const size_t most = sizeof(ChunkSmem<D>) + 3 * kMaxBatch * sizeof(int), items = (size_t)a.B * a.c.kvh * a.own_chunks;
+  const size_t most = sizeof(ChunkSmem<D>) + 5 * kMaxBatch * sizeof(int), items = (size_t)a.B * a.c.kvh * a.own_chunks;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = once_per_device(
       done, [&] { return cudaFuncSetAttribute(k_kv8_chunk<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most); });
   if (e == cudaSuccess && a.p_chunks > 0) e = launch_kv8_prefix(a, FMT, D, s);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<size_t>(items, kSms * 3);
-  e = launch_k(a.p_chunks > 0, k_kv8_chunk<D, FMT>, dim3(grid), dim3(kWarpsPerItem * 32), sizeof(ChunkSmem<D>) + 3 * a.B * sizeof(int), s, a);
+  e = launch_k(a.p_chunks > 0, k_kv8_chunk<D, FMT>, dim3(grid), dim3(kWarpsPerItem * 32), sizeof(ChunkSmem<D>) + 5 * a.B * sizeof(int), s, a);
   if (e != cudaSuccess) return e;
   return launch_k(true, k_kv8_merge<D>, dim3((a.B * a.qh + kMergeWarps - 1) / kMergeWarps), dim3(kMergeWarps * 32), 0, s, a);
 }
