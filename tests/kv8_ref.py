@@ -110,7 +110,7 @@ def sample(x, temp, top_k, top_p, min_p, u):
             continue
         order = np.argsort(-row, kind="stable")
         with np.errstate(invalid="ignore"):
-            w = np.where(row == top, 1.0, np.exp((row - top) / float(temp[b])))
+            w = np.where(row == top, 1.0, np.where(row == -np.inf, 0.0, np.exp((row - top) / float(temp[b]))))
         s = w[order]
         n = V if top_k[b] <= 0 else min(V, int(top_k[b]))
         s = s[:n]

@@ -87,7 +87,7 @@ def _check_append(bm, fmt, T, qh, kvh, d, norm, rotate, weights=True, ld_pad=0, 
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,qh,kvh,d", [(1, 8, 2, 64), (5, 32, 4, 128), (33, 12, 4, 128), (7, 4, 4, 64), (3, 128, 16, 128),
-                                        (2, 1, 1, 64), (300, 8, 8, 128)])
+                                        (2, 1, 1, 64), (300, 8, 8, 128), (5000, 6, 2, 64), (2500, 32, 4, 128)])
 def test_append(bm, fmt, T, qh, kvh, d):
     _check_append(bm, fmt, T, qh, kvh, d, norm=True, rotate=True)
 
@@ -291,6 +291,26 @@ def test_offsets_past_32_bits(bm):
     assert ((O[0].double() - want).abs() <= BF16_HALF * want.abs() + size * 2.0 ** -10).all()
 
 
+@pytest.mark.parametrize("P", [0, 130])
+def test_largest_batch(bm, P):
+    """1024 rows, some of them of one slot, with and without a prefix."""
+    B, qh, kvh, d = 1024, 8, 1, 64
+    cache = ref.random_cache(E4M3, 50, 40, kvh, d, 14)
+    slots, lens = torch.randint(-1, 50, (B,)).int().cuda(), torch.randint(0, 41, (B,)).int().cuda()
+    Q = torch.randn(B, qh, d, device="cuda").bfloat16()
+    prefix = ref.random_cache(E4M3, 1, 130, kvh, d, 15) if P else None
+    O = _attend(bm, cache, Q, slots, lens, prefix=prefix, p_len=P)
+    _check_rows(O, *ref.attend(cache, Q, slots, lens, d ** -0.5, prefix=(prefix, 0, P) if P else None))
+
+
+def test_nothing_to_attend_over(bm):
+    """All rows empty or padding: zeros, or what was there."""
+    cache = ref.random_cache(INT8, 3, 20, 2, 64, 16)
+    Q = torch.randn(4, 4, 64, device="cuda").bfloat16()
+    O = _attend(bm, cache, Q, _i32(0, -1, 2, 7), _i32(0, 5, 0, 5))
+    assert (O[0] == 0).all() and (O[1] == 5).all() and (O[2] == 0).all() and (O[3] == 5).all()
+
+
 # ---------------------------------------------------------------- shared prefix
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -387,6 +407,27 @@ def test_streams_and_graph_replay(bm):
     b = _attend(bm, cache, Q, slots, lens)
     torch.cuda.synchronize()
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_two_streams_at_once(bm):
+    """Calls that overlap on the GPU, each with a workspace of its own, give what they give alone."""
+    kvh, d, qh, B, P = 2, 128, 16, 20, 3000
+    prefix = ref.random_cache(E4M3, 1, P, kvh, d, 61)
+    cache = ref.random_cache(E4M3, B, 2000, kvh, d, 62)
+    h, hp = bm.kv8_cache(**cache), bm.kv8_cache(**prefix)
+    slots, lens = torch.arange(B, dtype=torch.int32, device="cuda"), torch.randint(1, 2001, (B,)).int().cuda()
+    Q = [torch.randn(B, qh, d, device="cuda").bfloat16() for _ in range(2)]
+    want = [_attend(bm, cache, q, slots, lens, prefix=prefix, p_len=P) for q in Q]
+    O = [torch.zeros_like(q) for q in Q]
+    ws = [torch.empty(bm.kv8_workspace_bytes(B, qh, kvh, d, 2000, P), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            bm.kv8_attend_prefix(h, hp, 0, P, Q[i], slots, lens, O[i], ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(O[i].view(torch.int16), want[i].view(torch.int16))
 
 
 def test_serving_loop(bm):

@@ -154,6 +154,32 @@ def test_rows_strides_streams_and_optional_arguments(bm):
     _check(bm, odd, np.ones(3), [5, 0, 0], [1, 0.5, 1], [0, 0, 0.1], [0.1, 0.5, 0.9], least=0.3)
 
 
+def test_temperatures_at_the_ends(bm):
+    """An infinite temperature makes all finite logits equal; the smallest ones leave the first of the largest."""
+    V = 40000
+    x = _logits(4, V, 21)
+    x[1, 5:] = -float("inf")
+    x[3] = 1.25
+    for T in (float("inf"), 3e38):
+        for p in (1.0, 0.5):
+            ids = _check(bm, x, np.full(4, T), np.zeros(4, int), np.full(4, p), np.zeros(4), np.full(4, 0.3), least=0.0)
+            assert ids[1] < 5 and (p == 1.0) <= (abs(ids[0] - 0.3 * V) <= 1) and abs(ids[3] - 0.3 * p * V) <= 1
+    for T in (1e-45, 1e-38, 1e-20):
+        ids, lp = _call(bm, x[:2], temp=np.full(2, T), top_p=np.full(2, 0.9), u=np.full(2, 0.999))
+        assert (ids == x[:2].argmax(1).cpu().numpy()).all() and (lp == 0).all()
+
+
+@pytest.mark.parametrize("V", [151936, 300001])
+def test_few_distinct_values(bm, V):
+    """Steps that hold far more logits than are gathered: cuts inside runs of equal values, across every CTA."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    x = torch.randint(0, 3, (6, V), generator=g, device="cuda").float() * 0.01
+    x[4:] = torch.randint(0, 400, (2, V), generator=g, device="cuda").float() * 1e-5
+    k, p = [7, V // 2, 0, V - V // 5, 60000, 0], [1.0, 1.0, 0.4, 0.9, 0.7, 0.55]
+    _check(bm, x, np.full(6, 0.9), k, p, np.zeros(6), [0.99, 0.7, 0.8, 0.999, 0.6, 0.1], least=0.5)
+
+
 def test_u_outside_its_range(bm):
     x = _logits(4, 500, 8)
     ids, _ = _call(bm, x, u=[-1.0, float("nan"), 1.0, 5.0])
