@@ -8,12 +8,18 @@
 // with M = 448 (e4m3) or 127 (int8).  One rounding each: q and the codes are
 // rounded from fp32, with no bf16 step between the norm and the rotation.
 //
-// It is bound by the bytes of the rows (each read once and written once).  A
-// head belongs to d / 8 lanes, 4 elements and their 4 partners of the rotation
-// each: a head's sums and maxima are 3 or 4 shuffles, a rotation none.  A thread keeps its
-// place in the row and walks over rows, so norm weights and frequencies are
-// read once; two rows are on their way while one is worked on, and a CTA's
-// first d / 2 threads make the next row's cosines and sines meanwhile.
+// Each row is read once and written once.  A head belongs to d / 8 lanes, 4
+// elements and their 4 partners of the rotation each: a head's sums and maxima
+// are 3 or 4 shuffles, a rotation none.  A thread keeps its place in the row
+// and walks over rows, so norm weights and frequencies are read once; two rows
+// are on their way while one is worked on, and a CTA's first d / 2 threads make
+// the next row's cosines and sines meanwhile.
+//
+// 4000 rows of 32 + 2 x 4 heads of 128, e4m3: 22.1 us, 3.5 TB/s.  Instructions
+// and the latency of a row's two shuffle chains bound it, not the bytes
+// (11.6 us): more CTAs an SM (42 registers) spilled and took 26.6 us, element
+// pairs split over lanes 32.7 us, a CTA of a whole row's heads 46.6 us.  A
+// call of 1 to 32 rows is one latency chain: 2.4 to 2.8 us.
 #include <algorithm>
 
 #include "kv8.cuh"
@@ -177,7 +183,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv8_append(AppendArgs a) {
   }
 }
 
-// bf16(code * scale), 16 codes to a thread; K in blockIdx.z = 0, V in 1.
+// bf16(code * scale), 16 codes to a thread; K in blockIdx.z = 0, V in 1: one
+// 16-byte load and two 16-byte stores a thread, bound by HBM.  65536 positions
+// of 4 heads of 128: 32.1 us, 6.3 TB/s (94% of a plain copy).
 template <int D, int FMT>
 __global__ void __launch_bounds__(256) k_kv8_read(Cache c, int slot, int first, int count, bf16* K, bf16* V) {
   constexpr int kLanes = D / 16;

@@ -44,6 +44,14 @@ using namespace kv8;
 // magnitude, and what is rounded away is small against the largest term of
 // the sum.  The reference moves only when it is passed by 2^8 (an fp16 holds
 // that), so the output is seldom rescaled.
+//
+// Three CTAs an SM take items in order of size, so the grid ends together.
+// 32 streams of 8192 positions, 32 + 2 x 4 heads of 128, e4m3: 54 us with the
+// merge, 5.1 TB/s of codes and scales; 12 warps an SM keep 65% of HBM busy
+// (four CTAs with stages of half the size took longer, two with twice as
+// much shared memory 84 us).  16 streams of 1 to 8192: 17.0 us, where the
+// items' uneven ends and the chain of two launches show.  One stream of 4096:
+// 7.2 us, latency alone.
 constexpr int kWarpsPerItem = 4, kTake = 32, kStage = kWarpsPerItem * kTake, kRing = 2;
 
 template <int D>
@@ -438,7 +446,8 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
 // One head of one stream to a warp: its records in ascending order, a lane
 // d / 32 elements.  The kernel is a chain of latencies, so everything is
 // asked for at once: the maxima and sums (a record to a lane), and the first
-// outputs before their weights are known.
+// outputs before their weights are known.  About 2 us behind the chunks,
+// whatever the sizes; it starts with them (programmatic dependent launch).
 constexpr int kMergeWarps = 4, kMergeAhead = 8;
 
 template <int D>

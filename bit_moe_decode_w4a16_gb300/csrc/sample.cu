@@ -30,8 +30,11 @@
 // through distributed shared memory: each sums a share of the bins and writes
 // it to all.
 //
-// What bounds it is instructions: about 45 for a weight, one weight a logit
-// without filters.
+// What bounds it is instructions (about 31 for a weight, a weight a logit and
+// filter) and the cluster's barriers, 1300 cycles each.  Rows of 151936 fp32
+// logits, all filters: 23 us for one, where 16 CTAs share the row, 45 us for
+// 32, where 8 do; reading those takes 3 us.  Histograms in 64-bit shared
+// atomics, which are loops of compare and swap, took 59 us.
 #include <cooperative_groups.h>
 #include <float.h>
 #include <stddef.h>
@@ -705,11 +708,21 @@ cudaError_t ensure_attributes() {
   });
 }
 
-// CTAs per row.
+// CTAs per row: the largest cluster that still pays, and at least one whose shared memory holds the row (20 tiles a
+// warp).  A wider cluster shortens every sweep but costs barriers, and its rows start together only while they fit:
+// 15 clusters of 8 or 7 of 16 (they lie within a GPC), 128 CTAs of the smaller ones an SM each, two an SM after that.
+// Sharing an SM, or waiting for a second wave, pays for longer rows only.  Times of 4 / 8 / 16 CTAs a row, us:
+//   V = 32000:   9 rows 17.8 / 15.2 / 18.1;  16 rows 19.3 / 21.6 / 23.0;  128 rows 43.7 / 61.6 / 120 (2 CTAs: 36.3)
+//   V = 151936:  8 rows 58.3 / 37.1 / 25.6;  16 rows 58.8 / 38.9 / 31.0;  32 rows 48.2 / 45.1 / 53.8
+//   V = 1000:   any rows below 64, 1 CTA 10.5, 4 12.5
 int cluster_size(int B, int V) {
-  int n = 1;
-  while (n < 8 && n * 4096 < V) n *= 2;
-  if (V > 8 * kWarps * kTile * 20 || (n == 8 && B <= 4)) n = 16;
+  int n = kMaxCluster;
+  for (; n > 1 && n * kWarps * kTile * 10 >= V; n /= 2) {
+    const int64_t ctas = (int64_t)B * n;
+    if (ctas <= (n > 4 ? 120 : 128) && n * 2048 <= V) break;
+    if (ctas <= 256 && n * 4096 <= V) break;
+    if (ctas <= 512 && n * 12288 <= V) break;
+  }
   return n;
 }
 

@@ -247,3 +247,21 @@ def test_refusals(bm):
         with pytest.raises(bm.BitMoeError):
             call()
             pytest.fail(f"call {i} was accepted")
+
+
+@pytest.mark.parametrize("V", [1000, 20000, 60000])
+def test_rows_do_not_depend_on_the_batch(bm, V):
+    """From one row to a thousand the work is cut into clusters of 16 to 1 CTAs; ids and log probabilities are the same bits."""
+    n = 7
+    x = _logits(n, V, 31)
+    x[5, 100:] = -float("inf")
+    x[6] = x[6].bfloat16().float()
+    s = dict(temp=[1.0, 0.7, 1.3, 0.9, 0.0, 1.0, 1.0], top_k=[0, 50, 0, 5000, 0, 0, 0], top_p=[0.9, 0.95, 1, 0.5, 1, 0.8, 0.7],
+             min_p=[0, 0, 0.02, 0.001, 0, 0, 0], u=[0.5, 0.1, 0.9, 0.3, 0.2, 0.6, 0.999])
+    alone = [_call(bm, x[i:i + 1], **{k: [v[i]] for k, v in s.items()}) for i in range(n)]
+    want, wlp = np.concatenate([a[0] for a in alone]), np.concatenate([a[1] for a in alone])
+    for B in (n, 15, 16, 33, 65, 130, 257, 1000):
+        row = np.arange(B) % n
+        ids, lp = _call(bm, x[torch.as_tensor(row).cuda()], **{k: np.asarray(v)[row] for k, v in s.items()})
+        np.testing.assert_array_equal(ids, want[row])
+        np.testing.assert_array_equal(lp, wlp[row])
