@@ -8,18 +8,19 @@
 // with M = 448 (e4m3) or 127 (int8).  One rounding each: q and the codes are
 // rounded from fp32, with no bf16 step between the norm and the rotation.
 //
-// Each row is read once and written once.  A head belongs to d / 8 lanes, 4
-// elements and their 4 partners of the rotation each: a head's sums and maxima
-// are 3 or 4 shuffles, a rotation none.  A thread keeps its place in the row
+// Each row is read once and written once.  A head belongs to d / 16 lanes, 8
+// elements and their 8 partners of the rotation each: a head's sums and maxima
+// are 2 or 3 shuffles, a rotation none.  A thread keeps its place in the row
 // and walks over rows, so norm weights and frequencies are read once; two rows
 // are on their way while one is worked on, and a CTA's first d / 2 threads make
 // the next row's cosines and sines meanwhile.
 //
-// 4000 rows of 32 + 2 x 4 heads of 128, e4m3: 22.1 us, 3.5 TB/s.  Instructions
-// and the latency of a row's two shuffle chains bound it, not the bytes
-// (11.6 us): more CTAs an SM (42 registers) spilled and took 26.6 us, element
-// pairs split over lanes 32.7 us, a CTA of a whole row's heads 46.6 us.  A
-// call of 1 to 32 rows is one latency chain: 2.4 to 2.8 us.
+// 4000 rows of 32 + 2 x 4 heads of 128, e4m3: 15.6 us, 5.0 TB/s.  What is paid
+// per thread and row (its addresses, loads, shuffles, branches) came before
+// the bytes (11.6 us): 8 elements to a thread took 22 us, with fp32 pairs in
+// one instruction or without, 4 took 33; a third more threads on an SM, at
+// fewer registers, 20.  A call of 1 to 32 rows is one latency chain of 2.1 to
+// 2.5 us, longer by 0.4 with CTAs of 320 threads, whose rows start together.
 #include <algorithm>
 
 #include "kv8.cuh"
@@ -60,118 +61,155 @@ __device__ __forceinline__ float2 rotation(int pos, unsigned long long turns) {
   return make_float2(c, s);
 }
 
-__device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
-  x[0] = bf_lo(r.x); x[1] = bf_hi(r.x); x[2] = bf_lo(r.y); x[3] = bf_hi(r.y);
-  x[4] = bf_lo(r.z); x[5] = bf_hi(r.z); x[6] = bf_lo(r.w); x[7] = bf_hi(r.w);
+// Eight bf16 -> four pairs of fp32, two values to an instruction from there on.
+__device__ __forceinline__ void unpack8(uint4 r, uint64_t* x) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pack2(bf_lo(w[i]), bf_hi(w[i]));
+}
+__device__ __forceinline__ uint4 round8(const uint64_t* x) {
+  uint32_t p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(first(x[i]), second(x[i]));
+    p[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(p[0], p[1], p[2], p[3]);
+}
+template <int FMT>
+__device__ __forceinline__ uint2 encode8(const uint64_t* x, float inv) {
+  float f[8];
+  const uint64_t inv2 = pack2(inv, inv);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t v = mul2(x[i], inv2);
+    f[2 * i] = first(v);
+    f[2 * i + 1] = second(v);
+  }
+  return make_uint2(encode4<FMT>(f), encode4<FMT>(f + 4));
 }
 
-constexpr int kMaxThreads = 512;
+// The largest of three magnitudes; NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+constexpr int kMaxThreads = 160, kCtasPerSm = 4;
 
 struct AppendRow {
-  uint4 raw;
+  uint4 lo, hi;
   int slot, idx, pos;
 };
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kMaxThreads) k_kv8_append(AppendArgs a) {
-  constexpr int kLanes = D / 8;   // lanes of a head
-  __shared__ __align__(16) float2 cs[2][D / 2];
+__global__ void __launch_bounds__(kMaxThreads, kCtasPerSm) k_kv8_append(AppendArgs a) {
+  constexpr int kLanes = D / 16;   // lanes of a head
+  __shared__ __align__(16) float cs[2][2][D / 2];   // cosines and sines of a row's angles
   const int l = threadIdx.x % kLanes, h = blockIdx.y * a.heads_per_cta + threadIdx.x / kLanes;
   const int kvh = a.c.kvh, heads = a.qh + 2 * kvh;
   const bool live = h < heads && (int)(threadIdx.x / kLanes) < a.heads_per_cta;
   const bool is_v = h >= a.qh + kvh, is_q = h < a.qh, all_v = __all_sync(0xffffffffu, is_v), any_kv = __any_sync(0xffffffffu, live && !is_q);
   const bool rotated = a.inv_freq != nullptr, turns_here = rotated && threadIdx.x < D / 2;
   // Rows outside the cache are padding: nothing of theirs is written.
-  auto valid = [&](const AppendRow& r) { return r.slot >= 0 && r.slot < a.c.slots && r.idx >= 0 && r.idx < a.c.cap; };
-  // elements 4l .. 4l + 3 and their partners of the rotation, d / 2 further on
-  auto both_halves = [&](const bf16* head) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(head + 4 * l)), y = __ldg(reinterpret_cast<const uint2*>(head + D / 2 + 4 * l));
-    return make_uint4(x.x, x.y, y.x, y.y);
-  };
+  auto valid = [&](const AppendRow& r) { return (unsigned)r.slot < (unsigned)a.c.slots && (unsigned)r.idx < (unsigned)a.c.cap; };
+  // elements 8l .. 8l + 7 and their partners of the rotation, d / 2 further on
+  const bf16* mine = a.qkv + (size_t)h * D + 8 * l;
+  const int32_t* positions = a.pos ? a.pos : a.index;
   auto load = [&](int t) {
-    AppendRow r{make_uint4(0, 0, 0, 0), -1, -1, 0};
+    AppendRow r{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), -1, -1, 0};
     if (t < a.T) {
       r.slot = __ldg(a.slots + t);
       r.idx = __ldg(a.index + t);
-      if (turns_here) r.pos = a.pos ? __ldg(a.pos + t) : r.idx;
-      if (live) r.raw = both_halves(a.qkv + t * a.ld + (size_t)h * D);
+      if (turns_here) r.pos = __ldg(positions + t);
+      if (live) {
+        const uint4* at = reinterpret_cast<const uint4*>(mine + t * a.ld);
+        r.lo = __ldg(at);
+        r.hi = __ldg(at + D / 16);
+      }
     }
     return r;
   };
   const int step = gridDim.x;
   AppendRow now = load(blockIdx.x), next = load(blockIdx.x + step);
   const unsigned long long turns = turns_here ? turns64(a.inv_freq[threadIdx.x]) : 0;
+  auto rotate = [&](int b, int pos) {
+    const float2 r = rotation(pos, turns);
+    cs[b][0][threadIdx.x] = r.x;
+    cs[b][1][threadIdx.x] = r.y;
+  };
   const bf16* nw = is_q ? a.q_norm : a.k_norm;
-  uint4 w8 = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // ones
-  if (a.norm && !is_v && nw) w8 = both_halves(nw);
-  if (turns_here) cs[0][threadIdx.x] = rotation(now.pos, turns);
+  uint4 w_lo = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), w_hi = w_lo;   // ones
+  if (a.norm && !is_v && nw) {
+    const uint4* at = reinterpret_cast<const uint4*>(nw + 8 * l);
+    w_lo = __ldg(at);
+    w_hi = __ldg(at + D / 16);
+  }
+  if (turns_here) rotate(0, now.pos);
   if (rotated) __syncthreads();
   int b = 0;
   for (int t = blockIdx.x; t < a.T; t += step) {
     const AppendRow after = load(t + 2 * step);
-    if (turns_here && t + step < a.T) cs[b ^ 1][threadIdx.x] = rotation(next.pos, turns);
+    if (turns_here) rotate(b ^ 1, next.pos);
     if (valid(now)) {
-      float x[8];
-      unpack8(now.raw, x);
+      uint64_t x[8];
+      unpack8(now.lo, x);
+      unpack8(now.hi, x + 4);
       if (a.norm && !all_v) {
-        float ss = 0.f, w[8];
+        uint64_t s2 = mul2(x[0], x[0]), w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-        ss = group_sum<kLanes>(ss);
+        for (int i = 1; i < 8; ++i) s2 = fma2(x[i], x[i], s2);
+        const float ss = group_sum<kLanes>(first(s2) + second(s2));
         const float inv = is_v ? 1.f : rsqrtf(fmaf(ss, 1.0f / D, a.eps));
-        unpack8(w8, w);
+        const uint64_t inv2 = pack2(inv, inv);
+        unpack8(w_lo, w);
+        unpack8(w_hi, w + 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= inv * w[i];
+        for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], mul2(inv2, w[i]));
       }
-      if (rotated && !all_v) {
-        const float4* at = reinterpret_cast<const float4*>(&cs[b][4 * l]);
+      if (rotated && !is_v) {
+        const uint64_t minus = pack2(-1.f, -1.f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 r = at[i];   // two pairs' cosine and sine
-          if (!is_v) {
-            const float p = x[2 * i], q = x[2 * i + 1];
-            x[2 * i] = fmaf(p, r.x, -(x[2 * i + 4] * r.y));
-            x[2 * i + 1] = fmaf(q, r.z, -(x[2 * i + 5] * r.w));
-            x[2 * i + 4] = fmaf(x[2 * i + 4], r.x, p * r.y);
-            x[2 * i + 5] = fmaf(x[2 * i + 5], r.z, q * r.w);
+        for (int j = 0; j < 2; ++j) {
+          const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&cs[b][0][8 * l + 4 * j]), s = *reinterpret_cast<const ulonglong2*>(&cs[b][1][8 * l + 4 * j]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t p = x[2 * j + i], q = x[2 * j + i + 4], ci = i ? c.y : c.x, si = i ? s.y : s.x;
+            x[2 * j + i] = fma2(p, ci, mul2(mul2(q, si), minus));
+            x[2 * j + i + 4] = fma2(q, ci, mul2(p, si));
           }
         }
       }
-      if (is_q) {
-        if (live) {
-          uint32_t p[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            p[i] = *reinterpret_cast<const uint32_t*>(&v);
-          }
-          bf16* q = a.Q + ((size_t)t * a.qh + h) * D + 4 * l;
-          *reinterpret_cast<uint2*>(q) = make_uint2(p[0], p[1]);
-          *reinterpret_cast<uint2*>(q + D / 2) = make_uint2(p[2], p[3]);
-        }
+      if (is_q && live) {
+        uint4* q = reinterpret_cast<uint4*>(a.Q + ((size_t)t * a.qh + h) * D + 8 * l);
+        q[0] = round8(x);
+        q[D / 16] = round8(x + 4);
       }
-      // the largest magnitude, on the bit patterns: NaN > infinity > any number
       if (any_kv) {
-        uint32_t mx = 0;
+        float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 8; ++i) amax = max_abs(amax, first(x[i]), second(x[i]));
+        uint32_t mx = __float_as_uint(amax) & 0x7FFFFFFFu;   // as bit patterns, NaN > infinity > any number
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         if (live && !is_q) {
-          const float amax = __uint_as_float(mx);
+          amax = __uint_as_float(mx);
           float inv = 0.f, scale = 0.f;
-          if (mx >= 0x7F800000u) {
-            scale = __uint_as_float(0x7FC00000u);   // a head with infinity or NaN reads back as NaN
-          } else if (amax >= kTinyHead) {
+          const bool finite = mx < 0x7F800000u;
+          if (finite && amax >= kTinyHead) {
             inv = code_max<FMT>() / amax;
             scale = amax / code_max<FMT>();
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = scale == scale ? x[i] * inv : 0.f;
+          uint2 lo = encode8<FMT>(x, inv), hi = encode8<FMT>(x + 4, inv);
+          if (!finite) {   // a head with infinity or NaN reads back as NaN
+            lo = hi = make_uint2(0, 0);
+            scale = __uint_as_float(0x7FC00000u);
+          }
           const size_t row = a.c.row(now.slot, is_v ? h - a.qh - kvh : h - a.qh, now.idx);
-          uint8_t* codes = is_v ? a.c.V : a.c.K;
-          *reinterpret_cast<uint32_t*>(codes + row * D + 4 * l) = encode4<FMT>(x);
-          *reinterpret_cast<uint32_t*>(codes + row * D + D / 2 + 4 * l) = encode4<FMT>(x + 4);
+          uint2* codes = reinterpret_cast<uint2*>((is_v ? a.c.V : a.c.K) + row * D + 8 * l);
+          codes[0] = lo;
+          codes[D / 16] = hi;
           if (l == 0) (is_v ? a.c.Vs : a.c.Ks)[row] = scale;
         }
       }
@@ -216,13 +254,13 @@ __global__ void __launch_bounds__(256) k_kv8_read(Cache c, int slot, int first, 
 template <int D, int FMT>
 cudaError_t launch_append(const AppendArgs& args, int T, cudaStream_t s) {
   AppendArgs a = args;
-  const int heads = a.qh + 2 * a.c.kvh, per = kMaxThreads / (D / 8);
+  const int heads = a.qh + 2 * a.c.kvh, per = kMaxThreads / (D / 16);
   const int ny = (heads + per - 1) / per;
   a.heads_per_cta = (heads + ny - 1) / ny;
-  const int threads = ((max(a.heads_per_cta * (D / 8), D / 2) + 31) / 32) * 32;
+  const int threads = ((max(a.heads_per_cta * (D / 16), D / 2) + 31) / 32) * 32;
   a.T = T;
-  // as many CTAs as an SM's threads hold, on every SM
-  const int ctas = std::max(1, 152 * (1024 / threads) / ny);
+  // as many CTAs as an SM's registers hold, on every SM
+  const int ctas = std::max(1, 152 * (kCtasPerSm * kMaxThreads / threads) / ny);
   k_kv8_append<D, FMT><<<dim3(std::min(T, ctas), ny), threads, 0, s>>>(a);
   return cudaGetLastError();
 }

@@ -32,7 +32,7 @@
 // 32 streams of 8 heads a group over 32768 positions of 4 kv heads of 128: 44
 // us with the merge, 387 TFLOP/s.  The softmax bounds it: a tile of 128 x 128
 // weights is about 11 thousand warp instructions, 3150 cycles of an SM's issue,
-// while the tensor pipe is busy for a tenth of the time.  A CTA's start (query
+// while the tensor pipe is busy for a fifth of the time.  A CTA's start (query
 // rows and the first tile's codes) and end (records) add 10 thousand cycles, an
 // SM's two CTAs of this case one after the other.  Taking both through one CTA
 // took 48 us: query rows and records then wait for each other.
@@ -80,25 +80,6 @@ __device__ __forceinline__ uint32_t piece(int rows, int r, int c) { return (c >>
 __device__ __forceinline__ uint64_t operand(uint32_t base, int rows, int k16) {
   const uint32_t at = base + (k16 >> 2) * rows * 128 + (k16 & 3) * 32;
   return (uint64_t)((at >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-__device__ __forceinline__ uint64_t pack2(float a, float b) { return (uint64_t)__float_as_uint(a) | (uint64_t)__float_as_uint(b) << 32; }
-__device__ __forceinline__ float first(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float second(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
 }
 
 template <int D, int FMT>
