@@ -24,17 +24,20 @@
 // cut is found in two steps: a histogram over 1/32-wide steps of log2(w), of
 // counts for top-k and of weights for top-p, names the step that holds it;
 // the logits of that step, a few hundred as a rule, are gathered by every
-// CTA and searched there.  (A step that holds more than 2048, as in a row of
-// equal logits, is searched where it lies, by histograms over ten bits of the
-// logits' ordered bit patterns at a time.)  The CTAs add up histograms
-// through distributed shared memory: each sums a share of the bins and writes
-// it to all.
+// CTA and searched there, by a histogram of their ordered bit patterns and,
+// among what is left in a bin of that, one against the other.  (A step that
+// holds more than 2048, as in a row of equal logits, is searched where it
+// lies, by histograms over ten bits of the patterns at a time.)  Top-k mostly
+// needs no histogram of the row: the threads' largest logits bound the cut.
+// The CTAs add up histograms through distributed shared memory: each sums a
+// share of the bins and writes it to all.
 //
-// What bounds it is instructions (about 31 for a weight, a weight a logit and
-// filter) and the cluster's barriers, 1300 cycles each.  Rows of 151936 fp32
-// logits, all filters: 23 us for one, where 16 CTAs share the row, 45 us for
-// 32, where 8 do; reading those takes 3 us.  Histograms in 64-bit shared
-// atomics, which are loops of compare and swap, took 59 us.
+// What bounds it is instructions (about 31 for a weight, two shared atomics for
+// one in a histogram) and the barriers: 1300 cycles across a cluster.  Rows of
+// 151936 fp32 logits, us for 1 / 32 / 128 rows: no filter 8.6 / 18 / 69, top-k
+// 14 / 22 / 77, top-p 23 / 41 / 151; reading 32 of them takes 3.  A histogram
+// of the whole row for top-k took 15 / 25 / 89.  64-bit shared atomics, which
+// are loops of compare and swap, took 59 for 32 mixed rows (now 42).
 #include <cooperative_groups.h>
 #include <float.h>
 #include <stddef.h>
@@ -116,7 +119,7 @@ struct Smem {
   uint2 exp2[128];                    // kExp2 and its fp32 value
   // by rank; each is told once, so no CTA overwrites what another still reads
   float top[kMaxCluster];             // largest logit
-  uint32_t listed[2][kMaxCluster];    // logits of the step that holds the cut: top-k's, top-p's
+  uint32_t listed[3][kMaxCluster];    // logits gathered for a cut: top-k's twice, top-p's
   u64 kept[kMaxCluster];              // weight above the cut
   uint32_t equal[kMaxCluster];        // logits equal to the cut
   u64 warp64[kWarps];
@@ -126,8 +129,9 @@ struct Smem {
   uint32_t tile32[kMaxTiles];
   u64 mine[kBins], all[kBins];        // a histogram, the CTA's and the row's; counts in 32-bit words.  mine: also the CTA's list
   float list[kList];                  // the row's list
+  uint32_t few[32];                   // keys that a search has left
   int at;
-  uint32_t count;
+  uint32_t count, few_count;
   u64 before;
   float x[1];                         // [kWarps][tiles][kTile]
 };
@@ -375,21 +379,24 @@ struct Row {
   }
   // The key at which the weight (MASS) or the number of the logits of step
   // f.bin that are at least `least` reaches `need`, from the largest down,
-  // counted on from f.before; *before is what the keys above it hold.
-  template <bool MASS>
+  // counted on from f.before; *before is what the keys above it hold.  FROM_TOP:
+  // of all steps down to f.bin; 0 if those are more than a list holds.
+  template <bool MASS, bool FROM_TOP>
   __device__ uint32_t find(Found f, uint32_t least, u64 need, uint32_t* listed, u64* before) const {
     using Word = typename std::conditional<MASS, u64, uint32_t>::type;
     uint32_t lo, hi;
     key_range(f.bin, lo, hi);
+    if (FROM_TOP) hi = key_of(w.m);
     lo = max(lo, least);
     hi = max(hi, lo);
     const float vlo = value_of(lo), vhi = value_of(hi);
+    auto in = [&](float x) { return FROM_TOP ? w.bin(x) <= f.bin : w.bin(x) == f.bin; };
     // every CTA's logits of the step to every CTA
     float* own = reinterpret_cast<float*>(s.mine);
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
     sweep_range(vlo, vhi, [&](float x) {
-      if (w.bin(x) != f.bin) return;
+      if (!in(x)) return;
       const uint32_t i = atomicAdd(&s.count, 1u);
       if (i < kList) own[i] = x;
     });
@@ -398,6 +405,7 @@ struct Row {
     sync();
     const uint32_t count = total(listed);
     const bool gathered = count <= kList;
+    if (FROM_TOP && !gathered) return 0;
     if (gathered) {
       const int i = threadIdx.x >> 5;   // warp i takes the list of CTA i
       if (i < n) {
@@ -414,6 +422,7 @@ struct Row {
       const int shift = max(0, 32 - __clz(hi - lo) - 10);
       for (int i = threadIdx.x; i < kBins; i += kThreads) mine[i] = 0;
       __syncthreads();
+      if (threadIdx.x == 0) s.few_count = 0;
       auto put = [&](float x) {
         const uint32_t k = key_of(x);
         if (k >= lo && k <= hi) {
@@ -426,7 +435,7 @@ struct Row {
         __syncthreads();
       } else {
         sweep_range(vlo, vhi, [&](float x) {
-          if (w.bin(x) == f.bin) put(x);
+          if (in(x)) put(x);
         });
         add_up(mine, all);
       }
@@ -436,6 +445,37 @@ struct Row {
       const uint32_t span = (1u << shift) - 1;
       lo = hi - lo > span ? hi - span : lo;
       if (lo == hi) break;
+      if (gathered) {                 // up to 32 keys: every warp ranks them
+        for (uint32_t i = threadIdx.x; i < count; i += kThreads) {
+          const uint32_t k = key_of(s.list[i]);
+          if (k >= lo && k <= hi) {
+            const uint32_t at = atomicAdd(&s.few_count, 1u);
+            if (at < 32) s.few[at] = k;
+          }
+        }
+        __syncthreads();
+        const int few = (int)s.few_count, lane = threadIdx.x & 31;
+        if (few <= 32) {
+          const uint32_t k = lane < few ? s.few[lane] : 0u;
+          const u64 v = lane >= few ? 0 : MASS ? w(value_of(k), s.exp2) : 1;
+          u64 above = base, upto = base, sum = base;
+          for (int j = 0; j < few; ++j) {
+            const uint32_t kj = __shfl_sync(0xffffffffu, k, j);
+            const u64 vj = __shfl_sync(0xffffffffu, v, j);
+            sum += vj;
+            above += kj > k ? vj : 0;
+            upto += kj >= k ? vj : 0;
+          }
+          need = min(need, sum);
+          unsigned hit = __ballot_sync(0xffffffffu, above < need && need <= upto && lane < few);
+          if (!hit) hit = __ballot_sync(0xffffffffu, above == base && lane < few);   // weights that round to nothing
+          if (hit) {
+            lo = __shfl_sync(0xffffffffu, k, __ffs(hit) - 1);
+            base = __shfl_sync(0xffffffffu, above, __ffs(hit) - 1);
+          }
+          break;
+        }
+      }
     }
     *before = base;
     return lo;
@@ -487,6 +527,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
     }
     r.tile[32 * t + lane] = make_float4(v[0], v[1], v[2], v[3]);
   }
+  float thread_best = best;
   best = warp_max(best);
   if (lane == 0) s.warpf[warp] = best;
   if (tid < 128) s.exp2[tid] = make_uint2(kExp2[tid], __float_as_uint((float)kExp2[tid]));
@@ -518,6 +559,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
       v.w = v.w == INFINITY ? 0.f : -INFINITY;
     }
     best = 0.f;
+    thread_best = thread_best == INFINITY ? 0.f : -INFINITY;
   }
   r.w.m = best;
   const Weights& w = r.w;
@@ -531,20 +573,34 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
     if (k > 0 && k < V) {
       uint32_t* mine = reinterpret_cast<uint32_t*>(s.mine);
       uint32_t* all = reinterpret_cast<uint32_t*>(s.all);
-      for (int i = tid; i < kBins; i += kThreads) mine[i] = 0;
-      __syncthreads();
-      r.sweep([&](float x) {
-        if (x > -INFINITY) atomicAdd(&mine[w.bin(x)], 1u);
-      });
-      r.add_up(mine, all);
-      u64 have = 0;
-      const Found f = r.reach(all, 0, [&](u64 sum) {
-        have = sum;
-        return (u64)k;
-      });
-      if (have > (u64)k) {            // else there are no more than k
-        u64 before;
-        cut = r.template find<false>(f, 1, (u64)k, s.listed[0], &before);
+      u64 have = 0, before = 0;
+      auto count = [&](bool maxima) {
+        for (int i = tid; i < kBins; i += kThreads) mine[i] = 0;
+        __syncthreads();
+        if (maxima) {
+          if (thread_best > -INFINITY) atomicAdd(&mine[w.bin(thread_best)], 1u);
+        } else {
+          r.sweep([&](float x) {
+            if (x > -INFINITY) atomicAdd(&mine[w.bin(x)], 1u);
+          });
+        }
+        r.add_up(mine, all);
+        return r.reach(all, 0, [&](u64 sum) {
+          have = sum;
+          return (u64)k;
+        });
+      };
+      // The k-th of the threads' largest logits is no larger than the k-th of all, and while k is a fraction of the
+      // threads not many are between the two: those down to its step are listed without a histogram of the row.
+      if (k <= n * (kThreads / 4)) {
+        const Found f = count(true);
+        if (have >= (u64)k) cut = r.template find<false, true>(Found{f.bin, 0}, 1, (u64)k, s.listed[0], &before);
+      }
+      if (!cut) {
+        const Found f = count(false);
+        if (have > (u64)k) cut = r.template find<false, false>(f, 1, (u64)k, s.listed[1], &before);   // else there are no more than k
+      }
+      if (cut) {
         ties = (uint32_t)(k - before);
         if (p < 1.f) r.sync();        // every CTA has read the lists
       }
@@ -569,7 +625,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
       const Found f = r.reach(s.all, 0, [&](u64 sum) { return need = max(1ull, __umul64hi(sum, p64) + (sum * p64 != 0)); });
       const uint32_t k_cut = cut, k_ties = ties;
       u64 before;
-      cut = r.template find<true>(f, max(1u, k_cut), need, s.listed[1], &before);
+      cut = r.template find<true, false>(f, max(1u, k_cut), need, s.listed[2], &before);
       const u64 wc = w(value_of(cut), s.exp2);
       const u64 rest = need - min(need, before), want = rest <= wc ? 1 : wc ? (rest + wc - 1) / wc : 1;
       ties = (uint32_t)min(want, (u64)V);

@@ -265,3 +265,17 @@ def test_rows_do_not_depend_on_the_batch(bm, V):
         ids, lp = _call(bm, x[torch.as_tensor(row).cuda()], **{k: np.asarray(v)[row] for k, v in s.items()})
         np.testing.assert_array_equal(ids, want[row])
         np.testing.assert_array_equal(lp, wlp[row])
+
+
+@pytest.mark.parametrize("V", [1000, 20000, 151936])
+def test_top_k_of_every_size(bm, V):
+    """k below, at and above what the threads' largest logits can bound, in rows whose largest lie together or apart."""
+    ks = [1, 2, 31, 32, 33, 127, 128, 129, 500, 1024, 1025, 2048, 2049, 5000, V - 1, V]
+    n = len(ks)
+    x = _logits(n, V, 41)
+    x[1::4] = x[1::4].sort(dim=1, descending=True).values       # the largest in one thread's and one warp's runs
+    x[2::4] = (x[2::4] * 4).round() / 4                         # runs of equal logits at every cut
+    x[3::4, 7:] = torch.where(torch.arange(7, V, device="cuda") % 5 == 0, x[3::4, 7:], -float("inf"))
+    u = (np.arange(n) + 0.5) / n
+    _check(bm, x, np.full(n, 1.1), ks, np.ones(n), np.zeros(n), u, least=0.8)
+    _check(bm, x, np.full(n, 0.8), ks, np.full(n, 0.9), np.zeros(n), 1 - u, least=0.8)
