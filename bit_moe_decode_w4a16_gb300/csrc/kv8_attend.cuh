@@ -1,6 +1,8 @@
 // What the kernels of attention over the 8-bit cache share.
 #pragma once
 
+#include <algorithm>
+
 #include "kv8.cuh"
 
 namespace bm {
@@ -73,7 +75,7 @@ __device__ __forceinline__ void row_scale(float amax, float& down, float& up) {
 // for one tile of query rows.
 inline int prefix_chunk(int len, int kvh) {
   const int most = kSms / kvh > 1 ? kSms / kvh : 1, tiles = len > 0 ? (len - 1) / 128 + 1 : 1;
-  return (tiles + most - 1) / most * 128;
+  return std::min((tiles + most - 1) / most, 1 << 23) * 128;   // below 2^31
 }
 inline int prefix_chunks(int len, int kvh) {
   return len > 0 ? (len - 1) / prefix_chunk(len, kvh) + 1 : 0;

@@ -164,6 +164,10 @@ def test_temperatures_at_the_ends(bm):
         for p in (1.0, 0.5):
             ids = _check(bm, x, np.full(4, T), np.zeros(4, int), np.full(4, p), np.zeros(4), np.full(4, 0.3), least=0.0)
             assert ids[1] < 5 and (p == 1.0) <= (abs(ids[0] - 0.3 * V) <= 1) and abs(ids[3] - 0.3 * p * V) <= 1
+    ids, lp = _call(bm, x, temp=np.full(4, float("inf")), top_k=np.array([10, 3, 100, V]), u=np.full(4, 0.5))
+    top = x[0].topk(10).indices.sort().values.cpu().numpy()
+    assert ids[0] == top[5] and ids[1] in x[1].topk(3).indices and ids[3] == V // 2
+    np.testing.assert_allclose(lp, -np.log([10, 3, 100, V]), rtol=2 ** -23)
     for T in (1e-45, 1e-38, 1e-20):
         ids, lp = _call(bm, x[:2], temp=np.full(2, T), top_p=np.full(2, 0.9), u=np.full(2, 0.999))
         assert (ids == x[:2].argmax(1).cpu().numpy()).all() and (lp == 0).all()

@@ -94,6 +94,8 @@ def test_workspace_sizes():
     one = bm.kv8_workspace_bytes(1, 8, 2, 64, 256)
     assert one > 0 and bm.kv8_workspace_bytes(3, 8, 2, 64, 256) >= 3 * one > 0
     assert bm.kv8_workspace_bytes(1, 8, 2, 64, 256, 5000) > one
+    # a prefix of the largest length, for many kv heads: chunks of 2^30 positions at most
+    assert bm.kv8_workspace_bytes(1, 1000, 500, 64, 256, 2 ** 31 - 1) == 1000 * (1 + 2) * (64 + 2) * 4
     # a stream has a bounded number of chunks, however long
     assert bm.kv8_workspace_bytes(1, 8, 2, 64, 131072) == bm.kv8_workspace_bytes(1, 8, 2, 64, 2 ** 31 - 1)
 
