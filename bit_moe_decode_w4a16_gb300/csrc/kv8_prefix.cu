@@ -61,16 +61,12 @@ struct PrefixSmem {
   uint8_t v[2][kTokens * D * 2];                   // [position / 64][element][64]
   // scales and log2 of V's, of four tiles: they are written with a tile's K, when the softmax may be two tiles back
   float ks[4][kTokens], vs[4][kTokens], lg[4][kTokens];
-  float m[kRows], l[kRows], up[kRows];
+  float up[kRows];
   // by the tile's parity; their phase is the tile's half
   uint64_t k_full[2], v_full[2], s_ready[2], p_ready[2], o_ready[2], drained;
   uint32_t tmem;
   int gave_up;
 };
-constexpr int kOutStride = 129;                    // floats of a row of O on its way out, over q, k and v
-static_assert(kRows * kOutStride * 4 <= 3 * kRows * 128 * 2, "O fits over the operands (d = 128)");
-static_assert(kRows * (64 + 1) * 4 <= 3 * kRows * 64 * 2, "O fits over the operands (d = 64)");
-
 // 16-byte piece c of row r of a K-major operand of `rows` rows: 128-byte rows of 64 fp16, pieces swizzled by the row.
 __device__ __forceinline__ uint32_t piece(int rows, int r, int c) { return (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
 
@@ -83,14 +79,16 @@ __device__ __forceinline__ uint64_t operand(uint32_t base, int rows, int k16) {
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a, int per_cta) {
   extern __shared__ unsigned char raw[];
   const uint32_t raw_at = tc::smem_u32(raw);
   PrefixSmem<D>& sm = *reinterpret_cast<PrefixSmem<D>*>(raw + ((1024u - (raw_at & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int chunk = blockIdx.x, row0 = blockIdx.y * kRows, kh = blockIdx.z;
+  const int chunk0 = blockIdx.x * per_cta, row0 = blockIdx.y * kRows, kh = blockIdx.z;
   const int kvh = a.c.kvh, G = a.qh / kvh, rows = a.B * G;
-  const int j0 = chunk * a.p_chunk, n = min(a.p_chunk, a.p_len - j0), tiles = (n + kTokens - 1) / kTokens;
+  // the CTA's chunks lie one behind the other, each of `per_chunk` tiles but for the prefix's last
+  const int j0 = chunk0 * a.p_chunk, n = (int)min((long long)per_cta * a.p_chunk, (long long)(a.p_len - j0));
+  const int tiles = (n + kTokens - 1) / kTokens, per_chunk = a.p_chunk / kTokens;
   const float inv_g = 1.f / G;
   auto stream_of = [&](int r) { return (int)((r + 0.5f) * inv_g); };   // r / G, exact below 2^20
   const size_t at = a.p.row(a.p_slot, kh, j0);
@@ -152,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
     if (lane == 0) {
       const uint32_t qk = tc::idesc_f16_f32(kRows, kTokens), pv = tc::idesc_f16_f32(kRows, D);
       const uint32_t q_at = tc::smem_u32(sm.q);
+      int in_chunk = 0;                            // tiles of the chunk before the next output's
       // tile i's scores, once its K is there
       auto issue_scores = [&](int i) {
         if (!wait(sm.k_full, i)) return false;
@@ -171,7 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
         const uint32_t v_at = tc::smem_u32(sm.v[i & 1]);
 #pragma unroll
         for (int k = 0; k < kTokens / 16; ++k)
-          tc::mma_f16_tmem_a(o_cols, p_cols + (i & 1) * (kTokens / 2) + 8 * k, operand(v_at, D, k), pv, i > 0 || k > 0);
+          tc::mma_f16_tmem_a(o_cols, p_cols + (i & 1) * (kTokens / 2) + 8 * k, operand(v_at, D, k), pv, in_chunk > 0 || k > 0);
+        if (++in_chunk == per_chunk) in_chunk = 0;
         tc::mma_commit(tc::smem_u32(&sm.o_ready[i & 1]));
         return true;
       };
@@ -277,7 +277,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
       m[r] = -1e30f;
       l[r] = 0.f;
     }
-    for (int i = 0; i < tiles; ++i) {
+    // a chunk's records, once its last tile `i` is in O.  B's row n is element 4 (n % (d / 4)) + n / (d / 4): what a
+    // thread has of the four quarters of the columns are 4 consecutive elements
+    auto store = [&](int i, int chunk) {
+      if (lane == 0) ok = wait(sm.o_ready, i);
+      if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) return;
+      tc::fence_after_sync();
+      float4* to[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        const int q = row0 + row + g + 8 * r, b = stream_of(q);
+        to[r] = nullptr;
+        if (q < rows) {
+          const size_t rec = a.record(b, kh * G + q - b * G, chunk);
+          if (t == 0) a.rec_ml[rec] = make_float2(m[r], l[r]);
+          to[r] = reinterpret_cast<float4*>(a.rec_o + rec * D) + 2 * t;
+        }
+        m[r] = -1e30f;
+        l[r] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < D / 4; j += 8) {
+        uint32_t o[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::tmem_ld_frag8(o_cols + lanes + k * (D / 4) + j, o[k]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (to[r]) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              to[r][j + e] = make_float4(__uint_as_float(o[0][2 * r + e]), __uint_as_float(o[1][2 * r + e]), __uint_as_float(o[2][2 * r + e]), __uint_as_float(o[3][2 * r + e]));
+          }
+      }
+    };
+    int in_chunk = 0, chunk = chunk0;
+    for (int i = 0; i < tiles; ++i, ++in_chunk) {
+      if (in_chunk == per_chunk) {
+        store(i - 1, chunk++);
+        if (!ok) break;
+        in_chunk = 0;
+      }
       // tile i's scores, and tile i - 2's output, which read the weights that these will overwrite
       if (lane == 0) ok = wait(sm.s_ready, i) && (i < 2 || wait(sm.o_ready, i - 2));
       if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
@@ -325,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
           m[r] = mn;
           l[r] *= f[r];
         }
-        if (i > 0) {                               // O holds the tiles before
+        if (in_chunk > 0) {                        // O holds the chunk's tiles before
           if (lane == 0) ok = wait(sm.o_ready, i - 1);
           if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
           tc::fence_after_sync();
@@ -372,55 +414,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a) {
       tc::fence_before_sync();
       tc::mbar_arrive(tc::smem_u32(&sm.p_ready[i & 1]));
     }
-    if (lane == 0 && ok) ok = wait(sm.o_ready, tiles - 1);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    tc::fence_after_sync();
-    if (ok) {
-      // every MMA is done: O goes out over the operands, a row to a lane, half of the elements to a warp
-      float* out = reinterpret_cast<float*>(&sm) + (32 * (warp & 3) + lane) * (D == 128 ? kOutStride : 65);
-#pragma unroll 1
-      for (int c = (warp >> 2) * D / 2; c < ((warp >> 2) + 1) * D / 2; c += 32) {
-        uint32_t o[32];
-        tc::tmem_ld32(o_cols + ((uint32_t)(32 * (warp & 3)) << 16) + c, o);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int col = c + k;                   // B's row: element 4 (col % (d / 4)) + col / (d / 4)
-          out[4 * (col % (D / 4)) + col / (D / 4)] = __uint_as_float(o[k]);
-        }
-      }
-    }
+    if (ok) store(tiles - 1, chunk);
     tc::fence_before_sync();
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (t == 0) {
-        sm.l[row + g + 8 * r] = l[r];
-        sm.m[row + g + 8 * r] = m[r];
-      }
-    }
   }
   if (!ok) sm.gave_up = 1;
   __syncthreads();
   tc::fence_after_sync();
   if (warp == kSoftmax / 32) tc::tmem_dealloc(s_cols, kTmemCols);
-  const bool bad = sm.gave_up != 0;
-  // ---- records, a row to a warp at a time
-  const float* out = reinterpret_cast<const float*>(&sm);
-  constexpr int kOutWarps = (kSoftmax + kConvert) / 32;
-#pragma unroll 4
-  for (int k = 0; k < kRows / kOutWarps; ++k) {
-    const int at_row = warp + k * kOutWarps, r = row0 + at_row, b = stream_of(r), h = kh * G + r - b * G;
-    if (warp >= kOutWarps || r >= rows) continue;
-    const size_t rec = a.record(b, h, chunk);
-#pragma unroll
-    for (int d = lane; d < D; d += 32) a.rec_o[rec * D + d] = out[at_row * (D == 128 ? kOutStride : 65) + d];
-    if (lane == 0) {
-      a.rec_ml[rec] =
-          make_float2(bad ? 0.f : sm.m[at_row], bad ? __uint_as_float(0x7FC00000u) : sm.l[at_row]);
+  if (sm.gave_up && tid < kRows && row0 + tid < rows) {   // NaN in all of this CTA's records
+    const int r = row0 + tid, b = stream_of(r);
+    for (int c = chunk0; c < min(chunk0 + per_cta, a.p_chunks); ++c)
+      a.rec_ml[a.record(b, kh * G + r - b * G, c)] = make_float2(0.f, __uint_as_float(0x7FC00000u));
+  }
+}
+
+// Chunks that a CTA takes one after the other.  A CTA's start and end cost as much as three tiles, so those of a
+// second wave are better another CTA's next chunk; the records are the chunks' all the same.
+int chunks_per_cta(int chunks, int tiles, int others) {
+  int best = 1, waves = 2;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= chunks && waves > 1; ++n) {
+    waves = ((chunks + n - 1) / n * others + kSms - 1) / kSms;
+    const int64_t cost = waves * ((int64_t)n * tiles + 3);
+    if (cost < least) {
+      least = cost;
+      best = n;
     }
   }
+  return best;
 }
 
 template <int D, int FMT>
@@ -430,8 +451,9 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
   const cudaError_t e = once_per_device(
       done, [&] { return cudaFuncSetAttribute(k_kv8_prefix<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
   if (e != cudaSuccess) return e;
-  const int rows = a.B * (a.qh / a.c.kvh);
-  return launch_k(false, k_kv8_prefix<D, FMT>, dim3(a.p_chunks, (rows + kRows - 1) / kRows, a.c.kvh), dim3(kThreads), smem, s, a);
+  const int row_tiles = (a.B * (a.qh / a.c.kvh) + kRows - 1) / kRows;
+  const int per_cta = chunks_per_cta(a.p_chunks, a.p_chunk / kTokens, row_tiles * a.c.kvh);
+  return launch_k(false, k_kv8_prefix<D, FMT>, dim3((a.p_chunks + per_cta - 1) / per_cta, row_tiles, a.c.kvh), dim3(kThreads), smem, s, a, per_cta);
 }
 
 }  // namespace

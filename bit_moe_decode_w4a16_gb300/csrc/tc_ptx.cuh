@@ -107,6 +107,14 @@ __device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, uint32_t (&v)[16]
       : "r"(taddr)
       : "memory");
 }
+// 8 columns of it.
+__device__ __forceinline__ void tmem_ld_frag8(uint32_t taddr, uint32_t (&v)[4]) {
+  __syncwarp();
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(taddr)
+               : "memory");
+}
 // Its counterpart: store 32 columns.
 __device__ __forceinline__ void tmem_st_frag32(uint32_t taddr, const uint32_t (&v)[16]) {
   __syncwarp();
