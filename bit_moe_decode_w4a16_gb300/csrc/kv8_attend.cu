@@ -51,7 +51,7 @@ using namespace kv8;
 // (four CTAs with stages of half the size took longer, two with twice as
 // much shared memory 84 us).  16 streams of 1 to 8192: 17.0 us, where the
 // items' uneven ends and the chain of two launches show.  One stream of 4096:
-// 7.2 us, latency alone.
+// 6.9 us, latency alone.
 constexpr int kWarpsPerItem = 4, kTake = 32, kStage = kWarpsPerItem * kTake, kRing = 2;
 
 template <int D>
@@ -446,9 +446,11 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
 // One head of one stream to a warp: its records in ascending order, a lane
 // d / 32 elements.  The kernel is a chain of latencies, so everything is
 // asked for at once: the maxima and sums (a record to a lane), and the first
-// outputs before their weights are known.  About 2 us behind the chunks,
-// whatever the sizes; it starts with them (programmatic dependent launch).
-constexpr int kMergeWarps = 4, kMergeAhead = 8;
+// outputs before their weights are known (16 of them: a lone stream of 4096
+// took 7.2 us with 8, 32 streams behind a prefix 46.8, now 6.9 and 45.6).  It
+// starts with the chunks (programmatic dependent launch) and ends 2 to 5 us
+// behind them.
+constexpr int kMergeWarps = 4, kMergeAhead = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_merge(AttendArgs a) {

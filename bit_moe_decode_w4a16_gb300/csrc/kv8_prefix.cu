@@ -4,8 +4,9 @@
 // head r % G of its group of stream r / G), 128 at a time: over a prefix of P
 // positions that is a dense product of 128 x P x d, and the prefix's codes
 // are read and converted once per 128 rows instead of once per stream.  A CTA
-// takes 128 rows and one chunk of the prefix and leaves one record (o, m, l)
-// per row; the records are merged with those of the streams' own positions.
+// takes 128 rows and one or more chunks of the prefix, one behind the other,
+// and leaves a record (o, m, l) per row and chunk; the records are merged with
+// those of the streams' own positions.
 //
 // Per tile of 128 positions, on the 5th-generation tensor cores (fp16
 // operands, fp32 sums in tensor memory):
@@ -27,15 +28,16 @@
 //
 // An MMA takes about 100 cycles whether N is 16 or 128, so the tile is as
 // wide as tensor memory allows (two S of 128 columns and O; 64-position tiles
-// at two CTAs an SM measured 55 us where these take 44).
+// at two CTAs an SM measured 55 us where these took 44).
 //
-// 32 streams of 8 heads a group over 32768 positions of 4 kv heads of 128: 44
-// us with the merge, 387 TFLOP/s.  The softmax bounds it: a tile of 128 x 128
-// weights is about 11 thousand warp instructions, 3150 cycles of an SM's issue,
-// while the tensor pipe is busy for a fifth of the time.  A CTA's start (query
-// rows and the first tile's codes) and end (records) add 10 thousand cycles, an
-// SM's two CTAs of this case one after the other.  Taking both through one CTA
-// took 48 us: query rows and records then wait for each other.
+// 32 streams of 8 heads a group over 32768 positions of 4 kv heads of 128: 43
+// us with the merge, 402 TFLOP/s; the kernel alone 34, of which 14 tiles 1.9
+// each.  The softmax bounds it: a tile of 128 x 128 weights is about 10
+// thousand warp instructions, while the tensor pipe is busy for a fifth of the
+// time.  Storing the records takes 3.5 us.  A CTA walks over consecutive chunks
+// rather than leave them to a second wave (128 streams behind 8192: 87 -> 75
+// us); taking a chunk's tiles of query rows through one CTA instead took 48
+// us, as query rows and records then wait for each other.
 //
 // Every wait is bounded.  A wait that gives up leaves NaN in its CTA's
 // records, and so in the output rows.
@@ -428,8 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a, int pe
   }
 }
 
-// Chunks that a CTA takes one after the other.  A CTA's start and end cost as much as three tiles, so those of a
-// second wave are better another CTA's next chunk; the records are the chunks' all the same.
+// Chunks that a CTA takes one after the other.  A CTA's start and end cost about as much as three tiles, so the
+// chunks of a second wave are better some CTA's next ones: 32 streams of 8 heads behind 32768 positions 43.8 -> 42.7 us,
+// 512 behind 4096 315 -> 248 us.  The records are the same either way.
 int chunks_per_cta(int chunks, int tiles, int others) {
   int best = 1, waves = 2;
   int64_t least = INT64_MAX;
