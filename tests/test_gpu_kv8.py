@@ -359,6 +359,22 @@ def test_prefix_rows_do_not_depend_on_the_batch(bm):
         assert torch.equal(solo[0].view(torch.int16), whole[b].view(torch.int16))
 
 
+@pytest.mark.parametrize("fmt, B, P, qh, kvh, d", [(E4M3, 40, 20001, 16, 2, 128), (INT8, 300, 9999, 8, 1, 64), (E4M3, 130, 5000, 32, 4, 128)])
+def test_prefix_of_several_chunks_to_a_cta(bm, fmt, B, P, qh, kvh, d):
+    """More tiles of query rows than fit at once: a CTA takes several chunks of one and of three tiles, the last one short;
+    scores grow along the prefix, so references move in every chunk."""
+    prefix = ref.random_cache(fmt, 1, P, kvh, d, 45)
+    prefix["Ks"] *= torch.linspace(0.2, 3, P, device="cuda")
+    cache = ref.random_cache(fmt, B, 20, kvh, d, 46)
+    slots, lens = torch.arange(B, dtype=torch.int32, device="cuda"), torch.arange(B, dtype=torch.int32, device="cuda") % 21
+    Q = torch.randn(B, qh, d, device="cuda").bfloat16()
+    O = _attend(bm, cache, Q, slots, lens, prefix=prefix, p_len=P)
+    _check_rows(O, *ref.attend(cache, Q, slots, lens, d ** -0.5, prefix=(prefix, 0, P)))
+    for b in (0, B // 2, B - 1):
+        solo = _attend(bm, cache, Q[b:b + 1].clone(), slots[b:b + 1].clone(), lens[b:b + 1].clone(), prefix=prefix, p_len=P)
+        assert torch.equal(solo[0].view(torch.int16), O[b].view(torch.int16))
+
+
 def test_prefix_uneven_values(bm):
     """V scales over 12 binary orders and large scores in the shared part."""
     for fmt in (E4M3, INT8):
