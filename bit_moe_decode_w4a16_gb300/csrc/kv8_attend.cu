@@ -41,9 +41,10 @@ using namespace kv8;
 //     positions and interleaves them by byte.
 // A weight enters as fp16(p * vs).  Its reference is the running maximum of
 // s + log2(vs), not of s: the product stays in fp16's range whatever V's
-// magnitude, and what is rounded away is small against the largest term of
-// the sum.  The reference moves only when it is passed by 2^8 (an fp16 holds
-// that), so the output is seldom rescaled.
+// magnitude (its scales are 0 or lie in 2^-100 .. 2^100: the sum of the weights
+// has the same reference and fp32's range), and what is rounded away is small
+// against the largest term of the sum.  The reference moves only when it is
+// passed by 2^8 (an fp16 holds that), so the output is seldom rescaled.
 //
 // Three CTAs an SM take items in order of size, so the grid ends together.
 // 32 streams of 8192 positions, 32 + 2 x 4 heads of 128, e4m3: 54 us with the
@@ -346,8 +347,8 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         if (__any_sync(0xffffffffu, mx > m + 8.f)) {
           const float mn = mx > m + 8.f ? mx : m, f = exp2_fast(m - mn);
+          l = scaled_down(l, m - mn);
           m = mn;
-          l *= f;
           const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
           for (int j = 0; j < kTiles; ++j) {
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
 #pragma unroll
       for (int w = 0; w < kWarpsPerItem; ++w) {
         f[w] = exp2_fast(sm.m[w][r] - mx);
-        den += sm.l[w][r] * f[w];
+        den += scaled_down(sm.l[w][r], sm.m[w][r] - mx);
       }
       const size_t rec = a.record(done.b, done.kh * G + r, a.p_chunks + done.rec);
 #pragma unroll
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_merge(AttendArgs a) {
   for (int r0 = 0; r0 < n; r0 += 32) {
     if (r0) mine = r0 + lane < n ? ml[r0 + lane] : make_float2(-FLT_MAX, 0.f);
     const float f = exp2f(mine.x - mx);
-    den += mine.y * f;
+    den += mine.y * exp2f(fmaxf(mine.x - mx, -120.f)) * exp2f(fminf(mine.x - mx + 120.f, 0.f));   // scaled_down, not approximated
     for (int k0 = 0; k0 < 32 && r0 + k0 < n; k0 += kMergeAhead) {
       Part next[kMergeAhead];
       const int ahead = r0 + k0 + kMergeAhead;

@@ -54,6 +54,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// v * 2^d for d <= 0, in two factors: 2^d alone becomes zero below -126.  A sum of weights needs it, as positions
+// whose V is zero set the reference 100 below their score, which leaves the sum that much above 1.
+__device__ __forceinline__ float scaled_down(float v, float d) {
+  return v * exp2_fast(fmaxf(d, -120.f)) * exp2_fast(fminf(d + 120.f, 0.f));
+}
 __device__ __forceinline__ float log2_fast(float x) {
   float r;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -366,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefix(AttendArgs a, int pe
         for (int r = 0; r < 2; ++r) {
           const float mn = mx[r] > m[r] + 8.f ? mx[r] : m[r];
           f[r] = exp2_fast(m[r] - mn);
+          l[r] = scaled_down(l[r], m[r] - mn);
           m[r] = mn;
-          l[r] *= f[r];
         }
         if (in_chunk > 0) {                        // O holds the chunk's tiles before
           if (lane == 0) ok = wait(sm.o_ready, i - 1);

@@ -1,0 +1,52 @@
+"""Attention over the 8-bit cache where magnitudes lie far apart: against 64 bits,
+or bit for bit against the same problem in other units."""
+
+import pytest
+import torch
+
+import kv8_ref as ref
+from test_gpu_kv8 import BF16_HALF, E4M3, FORMATS, INT8, _attend, _check_rows, _i32, bm  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _v_zero_but(cache, slot, live, exp):
+    """V of a slot: heads of zeros, but at the positions `live`, whose scale becomes 2^exp."""
+    dead = torch.ones(cache["ctx_cap"], dtype=torch.bool)
+    dead[live] = False
+    dead = dead.to(cache["V"].device)
+    cache["V"][slot, :, dead] = 0
+    cache["Vs"][slot, :, dead] = 0
+    cache["Vs"][slot, :, ~dead] = 2.0 ** exp
+
+
+# positions of a stage of 128 are dealt out 32 to a warp: the live ones come later in the same warp's walk, in another
+# warp, in another chunk (256), before the zeros, and in their midst
+@pytest.mark.parametrize("exp", [-90, 0, 20, 27, 60, 95])
+@pytest.mark.parametrize("fmt,d", [(E4M3, 128), (INT8, 64)])
+@pytest.mark.parametrize("n,live", [(129, [128]), (128, [127]), (301, [300]), (600, [0]), (513, [40, 512]), (2, [1])])
+def test_heads_of_zeros_keep_their_share(bm, fmt, d, n, live, exp):
+    """Positions whose V is zero weigh in the denominator, whatever the magnitude of the others."""
+    cache = ref.random_cache(fmt, 1, n, 2, d, 71)
+    _v_zero_but(cache, 0, live, exp)
+    Q = torch.cat([torch.zeros(1, 8, d, device="cuda"), torch.randn(1, 8, d, device="cuda")]).bfloat16()
+    slots, lens = _i32(0, 0), _i32(n, n)
+    _check_rows(_attend(bm, cache, Q, slots, lens), *ref.attend(cache, Q, slots, lens, d ** -0.5))
+
+
+# 32 kv heads: 4 chunks of 256 positions, two tiles each; 2 kv heads: one tile to a chunk
+@pytest.mark.parametrize("exp", [0, 27, 95])
+@pytest.mark.parametrize("fmt,kvh,d", [(E4M3, 32, 64), (INT8, 2, 128), (E4M3, 32, 128)])
+@pytest.mark.parametrize("live", [[130], [1023], [0], None])
+def test_prefix_heads_of_zeros_keep_their_share(bm, fmt, kvh, d, live, exp):
+    P, qh = 1024, 2 * kvh
+    prefix, cache = ref.random_cache(fmt, 1, P, kvh, d, 72), ref.random_cache(fmt, 3, 9, kvh, d, 73)
+    if live is None:                       # what is not zero lies behind the prefix
+        _v_zero_but(prefix, 0, [], 0)
+        cache["Vs"][:] = 2.0 ** exp
+    else:
+        _v_zero_but(prefix, 0, live, exp)
+    Q = torch.cat([torch.zeros(1, qh, d, device="cuda"), torch.randn(2, qh, d, device="cuda")]).bfloat16()
+    slots, lens = _i32(0, 1, 2), _i32(9, 0 if live else 9, 5)
+    O = _attend(bm, cache, Q, slots, lens, prefix=prefix, p_len=P)
+    _check_rows(O, *ref.attend(cache, Q, slots, lens, d ** -0.5, prefix=(prefix, 0, P)))
