@@ -506,7 +506,9 @@ size_t kv8_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int c
  * length and merged in ascending order, so a row's bytes do not depend on
  * the other rows or on B.
  * Results are those of fp32 weights rounded to 16 bits while V's scales are 0
- * or between 2^-100 and 2^100; beyond that light weights lose accuracy.
+ * or between 2^-100 and 2^100 and scores (with `scale`) below 2^24 in
+ * magnitude; beyond the first, light weights lose accuracy; beyond the second,
+ * where fp32 scores have steps of 1 and more, outputs may be NaN.
  * Q, O: DEVICE bf16 [B][q_heads][head_dim], 16-byte aligned; slots, lens:
  * DEVICE int32 [B]; ws: DEVICE, 16-byte aligned, kv8_workspace_bytes(...)
  * bytes, caller-owned, contents irrelevant before and after; calls that may

@@ -50,3 +50,23 @@ def test_prefix_heads_of_zeros_keep_their_share(bm, fmt, kvh, d, live, exp):
     slots, lens = _i32(0, 1, 2), _i32(9, 0 if live else 9, 5)
     O = _attend(bm, cache, Q, slots, lens, prefix=prefix, p_len=P)
     _check_rows(O, *ref.attend(cache, Q, slots, lens, d ** -0.5, prefix=(prefix, 0, P)))
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("P", [0, 200])
+@pytest.mark.parametrize("n", [1, 5, 300])
+def test_scores_of_the_largest_size(bm, n, P, sign):
+    """Equal scores of +-1.6e7: some average of the values, whatever the steps of fp32 make of the weights."""
+    d = 64
+    cache, prefix = ref.random_cache(E4M3, 1, n, 1, d, 74), ref.random_cache(E4M3, 1, 200, 1, d, 75)
+    for c in (cache, prefix):
+        c["K"][:] = 0x7E if sign > 0 else 0xFE     # +-448
+        c["Ks"][:] = 2.0 ** -8
+    Q = torch.full((1, 4, d), 1.6e7 / (448 * 2.0 ** -8 * d * d ** -0.5), device="cuda").bfloat16()
+    O = _attend(bm, cache, Q, _i32(0), _i32(n), prefix=prefix if P else None, p_len=P)
+    v = torch.cat([ref.decode(c["V"][0, 0, :m], E4M3) * c["Vs"][0, 0, :m, None].double() for c, m in ((cache, n), (prefix, P))])
+    slack = v.abs().amax(0) * 2.0 ** -7
+    assert O.isfinite().all() and (O[0].double() <= v.amax(0) + slack).all() and (O[0].double() >= v.amin(0) - slack).all()
+    if not P:                              # all scores come from the same instructions: equal weights
+        want, size = v.mean(0), v.abs().mean(0)
+        assert ((O[0].double() - want).abs() <= BF16_HALF * want.abs() + size * (2.0 ** -11 + 2.0 ** -18) * (1 + BF16_HALF)).all()
