@@ -66,11 +66,13 @@ __device__ __forceinline__ float log2_fast(float x) {
 }
 
 // A power of two that brings a query row of largest magnitude `amax` into fp16's range; exact, and undone
-// on the scores by its inverse.
+// on the scores by its inverse.  The exponent is held where `down`, `up` and `up` times the score factor are normal
+// numbers: rows of the type's largest binade become 2 .. 4, those below 2^-119 less than 1.
 __device__ __forceinline__ void row_scale(float amax, float& down, float& up) {
   down = up = 1.f;
-  if (amax >= 1e-30f && amax <= 1e30f) {
-    const uint32_t e = __float_as_uint(amax) >> 23;
+  const uint32_t bits = __float_as_uint(amax);
+  if (bits < 0x7F800000u) {             // infinity and NaN stay, and make their scores NaN
+    const uint32_t e = min(max(bits >> 23, 8u), 253u);
     down = __uint_as_float((254u - e) << 23);
     up = __uint_as_float(e << 23);
   }

@@ -70,3 +70,45 @@ def test_scores_of_the_largest_size(bm, n, P, sign):
     if not P:                              # all scores come from the same instructions: equal weights
         want, size = v.mean(0), v.abs().mean(0)
         assert ((O[0].double() - want).abs() <= BF16_HALF * want.abs() + size * (2.0 ** -11 + 2.0 ** -18) * (1 + BF16_HALF)).all()
+
+
+def _in_units(exp, P, seed=76):
+    """(cache, prefix, Q) of one problem with query rows times 2^exp and keys divided by it."""
+    d = 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    cache, prefix = ref.random_cache(E4M3, 2, 300, 2, d, seed), ref.random_cache(E4M3, 1, P or 1, 2, d, seed + 1)
+    for c in (cache, prefix):
+        c["Ks"][:] = 2.0 ** (-7 - exp)
+    Q = torch.randn(2, 8, d, generator=g, device="cuda").bfloat16() * 2.0 ** exp
+    return cache, (prefix if P else None), Q.bfloat16()
+
+
+@pytest.mark.parametrize("P", [0, 200])
+@pytest.mark.parametrize("exp", [-110, -101, -60, 60, 100, 110, 124])
+def test_query_rows_of_any_magnitude(bm, exp, P):
+    """Query rows times 2^exp with keys of 2^-exp: the same bits."""
+    slots, lens = _i32(0, 1), _i32(300, 77)
+    out = []
+    for e in (0, exp):
+        cache, prefix, Q = _in_units(e, P)
+        assert Q.isfinite().all()
+        out.append(_attend(bm, cache, Q, slots, lens, prefix=prefix, p_len=P))
+    assert out[1].isfinite().all() and torch.equal(out[0].view(torch.int16), out[1].view(torch.int16))
+
+
+@pytest.mark.parametrize("P", [0, 200])
+def test_query_rows_at_the_ends_of_the_type(bm, P):
+    """Rows of the type's largest and smallest numbers, keys to match, against 64 bits."""
+    d = 64
+    slots, lens = _i32(0, 1), _i32(300, 77)
+    for value, ks in ((torch.finfo(torch.bfloat16).max, 2.0 ** -138), (2.0 ** -126, 2.0 ** 114), (2.0 ** -131, 2.0 ** 118)):
+        cache, prefix, Q = _in_units(0, P)
+        sign = torch.where(Q > 0, 1.0, -1.0)
+        Q = (sign * value).bfloat16()
+        for c in (cache, prefix):
+            if c is not None:
+                c["Ks"][:] = ks
+        assert Q.isfinite().all() and (Q != 0).all()
+        O = _attend(bm, cache, Q, slots, lens, prefix=prefix, p_len=P)
+        _check_rows(O, *ref.attend(cache, Q, slots, lens, d ** -0.5, prefix=(prefix, 0, P) if P else None))
