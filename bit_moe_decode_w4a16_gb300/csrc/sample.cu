@@ -13,9 +13,10 @@
 // weight exceeds u times the kept weight.
 //
 // A token on a border must fall where 64-bit arithmetic puts it, so a weight
-// is a 64-bit integer (2^44 for the largest), good to 2^-29 of itself: the
-// exponent in two fp32 words, 2^(j/128) from a table, the rest a cubic.  FP64
-// would do the same at a fortieth of the rate.  Integers also add up to the
+// is a 64-bit integer (2^44 for the largest), good to 2^-29 of itself and
+// 2^-45 of the largest (lighter ones are 0): the exponent in two fp32 words,
+// 2^(j/128) from a table, the rest a cubic.  FP64 would do the same at a
+// fortieth of the rate.  Integers also add up to the
 // same sum in any order, so histograms and sums may use atomics.
 //
 // A row belongs to a cluster of up to 16 CTAs that keep it in shared memory:
@@ -196,22 +197,23 @@ struct Weights {
   __device__ __forceinline__ int bin(float x) const { return (int)fminf((m - x) * (kSteps * ch), (float)kLastStep); }
 };
 
-// ln(v / total), 0 < v <= total, to fp32: an fp32 logarithm of the quotient's mantissa, corrected once
-// by its exponential in integers.
-__device__ float log_share(u64 v, u64 total, const uint2* table) {
-  const int zv = __clzll(v), zt = __clzll(total);
-  const u64 a = v << zv, b = total << zt;                  // v / total = a / b * 2^(zt - zv)
-  const u64 small = a < b ? a : b, large = a < b ? b : a;
-  const float y = fminf(log2f((float)small / (float)large), 0.f);
+// ln(w / total) to fp32, of a token whose weight is w = 2^(hi + lo) of the largest: from its exponent and not from
+// its integer, which has few bits left for a light token.  The logarithm of total, at least 2^kOne, is an fp32
+// one of its mantissa, corrected once by its exponential in integers.
+__device__ float log_share(float hi, float lo, u64 total, const uint2* table) {
+  const int z = __clzll(total);
+  const u64 b = total << z;                                // 2^63 / b: in (1/2, 1]
+  const float y = fminf(-log2f((float)b * 1.0842021724855044e-19f), 0.f);
   int down;
   const uint32_t w = exp2_parts(y, 0.f, table, down);
-  const u64 back = __umul64hi(large, (u64)w << (33 - down)) << 1;   // large * 2^y
-  const float off = (float)(long long)(small - back) / (float)small * 1.44269502f;
-  // log2(v / total) = hi + lo
-  const float e = (float)(zt - zv), l = a < b ? y : -y;
-  const float hi = e + l, lo = (l - (hi - e)) + (a < b ? off : -off);
-  const float r = hi * 0.693147182f;
-  return r + fmaf(lo, 0.693147182f, fmaf(hi, 0.693147182f, -r) + hi * -1.90465421e-09f);
+  const u64 back = __umul64hi(b, (u64)w << (33 - down)) << 1;   // b * 2^y
+  const float off = (float)(long long)((1ull << 63) - back) * (1.0842021724855044e-19f * 1.44269502f);
+  // log2(2^kOne / total) = h + l, and the weight's to it
+  const float e = (float)(z - 63 + kOne);
+  const float h = e + y, l = (y - (h - e)) + off;
+  const float s = h + hi, bb = s - h, t = (h - (s - bb)) + (hi - bb) + l + lo;
+  const float r = s * 0.693147182f;
+  return r + fmaf(t, 0.693147182f, fmaf(s, 0.693147182f, -r) + s * -1.90465421e-09f);
 }
 
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
@@ -744,7 +746,12 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
   for (int i = 0; i < 4; ++i) {
     if (cum <= target && target < cum + v[i]) {
       a.ids[b] = (rank * kWarps + own) * tiles * kTile + at * kTile + 4 * lane + i;
-      if (a.logp) a.logp[b] = temp > 0.f ? log_share(v[i], kept, s.exp2) : 0.f;
+      if (a.logp) {
+        const float4 x = tile[32 * at + lane];
+        float lo;
+        const float hi = w.exponent(i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w, lo);
+        a.logp[b] = temp > 0.f ? log_share(hi, lo, kept, s.exp2) : 0.f;
+      }
     }
     cum += v[i];
   }

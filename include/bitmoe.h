@@ -544,12 +544,15 @@ bm_status kv8_attend_prefix(const bm_kv8_cache* c, const bm_kv8_cache* prefix, i
  * as 1); the first is always kept.  The token is the lowest index whose
  * cumulated kept weight exceeds u times the whole kept weight.  Any other T
  * (0, negative, NaN) takes the argmax, lowest index first.
+ * Weights are held to 2^-29 of themselves and 2^-45 (3e-14) of the largest:
+ * lighter ones count as 0 and are drawn by no u, and a filter's border or u's
+ * may fall that much off.
  * NaN and -infinity are masked: never drawn.  Logits of +infinity share the
  * row.  A row with nothing to draw gets the id -1 and the logprob -infinity.
  * logits: DEVICE [B] rows of ld elements, dtype BM_F32 or BM_BF16;
  * temperature, top_p, min_p: DEVICE fp32 [B] or NULL (1, 1, 0); top_k: DEVICE
  * int32 [B] or NULL (all); u: DEVICE fp32 [B] in [0, 1) (below 0 or NaN counts
- * as 0, above as the last kept token); ids: DEVICE int32 [B]; logprobs: DEVICE
+ * as 0, above as the last kept token of any weight); ids: DEVICE int32 [B]; logprobs: DEVICE
  * fp32 [B] or NULL, the log of the token's share of the kept weight (0 for an
  * argmax).  A row's result does not depend on the other rows.
  * Errors: BM_ERR_INVALID_ARG (NULL logits, u or ids; B outside [1, 65535], V
