@@ -330,25 +330,31 @@ struct Row {
     return v;
   }
   // all[] = the CTAs' mine[] added up; mine[] is free again afterwards.  A CTA
-  // sums kBins / n of the bins, n / 2 lanes to a bin, and tells all CTAs.
+  // sums kBins / n of the bins, n / 2 lanes to a bin, and tells all CTAs.  What
+  // is rounded of a bin is its sum over the row, the same for any n.
   template <typename M, typename T>
   __device__ void add_up(M* mine, T* all) const {
     sync();
     if (n == 1) {
-      for (int b = threadIdx.x; b < kBins; b += kThreads) all[b] = whole(mine[b], b);
+      for (int b = threadIdx.x; b < kBins; b += kThreads) all[b] = scaled(mine[b], whole(mine[b]), b);
     } else {
       const int per = n / 2, b = rank * (kBins / n) + threadIdx.x / per, q = threadIdx.x & (per - 1);
       const M v0 = cl.map_shared_rank(mine, q)[b], v1 = cl.map_shared_rank(mine, q + per)[b];
-      T v = whole(v0, b) + whole(v1, b);
+      T v = whole(v0) + whole(v1);
       for (int o = per / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      v = scaled(v0, v, b);
       cl.map_shared_rank(all, q)[b] = v;
       cl.map_shared_rank(all, q + per)[b] = v;
     }
     sync();
   }
-  static __device__ __forceinline__ uint32_t whole(uint32_t v, int) { return v; }
-  static __device__ __forceinline__ u64 whole(u64 v, int) { return v; }
-  static __device__ __forceinline__ u64 whole(Halves v, int bin) { return Weights::from_step(v.sum(), bin); }
+  static __device__ __forceinline__ uint32_t whole(uint32_t v) { return v; }
+  static __device__ __forceinline__ u64 whole(u64 v) { return v; }
+  static __device__ __forceinline__ u64 whole(Halves v) { return v.sum(); }   // of 16 CTAs: below 2^52
+  // a bin's sum in weights, by what its histogram holds
+  template <typename T>
+  static __device__ __forceinline__ T scaled(T, T v, int) { return v; }
+  static __device__ __forceinline__ u64 scaled(Halves, u64 v, int bin) { return Weights::from_step(v, bin); }
   // The bin at which the histogram all[], of sum s, reaches need(s), counted
   // on from `base`; the last one that holds anything, should it not.
   // Between two calls there is a barrier.

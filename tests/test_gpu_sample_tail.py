@@ -43,3 +43,17 @@ def test_weights_below_the_smallest_are_never_drawn(bm):
         assert (ids == at).all()
         want = math.log(w / total)
         assert (np.abs(lp - want) <= 2.0 ** -24 * abs(want) + 2.0 ** -27).all()
+
+
+@pytest.mark.parametrize("V", [20000, 40000, 151936])
+def test_sums_of_tiny_weights_do_not_depend_on_the_batch(bm, V):
+    """Two equal largest logits at top-p 0.5: one of them holds half of the weight, unless anything else has any.  What
+    else there is are weights of 0.4 units (2^-44) far apart, which add up the same however many CTAs share the row."""
+    x = torch.full((1, V), -float("inf"), device="cuda")
+    x[0, :2] = 0.0
+    x[0, torch.arange(4, device="cuda") * (V // 4) + 77] = math.log(0.4) - 44 * math.log(2.0)
+    ids, lp = _call(bm, x, top_p=[0.5], u=[0.9])
+    assert ids[0] == 1 and abs(lp[0] + math.log(2.0)) <= 2.0 ** -24
+    for B in (2, 9, 17, 40, 70, 130, 300):
+        many, mlp = _call(bm, x.expand(B, V).contiguous(), top_p=np.full(B, 0.5), u=np.full(B, 0.9))
+        assert (many == ids[0]).all() and (mlp == lp[0]).all(), B
