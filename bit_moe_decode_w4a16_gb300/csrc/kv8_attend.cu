@@ -527,7 +527,7 @@ bool shapes_ok(int B, int qh, int kvh, int d) {
          (d == 64 || d == 128);
 }
 
-size_t records(int ctx_cap, int prefix_len, int kvh) { return (size_t)prefix_chunks(prefix_len, kvh) + most_chunks(ctx_cap); }
+size_t records(int ctx_cap, int prefix_len, int kvh) { return (size_t)most_prefix_chunks(prefix_len, kvh) + most_chunks(ctx_cap); }
 
 bm_status attend(const char* who, const bm_kv8_cache* c, const bm_kv8_cache* p, int p_slot, int p_len, const uint16_t* Q,
                  const int32_t* slots, const int32_t* lens, int q_heads, float scale, uint16_t* O, int B, void* ws,

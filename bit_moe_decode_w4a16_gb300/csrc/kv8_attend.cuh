@@ -88,6 +88,13 @@ inline int prefix_chunks(int len, int kvh) {
   return len > 0 ? (len - 1) / prefix_chunk(len, kvh) + 1 : 0;
 }
 
+// The most chunks a prefix of up to `len` positions can have: their number falls where a chunk becomes a tile longer,
+// and a workspace for the longest prefix has to do for all.
+inline int most_prefix_chunks(int len, int kvh) {
+  const int most = kSms / kvh > 1 ? kSms / kvh : 1, tiles = len > 0 ? (len - 1) / 128 + 1 : 0;
+  return std::max(std::min(tiles, most), prefix_chunks(len, kvh));   // the second where chunks are as long as they get
+}
+
 // The prefix's records (kv8_prefix.cu).
 cudaError_t launch_kv8_prefix(const AttendArgs& a, int format, int d, cudaStream_t s);
 

@@ -493,7 +493,9 @@ bm_status kv8_append(const bm_kv8_cache* c, const uint16_t* qkv, int64_t ld, int
 bm_status kv8_read(const bm_kv8_cache* c, int slot, int first, int count, uint16_t* K_out, uint16_t* V_out, void* stream);
 
 /* Bytes of DEVICE workspace kv8_attend (prefix_len = 0) and
- * kv8_attend_prefix need; 0 for sizes they reject. */
+ * kv8_attend_prefix need; 0 for sizes they reject.  It does not fall with B,
+ * ctx_cap or prefix_len: a workspace for the largest of each does for all
+ * smaller ones of the same heads. */
 size_t kv8_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int ctx_cap, int prefix_len);
 
 /* Decode attention of B streams over the cache: query head h of row b attends

@@ -112,3 +112,18 @@ def test_query_rows_at_the_ends_of_the_type(bm, P):
         assert Q.isfinite().all() and (Q != 0).all()
         O = _attend(bm, cache, Q, slots, lens, prefix=prefix, p_len=P)
         _check_rows(O, *ref.attend(cache, Q, slots, lens, d ** -0.5, prefix=(prefix, 0, P) if P else None))
+
+
+@pytest.mark.parametrize("kvh,d", [(4, 128), (8, 64)])
+def test_one_workspace_for_every_prefix(bm, kvh, d):
+    """A buffer made for the longest prefix, context and batch serves the shorter ones, which may have more chunks."""
+    qh, longest = 2 * kvh, 8192
+    prefix, cache = ref.random_cache(E4M3, 1, longest, kvh, d, 78), ref.random_cache(E4M3, 4, 60, kvh, d, 79)
+    ws = torch.full((bm.kv8_workspace_bytes(4, qh, kvh, d, 60, longest),), 255, dtype=torch.uint8, device="cuda")
+    Q = torch.randn(4, qh, d, device="cuda").bfloat16()
+    slots, lens = _i32(0, 1, 2, 3), _i32(60, 0, 31, 1)
+    for P in (longest, 2432, 4864, 4865, 2433, 4225, 1, 0):
+        for B in (4, 1):
+            q, s, n = Q[:B].clone(), slots[:B].clone(), lens[:B].clone()
+            O = _attend(bm, cache, q, s, n, prefix=prefix, p_len=P, ws=ws)
+            _check_rows(O, *ref.attend(cache, q, s, n, d ** -0.5, prefix=(prefix, 0, P)))
