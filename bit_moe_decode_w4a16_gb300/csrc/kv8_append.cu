@@ -305,6 +305,8 @@ bm_status kv8_append(const bm_kv8_cache* c, const uint16_t* qkv, int64_t ld, int
     return set_error(BM_ERR_INVALID_ARG, "kv8_append: ld must be a multiple of 8 and at least (q_heads + 2 kv_heads) * head_dim");
   if (((uintptr_t)qkv | (uintptr_t)Q | (uintptr_t)rope->q_norm | (uintptr_t)rope->k_norm) & 15)
     return set_error(BM_ERR_INVALID_ARG, "kv8_append: qkv, Q and the norm weights must be 16-byte aligned");
+  if (((uintptr_t)slots | (uintptr_t)index | (uintptr_t)rope_pos | (uintptr_t)rope->inv_freq) & 3)
+    return set_error(BM_ERR_INVALID_ARG, "kv8_append: slots, index, rope_pos and inv_freq must be 4-byte aligned");
   if (rope->norm && !(rope->eps >= 0.f)) return set_error(BM_ERR_INVALID_ARG, "kv8_append: eps must be >= 0");
   a.qkv = reinterpret_cast<const bf16*>(qkv);
   a.ld = ld;

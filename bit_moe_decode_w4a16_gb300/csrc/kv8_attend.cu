@@ -546,6 +546,7 @@ bm_status attend(const char* who, const bm_kv8_cache* c, const bm_kv8_cache* p, 
   if (!Q || !slots || !lens || !O || !ws) return refuse(BM_ERR_INVALID_ARG, "null pointer");
   if (((uintptr_t)Q | (uintptr_t)O | (uintptr_t)ws) & 15)
     return refuse(BM_ERR_INVALID_ARG, "Q, O and the workspace must be 16-byte aligned");
+  if (((uintptr_t)slots | (uintptr_t)lens) & 3) return refuse(BM_ERR_INVALID_ARG, "slots and lens must be 4-byte aligned");
   if (!shapes_ok(B, q_heads, c->kv_heads, c->head_dim))
     return refuse(BM_ERR_INVALID_ARG, "need 1 <= B <= 1024, q_heads <= 1024 and a multiple of kv_heads, at most 8 query heads per kv head");
   if (!(scale > 0.f) || !(scale < INFINITY)) return refuse(BM_ERR_INVALID_ARG, "scale must be positive and finite");

@@ -808,6 +808,8 @@ extern "C" bm_status bm_sample(const void* logits, int dtype, int64_t ld, int V,
     return set_error(BM_ERR_INVALID_ARG, "bm_sample: need 1 <= B <= 65535 and 1 <= V <= " + std::to_string(BM_SAMPLE_MAX_VOCAB));
   if (ld < V) return set_error(BM_ERR_INVALID_ARG, "bm_sample: ld must be at least V");
   if ((uintptr_t)logits & (dtype == BM_F32 ? 3 : 1)) return set_error(BM_ERR_INVALID_ARG, "bm_sample: misaligned logits");
+  if (((uintptr_t)temperature | (uintptr_t)top_k | (uintptr_t)top_p | (uintptr_t)min_p | (uintptr_t)u | (uintptr_t)ids | (uintptr_t)logprobs) & 3)
+    return set_error(BM_ERR_INVALID_ARG, "bm_sample: temperature, top_k, top_p, min_p, u, ids and logprobs must be 4-byte aligned");
   cudaError_t e = ensure_attributes();
   if (e == cudaSuccess) {
     const int n = cluster_size(B, V);

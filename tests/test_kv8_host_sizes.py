@@ -1,5 +1,7 @@
 """Sizes, addresses and shapes that the 8-bit cache calls and the sampler accept or refuse, without a device."""
 
+import ctypes
+
 import pytest
 
 import bit_moe_decode_w4a16_gb300 as bm
@@ -20,3 +22,28 @@ def test_a_workspace_does_for_everything_smaller(kvh):
         assert all(a <= b for a, b in zip(sizes, sizes[1:])), name
     sizes = [size(B=b, P=5000) for b in range(1, 512 // kvh + 2)]
     assert all(a < b for a, b in zip(sizes, sizes[1:]))
+
+
+P = 1 << 20   # an aligned address that no refused call may touch
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_misaligned_vectors_are_refused(off):
+    """int32 and fp32 vectors off a 4-byte boundary: refused on the host, as the GPU would fault on them."""
+    L, bad = bm.lib(), P + off
+    c = bm.bm_kv8_cache(0, 4, 100, 2, 64, P, P, P, P)
+    a = ctypes.addressof(c)
+    for i in range(4):
+        v = [bad if i == j else P for j in range(4)]           # slots, index, rope_pos, inv_freq
+        r = bm.bm_kv8_rope(0, 0.0, None, None, v[3])
+        assert L.kv8_append(a, P, 6 * 64, 2, ctypes.addressof(r), v[0], v[1], v[2], P, 3, None) == 1, i
+        assert bm.last_error().startswith("kv8_append: ")
+    for slots, lens in ((bad, P), (P, bad)):
+        assert L.kv8_attend(a, P, slots, lens, 4, 0.125, P, 3, P, 1 << 30, None) == 1
+        assert bm.last_error().startswith("kv8_attend: ")
+        assert L.kv8_attend_prefix(a, a, 0, 5, P, slots, lens, 4, 0.125, P, 3, P, 1 << 30, None) == 1
+        assert bm.last_error().startswith("kv8_attend_prefix: ")
+    for i in range(7):
+        v = [bad if i == j else P for j in range(7)]           # temperature, top_k, top_p, min_p, u, ids, logprobs
+        assert L.bm_sample(P, 0, 100, 100, 2, *v, None) == 1, i
+        assert bm.last_error().startswith("bm_sample: ")
