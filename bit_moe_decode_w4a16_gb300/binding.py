@@ -455,8 +455,17 @@ def kv8_rope(norm=False, q_norm=None, k_norm=None, eps=1e-6, inv_freq=None):
 
 
 def _on_device(c, what, dev):
-    if c.device != dev:
+    if getattr(c, "device", None) != dev:
+        if not hasattr(c, "device"):
+            raise BitMoeError(1, f"{what}: {type(c).__name__}, expected one that kv8_cache() or kv8_rope() made")
         raise BitMoeError(1, f"{what}: its tensors are on cuda:{c.device}, expected the current CUDA device")
+
+
+def _shape(x, call, name, dims):
+    """Shape of a tensor of that many dimensions."""
+    if x is None or x.dim() != dims:
+        raise BitMoeError(1, f"{call}: {name}: " + ("null tensor" if x is None else f"{x.dim()} dimensions, expected {dims}"))
+    return x.shape
 
 
 def kv8_append(cache, qkv, rope, slots, index, Q, rope_pos=None, stream=None):
@@ -464,14 +473,15 @@ def kv8_append(cache, qkv, rope, slots, index, Q, rope_pos=None, stream=None):
     t, dev = _t(), _here()
     _on_device(cache, "kv8_append: cache", dev)
     _on_device(rope, "kv8_append: rope", dev)
-    T, qh, d = Q.shape
-    if qkv.dim() != 2 or qkv.shape[0] != T or qkv.shape[1] < (qh + 2 * cache.kv_heads) * d or d != cache.head_dim:
+    T, qh, d = _shape(Q, "kv8_append", "Q", 3)
+    rows, width = _shape(qkv, "kv8_append", "qkv", 2)
+    if rows != T or width < (qh + 2 * cache.kv_heads) * d or d != cache.head_dim:
         raise BitMoeError(1, f"kv8_append: qkv {tuple(qkv.shape)} and Q {tuple(Q.shape)} do not fit the cache")
     if qkv.dtype is not t.bfloat16 or qkv.stride(1) != 1 or qkv.get_device() != dev:
         raise BitMoeError(1, "kv8_append: qkv must be bf16 rows of unit stride on the current CUDA device")
     if rope.fits and rope.fits != {d}:
         raise BitMoeError(1, f"kv8_append: q_norm and k_norm need {d} elements, inv_freq {d // 2}")
-    ld = qkv.stride(0) if T > 1 else qkv.shape[1] + (-qkv.shape[1]) % 8
+    ld = qkv.stride(0) if T > 1 else width + -width % 8
     i32, n = t.int32, (T,)
     _check(lib().kv8_append(cache.address, qkv.data_ptr(), ld, qh, rope.address, _tensor(slots, "kv8_append", "slots", i32, n, dev),
                             _tensor(index, "kv8_append", "index", i32, n, dev),
@@ -495,7 +505,7 @@ def kv8_workspace_bytes(B, q_heads, kv_heads, head_dim, ctx_cap, prefix_len=0):
 def _attend_args(what, cache, Q, slots, lens, O, ws, scale, dev):
     t = _t()
     _on_device(cache, what, dev)
-    shape = Q.shape
+    shape = _shape(Q, what, "Q", 3)
     B, qh, d = shape
     if d != cache.head_dim:
         raise BitMoeError(1, f"{what}: Q of head_dim {d}, the cache of {cache.head_dim}")
@@ -523,7 +533,7 @@ def bm_sample(logits, temperature, top_k, top_p, min_p, u, ids, logprobs=None, s
     """logits: fp32 or bf16 [B][V], rows may be strided; temperature, top_p, min_p (fp32) and top_k (int32) [B] or
     None; u: fp32 [B]; ids: int32 [B]; logprobs: fp32 [B] or None."""
     t, dev = _t(), _here()
-    B, V = logits.shape
+    B, V = _shape(logits, "bm_sample", "logits", 2)
     half = logits.dtype is t.bfloat16
     if not (half or logits.dtype is t.float32) or logits.stride(1) != 1 or logits.get_device() != dev:
         raise BitMoeError(1, "bm_sample: logits must be fp32 or bf16 rows of unit stride on the current CUDA device")

@@ -47,3 +47,26 @@ def test_misaligned_vectors_are_refused(off):
         v = [bad if i == j else P for j in range(7)]           # temperature, top_k, top_p, min_p, u, ids, logprobs
         assert L.bm_sample(P, 0, 100, 100, 2, *v, None) == 1, i
         assert bm.last_error().startswith("bm_sample: ")
+
+
+def test_missing_and_wrongly_shaped_arguments():
+    """The binding refuses what has no shape or another number of dimensions, with its own error."""
+    import torch
+    c, r = bm.bm_kv8_cache(0, 4, 100, 2, 64, P, P, P, P), bm.bm_kv8_rope(0, 0.0, None, None, None)
+    raw, c.address, r.address, r.fits = bm.bm_kv8_cache(0, 4, 100, 2, 64, P, P, P, P), P, P, set()
+    c.device = r.device = bm.binding._here()
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i, ws, x = torch.zeros(3, dtype=torch.int32), torch.zeros(10, dtype=torch.uint8), torch.zeros(3)
+    Q = bf(3, 4, 64)
+    bad = [lambda: bm.kv8_append(c, bf(3, 512), r, i, i, bf(3, 256)), lambda: bm.kv8_append(c, bf(3, 512), r, i, i, None),
+           lambda: bm.kv8_append(c, None, r, i, i, Q), lambda: bm.kv8_append(c, bf(3, 8, 64), r, i, i, Q),
+           lambda: bm.kv8_append(None, bf(3, 512), r, i, i, Q), lambda: bm.kv8_append(c, bf(3, 512), None, i, i, Q),
+           lambda: bm.kv8_append(raw, bf(3, 512), r, i, i, Q), lambda: bm.kv8_read(None, 0, 0, 1, Q, Q),
+           lambda: bm.kv8_attend(c, bf(3, 256), i, i, Q, ws), lambda: bm.kv8_attend(c, None, i, i, Q, ws),
+           lambda: bm.kv8_attend(None, Q, i, i, Q, ws), lambda: bm.kv8_attend_prefix(c, None, 0, 5, Q, i, i, Q, ws),
+           lambda: bm.kv8_attend_prefix(c, c, 0, 5, bf(64), i, i, Q, ws), lambda: bm.bm_sample(x, None, None, None, None, x, i),
+           lambda: bm.bm_sample(None, None, None, None, None, x, i), lambda: bm.bm_sample(torch.zeros(1, 3, 4), None, None, None, None, x, i)]
+    for n, call in enumerate(bad):
+        with pytest.raises(bm.BitMoeError) as e:
+            call()
+        assert e.value.args and ("kv8_" in str(e.value) or "bm_sample" in str(e.value)), n
