@@ -508,6 +508,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_merge(AttendArgs a) {
   for (int e = 0; e < E / 2; ++e) *reinterpret_cast<__nv_bfloat162*>(to + 2 * e) = out[e];
 }
 
+// CTAs of the chunk kernel that an SM holds at once: three, but two where the table of a large batch (20 bytes a row;
+// head_dim 128 from 448 rows on) leaves no room for a third.  The items are dealt out evenly to all CTAs of the grid,
+// so none of them may have to wait for another's end: 460 streams of 1000 positions, 32 + 2 x 4 heads of 128, took
+// 186 us with a grid of three CTAs an SM and take 143 with two (440 streams, three CTAs: 120).
+int ctas_per_sm(size_t smem) {
+  constexpr size_t kSmShared = 228 * 1024, kReserved = 1024;   // of an SM; of a CTA besides its own
+  return smem + kReserved <= kSmShared / 3 ? 3 : 2;
+}
+
 template <int D, int FMT>
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
   const size_t most = sizeof(ChunkSmem<D>) + 5 * kMaxBatch * sizeof(int), items = (size_t)a.B * a.c.kvh * a.own_chunks;
@@ -516,8 +525,9 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
       done, [&] { return cudaFuncSetAttribute(k_kv8_chunk<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most); });
   if (e == cudaSuccess && a.p_chunks > 0) e = launch_kv8_prefix(a, FMT, D, s);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)std::min<size_t>(items, kSms * 3);
-  e = launch_k(a.p_chunks > 0, k_kv8_chunk<D, FMT>, dim3(grid), dim3(kWarpsPerItem * 32), sizeof(ChunkSmem<D>) + 5 * a.B * sizeof(int), s, a);
+  const size_t smem = sizeof(ChunkSmem<D>) + 5 * a.B * sizeof(int);
+  const unsigned grid = (unsigned)std::min<size_t>(items, kSms * ctas_per_sm(smem));
+  e = launch_k(a.p_chunks > 0, k_kv8_chunk<D, FMT>, dim3(grid), dim3(kWarpsPerItem * 32), smem, s, a);
   if (e != cudaSuccess) return e;
   return launch_k(true, k_kv8_merge<D>, dim3((a.B * a.qh + kMergeWarps - 1) / kMergeWarps), dim3(kMergeWarps * 32), 0, s, a);
 }

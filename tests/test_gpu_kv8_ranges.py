@@ -127,3 +127,17 @@ def test_one_workspace_for_every_prefix(bm, kvh, d):
             q, s, n = Q[:B].clone(), slots[:B].clone(), lens[:B].clone()
             O = _attend(bm, cache, q, s, n, prefix=prefix, p_len=P, ws=ws)
             _check_rows(O, *ref.attend(cache, q, s, n, d ** -0.5, prefix=(prefix, 0, P)))
+
+
+@pytest.mark.parametrize("B", [447, 448, 1024])
+def test_large_batches_of_wide_heads(bm, B):
+    """Around the batch from which an SM holds two CTAs instead of three: every row, and the bits of rows alone."""
+    qh, kvh, d, cap = 6, 2, 128, 600
+    cache = ref.random_cache(INT8, 40, cap, kvh, d, 80)
+    slots, lens = torch.randint(-1, 41, (B,)).int().cuda(), torch.randint(0, cap + 2, (B,)).int().cuda()
+    Q = torch.randn(B, qh, d, device="cuda").bfloat16()
+    O = _attend(bm, cache, Q, slots, lens)
+    _check_rows(O, *ref.attend(cache, Q, slots, lens, d ** -0.5))
+    for b in (0, B // 2, B - 1):
+        solo = _attend(bm, cache, Q[b:b + 1].clone(), slots[b:b + 1].clone(), lens[b:b + 1].clone())
+        assert torch.equal(solo[0].view(torch.int16), O[b].view(torch.int16))
