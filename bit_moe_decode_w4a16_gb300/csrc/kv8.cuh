@@ -13,6 +13,8 @@
 namespace bm {
 namespace kv8 {
 
+constexpr int kSms = 152;
+
 struct Cache {
   int slots, cap, kvh;
   uint8_t* K;
@@ -89,12 +91,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 
 // Positions per chunk of a stream of `len` positions: 256, doubled each time
 // the length passes four times the last border (4096, 16384, 65536), and
-// beyond that kept so large that there are at most kMaxChunks.  A chunk has
+// beyond that kept so large that there are at most 64 chunks.  A chunk has
 // a fixed cost, a record to merge among it, and a lone stream needs chunks to
 // spread over the GPU: half as many of each as the length grows fourfold.  It
 // depends on the stream's own length only, so a stream's result does not
 // depend on the batch it is attended in.
-constexpr int kMaxChunks = 64;
 __host__ __device__ inline int chunk_of(int len) {
   int c = 256;
   for (long long border = 4096; len > border; border *= border < 65536 ? 4 : 2) c *= 2;

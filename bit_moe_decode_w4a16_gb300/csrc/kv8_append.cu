@@ -47,9 +47,10 @@ struct AppendArgs {
   int heads_per_cta, T;
 };
 
-// f / (2 pi) in 2^-64 turns.  A product with a position wraps around at whole
-// turns, so the angle's fraction of a turn is exact to 2^-47 at position 2^17;
-// an fp32 product would be off by 2^-7 of a radian there.
+// f / (2 pi) in 2^-64 turns, good to 2^-55 for f up to 1 (an fp64 product).  A
+// product with a position wraps around at whole turns, so the angle is good to
+// 2^-38 of a turn at position 2^17, far below the fp32 rounding of the fraction
+// that follows; an fp32 product would be off by 2^-7 of a radian there.
 __device__ __forceinline__ unsigned long long turns64(float f) {
   const double t = (double)f * 0.15915494309189533577;
   return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
@@ -260,7 +261,7 @@ cudaError_t launch_append(const AppendArgs& args, int T, cudaStream_t s) {
   const int threads = ((max(a.heads_per_cta * (D / 16), D / 2) + 31) / 32) * 32;
   a.T = T;
   // as many CTAs as an SM's registers hold, on every SM
-  const int ctas = std::max(1, 152 * (kCtasPerSm * kMaxThreads / threads) / ny);
+  const int ctas = std::max(1, kSms * (kCtasPerSm * kMaxThreads / threads) / ny);
   k_kv8_append<D, FMT><<<dim3(std::min(T, ctas), ny), threads, 0, s>>>(a);
   return cudaGetLastError();
 }

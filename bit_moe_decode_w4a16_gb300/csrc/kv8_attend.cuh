@@ -9,7 +9,6 @@ namespace bm {
 namespace kv8 {
 
 constexpr int kMaxGroup = 8, kMaxBatch = 1024;
-constexpr int kSms = 152;
 
 struct AttendArgs {
   Cache c, p;            // the streams' cache, the prefix's
