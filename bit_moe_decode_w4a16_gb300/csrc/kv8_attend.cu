@@ -46,13 +46,15 @@ using namespace kv8;
 // against the largest term of the sum.  The reference moves only when it is
 // passed by 2^8 (an fp16 holds that), so the output is seldom rescaled.
 //
-// Three CTAs an SM take items in order of size, so the grid ends together.
-// 32 streams of 8192 positions, 32 + 2 x 4 heads of 128, e4m3: 54 us with the
-// merge, 5.1 TB/s of codes and scales; 12 warps an SM keep 65% of HBM busy
+// Three CTAs an SM (two in batches of hundreds of rows, see the launch) take
+// items in order of size, so the grid ends together.
+// 32 streams of 8192 positions, 32 + 2 x 4 heads of 128, e4m3: 53 us with the
+// merge, 5.2 TB/s of codes and scales; 12 warps an SM keep 69% of HBM busy
 // (four CTAs with stages of half the size took longer, two with twice as
-// much shared memory 84 us).  16 streams of 1 to 8192: 17.0 us, where the
+// much shared memory 84 us).  16 streams of 8192: 33 us, 4.2 TB/s, as 2.25
+// rounds of items take 3.  16 streams of 1 to 8192: 21 us, 17 from L2, where the
 // items' uneven ends and the chain of two launches show.  One stream of 4096:
-// 6.9 us, latency alone.
+// 7 us, latency alone.
 constexpr int kWarpsPerItem = 4, kTake = 32, kStage = kWarpsPerItem * kTake, kRing = 2;
 
 template <int D>
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kWarpsPerItem * 32, 3) k_kv8_chunk(AttendArgs 
 // d / 32 elements.  The kernel is a chain of latencies, so everything is
 // asked for at once: the maxima and sums (a record to a lane), and the first
 // outputs before their weights are known (16 of them: a lone stream of 4096
-// took 7.2 us with 8, 32 streams behind a prefix 46.8, now 6.9 and 45.6).  It
+// took 7.2 us with 8 and 6.9 with 16, 32 streams behind a prefix 46.8 and 45.6).  It
 // starts with the chunks (programmatic dependent launch) and ends 2 to 5 us
 // behind them.
 constexpr int kMergeWarps = 4, kMergeAhead = 16;

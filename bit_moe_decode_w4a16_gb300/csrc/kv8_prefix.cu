@@ -32,9 +32,10 @@
 //
 // 32 streams of 8 heads a group over 32768 positions of 4 kv heads of 128: 43
 // us with the merge, 402 TFLOP/s; the kernel alone 34, of which 14 tiles 1.9
-// each.  The softmax bounds it: a tile of 128 x 128 weights is about 10
-// thousand warp instructions, while the tensor pipe is busy for a fifth of the
-// time.  Storing the records takes 3.5 us.  A CTA walks over consecutive chunks
+// each.  The chain of a tile bounds it, scores to weights to product: a tile of
+// 128 x 128 weights is about 9 thousand warp instructions, which keep the issue
+// slots busy for half of the time and the tensor pipe for a fifth, while the
+// softmax warps wait for tensor memory.  Storing the records takes 3.5 us.  A CTA walks over consecutive chunks
 // rather than leave them to a second wave (128 streams behind 8192: 87 -> 75
 // us); taking a chunk's tiles of query rows through one CTA instead took 48
 // us, as query rows and records then wait for each other.

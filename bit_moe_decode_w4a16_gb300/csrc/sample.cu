@@ -33,10 +33,11 @@
 // The CTAs add up histograms through distributed shared memory: each sums a
 // share of the bins and writes it to all.
 //
-// What bounds it is instructions (about 31 for a weight, two shared atomics for
-// one in a histogram) and the barriers: 1300 cycles across a cluster.  Rows of
-// 151936 fp32 logits, us for 1 / 32 / 128 rows: no filter 8.6 / 18 / 69, top-k
-// 14 / 22 / 77, top-p 23 / 41 / 151; reading 32 of them takes 3.  A histogram
+// What bounds it is latency: a chain of sweeps and barriers, 1300 cycles each
+// across a cluster (they lead the stalls; of the issue slots 40% are busy, with
+// about 31 instructions for a weight and two shared atomics for one in a
+// histogram).  Rows of 151936 fp32 logits, us for 1 / 32 / 128 rows: no filter
+// 8.8 / 20 / 69, top-k 14 / 21 / 76, top-p 22 / 42 / 151; reading 32 takes 3.  A histogram
 // of the whole row for top-k took 15 / 25 / 89.  64-bit shared atomics, which
 // are loops of compare and swap, took 59 for 32 mixed rows (now 42).
 #include <cooperative_groups.h>

@@ -470,7 +470,8 @@ bm_status bm_engine_profile_step(bm_engine* e, int B, const int32_t* slots, cons
  * rope_pos[t] * inv_freq[i], reduced in 64 bits), then q rounded to bf16 into
  * Q and k, v quantised at position index[t] of slot slots[t]: amax = largest
  * |y| of the head, scale = amax / M, code = rn(y * (M / amax)), M = 448
- * (e4m3) or 127 (int8), everything in fp32 up to that one rounding.  A head
+ * (e4m3) or 127 (int8), everything in fp32 up to that one rounding (the norm's
+ * squares too: a head with elements above 1e19 becomes zeros).  A head
  * whose amax is below 2^-110 is stored as zeros; one that holds a NaN or an
  * infinity gets the scale NaN, and reads back as NaN.
  * qkv: DEVICE bf16 [T] rows of ld elements (q heads, then k, then v, as in
@@ -522,7 +523,8 @@ bm_status kv8_attend(const bm_kv8_cache* c, const uint16_t* Q, const int32_t* sl
 
 /* kv8_attend for streams that share a prefix: every row attends over
  * positions 0..prefix_len-1 of slot prefix_slot of `prefix` and then over its
- * own.  The prefix is read once for all rows.  `prefix` has c's format,
+ * own.  The prefix is read once per 128 query rows of a kv head (B times query
+ * heads per kv head), not once per stream.  `prefix` has c's format,
  * kv_heads and head_dim, and its own slots and ctx_cap; it may be c itself.
  * A row with no positions of its own attends over the prefix alone.  The
  * prefix's split depends on prefix_len alone, so a row's bytes do not depend
@@ -548,17 +550,18 @@ bm_status kv8_attend_prefix(const bm_kv8_cache* c, const bm_kv8_cache* prefix, i
  * (0, negative, NaN) takes the argmax, lowest index first.
  * Weights are held to 2^-29 of themselves and 2^-45 (3e-14) of the largest:
  * lighter ones count as 0 and are drawn by no u, and a filter's border or u's
- * may fall that much off.
+ * may fall that much off.  A logit that lies farther below the largest than the
+ * largest fp32 number has the weight 0 at any T.
  * NaN and -infinity are masked: never drawn.  Logits of +infinity share the
  * row.  A row with nothing to draw gets the id -1 and the logprob -infinity.
  * logits: DEVICE [B] rows of ld elements, dtype BM_F32 or BM_BF16;
  * temperature, top_p, min_p: DEVICE fp32 [B] or NULL (1, 1, 0); top_k: DEVICE
  * int32 [B] or NULL (all); u: DEVICE fp32 [B] in [0, 1) (below 0 or NaN counts
- * as 0, above as the last kept token of any weight); ids: DEVICE int32 [B]; logprobs: DEVICE
- * fp32 [B] or NULL, the log of the token's share of the kept weight (0 for an
+ * as 0, above as the last kept token of any weight); ids: DEVICE int32 [B];
+ * logprobs: DEVICE fp32 [B] or NULL, the log of the token's share of the kept weight (0 for an
  * argmax).  A row's result does not depend on the other rows.
  * Errors: BM_ERR_INVALID_ARG (NULL logits, u or ids; B outside [1, 65535], V
- * outside [1, BM_SAMPLE_MAX_VOCAB], ld < V, misaligned logits). */
+ * outside [1, BM_SAMPLE_MAX_VOCAB], ld < V, misaligned pointers). */
 bm_status bm_sample(const void* logits, int dtype, int64_t ld, int V, int B, const float* temperature,
                     const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* ids,
                     float* logprobs, void* stream);
