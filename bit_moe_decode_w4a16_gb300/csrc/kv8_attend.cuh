@@ -65,8 +65,8 @@ __device__ __forceinline__ float log2_fast(float x) {
 }
 
 // A power of two that brings a query row of largest magnitude `amax` into fp16's range; exact, and undone
-// on the scores by its inverse.  The exponent is held where `down`, `up` and `up` times the score factor are normal
-// numbers: rows of the type's largest binade become 2 .. 4, those below 2^-119 less than 1.
+// on the scores by its inverse.  The exponent is held where `down`, `up` and `up` times a score factor of 2^-7 to 2
+// are normal numbers: rows of the type's largest binade become 2 .. 4, those below 2^-119 less than 1.
 __device__ __forceinline__ void row_scale(float amax, float& down, float& up) {
   down = up = 1.f;
   const uint32_t bits = __float_as_uint(amax);

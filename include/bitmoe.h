@@ -516,8 +516,9 @@ size_t kv8_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int c
  * DEVICE int32 [B]; ws: DEVICE, 16-byte aligned, kv8_workspace_bytes(...)
  * bytes, caller-owned, contents irrelevant before and after; calls that may
  * overlap on the GPU need workspaces of their own.
- * Errors: BM_ERR_INVALID_ARG (NULL, B outside [1, 1024], more than 8 query
- * heads per kv head, scale not positive and finite, ws too small). */
+ * Errors: BM_ERR_INVALID_ARG (NULL or misaligned pointers, B outside [1, 1024],
+ * more than 8 query heads per kv head, scale not positive and finite, ws too
+ * small). */
 bm_status kv8_attend(const bm_kv8_cache* c, const uint16_t* Q, const int32_t* slots, const int32_t* lens, int q_heads,
                      float scale, uint16_t* O, int B, void* ws, size_t ws_bytes, void* stream);
 
