@@ -21,6 +21,7 @@ STATUS_NAMES = {
     8: "BM_ERR_DEVICE_CHECK", 9: "BM_ERR_UNSUPPORTED",
 }
 KV8_E4M3, KV8_INT8 = 0, 1
+KV8_DRAFTS = 64
 POLICY_AUTO, POLICY_SIMT, POLICY_TC, POLICY_MMA = 0, 1, 2, 3
 
 
@@ -118,6 +119,12 @@ def lib():
             "kv8_workspace_bytes": ([I, I, I, I, I, I], SZ),
             "kv8_attend": ([V, V, V, V, I, ctypes.c_float, V, I, V, SZ, V], S),
             "kv8_attend_prefix": ([V, V, I, I, V, V, V, I, ctypes.c_float, V, I, V, SZ, V], S),
+            "kv8_plan_bytes": ([I, I, I, I], SZ),
+            "kv8_plan": ([V, I, V, V, V, V, V, V, V, V, V, I, I, V, SZ, V], S),
+            "kv8_rows_workspace_bytes": ([I, I, I, I, I, I], SZ),
+            "kv8_attend_rows": ([V, V, SZ, V, I, ctypes.c_float, V, I, I, V, SZ, V], S),
+            "kv8_tree_accept": ([V, SZ, V, V, V, V, V, V, V, I, I, V], S),
+            "kv8_tree_keep": ([V, V, SZ, V, V, I, V], S),
             "bm_sample": ([V, I, ctypes.c_int64, I, I, V, V, V, V, V, V, V, V], S),
             "bm_w4_quantize": ([V, I, I, I, V, V, V], S),
             "bm_engine_moe": ([V, I, V, V, V, V, I, V], S),
@@ -527,6 +534,66 @@ def kv8_attend_prefix(cache, prefix, prefix_slot, prefix_len, Q, slots, lens, O,
     _on_device(prefix, "kv8_attend_prefix: prefix", dev)
     args = _attend_args("kv8_attend_prefix", cache, Q, slots, lens, O, ws, scale, dev)
     _check(lib().kv8_attend_prefix(cache.address, prefix.address, prefix_slot, prefix_len, *args, _stream(stream, dev)))
+
+
+def kv8_plan_bytes(B, T, q_heads, kv_heads):
+    return lib().kv8_plan_bytes(B, T, q_heads, kv_heads)
+
+
+def kv8_plan(cache, q_heads, slots, lens, counts, row_start, after, row_slot, row_index, row_pos, plan, parents=None, stream=None):
+    """slots, lens, counts, after: int32 [B]; row_start: int32 [B + 1]; row_slot, row_index, parents, row_pos (the last two
+    or None): int32 [T]; plan: uint8 tensor of kv8_plan_bytes(...)."""
+    t, dev, w = _t(), _here(), "kv8_plan"
+    _on_device(cache, "kv8_plan: cache", dev)
+    (B,), (T,) = _shape(slots, w, "slots", 1), _shape(row_slot, w, "row_slot", 1)
+    i32, b, r = t.int32, (B,), (T,)
+    _check(lib().kv8_plan(cache.address, q_heads, _tensor(slots, w, "slots", i32, b, dev), _tensor(lens, w, "lens", i32, b, dev),
+                          _tensor(counts, w, "counts", i32, b, dev), _optional(parents, w, "parents", i32, r, dev),
+                          _tensor(row_start, w, "row_start", i32, (B + 1,), dev), _tensor(after, w, "after", i32, b, dev),
+                          _tensor(row_slot, w, "row_slot", i32, r, dev), _tensor(row_index, w, "row_index", i32, r, dev),
+                          _optional(row_pos, w, "row_pos", i32, r, dev), B, T, _tensor(plan, w, "plan", t.uint8, None, dev),
+                          plan.numel(), _stream(stream, dev)))
+
+
+def kv8_rows_workspace_bytes(B, T, q_heads, kv_heads, head_dim, ctx_cap):
+    return lib().kv8_rows_workspace_bytes(B, T, q_heads, kv_heads, head_dim, ctx_cap)
+
+
+def kv8_attend_rows(cache, plan, Q, O, B, ws, scale=None, stream=None):
+    """Q, O: bf16 [T][q_heads][head_dim], plan: of kv8_plan for B streams and T rows; ws: uint8 tensor of
+    kv8_rows_workspace_bytes(...); scale: 1 / sqrt(head_dim) if None."""
+    t, dev, w = _t(), _here(), "kv8_attend_rows"
+    _on_device(cache, "kv8_attend_rows: cache", dev)
+    shape = _shape(Q, w, "Q", 3)
+    T, qh, d = shape
+    if d != cache.head_dim:
+        raise BitMoeError(1, f"{w}: Q of head_dim {d}, the cache of {cache.head_dim}")
+    _check(lib().kv8_attend_rows(cache.address, _tensor(plan, w, "plan", t.uint8, None, dev), plan.numel(),
+                                 _tensor(Q, w, "Q", t.bfloat16, None, dev), qh, d ** -0.5 if scale is None else scale,
+                                 _tensor(O, w, "O", t.bfloat16, shape, dev), B, T, _tensor(ws, w, "ws", t.uint8, None, dev),
+                                 ws.numel(), _stream(stream, dev)))
+
+
+def kv8_tree_accept(plan, tokens, ids, path, kept, fresh, n_fresh, lens, stream=None):
+    """tokens, ids: int32 [T]; path, fresh: int32 [B][KV8_DRAFTS]; kept, n_fresh, lens: int32 [B]."""
+    t, dev, w = _t(), _here(), "kv8_tree_accept"
+    (T,), (B,) = _shape(tokens, w, "tokens", 1), _shape(kept, w, "kept", 1)
+    i32, b, many = t.int32, (B,), (B, KV8_DRAFTS)
+    _check(lib().kv8_tree_accept(_tensor(plan, w, "plan", t.uint8, None, dev), plan.numel(), _tensor(tokens, w, "tokens", i32, None, dev),
+                                 _tensor(ids, w, "ids", i32, (T,), dev), _tensor(path, w, "path", i32, many, dev),
+                                 _tensor(kept, w, "kept", i32, b, dev), _tensor(fresh, w, "fresh", i32, many, dev),
+                                 _tensor(n_fresh, w, "n_fresh", i32, b, dev), _tensor(lens, w, "lens", i32, b, dev), B, T,
+                                 _stream(stream, dev)))
+
+
+def kv8_tree_keep(cache, plan, path, kept, stream=None):
+    """path: int32 [B][KV8_DRAFTS]; kept: int32 [B]."""
+    t, dev, w = _t(), _here(), "kv8_tree_keep"
+    _on_device(cache, "kv8_tree_keep: cache", dev)
+    (B,) = _shape(kept, w, "kept", 1)
+    _check(lib().kv8_tree_keep(cache.address, _tensor(plan, w, "plan", t.uint8, None, dev), plan.numel(),
+                               _tensor(path, w, "path", t.int32, (B, KV8_DRAFTS), dev), _tensor(kept, w, "kept", t.int32, (B,), dev), B,
+                               _stream(stream, dev)))
 
 
 def bm_sample(logits, temperature, top_k, top_p, min_p, u, ids, logprobs=None, stream=None):

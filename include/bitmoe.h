@@ -535,6 +535,108 @@ bm_status kv8_attend_prefix(const bm_kv8_cache* c, const bm_kv8_cache* prefix, i
                             const uint16_t* Q, const int32_t* slots, const int32_t* lens, int q_heads, float scale,
                             uint16_t* O, int B, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- ragged steps of the 8-bit cache
+ * A step in which every stream brings its own number of rows: a prompt or a
+ * part of one, one token, or a tree of drafted tokens.  kv8_plan lays the step
+ * out once, on the device, from the streams' lengths; then, per layer,
+ * kv8_append writes the rows (row_slot, row_index, row_pos are its slots,
+ * index and rope_pos) and kv8_attend_rows attends; a step of drafts ends with
+ * kv8_tree_accept and, per layer, kv8_tree_keep.  Like the calls above they
+ * only enqueue kernels, read everything on the device when the kernels run,
+ * and can be captured. */
+
+#define BM_KV8_DRAFTS 64   /* rows of a tree */
+
+/* Bytes of DEVICE memory of a plan; 0 for sizes that kv8_plan rejects.  It does
+ * not fall with B or T. */
+size_t kv8_plan_bytes(int B, int T, int q_heads, int kv_heads);
+
+/* Lay out a step of B streams: stream b holds lens[b] positions of slot
+ * slots[b] and brings counts[b] rows (0: it sits this step out).  Rows stand
+ * packed in the order of the streams: those of stream b are row_start[b] ..
+ * row_start[b + 1] - 1, the j-th goes to position lens[b] + j (row_slot,
+ * row_index), and its rotary position row_pos is the same or, in a tree,
+ * lens[b] + the row's depth (roots: 0).  after[b] = lens[b] + counts[b].
+ * parents NULL: every stream's rows are consecutive tokens.  Otherwise
+ * parents[t] is the place in its stream of row t's parent, -1 for a root, and
+ * a stream has at most BM_KV8_DRAFTS rows, each behind its parent; -2 at a stream's first row
+ * says that this stream's rows are consecutive tokens, any number of them (their other
+ * entries are not read).
+ * A stream that does not fit (slot outside the cache, a negative length or
+ * count, lens[b] + counts[b] > ctx_cap, rows beyond T, a tree that is none) is
+ * refused by itself: after[b] = -1, its rows and those behind the last
+ * stream's get row_slot -1 (padding for kv8_append), index and pos 0, and the
+ * other calls leave their outputs for it alone where they say so.
+ * `plan` also holds how the attention splits the step, for caches of c's
+ * slots, ctx_cap and kv_heads and these q_heads (of c, K, V and their scales
+ * are not touched).  The calls below take it as it is; while they run it may
+ * not be planned anew.
+ * slots, lens, counts: DEVICE int32 [B]; parents: DEVICE int32 [T] or NULL;
+ * row_start: DEVICE int32 [B + 1]; after: DEVICE int32 [B]; row_slot,
+ * row_index, row_pos: DEVICE int32 [T], row_pos may be NULL; plan: DEVICE,
+ * 16-byte aligned, kv8_plan_bytes(...) bytes, caller-owned.  Outputs must not overlap
+ * inputs.
+ * Errors: BM_ERR_INVALID_ARG (NULL or misaligned pointers, B outside [1, 1024],
+ * T outside [1, 1048576], more than 8 query heads per kv head, plan_bytes too
+ * small). */
+bm_status kv8_plan(const bm_kv8_cache* c, int q_heads, const int32_t* slots, const int32_t* lens, const int32_t* counts,
+                   const int32_t* parents, int32_t* row_start, int32_t* after, int32_t* row_slot, int32_t* row_index,
+                   int32_t* row_pos, int B, int T, void* plan, size_t plan_bytes, void* stream);
+
+/* Bytes of DEVICE workspace kv8_attend_rows needs; 0 for sizes it rejects.  It
+ * does not fall with B, T or ctx_cap. */
+size_t kv8_rows_workspace_bytes(int B, int T, int q_heads, int kv_heads, int head_dim, int ctx_cap);
+
+/* Attention of a planned step's rows over the cache, in which they have been
+ * appended: the j-th of a stream's n rows attends over positions 0 .. len - n
+ * + j of its slot (len = after[b]), or in a tree over positions 0 .. len - n -
+ * 1, its ancestors and itself, with KV head h / (q_heads / kv_heads) and score
+ * factor `scale`; output rounded to bf16 once.  Rows of refused streams and
+ * rows behind the last stream's are left as they were, as is all of O if
+ * `plan` was not made for this B, T, q_heads and a cache of c's sizes.  What
+ * the cache holds at positions that a row does not attend to does not touch
+ * it, whatever it is.  A row's bytes depend on its own stream's rows and
+ * length, not on the rest of the step.  A position whose V holds a NaN code
+ * may make all of an attending row's output NaN.  Ranges of scales and scores as for
+ * kv8_attend.
+ * Q, O: DEVICE bf16 [T][q_heads][head_dim], 16-byte aligned; ws: DEVICE, 16-byte
+ * aligned, kv8_rows_workspace_bytes(...) bytes, caller-owned, contents
+ * irrelevant before and after; calls that may overlap on the GPU need
+ * workspaces of their own (they may share a plan).
+ * Errors: BM_ERR_INVALID_ARG (sizes as kv8_plan, NULL or misaligned pointers,
+ * scale not positive and finite, plan or workspace too small). */
+bm_status kv8_attend_rows(const bm_kv8_cache* c, const void* plan, size_t plan_bytes, const uint16_t* Q, int q_heads,
+                          float scale, uint16_t* O, int B, int T, void* ws, size_t ws_bytes, void* stream);
+
+/* Walk down a planned step's trees: from a stream's first row on, to the first
+ * child whose token is what the model chose behind its parent, until none is.
+ * tokens: DEVICE int32 [T], the rows' own tokens (the first row's, the stream's
+ * last certain one, is not looked at); ids: DEVICE int32 [T], the model's
+ * choices behind the rows (bm_sample's; negative: nothing follows).  Out,
+ * DEVICE int32: path [B][BM_KV8_DRAFTS], the kept rows' places in the stream, then
+ * -1; kept [B], their number, at least 1; fresh [B][BM_KV8_DRAFTS], ids of the
+ * kept rows (the stream's new tokens, the last of them in no cache yet), then
+ * -1; n_fresh [B], their number; lens [B] = the positions held before the step
+ * + kept.  A stream of consecutive rows keeps them all: kept = its rows, path
+ * all -1, and one fresh token, the choice behind its last row.  A stream
+ * without rows: 0, -1 and its length.  A refused stream: 0 and -1, and lens is left as
+ * it was (lens may be the array that kv8_plan read).  If `plan` was not made
+ * for this B and T, nothing is written.
+ * Errors: BM_ERR_INVALID_ARG. */
+bm_status kv8_tree_accept(const void* plan, size_t plan_bytes, const int32_t* tokens, const int32_t* ids, int32_t* path,
+                          int32_t* kept, int32_t* fresh, int32_t* n_fresh, int32_t* lens, int B, int T, void* stream);
+
+/* Close up the kept rows of a planned step's trees in one layer's cache: K, V
+ * and scales of position base + path[b][i] move to base + i, i < kept[b], as if all
+ * were read before any is written (base: the positions held before the step).  Other
+ * positions are left as they are.  A stream of consecutive rows, a refused one, one with kept[b]
+ * < 2, and one whose kept[b] or path names rows that it does not have, are left
+ * alone, as is all of the cache if `plan` was not made for this B and a cache of
+ * c's sizes.  The keys stay rotated for their depth, which along a path is i.
+ * Errors: BM_ERR_INVALID_ARG. */
+bm_status kv8_tree_keep(const bm_kv8_cache* c, const void* plan, size_t plan_bytes, const int32_t* path, const int32_t* kept,
+                        int B, void* stream);
+
 /* ---------------------------------------------------------------- sampling */
 
 #define BM_SAMPLE_MAX_VOCAB 524288
