@@ -4,12 +4,33 @@
 // Row j of a stream with n rows and len positions (its own n included) attends
 // to positions 0 .. len - n + j of its slot, or, in a tree, to 0 .. len - n - 1
 // and those of its ancestors and itself:
-//   o = sum_p w_p v_p / sum_p w_p,   w_p = 2^(x_p - max x),  x_p = scale log2(e) q . k_p
+//   o = sum_p w_p v_p / sum_p w_p,   w_p = 2^(x_p - m),  x_p = scale log2(e) q . k_p
+// A stream's rows are gathered per kv head (row r is head r % G of row r / G),
+// 256 to a block; a CTA takes pieces of blocks from the plan's list (longest
+// first, dealt out back and forth) and walks over a piece's tiles of 128
+// positions on the 5th-generation tensor cores (fp16 operands, fp32 sums in
+// tensor memory):
+//   S[row][position] = Q K^T, MMAs of 128 x 128 x 16, both in shared memory;
+//   weights 2^(S ks qf - m) vs, as fp16, over S's place in tensor memory; m is
+//     the running maximum of x + log2 vs, moved only when it rises by 2^8;
+//   O[row][element] += P V, MMAs of 128 x d x 16, A in tensor memory, B the
+//     tile's V as it lies (positions down, elements along: N-major).
+// K and V are converted to fp16 with the same layout (128-byte swizzle), once
+// for the block's two halves of 128 rows, which two warpgroups of softmax work
+// on in turn: while one makes weights the other's products run.  A block of up
+// to 128 rows instead gives its even tiles to one warpgroup and the odd ones
+// to the other, each with sums of its own, which are joined at the end.
+// A thread has 4 rows x 32 positions of a tile, so that a load of scales serves
+// 8 scores, and holds the scores in registers between maximum and weights.
+// A warpgroup converts codes, one lane issues the MMAs.
 //
-// A warp takes a head of a row and walks over its positions, 32 / (d / 16)
-// at once and 16 elements to a lane, with the running maximum and sum of the weights.
+// Every wait is bounded.  A CTA in which one gave up leaves NaN in the rows of all
+// of its pieces.
+#include <type_traits>
+
 #include "kv8_attend.cuh"
 #include "kv8_step.cuh"
+#include "tc_ptx.cuh"
 
 namespace bm {
 namespace {
@@ -21,93 +42,640 @@ struct RowsArgs {
   const void* plan;
   const bf16* Q;
   bf16* O;
+  float* rec_o;        // records: unnormalised output [d]
+  float2* rec_ml;      // and its maximum and sum
   int B, T, qh;
   float scale_log2;
 };
 
-constexpr int kWarps = 4;
+// The plan is for these sizes.
+__device__ __forceinline__ bool fits(const PlanHead& h, const RowsArgs& a) {
+  return h.magic == kPlanMagic && h.B == a.B && h.T == a.T && h.qh == a.qh && h.kvh == a.c.kvh && h.slots == a.c.slots && h.cap == a.c.cap;
+}
+
+constexpr int kSub = 128;                                   // rows of a half block
+constexpr int kThreads = 512;                               // two warpgroups of softmax, one of conversion, one that issues MMAs
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 200, kConvertRegs = 80, kIssueRegs = 32;
+static_assert(2 * kSoftmaxRegs + kConvertRegs + kIssueRegs <= 4 * kLaunchRegs, "warpgroups share what the launch has");
+constexpr uint32_t kTmemCols = 512;                         // S of both halves (later P), O of both halves
+constexpr uint32_t kWaitLimit = 1u << 18;                   // polls of ~3.7 us: a wait gives up after about a second
+
+template <int D>
+struct RowsSmem {
+  uint8_t q[2][kSub * D * 2];                               // [d / 64][row][64] fp16, swizzled
+  uint8_t k[2][kTile * D * 2], v[2][kTile * D * 2];         // [d / 64][position][64]
+  // scales and log2 of V's, of four tiles: they are written with a tile's K, when the softmax may be two tiles back
+  float ks[4][kTile], vs[4][kTile], lg[4][kTile];
+  float up[kBlockRows];
+  float m[kSub], l[kSub];                                   // of the second warpgroup, where both have the same rows
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];      // by the tile's parity
+  uint64_t s_ready[2], p_ready[2], o_ready[2];              // by warpgroup
+  uint64_t q_full, drained;
+  uint32_t tmem;
+  int gave_up;
+};
+
+// 16-byte piece c of row r: 128-byte rows of 64 fp16, pieces swizzled by the row.
+__device__ __forceinline__ uint32_t piece(int r, int c) { return (c >> 3) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
+// Descriptors with the 128-byte swizzle (layout type 2), 8-row atoms of 1024 bytes.  Rows of K: the start moves by 32 bytes per 16
+// elements.  V, N-major: by 16 rows per 16 positions, and blocks of 64 elements lie 128 rows apart.
+__device__ __forceinline__ uint64_t k_major(uint32_t base, int k16) {
+  const uint32_t at = base + (k16 >> 2) * kTile * 128 + (k16 & 3) * 32;
+  return (uint64_t)((at >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t n_major(uint32_t base, int k16) {
+  const uint32_t at = base + k16 * 16 * 128;
+  return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)(kTile * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void sync_some(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t join(uint32_t lo, uint32_t hi) { return (uint64_t)lo | (uint64_t)hi << 32; }
+
+// The CTA's r-th piece.
+__device__ __forceinline__ int turn(int r) { return r * (int)gridDim.x + (int)(r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); }
+
+// A piece as all roles see it.
+struct Work {
+  PlanStream st;
+  int kh, q0, rows, tiles, t0, piece;   // kv head; first of its rows and their number; tiles from t0 on; 65535: the whole block
+  bool wide;                            // both halves have rows
+  __device__ Work(const Plan& plan, int i, int G) {
+    const PlanItem it = plan.items[i];
+    st = plan.streams[it.who & 1023];
+    kh = it.who >> 10;
+    q0 = (it.what & 65535) * kBlockRows;
+    rows = min(kBlockRows, st.n * G - q0);
+    t0 = it.t0;
+    tiles = it.t1 - it.t0;
+    piece = it.what >> 16;
+    wide = rows > kSub;
+  }
+};
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) k_kv8_rows(RowsArgs a) {
-  constexpr int kLanes = D / 16, kAt = 32 / kLanes;   // lanes of a position, positions at once
+__global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
+  extern __shared__ unsigned char raw[];
+  const uint32_t raw_at = tc::smem_u32(raw);
+  RowsSmem<D>& sm = *reinterpret_cast<RowsSmem<D>*>(raw + ((1024u - (raw_at & 1023u)) & 1023u));
   const Plan plan(const_cast<void*>(a.plan), a.B, a.T);
-  const PlanHead& h = *plan.head;
-  if (h.magic != kPlanMagic || h.B != a.B || h.T != a.T || h.qh != a.qh || h.kvh != a.c.kvh || h.slots != a.c.slots || h.cap != a.c.cap) return;
-  const int t = blockIdx.x, lane = threadIdx.x & 31, l = lane % kLanes, g = lane / kLanes, G = a.qh / a.c.kvh;
-  int lo = 0, hi = a.B;                               // the last stream that begins at or before the row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (plan.streams[mid].start <= t) lo = mid;
-    else hi = mid;
+  pdl_trigger();                                            // the merge starts when this grid lets it
+  const int items = fits(*plan.head, a) ? plan.head->items : 0;
+  if ((int)blockIdx.x >= items) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.qh / a.c.kvh;
+
+  if (warp == 12) {
+    tc::tmem_alloc(tc::smem_u32(&sm.tmem), kTmemCols);
+    tc::tmem_relinquish();
   }
-  const PlanStream st = plan.streams[lo];
-  const int j = t - st.start;
-  if (j < 0 || j >= st.n) return;
-  const int own = st.len - st.n;
-  const unsigned long long mask = st.tree ? plan.masks[t] : 0;
-  const int last = st.tree ? st.len : own + j + 1;
-  for (int head = threadIdx.x >> 5; head < a.qh; head += kWarps) {
-    float q[16], o[16] = {}, m = -1e30f, den = 0.f;
-    const uint32_t* qw = reinterpret_cast<const uint32_t*>(a.Q + ((size_t)t * a.qh + head) * D + 16 * l);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      q[2 * e] = bf_lo(qw[e]);
-      q[2 * e + 1] = bf_hi(qw[e]);
+  if (tid == 0) {
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(tc::smem_u32(&sm.k_full[b]), 128);
+      tc::mbar_init(tc::smem_u32(&sm.v_full[b]), 128);
+      tc::mbar_init(tc::smem_u32(&sm.k_free[b]), 1);
+      tc::mbar_init(tc::smem_u32(&sm.v_free[b]), 1);
+      tc::mbar_init(tc::smem_u32(&sm.s_ready[b]), 2);
+      tc::mbar_init(tc::smem_u32(&sm.p_ready[b]), 128);
+      tc::mbar_init(tc::smem_u32(&sm.o_ready[b]), 1);
     }
-    float mx = 0.f, down, up;
+    tc::mbar_init(tc::smem_u32(&sm.q_full), 256);
+    tc::mbar_init(tc::smem_u32(&sm.drained), 1);
+    tc::fence_mbar_init();
+    sm.gave_up = 0;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t s_cols = sm.tmem, o_cols = s_cols + 2 * kTile;
+  // Completion number n (from 0) of a barrier.  A thread whose wait gave up goes on without waiting and arrives nowhere, so that
+  // all threads take the same way through the barriers of their warpgroup.
+  bool ok = true;
+  auto wait = [&](uint64_t& bar, int n) {
+    if (ok) ok = tc::mbar_wait(tc::smem_u32(&bar), n & 1, kWaitLimit);
+  };
+  auto arrive = [&](uint64_t& bar) {
+    if (ok) tc::mbar_arrive(tc::smem_u32(&bar));
+  };
+
+  if (warp >= 12) {
+    // ---------------- MMAs.  They run in the order in which this lane issues them, so scores may be issued behind the product
+    // that reads the weights they overwrite.
+    regs_down<kIssueRegs>();
+    if (warp == 12 && lane == 0) {
+      const uint32_t qk = tc::idesc_f16_f32(kSub, kTile), pv = tc::idesc_f16_f32(kSub, D) | tc::kIdescBMajorN;
+      int tile0 = 0, count[2] = {0, 0};                     // tiles before this piece; products issued for either warpgroup
+      for (int r = 0; turn(r) < items; ++r) {
+        const Work w(plan, turn(r), G);
+        const int steps = w.wide ? 2 * w.tiles : w.tiles;   // step k is warpgroup k % 2's
+        wait(sm.q_full, r);
+        auto scores = [&](int k) {
+          const int tile = tile0 + (w.wide ? k >> 1 : k), s = k & 1;
+          wait(sm.k_full[tile & 1], tile >> 1);
+          if (!ok) return;
+          tc::fence_after_sync();
+          const uint32_t q_at = tc::smem_u32(sm.q[w.wide ? s : 0]), k_at = tc::smem_u32(sm.k[tile & 1]);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(q[e]));
+          for (int e = 0; e < D / 16; ++e) tc::mma_f16_ss(s_cols + s * kTile, k_major(q_at, e), k_major(k_at, e), qk, e > 0);
+          tc::mma_commit(tc::smem_u32(&sm.s_ready[s]));
+          tc::mbar_arrive(tc::smem_u32(&sm.s_ready[s]));    // a release by this thread: it passes the scales on
+          if (!w.wide || s) tc::mma_commit(tc::smem_u32(&sm.k_free[tile & 1]));
+        };
+        scores(0);
+        if (steps > 1) scores(1);
+        for (int k = 0; k < steps; ++k) {
+          const int tile = tile0 + (w.wide ? k >> 1 : k), s = k & 1;
+          wait(sm.v_full[tile & 1], tile >> 1);
+          wait(sm.p_ready[s], count[s]++);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t v_at = tc::smem_u32(sm.v[tile & 1]);
 #pragma unroll
-    for (int s = kLanes / 2; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-    row_scale(mx, down, up);
+          for (int e = 0; e < kTile / 16; ++e)
+            tc::mma_f16_tmem_a(o_cols + s * 128, s_cols + s * kTile + 8 * e, n_major(v_at, e), pv, k > 1 || e > 0);
+          tc::mma_commit(tc::smem_u32(&sm.o_ready[s]));
+          if (!w.wide || s) tc::mma_commit(tc::smem_u32(&sm.v_free[tile & 1]));
+          if (k + 2 < steps) scores(k + 2);
+        }
+        tile0 += w.tiles;
+      }
+      // nothing of this CTA's is in flight when it ends
+      tc::mma_commit(tc::smem_u32(&sm.drained));
+      if (!tc::mbar_wait(tc::smem_u32(&sm.drained), 0, kWaitLimit)) ok = false;
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ---------------- conversion: 16 codes to a thread and turn
+    regs_down<kConvertRegs>();
+    constexpr int kLanes = D / 16, kTurns = kTile * kLanes / 128;
+    const int ct = tid - 256, row0 = ct / kLanes, c = ct % kLanes;
+    const bool swap = c & 4;                                // the second half's pieces in the other order: no bank conflict
+    uint4 kr[kTurns], vr[kTurns];
+    float ks = 0.f, vs = 0.f;
+    auto load = [&](const Work& w, int i, bool v) {
+      const int p0 = (w.t0 + i) * kTile;
+      const size_t at = a.c.row(w.st.slot, w.kh, p0);
+      const uint8_t* from = (v ? a.c.V : a.c.K) + at * D + 16 * ct;
+      const int left = w.st.len - p0;
+      uint4* to = v ? vr : kr;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) q[e] *= down;
-    const size_t at = a.c.row(st.slot, head / G, 0);
-    for (int p0 = 0; p0 < last; p0 += kAt) {
-      const int p = p0 + g;
-      const bool see = p < last && (!st.tree || p < own || mask >> (p - own) & 1);
-      float x = 0.f, v[16] = {};
-      if (see) {
-        const uint4 kw = *reinterpret_cast<const uint4*>(a.c.K + (at + p) * D + 16 * l), vw = *reinterpret_cast<const uint4*>(a.c.V + (at + p) * D + 16 * l);
-        const uint32_t k4[4] = {kw.x, kw.y, kw.z, kw.w}, v4[4] = {vw.x, vw.y, vw.z, vw.w};
-        const float vs = a.c.Vs[at + p];
+      for (int u = 0; u < kTurns; ++u)
+        to[u] = u * (128 / kLanes) + row0 < left ? ldg_nc_v4(from + u * 2048) : make_uint4(0, 0, 0, 0);
+      if (v) vs = ct < left ? __ldg(a.c.Vs + at + ct) : 0.f;
+      else ks = ct < left ? __ldg(a.c.Ks + at + ct) : 0.f;
+    };
+    auto convert = [&](uint8_t* to, const uint4 (&x)[kTurns]) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          float k[4];
-          decode4<FMT>(k4[w], k);
-          decode4<FMT>(v4[w], v + 4 * w);
+      for (int u = 0; u < kTurns; ++u) {
+        const int row = u * (128 / kLanes) + row0;
+        uint32_t f[8];
+        codes4<FMT>(x[u].x, f[0], f[1]);
+        codes4<FMT>(x[u].y, f[2], f[3]);
+        codes4<FMT>(x[u].z, f[4], f[5]);
+        codes4<FMT>(x[u].w, f[6], f[7]);
+        *reinterpret_cast<uint4*>(to + piece(row, 2 * c + swap)) = swap ? make_uint4(f[4], f[5], f[6], f[7]) : make_uint4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<uint4*>(to + piece(row, 2 * c + !swap)) = swap ? make_uint4(f[0], f[1], f[2], f[3]) : make_uint4(f[4], f[5], f[6], f[7]);
+      }
+    };
+    int tile = 0;
+    for (int r = 0; turn(r) < items; ++r) {
+      const Work w(plan, turn(r), G);
+      const int own = w.st.len - w.st.n, all_see = own + (w.st.tree ? 0 : w.q0 / G + 1);   // positions that every row attends to
+      load(w, 0, false);
+      load(w, 0, true);
+      for (int i = 0; i < w.tiles; ++i, ++tile) {
+        const int b = tile & 1, slot = tile & 3;
+        if (tile > 1) wait(sm.k_free[b], (tile >> 1) - 1);
+        sm.ks[slot][ct] = ks;
+        sm.vs[slot][ct] = vs;
+        sm.lg[slot][ct] = fmaxf(log2_fast(vs), -100.f);
+        if (FMT == BM_KV8_E4M3 && (w.t0 + i + 1) * kTile > all_see) {
+          // some rows do not attend to some of these positions, and 0 * NaN is NaN: a NaN code becomes 0, and its position's scale NaN
+          sync_some(2, 128);
+#pragma unroll
+          for (int u = 0; u < kTurns; ++u) {
+            uint32_t* x = reinterpret_cast<uint32_t*>(&vr[u]);
+            uint32_t any = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t nan = ((x[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+              x[e] &= ~((nan >> 7) * 0xFFu);
+              any |= nan;
+            }
+            if (any) sm.vs[slot][u * (128 / kLanes) + row0] = __uint_as_float(0x7FC00000u);
+          }
+        }
+        convert(sm.k[b], kr);
+        tc::fence_proxy_async_smem();
+        arrive(sm.k_full[b]);
+        if (i + 1 < w.tiles) load(w, i + 1, false);
+        if (tile > 1) wait(sm.v_free[b], (tile >> 1) - 1);
+        convert(sm.v[b], vr);
+        tc::fence_proxy_async_smem();
+        arrive(sm.v_full[b]);
+        if (i + 1 < w.tiles) load(w, i + 1, true);
+      }
+    }
+  } else {
+    // ---------------- softmax: thread (g, t) of a warp has rows g, g + 8, g + 16, g + 24 of its 32 (index r) and positions
+    // 8 j + 2 t and the next, j = 0 .. 15.
+    regs_up<kSoftmaxRegs>();
+    const int s = warp >> 2, g = lane >> 2, t = lane & 3, wt = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, half = 16u << 16;
+    const uint32_t s_at = s_cols + s * kTile + lanes, o_at = o_cols + s * 128 + lanes;
+    int count = 0, tile0 = 0;                               // this warpgroup's steps and the CTA's tiles so far
+    for (int turn_no = 0; turn(turn_no) < items; ++turn_no) {
+      const Work w(plan, turn(turn_no), G);
+      const int n_rows = w.st.n * G, own = w.st.len - w.st.n;
+      sync_some(1, 256);                                    // both warpgroups are done with the piece before: its rows may go
+      // ---- the query rows as fp16 of about their own magnitude, d / 8 lanes to a row
+      {
+        constexpr int kPieces = D / 8;
+        const int first = w.wide ? kSub * s : 64 * s, many = w.wide ? kSub : 64;
+        for (int u = wt; u < many * kPieces; u += 128) {
+          const int row = first + u / kPieces, c = u % kPieces, q = w.q0 + row, j = q / G;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (q < n_rows) x = *reinterpret_cast<const uint4*>(a.Q + ((size_t)(w.st.start + j) * a.qh + w.kh * G + q - j * G) * D + 8 * c);
+          const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+          float mx = 0.f, down, up;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(in[e])), fabsf(bf_hi(in[e]))));
+#pragma unroll
+          for (int o = kPieces / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          row_scale(mx, down, up);
+          uint32_t f[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x = fmaf(q[4 * w + e], k[e], x);
-            v[4 * w + e] *= vs;
+            const __half2 v = __floats2half2_rn(bf_lo(in[e]) * down, bf_hi(in[e]) * down);
+            f[e] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          *reinterpret_cast<uint4*>(sm.q[row >> 7] + piece(row & 127, c)) = make_uint4(f[0], f[1], f[2], f[3]);
+          if (c == 0) sm.up[row] = up;
+        }
+      }
+      tc::fence_proxy_async_smem();
+      arrive(sm.q_full);
+      sync_some(1, 256);
+      const int sub = w.wide ? kSub * s : 0, row = 32 * (warp & 3) + g;   // this thread's rows: sub + row + 8 r
+      float qf[4], m[4], l[4];
+      int lim[4];                                           // positions below it are attended to,
+      unsigned long long bits[4];                           // and of the step's own rows these
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int q = w.q0 + sub + row + 8 * r;
+        qf[r] = a.scale_log2 * sm.up[sub + row + 8 * r];
+        m[r] = -1e30f;
+        l[r] = 0.f;
+        lim[r] = q >= n_rows ? 0 : w.st.tree ? own : own + q / G + 1;
+        bits[r] = q < n_rows && w.st.tree ? plan.masks[w.st.start + q / G] : 0;
+      }
+      const int all_see = own + (w.st.tree ? 0 : (w.q0 + sub) / G + 1);   // positions that every row of this half attends to
+      const int steps = w.wide ? w.tiles : (w.tiles + 1 - s) >> 1;
+      for (int it = 0; it < steps; ++it, ++count) {
+        const int i = w.wide ? it : 2 * it + s, slot = (tile0 + i) & 3, p0 = (w.t0 + i) * kTile + 2 * t;   // this thread's first position
+        wait(sm.s_ready[s], count);
+        tc::fence_after_sync();
+        uint64_t y[4][16];                                  // [row][pair of positions]
+        {
+          uint32_t v[4][32];                                // rows 0 and 1, then 2 and 3, 64 positions each
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tc::tmem_ld_frag64(s_at + (q >> 1) * half + 64 * (q & 1), v[q]);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(v[q][e]));   // not used before the wait
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) y[2 * (q >> 1) + r][8 * (q & 1) + j] = join(v[q][4 * j + 2 * r], v[q][4 * j + 2 * r + 1]);
+        }
+        auto pair = [&](const float (*of)[kTile], int j) { return *reinterpret_cast<const uint64_t*>(&of[slot][8 * j + 2 * t]); };
+        auto weights = [&](auto masked) {
+          constexpr bool kMasked = decltype(masked)::value;
+          uint32_t see[4];                                  // bit 2 j + e: position 8 j + e of this thread's is attended to
+          if (kMasked) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              see[r] = 0;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int p = p0 + 8 * j + e;
+                  const unsigned of = (unsigned)(p - own);
+                  if (p < lim[r] || (of < 64u && (bits[r] >> of & 1))) see[r] |= 1u << (2 * j + e);
+                }
+            }
+          }
+          float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t ks = pair(sm.ks, j), lg = pair(sm.lg, j);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              y[r][j] = mul2(mul2(y[r][j], ks), pack2(qf[r], qf[r]));
+              const uint64_t x = add2(y[r][j], lg);
+              if (kMasked) {
+                if (see[r] >> (2 * j) & 1) mx[r] = fmaxf(mx[r], first(x));
+                if (see[r] >> (2 * j + 1) & 1) mx[r] = fmaxf(mx[r], second(x));
+              } else {
+                mx[r] = max3(mx[r], first(x), second(x));
+              }
+            }
+          }
+          bool moves = false;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            moves |= mx[r] > m[r] + 8.f;
+          }
+          if (__any_sync(0xffffffffu, moves)) {             // each row by itself: its neighbours may be other streams' in another step
+            float f[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float mn = mx[r] > m[r] + 8.f ? mx[r] : m[r];
+              f[r] = exp2_fast(m[r] - mn);
+              l[r] = scaled_down(l[r], m[r] - mn);
+              m[r] = mn;
+            }
+            if (it > 0) {                                   // O holds the tiles before
+              wait(sm.o_ready[s], count - 1);
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int c = 0; c < 2 * D; c += 32) {         // both pairs of rows
+                const int h = c >= D;
+                uint32_t o[16];
+                tc::tmem_ld_frag32(o_at + h * half + (c - h * D), o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[e]));
+                const float f0 = h ? f[2] : f[0], f1 = h ? f[3] : f[1];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? f1 : f0));
+                tc::tmem_st_frag32(o_at + h * half + (c - h * D), o);
+              }
+            }
+          }
+          uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t out[2][16];
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) {
+              const int j = 8 * c + jj;
+              const uint64_t vs = pair(sm.vs, j);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const uint64_t x = add2(y[r][j], pack2(-m[r], -m[r]));
+                uint64_t p = pack2(exp2_fast(first(x)), exp2_fast(second(x)));
+                const bool see0 = !kMasked || (see[r] >> (2 * j) & 1), see1 = !kMasked || (see[r] >> (2 * j + 1) & 1);
+                if (kMasked) p = pack2(see0 ? first(p) : 0.f, see1 ? second(p) : 0.f);
+                sum[r] = add2(sum[r], p);
+                p = mul2(p, vs);
+                if (kMasked) p = pack2(see0 ? first(p) : 0.f, see1 ? second(p) : 0.f);   // a scale there may be NaN
+                const __half2 h2 = __floats2half2_rn(first(p), second(p));
+                out[r >> 1][2 * jj + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+            }
+            tc::tmem_st_pairs32(s_at + 32 * c, out[0]);
+            tc::tmem_st_pairs32(s_at + half + 32 * c, out[1]);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) l[r] += first(sum[r]) + second(sum[r]);
+        };
+        if ((w.t0 + i + 1) * kTile > all_see) weights(std::true_type());
+        else weights(std::false_type());
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        arrive(sm.p_ready[s]);
+      }
+      tile0 += w.tiles;
+
+      // ---- the rows' outputs, or this piece's records
+      if (steps > 0) wait(sm.o_ready[s], count - 1);
+      tc::fence_after_sync();
+      float f0[4], f1[4];                                   // factors of this warpgroup's sums, and of the other's
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        f0[r] = 1.f;
+        f1[r] = 0.f;
+      }
+      if (!w.wide) {
+        if (s == 1 && t == 0) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sm.m[row + 8 * r] = m[r];
+            sm.l[row + 8 * r] = l[r];
           }
         }
       }
-      x = group_sum<kLanes>(x);
-      x = see ? x * a.c.Ks[at + p] * (a.scale_log2 * up) : -1e30f;
-      const float mn = fmaxf(m, x), f = exp2f(m - mn), w = see ? exp2f(x - mn) : 0.f;
-      den = den * f + w;
+      float* other = reinterpret_cast<float*>(sm.q[1]) + wt;   // the second half's rows are free where both have the same
+#pragma unroll 1
+      for (int hc = 0; hc < 2; ++hc) {                      // a half of the elements
+        constexpr int kF = D / 64;
+        float o[2][kF][16];                                 // [pair of rows][32 elements]
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = fmaf(o[e], f, see ? w * v[e] : 0.f);
-      m = mn;
-    }
-    // the groups' parts
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int s = kLanes; s < 32; s <<= 1) {
-      const float om = __shfl_xor_sync(0xffffffffu, m, s), od = __shfl_xor_sync(0xffffffffu, den, s);
-      const float mn = fmaxf(m, om), f = exp2f(m - mn), of = exp2f(om - mn);
-      den = den * f + od * of;
+          for (int f = 0; f < kF; ++f) {
+            uint32_t x[16];
+            tc::tmem_ld_frag32(o_at + h * half + hc * (D / 2) + 32 * f, x);
+            tc::tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = o[e] * f + __shfl_xor_sync(0xffffffffu, o[e], s) * of;
-      m = mn;
-    }
-    if (g == 0) {
-      const float inv = den == 0.f ? 0.f : 1.f / den;
-      bf16* to = a.O + ((size_t)t * a.qh + head) * D + 16 * l;
+            for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(x[e]));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) to[e] = f2bf(o[e] * inv);
+            for (int e = 0; e < 16; ++e) o[h][f][e] = steps > 0 ? __uint_as_float(x[e]) : 0.f;
+          }
+        if (!w.wide) {
+          if (s == 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int f = 0; f < kF; ++f)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) other[((h * kF + f) * 16 + e) * 128] = o[h][f][e];
+          }
+          sync_some(1, 256);
+          if (s == 0) {
+            if (hc == 0) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float om = sm.m[row + 8 * r], mn = fmaxf(m[r], om);
+                f0[r] = exp2_fast(m[r] - mn);
+                f1[r] = exp2_fast(om - mn);
+                l[r] = scaled_down(l[r], m[r] - mn) + scaled_down(sm.l[row + 8 * r], om - mn);
+                m[r] = mn;
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int f = 0; f < kF; ++f)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const int r = 2 * h + (e >> 1 & 1);
+                  o[h][f][e] = fmaf(other[((h * kF + f) * 16 + e) * 128], f1[r], o[h][f][e] * f0[r]);
+                }
+          }
+          sync_some(1, 256);
+          if (s == 1) continue;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int q = w.q0 + sub + row + 8 * r, j = q / G, head = w.kh * G + q - j * G;
+          if (w.piece != (int)kWhole) {
+            if (q < n_rows) {
+              const size_t rec = (size_t)w.st.rec + ((size_t)j * a.qh + head) * w.st.most + w.piece;
+              if (hc == 0 && t == 0) a.rec_ml[rec] = make_float2(m[r], l[r]);
+              float* to = a.rec_o + rec * D + hc * (D / 2) + 2 * t;
+#pragma unroll
+              for (int f = 0; f < kF; ++f)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float* x = &o[r >> 1][f][4 * e + 2 * (r & 1)];
+                  *reinterpret_cast<float2*>(to + 32 * f + 8 * e) = make_float2(x[0], x[1]);
+                }
+            }
+          } else {
+            const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];   // nothing to attend to: zeros
+#pragma unroll
+            for (int f = 0; f < kF; ++f) {
+              uint32_t p[4];                                // elements 8 e + 2 t and the next of 32
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float* x = &o[r >> 1][f][4 * e + 2 * (r & 1)];
+                const __nv_bfloat162 v = __floats2bfloat162_rn(x[0] * inv, x[1] * inv);
+                p[e] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              // turned among the row's four threads: elements 8 t .. 8 t + 7
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const uint32_t back = __shfl_xor_sync(0xffffffffu, t & 1 ? p[e] : p[e + 1], 1);
+                if (t & 1) p[e] = back;
+                else p[e + 1] = back;
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t back = __shfl_xor_sync(0xffffffffu, t & 2 ? p[e] : p[e + 2], 2);
+                if (t & 2) p[e] = back;
+                else p[e + 2] = back;
+              }
+              if (q < n_rows)
+                *reinterpret_cast<uint4*>(a.O + ((size_t)(w.st.start + j) * a.qh + head) * D + hc * (D / 2) + 32 * f + 8 * t) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+          }
+        }
+      }
+      tc::fence_before_sync();                              // O is read before the next piece's products
     }
   }
+  if (!ok) sm.gave_up = 1;
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 12) tc::tmem_dealloc(s_cols, kTmemCols);
+  if (sm.gave_up) {                                         // NaN in all rows of this CTA's pieces
+    for (int r = 0; turn(r) < items; ++r) {
+      const Work w(plan, turn(r), G);
+      for (int u = tid; u < w.rows * D; u += kThreads) {
+        const int q = w.q0 + u / D, j = q / G, head = w.kh * G + q - j * G;
+        if (w.piece != (int)kWhole) a.rec_ml[(size_t)w.st.rec + ((size_t)j * a.qh + head) * w.st.most + w.piece] = make_float2(0.f, __uint_as_float(0x7FC00000u));
+        else a.O[((size_t)(w.st.start + j) * a.qh + head) * D + u % D] = __ushort_as_bfloat16(0x7FC0);
+      }
+    }
+  }
+}
+
+// The rows of cut blocks: a head of a row to a warp and turn, its records in
+// ascending order, a lane d / 32 elements.
+constexpr int kMergeWarps = 8, kMergeAhead = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_rows_merge(RowsArgs a) {
+  constexpr int E = D / 32;
+  using Part = typename std::conditional<E == 4, float4, float2>::type;
+  __shared__ int unit[kMaxStreams];
+  const Plan plan(const_cast<void*>(a.plan), a.B, a.T);
+  const bool mine = fits(*plan.head, a);
+  const int units = mine ? plan.head->units : 0, lane = threadIdx.x & 31, G = a.qh / a.c.kvh;
+  for (int b = threadIdx.x; b < a.B && mine; b += kMergeWarps * 32) unit[b] = plan.streams[b].unit;
+  __syncthreads();
+  pdl_wait();
+  for (int u = blockIdx.x * kMergeWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kMergeWarps) {
+    int lo = 0, hi = a.B;                                   // the last stream whose units begin at or before u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (unit[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    const PlanStream st = plan.streams[lo];
+    const int local = u - st.unit, j = local / a.qh, head = local - j * a.qh, kh = head / G, block = (j * G + head - kh * G) / kBlockRows;
+    const int n = Pieces(block * a.c.kvh + kh, Cut{st.cut, st.pitch}, extent_of(block, st.n, st.len, G, st.tree)).count;
+    if (n == 1) continue;                                   // the block is whole: its outputs are there
+    const size_t rec = (size_t)st.rec + (size_t)local * st.most;
+    const Part* o = reinterpret_cast<const Part*>(a.rec_o + rec * D) + lane;
+    const float2* ml = a.rec_ml + rec;
+    float mx = -1e30f, den = 0.f, acc[E] = {};
+    for (int r = lane; r < n; r += 32) mx = fmaxf(mx, ml[r].x);
+    mx = warp_max(mx);
+    for (int r0 = 0; r0 < n; r0 += kMergeAhead) {
+      Part part[kMergeAhead];
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k)
+        if (r0 + k < n) part[k] = o[(r0 + k) * 32];
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k)
+        if (r0 + k < n) {
+          const float2 x = ml[r0 + k];
+          const float f = exp2f(x.x - mx);
+          den += x.y * exp2f(fmaxf(x.x - mx, -120.f)) * exp2f(fminf(x.x - mx + 120.f, 0.f));   // as scaled_down
+          const float* p = reinterpret_cast<const float*>(&part[k]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(p[e], f, acc[e]);
+        }
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    bf16* to = a.O + ((size_t)(st.start + j) * a.qh + head) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) *reinterpret_cast<__nv_bfloat162*>(to + 2 * e) = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  }
+}
+
+template <int D, int FMT>
+cudaError_t launch_rows(const RowsArgs& a, int64_t records, cudaStream_t s) {
+  const size_t smem = sizeof(RowsSmem<D>) + 1024;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = once_per_device(done, [&] {
+    cudaFuncAttributes at;
+    cudaError_t x = cudaFuncGetAttributes(&at, k_kv8_rows<D, FMT>);
+    // the warpgroups' shares are cut from this many; with fewer, one would wait for registers that never come
+    if (x == cudaSuccess && at.numRegs != kLaunchRegs) x = cudaErrorInvalidKernelImage;
+    return x != cudaSuccess ? x : cudaFuncSetAttribute(k_kv8_rows<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min<int64_t>(kSms, most_items(a.B, a.T, a.qh, a.c.kvh));
+  e = launch_k(false, k_kv8_rows<D, FMT>, dim3(grid), dim3(kThreads), smem, s, a);
+  if (e != cudaSuccess || records == 0) return e;
+  const int64_t units = std::min<int64_t>(records, (int64_t)a.T * a.qh);
+  return launch_k(true, k_kv8_rows_merge<D>, dim3((unsigned)std::min<int64_t>((units + kMergeWarps - 1) / kMergeWarps, 4 * kSms)), dim3(kMergeWarps * 32), 0, s, a);
 }
 
 }  // namespace
@@ -136,20 +704,20 @@ bm_status kv8_attend_rows(const bm_kv8_cache* c, const void* plan, size_t plan_b
   if (plan_bytes < kv8::plan_bytes(B, T, q_heads, c->kv_heads)) return refuse("a plan of " + std::to_string(plan_bytes) + " bytes is none of this B, T and heads");
   const size_t need = kv8_rows_workspace_bytes(B, T, q_heads, c->kv_heads, c->head_dim, c->ctx_cap);
   if (ws_bytes < need) return refuse("workspace of " + std::to_string(ws_bytes) + " bytes, " + std::to_string(need) + " needed");
+  const int64_t records = kv8::most_records(B, T, q_heads, c->kv_heads, c->ctx_cap);
   a.plan = plan;
   a.Q = reinterpret_cast<const bf16*>(Q);
   a.O = reinterpret_cast<bf16*>(O);
+  a.rec_o = static_cast<float*>(ws);
+  a.rec_ml = reinterpret_cast<float2*>(a.rec_o + (size_t)records * c->head_dim);
   a.B = B;
   a.T = T;
   a.qh = q_heads;
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4 = c->format == BM_KV8_E4M3, d128 = c->head_dim == 128;
-  if (d128 && e4) k_kv8_rows<128, BM_KV8_E4M3><<<T, kWarps * 32, 0, s>>>(a);
-  else if (d128) k_kv8_rows<128, BM_KV8_INT8><<<T, kWarps * 32, 0, s>>>(a);
-  else if (e4) k_kv8_rows<64, BM_KV8_E4M3><<<T, kWarps * 32, 0, s>>>(a);
-  else k_kv8_rows<64, BM_KV8_INT8><<<T, kWarps * 32, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = d128 ? (e4 ? launch_rows<128, BM_KV8_E4M3>(a, records, s) : launch_rows<128, BM_KV8_INT8>(a, records, s))
+                             : (e4 ? launch_rows<64, BM_KV8_E4M3>(a, records, s) : launch_rows<64, BM_KV8_INT8>(a, records, s));
   if (e != cudaSuccess) return set_error(BM_ERR_CUDA, std::string("kv8_attend_rows: ") + cudaGetErrorString(e));
   return ok();
 }

@@ -62,7 +62,9 @@ def attend(cache, Q, slots, lens, streams, scale, parents=None):
 
     The bound per element is that of decode attention over this cache (kv8_ref.attend): weights rounded to 16 bits
     (2^-11), scores of d fp32 products (each weight and the normalising sum off by (d + 8) 2^-24 scale sum|q||k|),
-    2^-18 for e^x and the sums, and fp16's smallest step against the row's largest term."""
+    2^-18 for e^x and the sums, and fp16's smallest step against the row's largest term.  V scales below 2^-100 count
+    as that there (the calls' stated range): weights are held against the maximum of x + max(log2 vs, -100), so a scale of
+    2^-107 leaves the largest weight at 2^-7, and half of fp16's smallest step, 2^-25, is 2^-18 of it."""
     T, qh, d = Q.shape
     kvh = cache["kv_heads"]
     G = qh // kvh
@@ -91,7 +93,7 @@ def attend(cache, Q, slots, lens, streams, scale, parents=None):
             clean = lambda y: torch.where(y.isfinite(), y, 0)  # noqa: E731
             part = slice(t, t + n), slice(h * G, (h + 1) * G)
             o[part] = torch.einsum("tgp,pd->tgd", p, clean(v))
-            small = 2.0 ** -25 * (p * clean(vs)).amax(-1, keepdim=True) * (seen @ clean(vc.abs()))[:, None]
+            small = 2.0 ** -25 * (p * clean(vs).clamp(min=2.0 ** -100)).amax(-1, keepdim=True) * (seen @ clean(vc.abs()))[:, None]
             bound[part] = torch.einsum("tgp,pd->tgd", p, clean(v.abs())) * (2.0 ** -11 + 2.0 ** -18 + 2 * off) + small
     return o, bound, live
 
