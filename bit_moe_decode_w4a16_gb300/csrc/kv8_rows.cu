@@ -58,6 +58,8 @@ constexpr int kThreads = 512;                               // two warpgroups of
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 200, kConvertRegs = 80, kIssueRegs = 32;
 static_assert(2 * kSoftmaxRegs + kConvertRegs + kIssueRegs <= 4 * kLaunchRegs, "warpgroups share what the launch has");
 constexpr uint32_t kTmemCols = 512;                         // S of both halves (later P), O of both halves
+constexpr float kLargest = 8192.f;                          // a weight above it moves its row's maximum; fp16 ends at 65504
+constexpr float kLargestSum = 2.028240960365167e31f;        // 2^104: V scales below 2^-100 count as that in a maximum
 constexpr uint32_t kWaitLimit = 1u << 18;                   // polls of ~3.7 us: a wait gives up after about a second
 
 template <int D>
@@ -98,11 +100,6 @@ __device__ __forceinline__ void regs_down() {
 }
 __device__ __forceinline__ void sync_some(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 __device__ __forceinline__ uint64_t join(uint32_t lo, uint32_t hi) { return (uint64_t)lo | (uint64_t)hi << 32; }
 
 // The CTA's r-th piece.
@@ -347,120 +344,152 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
         const int i = w.wide ? it : 2 * it + s, slot = (tile0 + i) & 3, p0 = (w.t0 + i) * kTile + 2 * t;   // this thread's first position
         wait(sm.s_ready[s], count);
         tc::fence_after_sync();
-        uint64_t y[4][16];                                  // [row][pair of positions]
-        {
-          uint32_t v[4][32];                                // rows 0 and 1, then 2 and 3, 64 positions each
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tc::tmem_ld_frag64(s_at + (q >> 1) * half + 64 * (q & 1), v[q]);
+        const float *ks_at = sm.ks[slot] + 2 * t, *vs_at = sm.vs[slot] + 2 * t, *lg_at = sm.lg[slot] + 2 * t;
+        auto pair = [](const float* of, int j) { return *reinterpret_cast<const uint64_t*>(of + 8 * j); };
+        // Scores of 32 positions, rows 2 h and 2 h + 1: v[h][4 j + 2 (r & 1) + e].
+        auto read = [&](int c, uint32_t (&v)[2][16]) {
+          tc::tmem_ld_frag32(s_at + 32 * c, v[0]);
+          tc::tmem_ld_frag32(s_at + half + 32 * c, v[1]);
+        };
+        auto landed = [](uint32_t (&v)[2][16]) {            // nothing that was read is used before
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v[0][e]), "+r"(v[1][e]));
+        };
+        // ---- in one sweep against the present maxima, where every row attends to all of the tile
+        bool good = it > 0 && (w.t0 + i + 1) * kTile <= all_see;
+        if (good) {
+          uint32_t v[2][2][16], out[2][32];                 // out[pair of rows][2 j + (r & 1)]: weights of two positions
+          uint64_t sum[4] = {0, 0, 0, 0};
+          __half2 top = __float2half2_rn(0.f);              // the largest
+          read(0, v[0]);
+          landed(v[0]);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(v[q][e]));   // not used before the wait
+          for (int c = 0; c < 4; ++c) {
+            if (c < 3) read(c + 1, v[(c + 1) & 1]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+            for (int jj = 0; jj < 4; ++jj) {
+              const int j = 4 * c + jj;
+              const uint64_t ks = pair(ks_at, j), vs = pair(vs_at, j);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) y[2 * (q >> 1) + r][8 * (q & 1) + j] = join(v[q][4 * j + 2 * r], v[q][4 * j + 2 * r + 1]);
-        }
-        auto pair = [&](const float (*of)[kTile], int j) { return *reinterpret_cast<const uint64_t*>(&of[slot][8 * j + 2 * t]); };
-        auto weights = [&](auto masked) {
-          constexpr bool kMasked = decltype(masked)::value;
-          uint32_t see[4];                                  // bit 2 j + e: position 8 j + e of this thread's is attended to
-          if (kMasked) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              see[r] = 0;
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int p = p0 + 8 * j + e;
-                  const unsigned of = (unsigned)(p - own);
-                  if (p < lim[r] || (of < 64u && (bits[r] >> of & 1))) see[r] |= 1u << (2 * j + e);
-                }
-            }
-          }
-          float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint64_t ks = pair(sm.ks, j), lg = pair(sm.lg, j);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              y[r][j] = mul2(mul2(y[r][j], ks), pack2(qf[r], qf[r]));
-              const uint64_t x = add2(y[r][j], lg);
-              if (kMasked) {
-                if (see[r] >> (2 * j) & 1) mx[r] = fmaxf(mx[r], first(x));
-                if (see[r] >> (2 * j + 1) & 1) mx[r] = fmaxf(mx[r], second(x));
-              } else {
-                mx[r] = max3(mx[r], first(x), second(x));
+              for (int r = 0; r < 4; ++r) {
+                const uint32_t* x = &v[c & 1][r >> 1][4 * jj + 2 * (r & 1)];
+                const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
+                const uint64_t p = pack2(exp2_fast(first(e)), exp2_fast(second(e))), pv = mul2(p, vs);
+                sum[r] = add2(sum[r], p);
+                const __half2 h2 = __floats2half2_rn(first(pv), second(pv));
+                out[r >> 1][2 * j + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
+                top = __hmax2(top, h2);
               }
             }
+            if (c < 3) landed(v[(c + 1) & 1]);
+          }
+          float sums[4], most = 0.f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sums[r] = first(sum[r]) + second(sum[r]);
+            most = fmaxf(most, sums[r]);
+          }
+          // a sum by itself too: where V is zero the weight is, or NaN, whatever p is
+          good = __all_sync(0xffffffffu, fmaxf(__low2float(top), __high2float(top)) <= kLargest && most < kLargestSum);
+          if (good) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) l[r] += sums[r];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) tc::tmem_st_pairs32(s_at + h * half + 32 * c, *reinterpret_cast<const uint32_t(*)[16]>(&out[h][16 * c]));
+          }
+        }
+        // ---- in two: the rows' maxima of score + log2 of V's scale, then the weights against them
+        if (!good) {
+          uint32_t see[4];                                  // bit 2 j + e: position 8 j + e of this thread's is attended to
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int left = lim[r] - p0, k = left <= 0 ? 0 : 2 * (left >> 3) + min(left & 7, 2);
+            see[r] = k >= 32 ? 0xffffffffu : (1u << k) - 1;
+            if (bits[r] != 0) {
+#pragma unroll 1
+              for (int k = 0; k < 32; ++k) {
+                const unsigned of = (unsigned)(p0 + 8 * (k >> 1) + (k & 1) - own);
+                if (of < 64u && (bits[r] >> of & 1)) see[r] |= 1u << k;
+              }
+            }
+          }
+          // A score in two roundings: a maximum is one of the scores, and none lies above it by the product's own rounding.
+          auto score = [&](const uint32_t (&v)[2][16], int r, int jj, int e, float ks) {
+            return __fmul_rn(__fmul_rn(__uint_as_float(v[r >> 1][4 * jj + 2 * (r & 1) + e]), ks), qf[r]);
+          };
+          float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f}, f[4];
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[2][16];
+            read(c, v);
+            landed(v);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float ks = ks_at[32 * c + 8 * jj + e], lg = lg_at[32 * c + 8 * jj + e];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  if (see[r] >> (8 * c + 2 * jj + e) & 1) mx[r] = fmaxf(mx[r], __fadd_rn(score(v, r, jj, e, ks), lg));
+              }
           }
           bool moves = false;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
+          for (int r = 0; r < 4; ++r) {                     // each row by itself: its neighbours stand elsewhere in another step
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-            moves |= mx[r] > m[r] + 8.f;
+            const float mn = mx[r] > m[r] + 8.f ? mx[r] : m[r];
+            moves |= mn != m[r];
+            f[r] = exp2_fast(m[r] - mn);
+            l[r] = scaled_down(l[r], m[r] - mn);
+            m[r] = mn;
           }
-          if (__any_sync(0xffffffffu, moves)) {             // each row by itself: its neighbours may be other streams' in another step
-            float f[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float mn = mx[r] > m[r] + 8.f ? mx[r] : m[r];
-              f[r] = exp2_fast(m[r] - mn);
-              l[r] = scaled_down(l[r], m[r] - mn);
-              m[r] = mn;
-            }
-            if (it > 0) {                                   // O holds the tiles before
-              wait(sm.o_ready[s], count - 1);
-              tc::fence_after_sync();
+          if (it > 0 && __any_sync(0xffffffffu, moves)) {   // O holds the tiles before
+            wait(sm.o_ready[s], count - 1);
+            tc::fence_after_sync();
 #pragma unroll 1
-              for (int c = 0; c < 2 * D; c += 32) {         // both pairs of rows
-                const int h = c >= D;
-                uint32_t o[16];
-                tc::tmem_ld_frag32(o_at + h * half + (c - h * D), o);
-                tc::tmem_wait_ld();
+            for (int c = 0; c < 2 * D; c += 32) {           // both pairs of rows
+              const int h = c >= D;
+              uint32_t o[16];
+              tc::tmem_ld_frag32(o_at + h * half + (c - h * D), o);
+              tc::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[e]));
-                const float f0 = h ? f[2] : f[0], f1 = h ? f[3] : f[1];
+              for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[e]));
+              const float f0 = h ? f[2] : f[0], f1 = h ? f[3] : f[1];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? f1 : f0));
-                tc::tmem_st_frag32(o_at + h * half + (c - h * D), o);
-              }
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? f1 : f0));
+              tc::tmem_st_frag32(o_at + h * half + (c - h * D), o);
             }
           }
-          uint64_t sum[4] = {0, 0, 0, 0};
+          float sum[4] = {};
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {                     // weights go where scores of an earlier turn were, or this one's
+            uint32_t v[2][16], out[2][8];
+            read(c, v);
+            landed(v);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t out[2][16];
-#pragma unroll
-            for (int jj = 0; jj < 8; ++jj) {
-              const int j = 8 * c + jj;
-              const uint64_t vs = pair(sm.vs, j);
+            for (int jj = 0; jj < 4; ++jj) {
+              const float2 ks = *reinterpret_cast<const float2*>(ks_at + 32 * c + 8 * jj), vs = *reinterpret_cast<const float2*>(vs_at + 32 * c + 8 * jj);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                const uint64_t x = add2(y[r][j], pack2(-m[r], -m[r]));
-                uint64_t p = pack2(exp2_fast(first(x)), exp2_fast(second(x)));
-                const bool see0 = !kMasked || (see[r] >> (2 * j) & 1), see1 = !kMasked || (see[r] >> (2 * j + 1) & 1);
-                if (kMasked) p = pack2(see0 ? first(p) : 0.f, see1 ? second(p) : 0.f);
-                sum[r] = add2(sum[r], p);
-                p = mul2(p, vs);
-                if (kMasked) p = pack2(see0 ? first(p) : 0.f, see1 ? second(p) : 0.f);   // a scale there may be NaN
-                const __half2 h2 = __floats2half2_rn(first(p), second(p));
+                // the product is selected too: a scale that is not attended to may be NaN
+                const uint32_t here = see[r] >> (8 * c + 2 * jj);
+                const float x0 = exp2_fast(__fadd_rn(score(v, r, jj, 0, ks.x), -m[r])), x1 = exp2_fast(__fadd_rn(score(v, r, jj, 1, ks.y), -m[r]));
+                const float y0 = here & 1 ? x0 : 0.f, y1 = here & 2 ? x1 : 0.f;
+                sum[r] += y0 + y1;
+                const __half2 h2 = __floats2half2_rn(here & 1 ? x0 * vs.x : 0.f, here & 2 ? x1 * vs.y : 0.f);
                 out[r >> 1][2 * jj + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
               }
             }
-            tc::tmem_st_pairs32(s_at + 32 * c, out[0]);
-            tc::tmem_st_pairs32(s_at + half + 32 * c, out[1]);
+            tc::tmem_st_frag16(s_at + 16 * c, out[0]);
+            tc::tmem_st_frag16(s_at + half + 16 * c, out[1]);
           }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) l[r] += first(sum[r]) + second(sum[r]);
-        };
-        if ((w.t0 + i + 1) * kTile > all_see) weights(std::true_type());
-        else weights(std::false_type());
+          for (int r = 0; r < 4; ++r) l[r] += sum[r];
+        }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         arrive(sm.p_ready[s]);
