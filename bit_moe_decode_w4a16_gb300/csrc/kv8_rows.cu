@@ -54,11 +54,11 @@ __device__ __forceinline__ bool fits(const PlanHead& h, const RowsArgs& a) {
 }
 
 constexpr int kSub = 128;                                   // rows of a half block
-constexpr int kThreads = 512;                               // two warpgroups of softmax, one of conversion, one that issues MMAs
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 200, kConvertRegs = 80, kIssueRegs = 32;
-static_assert(2 * kSoftmaxRegs + kConvertRegs + kIssueRegs <= 4 * kLaunchRegs, "warpgroups share what the launch has");
+constexpr int kConvert = 256, kThreads = 128 + kConvert + 256;   // a warpgroup that issues MMAs, two of conversion, two of softmax
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 160, kConvertRegs = 64, kIssueRegs = 32;
+static_assert(2 * kSoftmaxRegs + 2 * kConvertRegs + kIssueRegs <= 5 * kLaunchRegs, "warpgroups share what the launch has");
 constexpr uint32_t kTmemCols = 512;                         // S of both halves (later P), O of both halves
-constexpr float kLargest = 8192.f;                          // a weight above it moves its row's maximum; fp16 ends at 65504
+constexpr float kLargest = 32768.f;                         // a weight above it moves its row's maximum; fp16 ends at 65504
 constexpr float kLargestSum = 2.028240960365167e31f;        // 2^104: V scales below 2^-100 count as that in a maximum
 constexpr uint32_t kWaitLimit = 1u << 18;                   // polls of ~3.7 us: a wait gives up after about a second
 
@@ -70,8 +70,9 @@ struct RowsSmem {
   float ks[4][kTile], vs[4][kTile], lg[4][kTile];
   float up[kBlockRows];
   float m[kSub], l[kSub];                                   // of the second warpgroup, where both have the same rows
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];      // by the tile's parity
-  uint64_t s_ready[2], p_ready[2], o_ready[2];              // by warpgroup
+  uint64_t k_full[2], v_full[2];                            // by the tile's parity
+  uint64_t s_ready[2][2], o_ready[2][2];                    // by half and the tile's parity: they also say that K, V may be overwritten
+  uint64_t p_ready[2], turn[2];                             // by half
   uint64_t q_full, drained;
   uint32_t tmem;
   int gave_up;
@@ -79,16 +80,12 @@ struct RowsSmem {
 
 // 16-byte piece c of row r: 128-byte rows of 64 fp16, pieces swizzled by the row.
 __device__ __forceinline__ uint32_t piece(int r, int c) { return (c >> 3) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
-// Descriptors with the 128-byte swizzle (layout type 2), 8-row atoms of 1024 bytes.  Rows of K: the start moves by 32 bytes per 16
-// elements.  V, N-major: by 16 rows per 16 positions, and blocks of 64 elements lie 128 rows apart.
-__device__ __forceinline__ uint64_t k_major(uint32_t base, int k16) {
-  const uint32_t at = base + (k16 >> 2) * kTile * 128 + (k16 & 3) * 32;
-  return (uint64_t)((at >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t n_major(uint32_t base, int k16) {
-  const uint32_t at = base + k16 * 16 * 128;
-  return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)(kTile * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// Descriptors with the 128-byte swizzle (layout type 2), 8-row atoms of 1024 bytes: the low word, to which a start 16 bytes further on
+// adds 1, and the whole.  Rows of K and Q: the start moves by 32 bytes per 16 elements.  V, N-major: by 16 rows per 16
+// positions, and blocks of 64 elements lie 128 rows apart.
+__device__ __forceinline__ uint32_t k_major(uint32_t at) { return at >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t n_major(uint32_t at) { return at >> 4 | (uint32_t)(kTile * 128 >> 4) << 16; }
+__device__ __forceinline__ uint64_t operand(uint32_t low) { return (uint64_t)low | (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32; }
 
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -101,6 +98,26 @@ __device__ __forceinline__ void regs_down() {
 __device__ __forceinline__ void sync_some(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 __device__ __forceinline__ uint64_t join(uint32_t lo, uint32_t hi) { return (uint64_t)lo | (uint64_t)hi << 32; }
+
+// Of a thread's positions 8 j + e (j < 16, e < 2), as bits 2 j + e: those below `left`; and those whose bit (offset + 8 j + e) of `bits` is set.
+__device__ __forceinline__ uint32_t below(int left) {
+  const int k = left <= 0 ? 0 : 2 * (left >> 3) + min(left & 7, 2);
+  return k >= 32 ? 0xffffffffu : (1u << k) - 1;
+}
+__device__ __forceinline__ uint32_t two_of_eight(unsigned long long x) {   // bits 0 and 1 of each byte, together
+  x &= 0x0303030303030303ull;
+  x = (x | x >> 6) & 0x000F000F000F000Full;
+  x = (x | x >> 12) & 0x000000FF000000FFull;
+  return (uint32_t)(x | x >> 24) & 0xFFFFu;
+}
+__device__ __forceinline__ uint32_t among(unsigned long long bits, int offset) {
+  const int up = -offset;
+  unsigned long long lo = 0, hi = 0;
+  if (offset >= 0) lo = offset < 64 ? bits >> offset : 0;
+  else if (up < 64) lo = bits << up, hi = bits >> (64 - up);
+  else hi = up < 128 ? bits << (up - 64) : 0;
+  return two_of_eight(lo) | two_of_eight(hi) << 16;
+}
 
 // The CTA's r-th piece.
 __device__ __forceinline__ int turn(int r) { return r * (int)gridDim.x + (int)(r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); }
@@ -130,26 +147,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
   RowsSmem<D>& sm = *reinterpret_cast<RowsSmem<D>*>(raw + ((1024u - (raw_at & 1023u)) & 1023u));
   const Plan plan(const_cast<void*>(a.plan), a.B, a.T);
   pdl_trigger();                                            // the merge starts when this grid lets it
-  const int items = fits(*plan.head, a) ? plan.head->items : 0;
+  // the same in all lanes by construction, which spares the warps that issue MMAs most of their instructions
+  auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  const int items = uniform(fits(*plan.head, a) ? plan.head->items : 0);
   if ((int)blockIdx.x >= items) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.qh / a.c.kvh;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, G = a.qh / a.c.kvh;
 
-  if (warp == 12) {
+  if (warp == 0) {
     tc::tmem_alloc(tc::smem_u32(&sm.tmem), kTmemCols);
     tc::tmem_relinquish();
   }
   if (tid == 0) {
     for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(tc::smem_u32(&sm.k_full[b]), 128);
-      tc::mbar_init(tc::smem_u32(&sm.v_full[b]), 128);
-      tc::mbar_init(tc::smem_u32(&sm.k_free[b]), 1);
-      tc::mbar_init(tc::smem_u32(&sm.v_free[b]), 1);
-      tc::mbar_init(tc::smem_u32(&sm.s_ready[b]), 2);
+      tc::mbar_init(tc::smem_u32(&sm.k_full[b]), kConvert);
+      tc::mbar_init(tc::smem_u32(&sm.v_full[b]), kConvert);
+      for (int s = 0; s < 2; ++s) {
+        tc::mbar_init(tc::smem_u32(&sm.s_ready[s][b]), 2);
+        tc::mbar_init(tc::smem_u32(&sm.o_ready[s][b]), 1);
+      }
       tc::mbar_init(tc::smem_u32(&sm.p_ready[b]), 128);
-      tc::mbar_init(tc::smem_u32(&sm.o_ready[b]), 1);
+      tc::mbar_init(tc::smem_u32(&sm.turn[b]), 1);
     }
     tc::mbar_init(tc::smem_u32(&sm.q_full), 256);
-    tc::mbar_init(tc::smem_u32(&sm.drained), 1);
+    tc::mbar_init(tc::smem_u32(&sm.drained), 2);
     tc::fence_mbar_init();
     sm.gave_up = 0;
   }
@@ -167,60 +187,89 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     if (ok) tc::mbar_arrive(tc::smem_u32(&bar));
   };
 
-  if (warp >= 12) {
-    // ---------------- MMAs.  They run in the order in which this lane issues them, so scores may be issued behind the product
-    // that reads the weights they overwrite.
+  if (warp < 4) {
+    // ---------------- MMAs, a warp for each half.  They run in the order in which a warp issues them, so a half's scores may be issued
+    // behind the product that reads the weights they overwrite.  The two take turns, a product and the next scores each: issued
+    // at once, both halves' MMAs end together, and the tensor cores wait while both make weights (a prompt of 8192 rows: 659 us;
+    // in turns 566; one warp for both, 702, as the pipe runs dry between its MMAs).
     regs_down<kIssueRegs>();
-    if (warp == 12 && lane == 0) {
-      const uint32_t qk = tc::idesc_f16_f32(kSub, kTile), pv = tc::idesc_f16_f32(kSub, D) | tc::kIdescBMajorN;
-      int tile0 = 0, count[2] = {0, 0};                     // tiles before this piece; products issued for either warpgroup
+    if (warp < 2) {
+      const int s = warp;
+      constexpr uint32_t qk = tc::idesc_f16_f32(kSub, kTile), pv = tc::idesc_f16_f32(kSub, D) | tc::kIdescBMajorN;
+      constexpr uint32_t kBuffer = kTile * D * 2 >> 4, kBlock = kTile * 128 >> 4;
+      const uint32_t k_at = k_major(tc::smem_u32(sm.k[0])), v_at = n_major(tc::smem_u32(sm.v[0])), q_at = k_major(tc::smem_u32(sm.q[0]));
+      const uint32_t leader = tc::elect_one();
+      const uint32_t s_at = s_cols + s * kTile, o_at = o_cols + s * 128;
+      int turns = 0;                                        // s = 0 begins
+      auto my_turn = [&]() {
+        if (turns >= 1 - s) wait(sm.turn[s], turns - (1 - s));
+        ++turns;
+      };
+      auto pass = [&]() {
+        if (leader && ok) tc::mbar_arrive(tc::smem_u32(&sm.turn[1 - s]));
+        __syncwarp();
+      };
+      int tile0 = 0, uses = 0;                              // tiles before this piece, the half's steps so far
       for (int r = 0; turn(r) < items; ++r) {
         const Work w(plan, turn(r), G);
-        const int steps = w.wide ? 2 * w.tiles : w.tiles;   // step k is warpgroup k % 2's
-        wait(sm.q_full, r);
+        const int wide = uniform(w.wide), tiles = uniform(w.tiles), steps = wide ? 2 * tiles : tiles;   // step k is half k % 2's
+        auto tile_of = [&](int k) { return tile0 + (wide ? k >> 1 : k); };
         auto scores = [&](int k) {
-          const int tile = tile0 + (w.wide ? k >> 1 : k), s = k & 1;
-          wait(sm.k_full[tile & 1], tile >> 1);
-          if (!ok) return;
+          const int b = tile_of(k) & 1;
+          __syncwarp();
           tc::fence_after_sync();
-          const uint32_t q_at = tc::smem_u32(sm.q[w.wide ? s : 0]), k_at = tc::smem_u32(sm.k[tile & 1]);
+          const uint32_t q = q_at + (wide ? s * kBuffer : 0), kk = k_at + b * kBuffer, on = leader && ok;
 #pragma unroll
-          for (int e = 0; e < D / 16; ++e) tc::mma_f16_ss(s_cols + s * kTile, k_major(q_at, e), k_major(k_at, e), qk, e > 0);
-          tc::mma_commit(tc::smem_u32(&sm.s_ready[s]));
-          tc::mbar_arrive(tc::smem_u32(&sm.s_ready[s]));    // a release by this thread: it passes the scales on
-          if (!w.wide || s) tc::mma_commit(tc::smem_u32(&sm.k_free[tile & 1]));
+          for (int e = 0; e < D / 16; ++e)
+            tc::warp_mma_f16_ss(s_at, operand(q + (e >> 2) * kBlock + (e & 3) * 2), operand(kk + (e >> 2) * kBlock + (e & 3) * 2), qk, e > 0, on);
+          if (on) {
+            tc::mma_commit(tc::smem_u32(&sm.s_ready[s][b]));
+            tc::mbar_arrive(tc::smem_u32(&sm.s_ready[s][b]));   // a release by this thread: it passes the scales on
+          }
+          __syncwarp();
         };
-        scores(0);
-        if (steps > 1) scores(1);
-        for (int k = 0; k < steps; ++k) {
-          const int tile = tile0 + (w.wide ? k >> 1 : k), s = k & 1;
-          wait(sm.v_full[tile & 1], tile >> 1);
-          wait(sm.p_ready[s], count[s]++);
-          if (!ok) break;
+        auto product = [&](int k) {
+          const int b = tile_of(k) & 1;
+          wait(sm.v_full[b], tile_of(k) >> 1);
+          wait(sm.p_ready[s], uses++);
+          my_turn();
+          __syncwarp();
           tc::fence_after_sync();
-          const uint32_t v_at = tc::smem_u32(sm.v[tile & 1]);
+          const uint32_t v = v_at + b * kBuffer, on = leader && ok;
 #pragma unroll
-          for (int e = 0; e < kTile / 16; ++e)
-            tc::mma_f16_tmem_a(o_cols + s * 128, s_cols + s * kTile + 8 * e, n_major(v_at, e), pv, k > 1 || e > 0);
-          tc::mma_commit(tc::smem_u32(&sm.o_ready[s]));
-          if (!w.wide || s) tc::mma_commit(tc::smem_u32(&sm.v_free[tile & 1]));
+          for (int e = 0; e < kTile / 16; ++e) tc::warp_mma_f16_tmem_a(o_at, s_at + 8 * e, operand(v + e * (16 * 128 >> 4)), pv, k > 1 || e > 0, on);
+          if (on) tc::mma_commit(tc::smem_u32(&sm.o_ready[s][b]));
+          __syncwarp();
+        };
+        wait(sm.q_full, r);
+        if (s < steps) wait(sm.k_full[tile_of(s) & 1], tile_of(s) >> 1);
+        my_turn();
+        if (s < steps) scores(s);
+        pass();
+        for (int k = s; k < steps; k += 2) {
+          if (k + 2 < steps) wait(sm.k_full[tile_of(k + 2) & 1], tile_of(k + 2) >> 1);
+          product(k);
           if (k + 2 < steps) scores(k + 2);
+          pass();
         }
-        tile0 += w.tiles;
+        if (s == 1 && (steps & 1)) {                        // the other half has one more
+          my_turn();
+          pass();
+        }
+        tile0 += tiles;
       }
       // nothing of this CTA's is in flight when it ends
-      tc::mma_commit(tc::smem_u32(&sm.drained));
+      tc::warp_mma_commit(tc::smem_u32(&sm.drained), leader);
       if (!tc::mbar_wait(tc::smem_u32(&sm.drained), 0, kWaitLimit)) ok = false;
     }
-    __syncwarp();
-  } else if (warp >= 8) {
+  } else if (warp < 4 + kConvert / 32) {
     // ---------------- conversion: 16 codes to a thread and turn
     regs_down<kConvertRegs>();
-    constexpr int kLanes = D / 16, kTurns = kTile * kLanes / 128;
-    const int ct = tid - 256, row0 = ct / kLanes, c = ct % kLanes;
+    constexpr int kLanes = D / 16, kTurns = kTile * kLanes / kConvert;
+    const int ct = tid - 128, row0 = ct / kLanes, c = ct % kLanes;
     const bool swap = c & 4;                                // the second half's pieces in the other order: no bank conflict
     uint4 kr[kTurns], vr[kTurns];
-    float ks = 0.f, vs = 0.f;
+    float scale = 0.f;                                      // of position ct % 128: K's in the first warpgroup, V's in the other
     auto load = [&](const Work& w, int i, bool v) {
       const int p0 = (w.t0 + i) * kTile;
       const size_t at = a.c.row(w.st.slot, w.kh, p0);
@@ -229,14 +278,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       uint4* to = v ? vr : kr;
 #pragma unroll
       for (int u = 0; u < kTurns; ++u)
-        to[u] = u * (128 / kLanes) + row0 < left ? ldg_nc_v4(from + u * 2048) : make_uint4(0, 0, 0, 0);
-      if (v) vs = ct < left ? __ldg(a.c.Vs + at + ct) : 0.f;
-      else ks = ct < left ? __ldg(a.c.Ks + at + ct) : 0.f;
+        to[u] = u * (kConvert / kLanes) + row0 < left ? ldg_nc_v4(from + u * kConvert * 16) : make_uint4(0, 0, 0, 0);
+      if (!v) scale = (ct & 127) < left ? __ldg((ct < 128 ? a.c.Ks : a.c.Vs) + at + (ct & 127)) : 0.f;
     };
     auto convert = [&](uint8_t* to, const uint4 (&x)[kTurns]) {
 #pragma unroll
       for (int u = 0; u < kTurns; ++u) {
-        const int row = u * (128 / kLanes) + row0;
+        const int row = u * (kConvert / kLanes) + row0;
         uint32_t f[8];
         codes4<FMT>(x[u].x, f[0], f[1]);
         codes4<FMT>(x[u].y, f[2], f[3]);
@@ -247,6 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       }
     };
     int tile = 0;
+    // bit 2 half + buffer: the parity of the half's steps with the buffer so far; the buffer's tile was a step of the half
+    unsigned uses = 0, theirs = 0;
     for (int r = 0; turn(r) < items; ++r) {
       const Work w(plan, turn(r), G);
       const int own = w.st.len - w.st.n, all_see = own + (w.st.tree ? 0 : w.q0 / G + 1);   // positions that every row attends to
@@ -254,13 +304,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       load(w, 0, true);
       for (int i = 0; i < w.tiles; ++i, ++tile) {
         const int b = tile & 1, slot = tile & 3;
-        if (tile > 1) wait(sm.k_free[b], (tile >> 1) - 1);
-        sm.ks[slot][ct] = ks;
-        sm.vs[slot][ct] = vs;
-        sm.lg[slot][ct] = fmaxf(log2_fast(vs), -100.f);
+        // the buffer's last tile was a step of one half or of both: its scores (its products) have been made
+        auto free_again = [&](uint64_t (&done)[2][2]) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (theirs >> (2 * s + b) & 1) wait(done[s][b], (uses >> (2 * s + b) & 1) ^ 1);
+        };
+        free_again(sm.s_ready);
+        if (ct < 128) {
+          sm.ks[slot][ct] = scale;
+        } else {
+          sm.vs[slot][ct - 128] = scale;
+          sm.lg[slot][ct - 128] = fmaxf(log2_fast(scale), -100.f);
+        }
         if (FMT == BM_KV8_E4M3 && (w.t0 + i + 1) * kTile > all_see) {
           // some rows do not attend to some of these positions, and 0 * NaN is NaN: a NaN code becomes 0, and its position's scale NaN
-          sync_some(2, 128);
+          sync_some(2, kConvert);
 #pragma unroll
           for (int u = 0; u < kTurns; ++u) {
             uint32_t* x = reinterpret_cast<uint32_t*>(&vr[u]);
@@ -271,17 +330,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
               x[e] &= ~((nan >> 7) * 0xFFu);
               any |= nan;
             }
-            if (any) sm.vs[slot][u * (128 / kLanes) + row0] = __uint_as_float(0x7FC00000u);
+            if (any) sm.vs[slot][u * (kConvert / kLanes) + row0] = __uint_as_float(0x7FC00000u);
           }
         }
         convert(sm.k[b], kr);
         tc::fence_proxy_async_smem();
         arrive(sm.k_full[b]);
         if (i + 1 < w.tiles) load(w, i + 1, false);
-        if (tile > 1) wait(sm.v_free[b], (tile >> 1) - 1);
+        free_again(sm.o_ready);
         convert(sm.v[b], vr);
         tc::fence_proxy_async_smem();
         arrive(sm.v_full[b]);
+        const unsigned now = (w.wide ? 5u : 1u << (2 * (i & 1))) << b;
+        theirs = (theirs & ~(5u << b)) | now;
+        uses ^= now;
         if (i + 1 < w.tiles) load(w, i + 1, true);
       }
     }
@@ -289,37 +351,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     // ---------------- softmax: thread (g, t) of a warp has rows g, g + 8, g + 16, g + 24 of its 32 (index r) and positions
     // 8 j + 2 t and the next, j = 0 .. 15.
     regs_up<kSoftmaxRegs>();
-    const int s = warp >> 2, g = lane >> 2, t = lane & 3, wt = tid & 127;
+    const int s = (warp >> 2) - 1 - kConvert / 128, g = lane >> 2, t = lane & 3, wt = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, half = 16u << 16;
     const uint32_t s_at = s_cols + s * kTile + lanes, o_at = o_cols + s * 128 + lanes;
-    int count = 0, tile0 = 0;                               // this warpgroup's steps and the CTA's tiles so far
+    int tile0 = 0;                                          // the CTA's tiles so far
+    unsigned uses = 0, last = 0, last_use = 0;              // bit b: the parity of this half's steps with buffer b; the latest step's buffer, and that parity before it
+    auto products_done = [&]() { wait(sm.o_ready[s][last], last_use); };
     for (int turn_no = 0; turn(turn_no) < items; ++turn_no) {
       const Work w(plan, turn(turn_no), G);
       const int n_rows = w.st.n * G, own = w.st.len - w.st.n;
       sync_some(1, 256);                                    // both warpgroups are done with the piece before: its rows may go
-      // ---- the query rows as fp16 of about their own magnitude, d / 8 lanes to a row
+      // ---- the query rows as fp16 of about their own magnitude, d / 8 lanes to a row; a batch is asked for at once
       {
-        constexpr int kPieces = D / 8;
-        const int first = w.wide ? kSub * s : 64 * s, many = w.wide ? kSub : 64;
-        for (int u = wt; u < many * kPieces; u += 128) {
-          const int row = first + u / kPieces, c = u % kPieces, q = w.q0 + row, j = q / G;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (q < n_rows) x = *reinterpret_cast<const uint4*>(a.Q + ((size_t)(w.st.start + j) * a.qh + w.kh * G + q - j * G) * D + 8 * c);
-          const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-          float mx = 0.f, down, up;
+        constexpr int kPieces = D / 8, kStep = 128 / kPieces, kBatch = 64 / kStep;
+        const int c = wt % kPieces, first = (w.wide ? kSub * s : 64 * s) + wt / kPieces, end = first + (w.wide ? kSub : 64);
+        const bf16* from = a.Q + ((size_t)w.st.start * a.qh + w.kh * G) * D + 8 * c;
+        const float inv_g = 1.f / G;
+#pragma unroll 1
+        for (int row0 = first; row0 < end; row0 += kBatch * kStep) {
+          uint4 x[kBatch];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(in[e])), fabsf(bf_hi(in[e]))));
-#pragma unroll
-          for (int o = kPieces / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          row_scale(mx, down, up);
-          uint32_t f[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __half2 v = __floats2half2_rn(bf_lo(in[e]) * down, bf_hi(in[e]) * down);
-            f[e] = *reinterpret_cast<const uint32_t*>(&v);
+          for (int u = 0; u < kBatch; ++u) {
+            const int q = w.q0 + row0 + u * kStep, j = w.q0 / G + (int)((w.q0 % G + row0 + u * kStep + 0.5f) * inv_g);   // q / G: exact, as the rest is below 2^20
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (q < n_rows) x[u] = *reinterpret_cast<const uint4*>(from + ((size_t)j * a.qh + q - j * G) * D);
           }
-          *reinterpret_cast<uint4*>(sm.q[row >> 7] + piece(row & 127, c)) = make_uint4(f[0], f[1], f[2], f[3]);
-          if (c == 0) sm.up[row] = up;
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const int row = row0 + u * kStep;
+            const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            float mx = 0.f, down, up;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(in[e])), fabsf(bf_hi(in[e]))));
+#pragma unroll
+            for (int o = kPieces / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            row_scale(mx, down, up);
+            uint32_t f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 v = __floats2half2_rn(bf_lo(in[e]) * down, bf_hi(in[e]) * down);
+              f[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            *reinterpret_cast<uint4*>(sm.q[row >> 7] + piece(row & 127, c)) = make_uint4(f[0], f[1], f[2], f[3]);
+            if (c == 0) sm.up[row] = up;
+          }
         }
       }
       tc::fence_proxy_async_smem();
@@ -340,49 +415,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       }
       const int all_see = own + (w.st.tree ? 0 : (w.q0 + sub) / G + 1);   // positions that every row of this half attends to
       const int steps = w.wide ? w.tiles : (w.tiles + 1 - s) >> 1;
-      for (int it = 0; it < steps; ++it, ++count) {
-        const int i = w.wide ? it : 2 * it + s, slot = (tile0 + i) & 3, p0 = (w.t0 + i) * kTile + 2 * t;   // this thread's first position
-        wait(sm.s_ready[s], count);
+      for (int it = 0; it < steps; ++it) {
+        const int i = w.wide ? it : 2 * it + s, tile = tile0 + i, slot = tile & 3, p0 = (w.t0 + i) * kTile + 2 * t;   // this thread's first position
+        wait(sm.s_ready[s][tile & 1], uses >> (tile & 1) & 1);
         tc::fence_after_sync();
         const float *ks_at = sm.ks[slot] + 2 * t, *vs_at = sm.vs[slot] + 2 * t, *lg_at = sm.lg[slot] + 2 * t;
         auto pair = [](const float* of, int j) { return *reinterpret_cast<const uint64_t*>(of + 8 * j); };
-        // Scores of 32 positions, rows 2 h and 2 h + 1: v[h][4 j + 2 (r & 1) + e].
-        auto read = [&](int c, uint32_t (&v)[2][16]) {
-          tc::tmem_ld_frag32(s_at + 32 * c, v[0]);
-          tc::tmem_ld_frag32(s_at + half + 32 * c, v[1]);
+        // Scores of 16 positions, rows 2 h and 2 h + 1: v[h][4 j + 2 (r & 1) + e].
+        auto read = [&](int c, uint32_t (&v)[2][8]) {
+          tc::tmem_ld_frag16(s_at + 16 * c, v[0]);
+          tc::tmem_ld_frag16(s_at + half + 16 * c, v[1]);
         };
-        auto landed = [](uint32_t (&v)[2][16]) {            // nothing that was read is used before
+        auto landed = [](uint32_t (&v)[2][8]) {             // nothing that was read is used before
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v[0][e]), "+r"(v[1][e]));
+          for (int e = 0; e < 8; ++e) asm volatile("" : "+r"(v[0][e]), "+r"(v[1][e]));
         };
-        // ---- in one sweep against the present maxima, where every row attends to all of the tile
-        bool good = it > 0 && (w.t0 + i + 1) * kTile <= all_see;
-        if (good) {
-          uint32_t v[2][2][16], out[2][32];                 // out[pair of rows][2 j + (r & 1)]: weights of two positions
+        const bool masked = (w.t0 + i + 1) * kTile > all_see;
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};             // bit 2 j + e: position 8 j + e of this thread's is attended to
+        if (masked) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) see[r] = below(lim[r] - p0) | (bits[r] ? among(bits[r], p0 - own) : 0);
+        }
+        // ---- weights in one sweep against the present maxima; stored if none turned out too large
+        auto sweep = [&](auto partly) {
+          constexpr bool kPartly = decltype(partly)::value;
+          uint32_t v[2][2][8], out[2][32];                  // out[pair of rows][2 j + (r & 1)]: weights of two positions
           uint64_t sum[4] = {0, 0, 0, 0};
           __half2 top = __float2half2_rn(0.f);              // the largest
           read(0, v[0]);
           landed(v[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c < 3) read(c + 1, v[(c + 1) & 1]);
+          for (int c = 0; c < 8; ++c) {
+            if (c < 7) read(c + 1, v[(c + 1) & 1]);
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-              const int j = 4 * c + jj;
+            for (int jj = 0; jj < 2; ++jj) {
+              const int j = 2 * c + jj;
               const uint64_t ks = pair(ks_at, j), vs = pair(vs_at, j);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const uint32_t* x = &v[c & 1][r >> 1][4 * jj + 2 * (r & 1)];
                 const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
-                const uint64_t p = pack2(exp2_fast(first(e)), exp2_fast(second(e))), pv = mul2(p, vs);
+                uint64_t p = pack2(exp2_fast(first(e)), exp2_fast(second(e))), pv = mul2(p, vs);
+                if (kPartly) {                              // both: a scale that is not attended to may be NaN
+                  const bool s0 = see[r] >> (2 * j) & 1, s1 = see[r] >> (2 * j + 1) & 1;
+                  p = pack2(s0 ? first(p) : 0.f, s1 ? second(p) : 0.f);
+                  pv = pack2(s0 ? first(pv) : 0.f, s1 ? second(pv) : 0.f);
+                }
                 sum[r] = add2(sum[r], p);
                 const __half2 h2 = __floats2half2_rn(first(pv), second(pv));
                 out[r >> 1][2 * j + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
                 top = __hmax2(top, h2);
               }
             }
-            if (c < 3) landed(v[(c + 1) & 1]);
+            if (c < 7) landed(v[(c + 1) & 1]);
           }
           float sums[4], most = 0.f;
 #pragma unroll
@@ -391,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
             most = fmaxf(most, sums[r]);
           }
           // a sum by itself too: where V is zero the weight is, or NaN, whatever p is
-          good = __all_sync(0xffffffffu, fmaxf(__low2float(top), __high2float(top)) <= kLargest && most < kLargestSum);
+          const bool good = __all_sync(0xffffffffu, fmaxf(__low2float(top), __high2float(top)) <= kLargest && most < kLargestSum);
           if (good) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) l[r] += sums[r];
@@ -400,42 +486,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
 #pragma unroll
               for (int c = 0; c < 2; ++c) tc::tmem_st_pairs32(s_at + h * half + 32 * c, *reinterpret_cast<const uint32_t(*)[16]>(&out[h][16 * c]));
           }
-        }
-        // ---- in two: the rows' maxima of score + log2 of V's scale, then the weights against them
-        if (!good) {
-          uint32_t see[4];                                  // bit 2 j + e: position 8 j + e of this thread's is attended to
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int left = lim[r] - p0, k = left <= 0 ? 0 : 2 * (left >> 3) + min(left & 7, 2);
-            see[r] = k >= 32 ? 0xffffffffu : (1u << k) - 1;
-            if (bits[r] != 0) {
-#pragma unroll 1
-              for (int k = 0; k < 32; ++k) {
-                const unsigned of = (unsigned)(p0 + 8 * (k >> 1) + (k & 1) - own);
-                if (of < 64u && (bits[r] >> of & 1)) see[r] |= 1u << k;
-              }
-            }
-          }
-          // A score in two roundings: a maximum is one of the scores, and none lies above it by the product's own rounding.
-          auto score = [&](const uint32_t (&v)[2][16], int r, int jj, int e, float ks) {
-            return __fmul_rn(__fmul_rn(__uint_as_float(v[r >> 1][4 * jj + 2 * (r & 1) + e]), ks), qf[r]);
-          };
-          float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f}, f[4];
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[2][16];
-            read(c, v);
-            landed(v);
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float ks = ks_at[32 * c + 8 * jj + e], lg = lg_at[32 * c + 8 * jj + e];
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  if (see[r] >> (8 * c + 2 * jj + e) & 1) mx[r] = fmaxf(mx[r], __fadd_rn(score(v, r, jj, e, ks), lg));
-              }
-          }
+          return good;
+        };
+        // ---- the rows' maxima of score + log2 of V's scale, of the tile's first `many` positions, and what goes by them
+        auto move = [&](float (&mx)[4]) {
+          float f[4];
           bool moves = false;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {                     // each row by itself: its neighbours stand elsewhere in another step
@@ -448,35 +503,93 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
             m[r] = mn;
           }
           if (it > 0 && __any_sync(0xffffffffu, moves)) {   // O holds the tiles before
-            wait(sm.o_ready[s], count - 1);
+            products_done();
             tc::fence_after_sync();
 #pragma unroll 1
-            for (int c = 0; c < 2 * D; c += 32) {           // both pairs of rows
-              const int h = c >= D;
-              uint32_t o[16];
-              tc::tmem_ld_frag32(o_at + h * half + (c - h * D), o);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[2][16];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) tc::tmem_ld_frag32(o_at + h * half + c, o[h]);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[e]));
-              const float f0 = h ? f[2] : f[0], f1 = h ? f[3] : f[1];
+              for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? f1 : f0));
-              tc::tmem_st_frag32(o_at + h * half + (c - h * D), o);
+                for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[h][e]));
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[h][e] = __float_as_uint(__uint_as_float(o[h][e]) * f[2 * h + (e >> 1 & 1)]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) tc::tmem_st_frag32(o_at + h * half + c, o[h]);
             }
           }
-          float sum[4] = {};
+        };
+        auto maxima = [&](int many) {
+          float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {                     // weights go where scores of an earlier turn were, or this one's
-            uint32_t v[2][16], out[2][8];
+          for (int c = 0; c < many / 16; c += 2) {
+            uint32_t v[2][2][8];
+            read(c, v[0]);
+            read(c + 1, v[1]);
+            landed(v[0]);
+            landed(v[1]);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+              const uint64_t ks = pair(ks_at + 16 * c, jj), lg = pair(lg_at + 16 * c, jj);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const uint32_t* x = &v[jj >> 1][r >> 1][4 * (jj & 1) + 2 * (r & 1)];
+                const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), lg);
+                if (see[r] >> (4 * c + 2 * jj) & 1) mx[r] = fmaxf(mx[r], first(e));
+                if (see[r] >> (4 * c + 2 * jj + 1) & 1) mx[r] = fmaxf(mx[r], second(e));
+              }
+            }
+          }
+          move(mx);
+        };
+        // A quarter's maxima will do to begin with: the sweep notices if they do not.
+        bool good = false;
+#pragma unroll 1
+        for (int many = it == 0 ? 32 : 0; !good && many <= kTile; many = many < kTile ? kTile : kTile + 1) {
+          if (many) maxima(many);
+          good = masked ? sweep(std::true_type()) : sweep(std::false_type());
+        }
+        // ---- or, where scores are so large that fp32's steps between them matter, in two roundings throughout
+        if (!good) {
+          // A score in two roundings: a maximum is one of the scores, and none lies above it by the product's own rounding.
+          auto score = [&](const uint32_t (&v)[2][8], int r, int jj, int e, float ks) {
+            return __fmul_rn(__fmul_rn(__uint_as_float(v[r >> 1][4 * jj + 2 * (r & 1) + e]), ks), qf[r]);
+          };
+          float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[2][8];
             read(c, v);
             landed(v);
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-              const float2 ks = *reinterpret_cast<const float2*>(ks_at + 32 * c + 8 * jj), vs = *reinterpret_cast<const float2*>(vs_at + 32 * c + 8 * jj);
+            for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float ks = ks_at[16 * c + 8 * jj + e], lg = lg_at[16 * c + 8 * jj + e];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  if (see[r] >> (4 * c + 2 * jj + e) & 1) mx[r] = fmaxf(mx[r], __fadd_rn(score(v, r, jj, e, ks), lg));
+              }
+          }
+          move(mx);
+          float sum[4] = {};
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {                     // weights go where scores of an earlier turn were, or this one's
+            uint32_t v[2][8], out[2][4];
+            read(c, v);
+            landed(v);
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+              const float2 ks = *reinterpret_cast<const float2*>(ks_at + 16 * c + 8 * jj), vs = *reinterpret_cast<const float2*>(vs_at + 16 * c + 8 * jj);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 // the product is selected too: a scale that is not attended to may be NaN
-                const uint32_t here = see[r] >> (8 * c + 2 * jj);
+                const uint32_t here = see[r] >> (4 * c + 2 * jj);
                 const float x0 = exp2_fast(__fadd_rn(score(v, r, jj, 0, ks.x), -m[r])), x1 = exp2_fast(__fadd_rn(score(v, r, jj, 1, ks.y), -m[r]));
                 const float y0 = here & 1 ? x0 : 0.f, y1 = here & 2 ? x1 : 0.f;
                 sum[r] += y0 + y1;
@@ -484,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
                 out[r >> 1][2 * jj + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
               }
             }
-            tc::tmem_st_frag16(s_at + 16 * c, out[0]);
-            tc::tmem_st_frag16(s_at + half + 16 * c, out[1]);
+            tc::tmem_st_pairs8(s_at + 8 * c, out[0]);
+            tc::tmem_st_pairs8(s_at + half + 8 * c, out[1]);
           }
 #pragma unroll
           for (int r = 0; r < 4; ++r) l[r] += sum[r];
@@ -493,11 +606,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
         tc::tmem_wait_st();
         tc::fence_before_sync();
         arrive(sm.p_ready[s]);
+        last = tile & 1;
+        last_use = uses >> last & 1;
+        uses ^= 1u << last;
       }
       tile0 += w.tiles;
 
       // ---- the rows' outputs, or this piece's records
-      if (steps > 0) wait(sm.o_ready[s], count - 1);
+      if (steps > 0) products_done();
       tc::fence_after_sync();
       float f0[4], f1[4];                                   // factors of this warpgroup's sums, and of the other's
 #pragma unroll
@@ -620,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 12) tc::tmem_dealloc(s_cols, kTmemCols);
+  if (warp == 0) tc::tmem_dealloc(s_cols, kTmemCols);
   if (sm.gave_up) {                                         // NaN in all rows of this CTA's pieces
     for (int r = 0; turn(r) < items; ++r) {
       const Work w(plan, turn(r), G);
