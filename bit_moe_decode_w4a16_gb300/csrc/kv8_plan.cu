@@ -218,8 +218,9 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   if (tid == 0) a.row_start[B] = (int)min(total, (long long)T);
   long long items, units, records;
   const int from = (int)scan_before(pieces, sm.sums, &items);
-  st.unit = (int)scan_before(st.most > 1 ? (long long)st.n * a.qh : 0, sm.sums, &units);
-  st.rec = scan_before(st.most > 1 ? (long long)st.n * a.qh * st.most : 0, sm.sums, &records);
+  const long long slabs = st.most > 1 ? ((long long)st.n * G + 15) / 16 * a.kvh : 0;
+  st.unit = (int)scan_before(slabs, sm.sums, &units);
+  st.rec = scan_before(slabs * st.most, sm.sums, &records);
   if (tid < B) {
     plan.streams[tid] = st;
     sm.from[tid] = from;

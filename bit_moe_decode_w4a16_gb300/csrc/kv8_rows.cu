@@ -42,8 +42,8 @@ struct RowsArgs {
   const void* plan;
   const bf16* Q;
   bf16* O;
-  float* rec_o;        // records: unnormalised output [d]
-  float2* rec_ml;      // and its maximum and sum
+  float4* rec_o;       // records of 16 rows: unnormalised outputs [d / 32][4][lane], in the order in which a warp holds them
+  float2* rec_ml;      // [16] their maxima and sums
   int B, T, qh;
   float scale_log2;
 };
@@ -68,8 +68,13 @@ struct RowsSmem {
   uint8_t k[2][kTile * D * 2], v[2][kTile * D * 2];         // [d / 64][position][64]
   // scales and log2 of V's, of four tiles: they are written with a tile's K, when the softmax may be two tiles back
   float ks[4][kTile], vs[4][kTile], lg[4][kTile];
-  float up[kBlockRows];
-  float m[kSub], l[kSub];                                   // of the second warpgroup, where both have the same rows
+  // of the query rows of this piece and of the next: the factor that its scores are short of, its place among all heads of all rows
+  // (-1: none), below which position it attends to all, and which of the step's own rows it attends to besides
+  float up[2][kBlockRows];
+  int to[2][kBlockRows], lim[2][kBlockRows];
+  unsigned long long bits[2][kBlockRows];
+  float m[kSub], l[kSub];                                   // of the second warpgroup, where both have the same rows,
+  float other[kSub / 4 * kSub];                             // and 32 columns of its outputs
   uint64_t k_full[2], v_full[2];                            // by the tile's parity
   uint64_t s_ready[2][2], o_ready[2][2];                    // by half and the tile's parity: they also say that K, V may be overwritten
   uint64_t p_ready[2], turn[2];                             // by half
@@ -97,7 +102,36 @@ __device__ __forceinline__ void regs_down() {
 }
 __device__ __forceinline__ void sync_some(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t join(uint32_t lo, uint32_t hi) { return (uint64_t)lo | (uint64_t)hi << 32; }
+
+// A row's 32 elements, of which thread t of its four has x[4 j + e], element 8 j + 2 t + e: scaled and rounded to bf16, and turned among
+// the four so that thread t gets elements 8 t .. 8 t + 7.
+__device__ __forceinline__ uint4 rounded_row(const float* x, float by, int t) {
+  uint32_t p[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[4 * j] * by, x[4 * j + 1] * by);
+    p[j] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; j += 2) {
+    const uint32_t back = __shfl_xor_sync(0xffffffffu, t & 1 ? p[j] : p[j + 1], 1);
+    if (t & 1) p[j] = back;
+    else p[j + 1] = back;
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t back = __shfl_xor_sync(0xffffffffu, t & 2 ? p[j] : p[j + 2], 2);
+    if (t & 2) p[j] = back;
+    else p[j + 2] = back;
+  }
+  return make_uint4(p[0], p[1], p[2], p[3]);
+}
 
 // Of a thread's positions 8 j + e (j < 16, e < 2), as bits 2 j + e: those below `left`; and those whose bit (offset + 8 j + e) of `bits` is set.
 __device__ __forceinline__ uint32_t below(int left) {
@@ -241,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
           if (on) tc::mma_commit(tc::smem_u32(&sm.o_ready[s][b]));
           __syncwarp();
         };
-        wait(sm.q_full, r);
+        if (s < steps) wait(sm.q_full, r);
         if (s < steps) wait(sm.k_full[tile_of(s) & 1], tile_of(s) >> 1);
         my_turn();
         if (s < steps) scores(s);
@@ -357,251 +391,336 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     int tile0 = 0;                                          // the CTA's tiles so far
     unsigned uses = 0, last = 0, last_use = 0;              // bit b: the parity of this half's steps with buffer b; the latest step's buffer, and that parity before it
     auto products_done = [&]() { wait(sm.o_ready[s][last], last_use); };
-    for (int turn_no = 0; turn(turn_no) < items; ++turn_no) {
-      const Work w(plan, turn(turn_no), G);
-      const int n_rows = w.st.n * G, own = w.st.len - w.st.n;
-      sync_some(1, 256);                                    // both warpgroups are done with the piece before: its rows may go
-      // ---- the query rows as fp16 of about their own magnitude, d / 8 lanes to a row; a batch is asked for at once
-      {
-        constexpr int kPieces = D / 8, kStep = 128 / kPieces, kBatch = 64 / kStep;
-        const int c = wt % kPieces, first = (w.wide ? kSub * s : 64 * s) + wt / kPieces, end = first + (w.wide ? kSub : 64);
-        const bf16* from = a.Q + ((size_t)w.st.start * a.qh + w.kh * G) * D + 8 * c;
-        const float inv_g = 1.f / G;
-#pragma unroll 1
-        for (int row0 = first; row0 < end; row0 += kBatch * kStep) {
-          uint4 x[kBatch];
+    // ---- a block's query rows as fp16 of about their own magnitude, d / 8 lanes to a row; half of this warpgroup's are asked for while
+    // the piece before ends
+    constexpr int kPieces = D / 8, kStep = 128 / kPieces, kBatch = 64 / kStep;
+    const float inv_g = 1.f / G;
+    uint4 x[kBatch];
+    auto ask = [&](const Work& w, int row0) {
+      const int c = wt % kPieces, j0 = w.q0 / G, rest = w.q0 - j0 * G;
+      const bf16* from = a.Q + ((size_t)w.st.start * a.qh + w.kh * G) * D + 8 * c;
 #pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            const int q = w.q0 + row0 + u * kStep, j = w.q0 / G + (int)((w.q0 % G + row0 + u * kStep + 0.5f) * inv_g);   // q / G: exact, as the rest is below 2^20
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (q < n_rows) x[u] = *reinterpret_cast<const uint4*>(from + ((size_t)j * a.qh + q - j * G) * D);
-          }
+      for (int u = 0; u < kBatch; ++u) {
+        const int row = row0 + wt / kPieces + u * kStep, q = w.q0 + row, j = j0 + (int)((rest + row + 0.5f) * inv_g);   // q / G: the quotient's argument is below 2^9
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (q < w.st.n * G) x[u] = *reinterpret_cast<const uint4*>(from + ((size_t)j * a.qh + q - j * G) * D);
+      }
+    };
+    auto place = [&](const Work& w, int row0, int slot) {
+      const int c = wt % kPieces, j0 = w.q0 / G, rest = w.q0 - j0 * G, own = w.st.len - w.st.n;
 #pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            const int row = row0 + u * kStep;
-            const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-            float mx = 0.f, down, up;
+      for (int u = 0; u < kBatch; ++u) {
+        const int row = row0 + wt / kPieces + u * kStep;
+        const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t mx2 = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(in[e])), fabsf(bf_hi(in[e]))));
+        for (int e = 0; e < 4; ++e) mx2 = max_bf16x2(mx2, in[e] & 0x7FFF7FFFu);
 #pragma unroll
-            for (int o = kPieces / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            row_scale(mx, down, up);
-            uint32_t f[4];
+        for (int o = kPieces / 2; o > 0; o >>= 1) mx2 = max_bf16x2(mx2, __shfl_xor_sync(0xffffffffu, mx2, o));
+        float down, up;
+        row_scale(fmaxf(bf_lo(mx2), bf_hi(mx2)), down, up);
+        uint32_t f[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __half2 v = __floats2half2_rn(bf_lo(in[e]) * down, bf_hi(in[e]) * down);
-              f[e] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            *reinterpret_cast<uint4*>(sm.q[row >> 7] + piece(row & 127, c)) = make_uint4(f[0], f[1], f[2], f[3]);
-            if (c == 0) sm.up[row] = up;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t y = mul2(pack2(bf_lo(in[e]), bf_hi(in[e])), pack2(down, down));
+          const __half2 v = __floats2half2_rn(first(y), second(y));
+          f[e] = *reinterpret_cast<const uint32_t*>(&v);
         }
+        *reinterpret_cast<uint4*>(sm.q[row >> 7] + piece(row & 127, c)) = make_uint4(f[0], f[1], f[2], f[3]);
+        if (c == 0) sm.up[slot][row] = up;
+      }
+      // a row to a thread: what else there is to know of it
+      if (wt < 64) {
+        const int row = row0 + wt, q = w.q0 + row, j = j0 + (int)((rest + row + 0.5f) * inv_g);
+        const bool live = q < w.st.n * G;
+        sm.to[slot][row] = live ? (w.st.start + j) * a.qh + w.kh * G + q - j * G : -1;
+        sm.lim[slot][row] = w.st.tree ? own : own + j + 1;
+        sm.bits[slot][row] = live && w.st.tree ? plan.masks[w.st.start + j] : 0;
+      }
+    };
+    // All rows of the halves in use are written, whatever the block's own: 128 of this half's, or 64 of the half that both share.
+    auto first_row = [&](const Work& w) { return w.wide ? kSub * s : 64 * s; };
+    auto place_all = [&](const Work& w, int slot) {
+      place(w, first_row(w), slot);
+      if (w.wide) {
+        ask(w, first_row(w) + 64);
+        place(w, first_row(w) + 64, slot);
       }
       tc::fence_proxy_async_smem();
       arrive(sm.q_full);
-      sync_some(1, 256);
-      const int sub = w.wide ? kSub * s : 0, row = 32 * (warp & 3) + g;   // this thread's rows: sub + row + 8 r
+    };
+    {
+      const Work w(plan, turn(0), G);
+      ask(w, first_row(w));
+      place_all(w, 0);
+    }
+    const int row = 32 * (warp & 3) + g;                    // this thread's rows of its half: row + 8 r
+    for (int turn_no = 0; turn(turn_no) < items; ++turn_no) {
+      // A piece's fields are read where they are needed (from L1) rather than held: the tiles' loop needs the registers.
+      bool wide;
+      int tiles, t0, lowest, highest;                       // below `lowest` all of the warp's rows attend to, from `highest` on none does
+      {
+        const Work w(plan, turn(turn_no), G);
+        wide = w.wide;
+        tiles = w.tiles;
+        t0 = w.t0;
+        const int own = w.st.len - w.st.n, row_a = w.q0 + (wide ? kSub * s : 0) + 32 * (warp & 3), row_z = min(row_a + 31, w.st.n * G - 1);
+        lowest = own + (w.st.tree ? 0 : row_a / G + 1);
+        highest = row_z < row_a ? 0 : own + (w.st.tree ? min(w.st.n, kDrafts) : row_z / G + 1);
+      }
+      const int info = turn_no & 1, mine_at = (wide ? kSub * s : 0) + row;
       float qf[4], m[4], l[4];
-      int lim[4];                                           // positions below it are attended to,
-      unsigned long long bits[4];                           // and of the step's own rows these
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int q = w.q0 + sub + row + 8 * r;
-        qf[r] = a.scale_log2 * sm.up[sub + row + 8 * r];
         m[r] = -1e30f;
         l[r] = 0.f;
-        lim[r] = q >= n_rows ? 0 : w.st.tree ? own : own + q / G + 1;
-        bits[r] = q < n_rows && w.st.tree ? plan.masks[w.st.start + q / G] : 0;
       }
-      const int all_see = own + (w.st.tree ? 0 : (w.q0 + sub) / G + 1);   // positions that every row of this half attends to
-      const int steps = w.wide ? w.tiles : (w.tiles + 1 - s) >> 1;
+      const int steps = wide ? tiles : (tiles + 1 - s) >> 1;
       for (int it = 0; it < steps; ++it) {
-        const int i = w.wide ? it : 2 * it + s, tile = tile0 + i, slot = tile & 3, p0 = (w.t0 + i) * kTile + 2 * t;   // this thread's first position
+        const int i = wide ? it : 2 * it + s, tile = tile0 + i, slot = tile & 3, p0 = (t0 + i) * kTile + 2 * t;   // this thread's first position
         wait(sm.s_ready[s][tile & 1], uses >> (tile & 1) & 1);
         tc::fence_after_sync();
+        if (it == 0) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) qf[r] = a.scale_log2 * sm.up[info][mine_at + 8 * r];
+        }
         const float *ks_at = sm.ks[slot] + 2 * t, *vs_at = sm.vs[slot] + 2 * t, *lg_at = sm.lg[slot] + 2 * t;
         auto pair = [](const float* of, int j) { return *reinterpret_cast<const uint64_t*>(of + 8 * j); };
-        // Scores of 16 positions, rows 2 h and 2 h + 1: v[h][4 j + 2 (r & 1) + e].
-        auto read = [&](int c, uint32_t (&v)[2][8]) {
-          tc::tmem_ld_frag16(s_at + 16 * c, v[0]);
-          tc::tmem_ld_frag16(s_at + half + 16 * c, v[1]);
+        // Scores of 32 positions, rows 2 h and 2 h + 1: v[h][4 j + 2 (r & 1) + e].
+        auto read = [&](int c, uint32_t (&v)[2][16]) {
+          tc::tmem_ld_frag32(s_at + 32 * c, v[0]);
+          tc::tmem_ld_frag32(s_at + half + 32 * c, v[1]);
         };
-        auto landed = [](uint32_t (&v)[2][8]) {             // nothing that was read is used before
+        auto landed = [](auto& v) {                         // nothing that was read is used before
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) asm volatile("" : "+r"(v[0][e]), "+r"(v[1][e]));
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (auto& x : v[h]) asm volatile("" : "+r"(x));
         };
-        const bool masked = (w.t0 + i + 1) * kTile > all_see;
+        // of this tile's positions; a row that ends among them has bits of its own
+        const int lo = lowest - (t0 + i) * kTile, hi = highest - (t0 + i) * kTile;
         uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};             // bit 2 j + e: position 8 j + e of this thread's is attended to
-        if (masked) {
+        if (lo < kTile) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) see[r] = below(lim[r] - p0) | (bits[r] ? among(bits[r], p0 - own) : 0);
-        }
-        // ---- weights in one sweep against the present maxima; stored if none turned out too large
-        auto sweep = [&](auto partly) {
-          constexpr bool kPartly = decltype(partly)::value;
-          uint32_t v[2][2][8], out[2][32];                  // out[pair of rows][2 j + (r & 1)]: weights of two positions
-          uint64_t sum[4] = {0, 0, 0, 0};
-          __half2 top = __float2half2_rn(0.f);              // the largest
-          read(0, v[0]);
-          landed(v[0]);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (c < 7) read(c + 1, v[(c + 1) & 1]);
-#pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-              const int j = 2 * c + jj;
-              const uint64_t ks = pair(ks_at, j), vs = pair(vs_at, j);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const uint32_t* x = &v[c & 1][r >> 1][4 * jj + 2 * (r & 1)];
-                const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
-                uint64_t p = pack2(exp2_fast(first(e)), exp2_fast(second(e))), pv = mul2(p, vs);
-                if (kPartly) {                              // both: a scale that is not attended to may be NaN
-                  const bool s0 = see[r] >> (2 * j) & 1, s1 = see[r] >> (2 * j + 1) & 1;
-                  p = pack2(s0 ? first(p) : 0.f, s1 ? second(p) : 0.f);
-                  pv = pack2(s0 ? first(pv) : 0.f, s1 ? second(pv) : 0.f);
-                }
-                sum[r] = add2(sum[r], p);
-                const __half2 h2 = __floats2half2_rn(first(pv), second(pv));
-                out[r >> 1][2 * j + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
-                top = __hmax2(top, h2);
-              }
-            }
-            if (c < 7) landed(v[(c + 1) & 1]);
+          for (int r = 0; r < 4; ++r) {
+            const int lim = sm.lim[info][mine_at + 8 * r];
+            const unsigned long long bits = sm.bits[info][mine_at + 8 * r];
+            see[r] = below(lim - p0);
+            if (bits) see[r] |= among(bits, p0 - lim);      // a tree's rows attend to all before the step's own
           }
+        }
+        // None of them too large, nor a sum by itself (where V is zero the weight is, or NaN, whatever p is): the sums are kept.
+        auto keep = [&](const uint64_t (&sum)[4], __half2 top) {
           float sums[4], most = 0.f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             sums[r] = first(sum[r]) + second(sum[r]);
             most = fmaxf(most, sums[r]);
           }
-          // a sum by itself too: where V is zero the weight is, or NaN, whatever p is
           const bool good = __all_sync(0xffffffffu, fmaxf(__low2float(top), __high2float(top)) <= kLargest && most < kLargestSum);
           if (good) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) l[r] += sums[r];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) tc::tmem_st_pairs32(s_at + h * half + 32 * c, *reinterpret_cast<const uint32_t(*)[16]>(&out[h][16 * c]));
           }
           return good;
         };
-        // ---- the rows' maxima of score + log2 of V's scale, of the tile's first `many` positions, and what goes by them
-        auto move = [&](float (&mx)[4]) {
+        // Weights of 32 positions against the present maxima.
+        auto weights = [&](int c, const uint32_t (&v)[2][16], uint32_t (&out)[2][8]) {
+          uint64_t sum[4] = {0, 0, 0, 0};
+          __half2 top = __float2half2_rn(0.f);
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            const uint64_t ks = pair(ks_at + 32 * c, jj), vs = pair(vs_at + 32 * c, jj);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t* x = &v[r >> 1][4 * jj + 2 * (r & 1)];
+              const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
+              uint64_t p = pack2(exp2_fast(first(e)), exp2_fast(second(e))), pv = mul2(p, vs);
+              // both: a scale that is not attended to may be NaN
+              const bool s0 = see[r] >> (8 * c + 2 * jj) & 1, s1 = see[r] >> (8 * c + 2 * jj + 1) & 1;
+              p = pack2(s0 ? first(p) : 0.f, s1 ? second(p) : 0.f);
+              pv = pack2(s0 ? first(pv) : 0.f, s1 ? second(pv) : 0.f);
+              sum[r] = add2(sum[r], p);
+              const __half2 h2 = __floats2half2_rn(first(pv), second(pv));
+              out[r >> 1][2 * jj + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
+              top = __hmax2(top, h2);
+            }
+          }
+          return keep(sum, top);
+        };
+        // Weights go where scores were read: 32 positions' into 16 columns.
+        auto put = [&](int c, const uint32_t (&out)[2][8]) {
+          tc::tmem_st_frag16(s_at + 16 * c, out[0]);
+          tc::tmem_st_frag16(s_at + half + 16 * c, out[1]);
+        };
+        // Maxima that have risen by more than 2^8 are moved there, by whole powers of two once there is one, so that the weights of the
+        // tile's positions before 32 c, which are made already, scale exactly.
+        auto move = [&](int c, float (&mx)[4]) {
           float f[4];
           bool moves = false;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {                     // each row by itself: its neighbours stand elsewhere in another step
+          for (int r = 0; r < 4; ++r) {
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-            const float mn = mx[r] > m[r] + 8.f ? mx[r] : m[r];
-            moves |= mn != m[r];
-            f[r] = exp2_fast(m[r] - mn);
-            l[r] = scaled_down(l[r], m[r] - mn);
-            m[r] = mn;
+            f[r] = 1.f;
+            if (mx[r] > m[r] + 8.f) {                       // each row by itself: its neighbours stand elsewhere in another step
+              const float by = m[r] == -1e30f ? 0.f : fminf(ceilf(mx[r] - m[r]), 200.f);
+              f[r] = by == 0.f || by > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)by) << 23);
+              const float mn = by == 0.f || by == 200.f ? mx[r] : fmaxf(m[r] + by, mx[r]);
+              l[r] = scaled_down(l[r], m[r] - mn);
+              m[r] = mn;
+              moves = true;
+            }
           }
-          if (it > 0 && __any_sync(0xffffffffu, moves)) {   // O holds the tiles before
+          if (!__any_sync(0xffffffffu, moves) || it + c == 0) return;
+          if (it > 0) {                                     // O holds the tiles before
             products_done();
             tc::fence_after_sync();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[2][16];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) tc::tmem_ld_frag32(o_at + h * half + c, o[h]);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t at = o_at + (k & 1 ? half : 0) + 32 * (k >> 1);
+              const float fa = k & 1 ? f[2] : f[0], fb = k & 1 ? f[3] : f[1];
+              uint32_t o[16];
+              tc::tmem_ld_frag32(at, o);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+              for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[e]));
 #pragma unroll
-                for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[h][e]));
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[h][e] = __float_as_uint(__uint_as_float(o[h][e]) * f[2 * h + (e >> 1 & 1)]);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) tc::tmem_st_frag32(o_at + h * half + c, o[h]);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? fb : fa));
+              tc::tmem_st_frag32(at, o);
             }
           }
-        };
-        auto maxima = [&](int many) {
-          float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
+          tc::tmem_wait_st();
 #pragma unroll 1
-          for (int c = 0; c < many / 16; c += 2) {
-            uint32_t v[2][2][8];
-            read(c, v[0]);
-            read(c + 1, v[1]);
-            landed(v[0]);
-            landed(v[1]);
+          for (int k = 0; k < 4 * c; ++k) {
+            const uint32_t at = s_at + (k & 1 ? half : 0) + 8 * (k >> 1);
+            const __half2 fa = __float2half2_rn(k & 1 ? f[2] : f[0]), fb = __float2half2_rn(k & 1 ? f[3] : f[1]);
+            uint32_t p[4];
+            tc::tmem_ld_pairs8(at, p);
+            tc::tmem_wait_ld();
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-              const uint64_t ks = pair(ks_at + 16 * c, jj), lg = pair(lg_at + 16 * c, jj);
+            for (int e = 0; e < 4; ++e) {
+              asm volatile("" : "+r"(p[e]));
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&p[e]), e & 1 ? fb : fa);
+              p[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            tc::tmem_st_pairs8(at, p);
+          }
+        };
+        // The maxima of score + log2 of V's scale.
+        auto maxima = [&](int c, const uint32_t (&v)[2][16]) {
+          float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const uint32_t* x = &v[jj >> 1][r >> 1][4 * (jj & 1) + 2 * (r & 1)];
-                const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), lg);
-                if (see[r] >> (4 * c + 2 * jj) & 1) mx[r] = fmaxf(mx[r], first(e));
-                if (see[r] >> (4 * c + 2 * jj + 1) & 1) mx[r] = fmaxf(mx[r], second(e));
-              }
+          for (int jj = 0; jj < 4; ++jj) {
+            const uint64_t ks = pair(ks_at + 32 * c, jj), lg = pair(lg_at + 32 * c, jj);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t* x = &v[r >> 1][4 * jj + 2 * (r & 1)];
+              const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), lg);
+              if (see[r] >> (8 * c + 2 * jj) & 1) mx[r] = fmaxf(mx[r], first(e));
+              if (see[r] >> (8 * c + 2 * jj + 1) & 1) mx[r] = fmaxf(mx[r], second(e));
             }
           }
-          move(mx);
+          move(c, mx);
         };
-        // A quarter's maxima will do to begin with: the sweep notices if they do not.
-        bool good = false;
-#pragma unroll 1
-        for (int many = it == 0 ? 32 : 0; !good && many <= kTile; many = many < kTile ? kTile : kTile + 1) {
-          if (many) maxima(many);
-          good = masked ? sweep(std::true_type()) : sweep(std::false_type());
-        }
-        // ---- or, where scores are so large that fp32's steps between them matter, in two roundings throughout
-        if (!good) {
-          // A score in two roundings: a maximum is one of the scores, and none lies above it by the product's own rounding.
-          auto score = [&](const uint32_t (&v)[2][8], int r, int jj, int e, float ks) {
-            return __fmul_rn(__fmul_rn(__uint_as_float(v[r >> 1][4 * jj + 2 * (r & 1) + e]), ks), qf[r]);
-          };
+        // Where scores are so large that fp32's steps between them matter, 8 positions at a time: products and differences rounded one
+        // by one, so that a maximum is one of the scores and none lies above it by its product's own rounding.
+        auto exact = [&](int c) {
           float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t v[2][8];
-            read(c, v);
+          for (int k = 0; k < 8; ++k) {                     // maxima, then weights
+            if (k == 4) move(c, mx);
+            const int j = 4 * c + (k & 3);
+            uint32_t v[2][4], out[2][2];
+            tc::tmem_ld_frag8(s_at + 8 * j, v[0]);
+            tc::tmem_ld_frag8(s_at + half + 8 * j, v[1]);
             landed(v);
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj)
+            for (int r = 0; r < 4; ++r) {
+              float z[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float ks = ks_at[16 * c + 8 * jj + e], lg = lg_at[16 * c + 8 * jj + e];
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  if (see[r] >> (4 * c + 2 * jj + e) & 1) mx[r] = fmaxf(mx[r], __fadd_rn(score(v, r, jj, e, ks), lg));
+                const bool here = see[r] >> (2 * j + e) & 1;
+                const float y = __fmul_rn(__fmul_rn(__uint_as_float(v[r >> 1][2 * (r & 1) + e]), ks_at[8 * j + e]), qf[r]), p = exp2_fast(__fadd_rn(y, -m[r]));
+                if (k < 4 && here) mx[r] = fmaxf(mx[r], __fadd_rn(y, lg_at[8 * j + e]));
+                if (k >= 4 && here) l[r] += p;
+                z[e] = here ? p * vs_at[8 * j + e] : 0.f;
               }
+              const __half2 h2 = __floats2half2_rn(z[0], z[1]);
+              out[r >> 1][r & 1] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            if (k >= 4) {
+              tc::tmem_st_pairs4(s_at + 4 * j, out[0]);
+              tc::tmem_st_pairs4(s_at + half + 4 * j, out[1]);
+            }
           }
-          move(mx);
-          float sum[4] = {};
+        };
+        int made = 0;                                       // positions, in 32, whose weights are there
+        if (lo >= kTile) {                                  // every row attends to all of the tile: the same way for all of the warp
+          uint32_t v[2][2][8];
+          auto read16 = [&](int c, uint32_t (&to)[2][8]) {
+            tc::tmem_ld_frag16(s_at + 16 * c, to[0]);
+            tc::tmem_ld_frag16(s_at + half + 16 * c, to[1]);
+          };
+          if (it == 0) {                                    // a quarter's maxima will do to begin with
+            uint32_t first32[2][16];
+            read(0, first32);
+            landed(first32);
+            maxima(0, first32);
+          }
+          read16(0, v[0]);
+          landed(v[0]);
+          bool good = true;
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {                     // weights go where scores of an earlier turn were, or this one's
-            uint32_t v[2][8], out[2][4];
+          for (int c = 0; c < 4 && good; c += 2) {          // half a tile at a time, read ahead by 16 positions
+            uint32_t out[2][2][8];
+            uint64_t sum[4] = {0, 0, 0, 0};
+            __half2 top = __float2half2_rn(0.f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k < 3 || c == 0) read16(2 * c + k + 1, v[(k + 1) & 1]);
+#pragma unroll
+              for (int jj = 0; jj < 2; ++jj) {
+                const int j = 2 * k + jj;
+                const uint64_t ks = pair(ks_at + 32 * c, j), vs = pair(vs_at + 32 * c, j);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  const uint32_t* x = &v[k & 1][r >> 1][4 * jj + 2 * (r & 1)];
+                  const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
+                  const uint64_t p = pack2(exp2_fast(first(e)), exp2_fast(second(e))), pv = mul2(p, vs);
+                  sum[r] = add2(sum[r], p);
+                  const __half2 h2 = __floats2half2_rn(first(pv), second(pv));
+                  out[k >> 1][r >> 1][2 * (j & 3) + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
+                  top = __hmax2(top, h2);
+                }
+              }
+              if (k < 3 || c == 0) landed(v[(k + 1) & 1]);
+            }
+            if ((good = keep(sum, top))) {
+              put(c, out[0]);
+              put(c + 1, out[1]);
+              made = c + 2;
+            }
+          }
+        }
+#pragma unroll 1
+        for (int c = made; c < 4; ++c) {                    // 32 positions at a time
+          uint32_t out[2][8] = {};
+          bool good = true;
+          if (32 * c < hi) {
+            uint32_t v[2][16];
             read(c, v);
             landed(v);
-#pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-              const float2 ks = *reinterpret_cast<const float2*>(ks_at + 16 * c + 8 * jj), vs = *reinterpret_cast<const float2*>(vs_at + 16 * c + 8 * jj);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                // the product is selected too: a scale that is not attended to may be NaN
-                const uint32_t here = see[r] >> (4 * c + 2 * jj);
-                const float x0 = exp2_fast(__fadd_rn(score(v, r, jj, 0, ks.x), -m[r])), x1 = exp2_fast(__fadd_rn(score(v, r, jj, 1, ks.y), -m[r]));
-                const float y0 = here & 1 ? x0 : 0.f, y1 = here & 2 ? x1 : 0.f;
-                sum[r] += y0 + y1;
-                const __half2 h2 = __floats2half2_rn(here & 1 ? x0 * vs.x : 0.f, here & 2 ? x1 * vs.y : 0.f);
-                out[r >> 1][2 * jj + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
+            good = false;
+#pragma unroll 1
+            for (int turn = it + c == 0; turn < 2 && !good; ++turn) {
+              if (turn) maxima(c, v);
+              good = weights(c, v, out);
             }
-            tc::tmem_st_pairs8(s_at + 8 * c, out[0]);
-            tc::tmem_st_pairs8(s_at + half + 8 * c, out[1]);
+            if (!good) exact(c);
           }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) l[r] += sum[r];
+          if (good) put(c, out);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -610,9 +729,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
         last_use = uses >> last & 1;
         uses ^= 1u << last;
       }
-      tile0 += w.tiles;
+      tile0 += tiles;
 
       // ---- the rows' outputs, or this piece's records
+      Plan anew = plan;
+      asm volatile("" : "+l"(anew.items), "+l"(anew.streams));
+      const Work w(anew, turn(turn_no), G);
+      const bool more = turn(turn_no + 1) < items;
+      const int n_rows = w.st.n * G, sub = w.wide ? kSub * s : 0;
+      if (more) {
+        const Work next(anew, turn(turn_no + 1), G);
+        ask(next, first_row(next));
+      }
       if (steps > 0) products_done();
       tc::fence_after_sync();
       float f0[4], f1[4];                                   // factors of this warpgroup's sums, and of the other's
@@ -620,8 +748,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       for (int r = 0; r < 4; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        f0[r] = 1.f;
-        f1[r] = 0.f;
       }
       if (!w.wide) {
         if (s == 1 && t == 0) {
@@ -631,105 +757,93 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
             sm.l[row + 8 * r] = l[r];
           }
         }
-      }
-      float* other = reinterpret_cast<float*>(sm.q[1]) + wt;   // the second half's rows are free where both have the same
-#pragma unroll 1
-      for (int hc = 0; hc < 2; ++hc) {                      // a half of the elements
-        constexpr int kF = D / 64;
-        float o[2][kF][16];                                 // [pair of rows][32 elements]
+        sync_some(1, 256);
+        if (s == 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int f = 0; f < kF; ++f) {
-            uint32_t x[16];
-            tc::tmem_ld_frag32(o_at + h * half + hc * (D / 2) + 32 * f, x);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(x[e]));
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[h][f][e] = steps > 0 ? __uint_as_float(x[e]) : 0.f;
+          for (int r = 0; r < 4; ++r) {
+            const float om = sm.m[row + 8 * r], mn = fmaxf(m[r], om);
+            f0[r] = exp2_fast(m[r] - mn);
+            f1[r] = exp2_fast(om - mn);
+            l[r] = scaled_down(l[r], m[r] - mn) + scaled_down(sm.l[row + 8 * r], om - mn);
+            m[r] = mn;
           }
-        if (!w.wide) {
+        }
+      }
+      const bool whole = w.piece == (int)kWhole, mine = w.wide || s == 0;
+      // the records of the warp's rows, 16 by 16: the stream's slabs of a kv head, piece by piece
+      const int slabs = (n_rows + 15) >> 4, slab = (w.q0 + sub + 32 * (warp & 3)) >> 4;
+      const size_t rec = (size_t)w.st.rec + ((size_t)w.kh * slabs + slab) * w.st.most + w.piece;
+      float inv[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) inv[r] = l[r] == 0.f ? 0.f : 1.f / l[r];   // nothing to attend to: zeros
+      if (!whole && mine && t == 0) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (slab + (r >> 1) < slabs) a.rec_ml[(rec + (size_t)(r >> 1) * w.st.most) * 16 + g + 8 * (r & 1)] = make_float2(m[r], l[r]);
+      }
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {                    // 32 elements: o[pair of rows][4 j + 2 (r & 1) + e] is element 8 j + 2 t + e
+        float o[2][16];
+        {
+          uint32_t x[2][16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) tc::tmem_ld_frag32(o_at + h * half + 32 * c, x[h]);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              asm volatile("" : "+r"(x[h][e]));
+              o[h][e] = __uint_as_float(x[h][e]);
+            }
+        }
+        if (!w.wide) {                                      // joined with the other half's
+          float4* other = reinterpret_cast<float4*>(sm.other) + wt;
           if (s == 1) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int f = 0; f < kF; ++f)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) other[((h * kF + f) * 16 + e) * 128] = o[h][f][e];
+              for (int e = 0; e < 4; ++e)
+                other[(4 * h + e) * 128] = steps > 0 ? make_float4(o[h][4 * e], o[h][4 * e + 1], o[h][4 * e + 2], o[h][4 * e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
           sync_some(1, 256);
           if (s == 0) {
-            if (hc == 0) {
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float om = sm.m[row + 8 * r], mn = fmaxf(m[r], om);
-                f0[r] = exp2_fast(m[r] - mn);
-                f1[r] = exp2_fast(om - mn);
-                l[r] = scaled_down(l[r], m[r] - mn) + scaled_down(sm.l[row + 8 * r], om - mn);
-                m[r] = mn;
-              }
-            }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int f = 0; f < kF; ++f)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const int r = 2 * h + (e >> 1 & 1);
-                  o[h][f][e] = fmaf(other[((h * kF + f) * 16 + e) * 128], f1[r], o[h][f][e] * f0[r]);
-                }
+              for (int e = 0; e < 4; ++e) {
+                const float4 x = other[(4 * h + e) * 128];
+                o[h][4 * e] = fmaf(x.x, f1[2 * h], o[h][4 * e] * f0[2 * h]);
+                o[h][4 * e + 1] = fmaf(x.y, f1[2 * h], o[h][4 * e + 1] * f0[2 * h]);
+                o[h][4 * e + 2] = fmaf(x.z, f1[2 * h + 1], o[h][4 * e + 2] * f0[2 * h + 1]);
+                o[h][4 * e + 3] = fmaf(x.w, f1[2 * h + 1], o[h][4 * e + 3] * f0[2 * h + 1]);
+              }
           }
           sync_some(1, 256);
-          if (s == 1) continue;
         }
+        if (!mine) continue;
+        if (!whole) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int q = w.q0 + sub + row + 8 * r, j = q / G, head = w.kh * G + q - j * G;
-          if (w.piece != (int)kWhole) {
-            if (q < n_rows) {
-              const size_t rec = (size_t)w.st.rec + ((size_t)j * a.qh + head) * w.st.most + w.piece;
-              if (hc == 0 && t == 0) a.rec_ml[rec] = make_float2(m[r], l[r]);
-              float* to = a.rec_o + rec * D + hc * (D / 2) + 2 * t;
+          for (int h = 0; h < 2; ++h)
+            if (slab + h < slabs) {
+              float4* at = a.rec_o + ((rec + (size_t)h * w.st.most) * (D / 32) + c) * 128 + lane;
 #pragma unroll
-              for (int f = 0; f < kF; ++f)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float* x = &o[r >> 1][f][4 * e + 2 * (r & 1)];
-                  *reinterpret_cast<float2*>(to + 32 * f + 8 * e) = make_float2(x[0], x[1]);
-                }
+              for (int e = 0; e < 4; ++e) at[32 * e] = make_float4(o[h][4 * e], o[h][4 * e + 1], o[h][4 * e + 2], o[h][4 * e + 3]);
             }
-          } else {
-            const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];   // nothing to attend to: zeros
+        } else {
 #pragma unroll
-            for (int f = 0; f < kF; ++f) {
-              uint32_t p[4];                                // elements 8 e + 2 t and the next of 32
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float* x = &o[r >> 1][f][4 * e + 2 * (r & 1)];
-                const __nv_bfloat162 v = __floats2bfloat162_rn(x[0] * inv, x[1] * inv);
-                p[e] = *reinterpret_cast<const uint32_t*>(&v);
-              }
-              // turned among the row's four threads: elements 8 t .. 8 t + 7
-#pragma unroll
-              for (int e = 0; e < 4; e += 2) {
-                const uint32_t back = __shfl_xor_sync(0xffffffffu, t & 1 ? p[e] : p[e + 1], 1);
-                if (t & 1) p[e] = back;
-                else p[e + 1] = back;
-              }
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t back = __shfl_xor_sync(0xffffffffu, t & 2 ? p[e] : p[e + 2], 2);
-                if (t & 2) p[e] = back;
-                else p[e + 2] = back;
-              }
-              if (q < n_rows)
-                *reinterpret_cast<uint4*>(a.O + ((size_t)(w.st.start + j) * a.qh + head) * D + hc * (D / 2) + 32 * f + 8 * t) = make_uint4(p[0], p[1], p[2], p[3]);
-            }
+          for (int r = 0; r < 4; ++r) {
+            const uint4 p = rounded_row(o[r >> 1] + 2 * (r & 1), inv[r], t);
+            const int to = sm.to[info][mine_at + 8 * r];
+            if (to >= 0) *reinterpret_cast<uint4*>(a.O + (size_t)to * D + 32 * c + 8 * t) = p;
           }
         }
       }
       tc::fence_before_sync();                              // O is read before the next piece's products
+      if (more) {
+        sync_some(1, 256);                                  // both halves' scores are made
+        place_all(Work(anew, turn(turn_no + 1), G), (turn_no + 1) & 1);
+      }
     }
   }
   if (!ok) sm.gave_up = 1;
@@ -740,67 +854,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
   if (sm.gave_up) {                                         // NaN in all rows of this CTA's pieces
     for (int r = 0; turn(r) < items; ++r) {
       const Work w(plan, turn(r), G);
+      const int slabs = (w.st.n * G + 15) >> 4;
       for (int u = tid; u < w.rows * D; u += kThreads) {
-        const int q = w.q0 + u / D, j = q / G, head = w.kh * G + q - j * G;
-        if (w.piece != (int)kWhole) a.rec_ml[(size_t)w.st.rec + ((size_t)j * a.qh + head) * w.st.most + w.piece] = make_float2(0.f, __uint_as_float(0x7FC00000u));
+        const int row = u / D, q = w.q0 + row, j = q / G, head = w.kh * G + q - j * G;
+        if (w.piece != (int)kWhole)
+          a.rec_ml[((size_t)w.st.rec + ((size_t)w.kh * slabs + (q >> 4)) * w.st.most + w.piece) * 16 + (q & 15)] = make_float2(0.f, __uint_as_float(0x7FC00000u));
         else a.O[((size_t)(w.st.start + j) * a.qh + head) * D + u % D] = __ushort_as_bfloat16(0x7FC0);
       }
     }
   }
 }
 
-// The rows of cut blocks: a head of a row to a warp and turn, its records in
-// ascending order, a lane d / 32 elements.
-constexpr int kMergeWarps = 8, kMergeAhead = 8;
+// The rows of cut blocks: 32 elements of 16 rows to a warp and turn, the
+// pieces' records in ascending order and in the layout of the warp that wrote
+// them (thread (g, t): rows g and g + 8, elements 8 j + 2 t and the next).
+constexpr int kMergeWarps = 4, kMergeAhead = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_rows_merge(RowsArgs a) {
-  constexpr int E = D / 32;
-  using Part = typename std::conditional<E == 4, float4, float2>::type;
   __shared__ int unit[kMaxStreams];
   const Plan plan(const_cast<void*>(a.plan), a.B, a.T);
   const bool mine = fits(*plan.head, a);
-  const int units = mine ? plan.head->units : 0, lane = threadIdx.x & 31, G = a.qh / a.c.kvh;
+  const int units = mine ? plan.head->units * (D / 32) : 0, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = a.qh / a.c.kvh;
   for (int b = threadIdx.x; b < a.B && mine; b += kMergeWarps * 32) unit[b] = plan.streams[b].unit;
   __syncthreads();
   pdl_wait();
   for (int u = blockIdx.x * kMergeWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kMergeWarps) {
-    int lo = 0, hi = a.B;                                   // the last stream whose units begin at or before u
+    const int slab_no = u / (D / 32), c = u % (D / 32);
+    int lo = 0, hi = a.B;                                   // the last stream whose units begin at or before this one
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (unit[mid] <= u) lo = mid;
+      if (unit[mid] <= slab_no) lo = mid;
       else hi = mid;
     }
     const PlanStream st = plan.streams[lo];
-    const int local = u - st.unit, j = local / a.qh, head = local - j * a.qh, kh = head / G, block = (j * G + head - kh * G) / kBlockRows;
+    const int n_rows = st.n * G, slabs = (n_rows + 15) >> 4, local = slab_no - st.unit, kh = local / slabs, slab = local - kh * slabs;
+    const int block = slab / (kBlockRows / 16);
     const int n = Pieces(block * a.c.kvh + kh, Cut{st.cut, st.pitch}, extent_of(block, st.n, st.len, G, st.tree)).count;
     if (n == 1) continue;                                   // the block is whole: its outputs are there
     const size_t rec = (size_t)st.rec + (size_t)local * st.most;
-    const Part* o = reinterpret_cast<const Part*>(a.rec_o + rec * D) + lane;
-    const float2* ml = a.rec_ml + rec;
-    float mx = -1e30f, den = 0.f, acc[E] = {};
-    for (int r = lane; r < n; r += 32) mx = fmaxf(mx, ml[r].x);
-    mx = warp_max(mx);
+    const float4* o = a.rec_o + (rec * (D / 32) + c) * 128 + lane;
+    const float2* ml = a.rec_ml + rec * 16 + g;
+    float mx[2] = {-1e30f, -1e30f}, den[2] = {0.f, 0.f}, acc[16] = {};
+    for (int r = 0; r < n; ++r) {
+      mx[0] = fmaxf(mx[0], ml[16 * r].x);
+      mx[1] = fmaxf(mx[1], ml[16 * r + 8].x);
+    }
     for (int r0 = 0; r0 < n; r0 += kMergeAhead) {
-      Part part[kMergeAhead];
-#pragma unroll
-      for (int k = 0; k < kMergeAhead; ++k)
-        if (r0 + k < n) part[k] = o[(r0 + k) * 32];
+      float4 part[kMergeAhead][4];
+      float2 x[kMergeAhead][2];
 #pragma unroll
       for (int k = 0; k < kMergeAhead; ++k)
         if (r0 + k < n) {
-          const float2 x = ml[r0 + k];
-          const float f = exp2f(x.x - mx);
-          den += x.y * exp2f(fmaxf(x.x - mx, -120.f)) * exp2f(fminf(x.x - mx + 120.f, 0.f));   // as scaled_down
-          const float* p = reinterpret_cast<const float*>(&part[k]);
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(p[e], f, acc[e]);
+          for (int j = 0; j < 4; ++j) part[k][j] = o[(size_t)(r0 + k) * (D / 32) * 128 + 32 * j];
+          x[k][0] = ml[16 * (r0 + k)];
+          x[k][1] = ml[16 * (r0 + k) + 8];
+        }
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k)
+        if (r0 + k < n) {
+          float f[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float d = x[k][h].x - mx[h];
+            f[h] = exp2f(d);
+            den[h] += x[k][h].y * exp2f(fmaxf(d, -120.f)) * exp2f(fminf(d + 120.f, 0.f));   // as scaled_down
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[4 * j] = fmaf(part[k][j].x, f[0], acc[4 * j]);
+            acc[4 * j + 1] = fmaf(part[k][j].y, f[0], acc[4 * j + 1]);
+            acc[4 * j + 2] = fmaf(part[k][j].z, f[1], acc[4 * j + 2]);
+            acc[4 * j + 3] = fmaf(part[k][j].w, f[1], acc[4 * j + 3]);
+          }
         }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    bf16* to = a.O + ((size_t)(st.start + j) * a.qh + head) * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) *reinterpret_cast<__nv_bfloat162*>(to + 2 * e) = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    for (int h = 0; h < 2; ++h) {
+      const uint4 p = rounded_row(acc + 2 * h, den[h] == 0.f ? 0.f : 1.f / den[h], t);
+      const int q = 16 * slab + g + 8 * h, j = q / G;
+      if (q < n_rows) *reinterpret_cast<uint4*>(a.O + ((size_t)(st.start + j) * a.qh + kh * G + q - j * G) * D + 32 * c + 8 * t) = p;
+    }
   }
 }
 
@@ -819,8 +954,8 @@ cudaError_t launch_rows(const RowsArgs& a, int64_t records, cudaStream_t s) {
   const unsigned grid = (unsigned)std::min<int64_t>(kSms, most_items(a.B, a.T, a.qh, a.c.kvh));
   e = launch_k(false, k_kv8_rows<D, FMT>, dim3(grid), dim3(kThreads), smem, s, a);
   if (e != cudaSuccess || records == 0) return e;
-  const int64_t units = std::min<int64_t>(records, (int64_t)a.T * a.qh);
-  return launch_k(true, k_kv8_rows_merge<D>, dim3((unsigned)std::min<int64_t>((units + kMergeWarps - 1) / kMergeWarps, 4 * kSms)), dim3(kMergeWarps * 32), 0, s, a);
+  const int64_t units = (records / 16 + (int64_t)a.T * a.qh / 16) * (D / 32);   // more than there can be
+  return launch_k(true, k_kv8_rows_merge<D>, dim3((unsigned)std::min<int64_t>((units + kMergeWarps - 1) / kMergeWarps, 8 * kSms)), dim3(kMergeWarps * 32), 0, s, a);
 }
 
 }  // namespace
@@ -853,8 +988,8 @@ bm_status kv8_attend_rows(const bm_kv8_cache* c, const void* plan, size_t plan_b
   a.plan = plan;
   a.Q = reinterpret_cast<const bf16*>(Q);
   a.O = reinterpret_cast<bf16*>(O);
-  a.rec_o = static_cast<float*>(ws);
-  a.rec_ml = reinterpret_cast<float2*>(a.rec_o + (size_t)records * c->head_dim);
+  a.rec_o = static_cast<float4*>(ws);
+  a.rec_ml = reinterpret_cast<float2*>(a.rec_o + (size_t)records * c->head_dim / 4);
   a.B = B;
   a.T = T;
   a.qh = q_heads;

@@ -24,14 +24,14 @@ constexpr int kPlanMagic = 0x6b763870;
 
 struct PlanHead {
   int magic, B, T, qh, kvh, slots, cap, items;
-  int units, pad[7];      // heads of rows whose positions are cut
+  int units, pad[7];      // slabs of 16 query rows of cut streams
 };
 struct PlanStream {
   int start, n, slot, len;    // first row, rows (0: none, or refused), slot, positions with the step's own
   int tree;                   // 1: the rows attend to each other by their masks
   int cut, pitch, most;       // tiles to a piece (0: uncut), to a block on the line; the most pieces a block has
-  int unit;                   // of the cut streams' rows x heads, the first of this one's
-  long long rec;              // its first record
+  int unit;                   // of the cut streams' slabs of 16 query rows, the first of this one's
+  long long rec;              // its first record: a slab has `most` of them
   int base, refused;          // positions before the step; 1: a stream that does not fit
   int pad[2];
 };
@@ -116,7 +116,8 @@ inline int64_t most_items(int B, int T, int qh, int kvh) {
 inline size_t plan_bytes(int B, int T, int qh, int kvh) {
   return sizeof(PlanHead) + B * sizeof(PlanStream) + (size_t)(T + 1) / 2 * 16 + most_items(B, T, qh, kvh) * sizeof(PlanItem);
 }
-// Records (a row, head and piece): at most kSms blocks' worth of a stream whose blocks are cut evenly, 9 kSms (kSms and twice 4 kSms) on a line.
+// Records, in query rows times pieces: a stream's rows of a kv head are rounded up to 16.  At most kSms blocks' worth of a
+// stream whose blocks are cut evenly, 9 kSms (kSms and twice 4 kSms) on a line.
 inline int64_t most_records(int B, int T, int qh, int kvh, int cap) {
   const int tiles = tiles_of(cap);
   int64_t most = 0, least = 4;
@@ -126,7 +127,7 @@ inline int64_t most_records(int B, int T, int qh, int kvh, int cap) {
   if (tiles >= 32) most = std::max<int64_t>(most, 4);
   if (most < 2) return 0;
   const bool line = (int64_t)blocks_of(T, qh / kvh) * kvh > kSms / 2;
-  return std::min<int64_t>((int64_t)T * qh * most, (int64_t)B * kBlockRows * kSms * (line ? 9 : 1));
+  return std::min<int64_t>(((int64_t)T * qh + (int64_t)B * 16 * kvh) / 16 * 16 * most, (int64_t)B * kBlockRows * kSms * (line ? 9 : 1));
 }
 
 inline bool step_shapes_ok(int B, int T, int qh, int kvh) {

@@ -141,24 +141,25 @@ __device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t (&v)[8])
                : "r"(taddr)
                : "memory");
 }
+// As tmem_st_frag16, 4 columns.
+__device__ __forceinline__ void tmem_st_pairs4(uint32_t taddr, const uint32_t (&v)[2]) {
+  __syncwarp();
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(v[0]), "r"(v[1]) : "memory");
+}
 // As tmem_st_frag16, 8 columns.
 __device__ __forceinline__ void tmem_st_pairs8(uint32_t taddr, const uint32_t (&v)[4]) {
   __syncwarp();
   asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                : "memory");
 }
-// As tmem_st_frag16, 32 columns.
-__device__ __forceinline__ void tmem_st_pairs32(uint32_t taddr, const uint32_t (&v)[16]) {
+// Its counterpart.
+__device__ __forceinline__ void tmem_ld_pairs8(uint32_t taddr, uint32_t (&v)[4]) {
   __syncwarp();
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {"
-      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
-      "};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+  asm volatile("tcgen05.ld.sync.aligned.16x128b.x2.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(taddr)
+               : "memory");
 }
-
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before_sync() {
