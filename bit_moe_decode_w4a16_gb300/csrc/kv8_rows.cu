@@ -62,6 +62,34 @@ constexpr float kLargest = 32768.f;                         // a weight above it
 constexpr float kLargestSum = 2.028240960365167e31f;        // 2^104: V scales below 2^-100 count as that in a maximum
 constexpr uint32_t kWaitLimit = 1u << 18;                   // polls of ~3.7 us: a wait gives up after about a second
 
+// A piece as all roles see it.
+struct Work {
+  int start, n, slot, len;              // of the stream: first row, rows, slot, positions
+  long long rec;                        // its first record
+  int most, tree;
+  int kh, q0, rows, wide;               // kv head; first of the block's query rows and their number; both halves have some
+  int t0, tiles, piece, pad;            // tiles from t0 on; 65535: the whole block
+  Work() = default;
+  __device__ Work(const Plan& plan, int i, int G) {
+    const PlanItem it = plan.items[i];
+    const PlanStream& st = plan.streams[it.who & 1023];
+    start = st.start;
+    n = st.n;
+    slot = st.slot;
+    len = st.len;
+    rec = st.rec;
+    most = st.most;
+    tree = st.tree;
+    kh = it.who >> 10;
+    q0 = (it.what & 65535) * kBlockRows;
+    rows = min(kBlockRows, n * G - q0);
+    wide = rows > kSub;
+    t0 = it.t0;
+    tiles = it.t1 - it.t0;
+    piece = it.what >> 16;
+  }
+};
+
 template <int D>
 struct RowsSmem {
   uint8_t q[2][kSub * D * 2];                               // [d / 64][row][64] fp16, swizzled
@@ -73,6 +101,7 @@ struct RowsSmem {
   float up[2][kBlockRows];
   int to[2][kBlockRows], lim[2][kBlockRows];
   unsigned long long bits[2][kBlockRows];
+  Work work[8];                                             // by turn: the softmax's, two or three behind the conversion's
   float m[kSub], l[kSub];                                   // of the second warpgroup, where both have the same rows,
   float other[kSub / 4 * kSub];                             // and 32 columns of its outputs
   uint64_t k_full[2], v_full[2];                            // by the tile's parity
@@ -155,24 +184,6 @@ __device__ __forceinline__ uint32_t among(unsigned long long bits, int offset) {
 
 // The CTA's r-th piece.
 __device__ __forceinline__ int turn(int r) { return r * (int)gridDim.x + (int)(r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); }
-
-// A piece as all roles see it.
-struct Work {
-  PlanStream st;
-  int kh, q0, rows, tiles, t0, piece;   // kv head; first of its rows and their number; tiles from t0 on; 65535: the whole block
-  bool wide;                            // both halves have rows
-  __device__ Work(const Plan& plan, int i, int G) {
-    const PlanItem it = plan.items[i];
-    st = plan.streams[it.who & 1023];
-    kh = it.who >> 10;
-    q0 = (it.what & 65535) * kBlockRows;
-    rows = min(kBlockRows, st.n * G - q0);
-    t0 = it.t0;
-    tiles = it.t1 - it.t0;
-    piece = it.what >> 16;
-    wide = rows > kSub;
-  }
-};
 
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
@@ -306,9 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     float scale = 0.f;                                      // of position ct % 128: K's in the first warpgroup, V's in the other
     auto load = [&](const Work& w, int i, bool v) {
       const int p0 = (w.t0 + i) * kTile;
-      const size_t at = a.c.row(w.st.slot, w.kh, p0);
+      const size_t at = a.c.row(w.slot, w.kh, p0);
       const uint8_t* from = (v ? a.c.V : a.c.K) + at * D + 16 * ct;
-      const int left = w.st.len - p0;
+      const int left = w.len - p0;
       uint4* to = v ? vr : kr;
 #pragma unroll
       for (int u = 0; u < kTurns; ++u)
@@ -333,9 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     unsigned uses = 0, theirs = 0;
     for (int r = 0; turn(r) < items; ++r) {
       const Work w(plan, turn(r), G);
-      const int own = w.st.len - w.st.n, all_see = own + (w.st.tree ? 0 : w.q0 / G + 1);   // positions that every row attends to
+      const int own = w.len - w.n, all_see = own + (w.tree ? 0 : w.q0 / G + 1);   // positions that every row attends to
       load(w, 0, false);
       load(w, 0, true);
+      if (ct == 0) {
+        if (r == 0) sm.work[0] = w;
+        if (turn(r + 1) < items) sm.work[(r + 1) & 7] = Work(plan, turn(r + 1), G);
+      }
       for (int i = 0; i < w.tiles; ++i, ++tile) {
         const int b = tile & 1, slot = tile & 3;
         // the buffer's last tile was a step of one half or of both: its scores (its products) have been made
@@ -391,23 +406,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     int tile0 = 0;                                          // the CTA's tiles so far
     unsigned uses = 0, last = 0, last_use = 0;              // bit b: the parity of this half's steps with buffer b; the latest step's buffer, and that parity before it
     auto products_done = [&]() { wait(sm.o_ready[s][last], last_use); };
-    // ---- a block's query rows as fp16 of about their own magnitude, d / 8 lanes to a row; half of this warpgroup's are asked for while
-    // the piece before ends
+    // ---- a block's query rows as fp16 of about their own magnitude, d / 8 lanes to a row, asked for while the piece before ends.  All rows
+    // of the halves in use are written, whatever the block's own: 128 of this half's, or 64 of the half that both share.
+    auto first_row = [&](const Work& w) { return w.wide ? kSub * s : 64 * s; };
     constexpr int kPieces = D / 8, kStep = 128 / kPieces, kBatch = 64 / kStep;
     const float inv_g = 1.f / G;
     uint4 x[kBatch];
     auto ask = [&](const Work& w, int row0) {
       const int c = wt % kPieces, j0 = w.q0 / G, rest = w.q0 - j0 * G;
-      const bf16* from = a.Q + ((size_t)w.st.start * a.qh + w.kh * G) * D + 8 * c;
+      const bf16* from = a.Q + ((size_t)w.start * a.qh + w.kh * G) * D + 8 * c;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int row = row0 + wt / kPieces + u * kStep, q = w.q0 + row, j = j0 + (int)((rest + row + 0.5f) * inv_g);   // q / G: the quotient's argument is below 2^9
         x[u] = make_uint4(0, 0, 0, 0);
-        if (q < w.st.n * G) x[u] = *reinterpret_cast<const uint4*>(from + ((size_t)j * a.qh + q - j * G) * D);
+        if (q < w.n * G) x[u] = *reinterpret_cast<const uint4*>(from + ((size_t)j * a.qh + q - j * G) * D);
       }
     };
     auto place = [&](const Work& w, int row0, int slot) {
-      const int c = wt % kPieces, j0 = w.q0 / G, rest = w.q0 - j0 * G, own = w.st.len - w.st.n;
+      const int c = wt % kPieces, j0 = w.q0 / G, rest = w.q0 - j0 * G, own = w.len - w.n;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int row = row0 + wt / kPieces + u * kStep;
@@ -432,19 +448,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       // a row to a thread: what else there is to know of it
       if (wt < 64) {
         const int row = row0 + wt, q = w.q0 + row, j = j0 + (int)((rest + row + 0.5f) * inv_g);
-        const bool live = q < w.st.n * G;
-        sm.to[slot][row] = live ? (w.st.start + j) * a.qh + w.kh * G + q - j * G : -1;
-        sm.lim[slot][row] = w.st.tree ? own : own + j + 1;
-        sm.bits[slot][row] = live && w.st.tree ? plan.masks[w.st.start + j] : 0;
+        const bool live = q < w.n * G;
+        sm.to[slot][row] = live ? (w.start + j) * a.qh + w.kh * G + q - j * G : -1;
+        sm.lim[slot][row] = w.tree ? own : own + j + 1;
+        sm.bits[slot][row] = live && w.tree ? plan.masks[w.start + j] : 0;
       }
     };
-    // All rows of the halves in use are written, whatever the block's own: 128 of this half's, or 64 of the half that both share.
-    auto first_row = [&](const Work& w) { return w.wide ? kSub * s : 64 * s; };
     auto place_all = [&](const Work& w, int slot) {
-      place(w, first_row(w), slot);
-      if (w.wide) {
-        ask(w, first_row(w) + 64);
-        place(w, first_row(w) + 64, slot);
+#pragma unroll 1
+      for (int k = 0; k <= w.wide; ++k) {
+        if (k) ask(w, first_row(w) + 64);
+        place(w, first_row(w) + 64 * k, slot);
       }
       tc::fence_proxy_async_smem();
       arrive(sm.q_full);
@@ -456,17 +470,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     }
     const int row = 32 * (warp & 3) + g;                    // this thread's rows of its half: row + 8 r
     for (int turn_no = 0; turn(turn_no) < items; ++turn_no) {
-      // A piece's fields are read where they are needed (from L1) rather than held: the tiles' loop needs the registers.
+      // a piece's other fields are read where they are needed rather than held: the tiles' loop needs the registers
       bool wide;
       int tiles, t0, lowest, highest;                       // below `lowest` all of the warp's rows attend to, from `highest` on none does
       {
-        const Work w(plan, turn(turn_no), G);
+        const Work w = turn_no ? sm.work[turn_no & 7] : Work(plan, turn(0), G);
         wide = w.wide;
         tiles = w.tiles;
         t0 = w.t0;
-        const int own = w.st.len - w.st.n, row_a = w.q0 + (wide ? kSub * s : 0) + 32 * (warp & 3), row_z = min(row_a + 31, w.st.n * G - 1);
-        lowest = own + (w.st.tree ? 0 : row_a / G + 1);
-        highest = row_z < row_a ? 0 : own + (w.st.tree ? min(w.st.n, kDrafts) : row_z / G + 1);
+        const int own = w.len - w.n, row_a = w.q0 + (wide ? kSub * s : 0) + 32 * (warp & 3), row_z = min(row_a + 31, w.n * G - 1);
+        lowest = own + (w.tree ? 0 : row_a / G + 1);
+        highest = row_z < row_a ? 0 : own + (w.tree ? min(w.n, kDrafts) : row_z / G + 1);
       }
       const int info = turn_no & 1, mine_at = (wide ? kSub * s : 0) + row;
       float qf[4], m[4], l[4];
@@ -555,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
           tc::tmem_st_frag16(s_at + half + 16 * c, out[1]);
         };
         // Maxima that have risen by more than 2^8 are moved there, by whole powers of two once there is one, so that the weights of the
-        // tile's positions before 32 c, which are made already, scale exactly.
+        // tile's positions before 32 c, which are made already, scale exactly; down to the power of two, so that a row's largest weight
+        // stays at 1 or above, 2^25 times what fp16 drops.
         auto move = [&](int c, float (&mx)[4]) {
           float f[4];
           bool moves = false;
@@ -565,9 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
             f[r] = 1.f;
             if (mx[r] > m[r] + 8.f) {                       // each row by itself: its neighbours stand elsewhere in another step
-              const float by = m[r] == -1e30f ? 0.f : fminf(ceilf(mx[r] - m[r]), 200.f);
+              const float by = m[r] == -1e30f ? 0.f : fminf(floorf(mx[r] - m[r]), 200.f);
               f[r] = by == 0.f || by > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)by) << 23);
-              const float mn = by == 0.f || by == 200.f ? mx[r] : fmaxf(m[r] + by, mx[r]);
+              const float mn = by == 0.f || by == 200.f ? mx[r] : m[r] + by;
               l[r] = scaled_down(l[r], m[r] - mn);
               m[r] = mn;
               moves = true;
@@ -595,14 +610,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
 #pragma unroll 1
           for (int k = 0; k < 4 * c; ++k) {
             const uint32_t at = s_at + (k & 1 ? half : 0) + 8 * (k >> 1);
-            const __half2 fa = __float2half2_rn(k & 1 ? f[2] : f[0]), fb = __float2half2_rn(k & 1 ? f[3] : f[1]);
+            const float fa = k & 1 ? f[2] : f[0], fb = k & 1 ? f[3] : f[1];   // in fp32: weights reach 2^15, and fp16 has no 2^-25
             uint32_t p[4];
             tc::tmem_ld_pairs8(at, p);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               asm volatile("" : "+r"(p[e]));
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&p[e]), e & 1 ? fb : fa);
+              const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&p[e]));
+              const __half2 y = __floats2half2_rn(w.x * (e & 1 ? fb : fa), w.y * (e & 1 ? fb : fa));
               p[e] = *reinterpret_cast<const uint32_t*>(&y);
             }
             tc::tmem_st_pairs8(at, p);
@@ -732,15 +748,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       tile0 += tiles;
 
       // ---- the rows' outputs, or this piece's records
-      Plan anew = plan;
-      asm volatile("" : "+l"(anew.items), "+l"(anew.streams));
-      const Work w(anew, turn(turn_no), G);
+      const Work& w = sm.work[turn_no & 7];
       const bool more = turn(turn_no + 1) < items;
-      const int n_rows = w.st.n * G, sub = w.wide ? kSub * s : 0;
-      if (more) {
-        const Work next(anew, turn(turn_no + 1), G);
-        ask(next, first_row(next));
-      }
+      const int n_rows = w.n * G, sub = w.wide ? kSub * s : 0;
+      if (more) ask(sm.work[(turn_no + 1) & 7], first_row(sm.work[(turn_no + 1) & 7]));
       if (steps > 0) products_done();
       tc::fence_after_sync();
       float f0[4], f1[4];                                   // factors of this warpgroup's sums, and of the other's
@@ -772,14 +783,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       const bool whole = w.piece == (int)kWhole, mine = w.wide || s == 0;
       // the records of the warp's rows, 16 by 16: the stream's slabs of a kv head, piece by piece
       const int slabs = (n_rows + 15) >> 4, slab = (w.q0 + sub + 32 * (warp & 3)) >> 4;
-      const size_t rec = (size_t)w.st.rec + ((size_t)w.kh * slabs + slab) * w.st.most + w.piece;
+      const size_t rec = (size_t)w.rec + ((size_t)w.kh * slabs + slab) * w.most + w.piece;
       float inv[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) inv[r] = l[r] == 0.f ? 0.f : 1.f / l[r];   // nothing to attend to: zeros
       if (!whole && mine && t == 0) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (slab + (r >> 1) < slabs) a.rec_ml[(rec + (size_t)(r >> 1) * w.st.most) * 16 + g + 8 * (r & 1)] = make_float2(m[r], l[r]);
+          if (slab + (r >> 1) < slabs) a.rec_ml[(rec + (size_t)(r >> 1) * w.most) * 16 + g + 8 * (r & 1)] = make_float2(m[r], l[r]);
       }
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {                    // 32 elements: o[pair of rows][4 j + 2 (r & 1) + e] is element 8 j + 2 t + e
@@ -826,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             if (slab + h < slabs) {
-              float4* at = a.rec_o + ((rec + (size_t)h * w.st.most) * (D / 32) + c) * 128 + lane;
+              float4* at = a.rec_o + ((rec + (size_t)h * w.most) * (D / 32) + c) * 128 + lane;
 #pragma unroll
               for (int e = 0; e < 4; ++e) at[32 * e] = make_float4(o[h][4 * e], o[h][4 * e + 1], o[h][4 * e + 2], o[h][4 * e + 3]);
             }
@@ -842,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       tc::fence_before_sync();                              // O is read before the next piece's products
       if (more) {
         sync_some(1, 256);                                  // both halves' scores are made
-        place_all(Work(anew, turn(turn_no + 1), G), (turn_no + 1) & 1);
+        place_all(sm.work[(turn_no + 1) & 7], (turn_no + 1) & 1);
       }
     }
   }
@@ -854,12 +865,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
   if (sm.gave_up) {                                         // NaN in all rows of this CTA's pieces
     for (int r = 0; turn(r) < items; ++r) {
       const Work w(plan, turn(r), G);
-      const int slabs = (w.st.n * G + 15) >> 4;
+      const int slabs = (w.n * G + 15) >> 4;
       for (int u = tid; u < w.rows * D; u += kThreads) {
         const int row = u / D, q = w.q0 + row, j = q / G, head = w.kh * G + q - j * G;
         if (w.piece != (int)kWhole)
-          a.rec_ml[((size_t)w.st.rec + ((size_t)w.kh * slabs + (q >> 4)) * w.st.most + w.piece) * 16 + (q & 15)] = make_float2(0.f, __uint_as_float(0x7FC00000u));
-        else a.O[((size_t)(w.st.start + j) * a.qh + head) * D + u % D] = __ushort_as_bfloat16(0x7FC0);
+          a.rec_ml[((size_t)w.rec + ((size_t)w.kh * slabs + (q >> 4)) * w.most + w.piece) * 16 + (q & 15)] = make_float2(0.f, __uint_as_float(0x7FC00000u));
+        else a.O[((size_t)(w.start + j) * a.qh + head) * D + u % D] = __ushort_as_bfloat16(0x7FC0);
       }
     }
   }

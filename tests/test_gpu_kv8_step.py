@@ -340,11 +340,13 @@ def test_nan_stays_with_the_rows_that_attend_to_it(bm):
 
 # ---------------------------------------------------------------- magnitudes
 
-@pytest.mark.parametrize("fmt", FORMATS)
-def test_peaked_and_uneven_values(bm, fmt):
+@pytest.mark.parametrize("seed", [0, 1, 47, 51, 89, 99, 114, 148, 179, 181, 205, 241, 259, 297])
+def test_peaked_and_uneven_values(bm, seed):
     """Scores far apart, V scales over 12 binary orders, heads of zeros."""
+    torch.manual_seed(seed)
+    fmt = seed & 1
     lens, counts = [600, 300, 0], [5, 64, 200]
-    cache = ref.random_cache(fmt, 3, 700, 2, 128, 28, spread=0.0)
+    cache = ref.random_cache(fmt, 3, 700, 2, 128, 28 + seed, spread=0.0)
     cache["Vs"] *= torch.exp2(torch.randint(-6, 7, cache["Vs"].shape, device="cuda").float())
     cache["Ks"] *= torch.exp2(torch.randint(-4, 5, cache["Ks"].shape, device="cuda").float())
     cache["K"][0, 0, 10:50] = 0
@@ -352,7 +354,7 @@ def test_peaked_and_uneven_values(bm, fmt):
     cache["V"][1] = 0
     cache["Vs"][1] = 0
     s = Step(bm, cache, 16, [0, 1, 2], lens, counts, 269)
-    Q = (4 * _rows(269, 16, 128).float()).bfloat16()
+    Q = (4 * _rows(269, 16, 128, seed).float()).bfloat16()
     O = s.attend(Q)
     s.check(Q, O)
     assert (O[5:69] == 0).all()
