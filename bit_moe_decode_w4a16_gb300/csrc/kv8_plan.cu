@@ -12,9 +12,8 @@
 // consecutive positions, all of a stream and head read before any is written.
 //
 // All three are latency: a few kB in the ordinary step.  One cluster of eight
-// CTAs plans it: every CTA makes the streams' running sum for itself (at most
-// 1024 of them), the rows are spread over all, and the first CTA sorts the
-// pieces once the others have reported the trees that are none.
+// CTAs plans it: every CTA makes the streams' running sum and table for itself (at most
+// 1024 of them), and rows and pieces are spread over all.
 #include <cooperative_groups.h>
 
 #include "kv8_step.cuh"
@@ -37,36 +36,48 @@ struct PlanArgs {
 
 struct PlanSmem {
   int start[kMaxStreams + 1], count[kMaxStreams], slot[kMaxStreams], base[kMaxStreams];   // slot -1: refused
-  int bad[kMaxStreams];                       // trees that are none, reported by the warp that looked (of the first CTA only)
+  int bad[kMaxStreams];                       // trees that are none, reported by the warp that looked, to all CTAs
   int from[kMaxStreams + 1];                  // a stream's first piece before sorting
-  int bins[kBins];
-  long long sums[kPlanThreads / 32];
+  Cut cuts[kMaxStreams];
+  int bins[kBins], places[kBins];             // this CTA's pieces by length; where the next of each goes
+  long long sums[3][kPlanThreads / 32];
 };
 
-// Sum of the values of the threads before this one, and of all; every thread of the CTA calls it.
-__device__ __forceinline__ long long scan_before(long long v, long long* sums, long long* all) {
+// Sums of the values of the threads before this one, and of all; every thread of the CTA calls it.
+template <int N>
+__device__ __forceinline__ void scan_before(long long (&v)[N], long long (*sums)[kPlanThreads / 32], long long (&all)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+  long long x[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(kAll, x, o);
-    if (lane >= o) x += y;
+  for (int i = 0; i < N; ++i) {
+    x[i] = v[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(kAll, x[i], o);
+      if (lane >= o) x[i] += y;
+    }
   }
   __syncthreads();                            // `sums` may still be read from the call before
-  if (lane == 31) sums[warp] = x;
+  if (lane == 31) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[i][warp] = x[i];
+  }
   __syncthreads();
-  if (warp == 0) {
-    long long s = sums[lane];
+  if (warp < N) {
+    long long s = sums[warp][lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(kAll, s, o);
       if (lane >= o) s += y;
     }
-    sums[lane] = s;
+    sums[warp][lane] = s;
   }
   __syncthreads();
-  *all = sums[kPlanThreads / 32 - 1];
-  return x - v + (warp ? sums[warp - 1] : 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    all[i] = sums[i][kPlanThreads / 32 - 1];
+    v[i] = x[i] - v[i] + (warp ? sums[i][warp - 1] : 0);
+  }
 }
 
 // The last of a[0 .. n - 1] (rising) that is at most x; a[0] is.
@@ -118,8 +129,10 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     if (slot < 0 || slot >= a.num_slots || base < 0 || count < 0 || (long long)base + count > a.cap) slot = -1;
     sm.bad[tid] = 0;
   }
-  long long total;
-  const int start = (int)scan_before(n, sm.sums, &total);   // at most 2^10 (2^20 + 1)
+  long long before[1] = {n}, all_rows[1];
+  scan_before(before, sm.sums, all_rows);
+  const int start = (int)before[0];           // at most 2^10 (2^20 + 1)
+  const long long total = all_rows[0];
   if (tid < B) {
     if (n > 0 && (long long)start + n > T) slot = -1;
     sm.start[tid] = start;
@@ -143,7 +156,6 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     }
   } else {
     for (int t = (int)min(total, (long long)T) + me; t < T; t += all) put(t, -1, 0, 0);
-    int* report = cluster.map_shared_rank(sm.bad, 0);
     for (int b = me >> 5; b < B; b += all >> 5) {
       const int s0 = sm.start[b], c = sm.count[b], p0 = sm.base[b];
       int to = sm.slot[b];
@@ -172,7 +184,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       fits = __all_sync(kAll, fits);
       if (!fits) {
         to = -1;
-        if (lane == 0) report[b] = 1;
+        if (lane < kPlanCtas) cluster.map_shared_rank(sm.bad, lane)[b] = 1;
         for (int j = lane; j < c; j += 32) put(s0 + j, -1, 0, 0);
         continue;
       }
@@ -188,50 +200,53 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     }
   }
   cluster.sync();
-  if (cta) return;
 
   // ---- the streams' table
   PlanStream st{};
-  Cut cut{0, 1};
-  int pieces = 0, blocks = 0;
+  int blocks = 0;
   if (tid < B) {
     const bool refused = slot < 0 || sm.bad[tid];
     st.start = min(start, T);
     st.base = base;
     st.refused = refused;
     st.slot = refused ? -1 : slot;
-    a.row_start[tid] = st.start;
-    a.after[tid] = refused ? -1 : base + n;
     st.n = refused ? 0 : n;
     st.len = base + st.n;
     st.most = 1;
     if (st.n > 0) {
       st.tree = a.parents && a.parents[start] != -2;
-      cut = cut_of(st.n, st.len, G, a.kvh);
+      const Cut cut = cut_of(st.n, st.len, G, a.kvh);
+      sm.cuts[tid] = cut;
       st.cut = cut.cut;
       st.pitch = cut.pitch;
       st.most = most_pieces(tiles_of(st.len), cut);
       blocks = blocks_of(st.n, G) * a.kvh;
-      pieces = blocks * st.most;
     }
   }
-  if (tid == 0) a.row_start[B] = (int)min(total, (long long)T);
-  long long items, units, records;
-  const int from = (int)scan_before(pieces, sm.sums, &items);
   const long long slabs = st.most > 1 ? ((long long)st.n * G + 15) / 16 * a.kvh : 0;
-  st.unit = (int)scan_before(slabs, sm.sums, &units);
-  st.rec = scan_before(slabs * st.most, sm.sums, &records);
+  long long at[3] = {(long long)blocks * st.most, slabs, slabs * st.most}, sum[3];
+  scan_before(at, sm.sums, sum);
+  st.unit = (int)at[1];
+  st.rec = at[2];
+  const int items = (int)sum[0];
   if (tid < B) {
-    plan.streams[tid] = st;
-    sm.from[tid] = from;
+    if (cta == 0) {
+      plan.streams[tid] = st;
+      a.row_start[tid] = st.start;
+      a.after[tid] = st.refused ? -1 : base + n;
+    }
+    sm.from[tid] = (int)at[0];
     sm.slot[tid] = st.n;                      // what the loops below need of a stream
     sm.base[tid] = st.len;
     sm.count[tid] = st.most;
     sm.bad[tid] = st.tree;
   }
-  if (tid == 0) sm.from[B] = (int)items;
+  if (tid == 0) {
+    sm.from[B] = items;
+    if (cta == 0) a.row_start[B] = (int)min(total, (long long)T);
+  }
 
-  // ---- its pieces, the longest first
+  // ---- its pieces, the longest first: each CTA counts a share of them by length, and puts them behind those of the CTAs before it
   int shift = 0;                              // bins of equal width hold the longest possible piece
   for (long long most = 2ll * tiles_of(a.cap) + 8; (most >> shift) >= kBins; ++shift) {}
   sm.bins[tid] = 0;
@@ -239,7 +254,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   auto piece = [&](int x, PlanItem& it) {     // the bin of piece x, -1: it holds nothing
     const int b = last_at_most(sm.from, B + 1, x), most = sm.count[b], local = x - sm.from[b], i = local / most, c = local - i * most;
     const int sn = sm.slot[b], len = sm.base[b], block = i / a.kvh;
-    const Pieces p(i, cut_of(sn, len, G, a.kvh), extent_of(block, sn, len, G, sm.bad[b]));
+    const Pieces p(i, sm.cuts[b], extent_of(block, sn, len, G, sm.bad[b]));
     if (c >= p.count) return -1;
     it.who = (unsigned)b | (unsigned)(i - block * a.kvh) << 10;
     it.what = (unsigned)block | (p.count == 1 ? kWhole : (unsigned)c) << 16;
@@ -249,21 +264,27 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     return kBins - 1 - (int)((((long long)(it.t1 - it.t0) << wide) + 6) >> shift);
   };
   PlanItem it;
-  for (int x = tid; x < (int)items; x += kPlanThreads) {
+  for (int x = me; x < items; x += all) {
     const int bin = piece(x, it);
     if (bin >= 0) atomicAdd(&sm.bins[bin], 1);
   }
-  __syncthreads();
-  long long kept;
-  const int first = (int)scan_before(sm.bins[tid], sm.sums, &kept);
-  __syncthreads();
-  sm.bins[tid] = first;
-  __syncthreads();
-  for (int x = tid; x < (int)items; x += kPlanThreads) {
-    const int bin = piece(x, it);
-    if (bin >= 0) plan.items[atomicAdd(&sm.bins[bin], 1)] = it;
+  cluster.sync();
+  long long first[1] = {0}, kept[1];
+  int ahead = 0;
+#pragma unroll
+  for (int k = 0; k < kPlanCtas; ++k) {
+    const int v = cluster.map_shared_rank(sm.bins, k)[tid];
+    first[0] += v;
+    if (k < cta) ahead += v;
   }
-  if (tid == 0) *plan.head = PlanHead{kPlanMagic, B, T, a.qh, a.kvh, a.num_slots, a.cap, (int)kept, (int)units, {}};
+  scan_before(first, sm.sums, kept);
+  sm.places[tid] = (int)first[0] + ahead;
+  cluster.sync();                             // nobody reads another CTA's counts any more
+  for (int x = me; x < items; x += all) {
+    const int bin = piece(x, it);
+    if (bin >= 0) plan.items[atomicAdd(&sm.places[bin], 1)] = it;
+  }
+  if (me == 0) *plan.head = PlanHead{kPlanMagic, B, T, a.qh, a.kvh, a.num_slots, a.cap, (int)kept[0], (int)sum[1], {}};
 }
 
 // ---------------------------------------------------------------- the end of a step of trees

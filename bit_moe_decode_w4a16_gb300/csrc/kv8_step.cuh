@@ -94,8 +94,16 @@ struct Pieces {
     cut = c.cut;
     ext = tiles_of(ext_positions);
     from = (long long)i * c.pitch;
-    first = cut ? from / cut : 0;
-    count = cut && ext > 0 ? (int)((from + ext - 1) / cut - first) + 1 : 1;
+    if (!cut || ext <= 0) {
+      first = 0;
+      count = 1;
+    } else if (from + ext < 0x7FFFFFFF) {           // as a rule: a 64-bit quotient takes far longer
+      first = (int)from / cut;
+      count = ((int)from + ext - 1) / cut - (int)first + 1;
+    } else {
+      first = from / cut;
+      count = (int)((from + ext - 1) / cut - first) + 1;
+    }
   }
   __host__ __device__ int begin(int c) const { return c == 0 || !cut ? 0 : (int)((first + c) * cut - from); }
   __host__ __device__ int end(int c) const { return c == count - 1 || !cut ? ext : (int)((first + c + 1) * cut - from); }
