@@ -113,10 +113,11 @@ __device__ __forceinline__ void ancestors(int (&up)[2], unsigned long long (&mas
   }
 }
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) k_kv8_plan(PlanArgs a) {
+// One cluster of one or kPlanCtas CTAs.
+__global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(PlanArgs a) {
   __shared__ PlanSmem sm;
   cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x, B = a.B, T = a.T, G = a.qh / a.kvh;
+  const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x, ctas = gridDim.x, B = a.B, T = a.T, G = a.qh / a.kvh;
   const Plan plan(a.plan, B, T);
 
   // ---- the streams
@@ -148,7 +149,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     a.row_index[t] = index;
     if (a.row_pos) a.row_pos[t] = pos;
   };
-  const int me = cta * kPlanThreads + tid, all = kPlanCtas * kPlanThreads;
+  const int me = cta * kPlanThreads + tid, all = ctas * kPlanThreads;
   if (!a.parents) {
     for (int t = me; t < T; t += all) {
       const int b = last_at_most(sm.start, B + 1, t), at = b < B && sm.slot[b] >= 0 ? sm.base[b] + t - sm.start[b] : 0;
@@ -184,7 +185,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       fits = __all_sync(kAll, fits);
       if (!fits) {
         to = -1;
-        if (lane < kPlanCtas) cluster.map_shared_rank(sm.bad, lane)[b] = 1;
+        if (lane < ctas) cluster.map_shared_rank(sm.bad, lane)[b] = 1;
         for (int j = lane; j < c; j += 32) put(s0 + j, -1, 0, 0);
         continue;
       }
@@ -271,8 +272,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   cluster.sync();
   long long first[1] = {0}, kept[1];
   int ahead = 0;
-#pragma unroll
-  for (int k = 0; k < kPlanCtas; ++k) {
+  for (int k = 0; k < ctas; ++k) {
     const int v = cluster.map_shared_rank(sm.bins, k)[tid];
     first[0] += v;
     if (k < cta) ahead += v;
@@ -415,8 +415,19 @@ bm_status kv8_plan(const bm_kv8_cache* c, int q_heads, const int32_t* slots, con
   const size_t need = kv8::plan_bytes(B, T, q_heads, c->kv_heads);
   if (plan_bytes < need) return refuse("plan of " + std::to_string(plan_bytes) + " bytes, " + std::to_string(need) + " needed");
   const PlanArgs a{plan, slots, lens, counts, parents, row_start, after, row_slot, row_index, row_pos, B, T, q_heads, c->kv_heads, c->slots, c->ctx_cap};
-  k_kv8_plan<<<kPlanCtas, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  // A CTA alone has less to wait for: 8 trees of 17 rows 9.6 us with eight, 8.3 with one; 512 streams of up to 128 rows 20.8 with eight.
+  const int ctas = T <= 2048 && B <= 64 ? 1 : kPlanCtas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv8_plan, a);
   if (e != cudaSuccess) return set_error(BM_ERR_CUDA, std::string("kv8_plan: ") + cudaGetErrorString(e));
   return ok();
 }

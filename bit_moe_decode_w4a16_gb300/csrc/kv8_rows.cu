@@ -315,17 +315,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     const bool swap = c & 4;                                // the second half's pieces in the other order: no bank conflict
     uint4 kr[kTurns], vr[kTurns];
     float scale = 0.f;                                      // of position ct % 128: K's in the first warpgroup, V's in the other
-    auto load = [&](const Work& w, int i, bool v) {
-      const int p0 = (w.t0 + i) * kTile;
-      const size_t at = a.c.row(w.slot, w.kh, p0);
-      const uint8_t* from = (v ? a.c.V : a.c.K) + at * D + 16 * ct;
-      const int left = w.len - p0;
-      uint4* to = v ? vr : kr;
-#pragma unroll
-      for (int u = 0; u < kTurns; ++u)
-        to[u] = u * (kConvert / kLanes) + row0 < left ? ldg_nc_v4(from + u * kConvert * 16) : make_uint4(0, 0, 0, 0);
-      if (!v) scale = (ct & 127) < left ? __ldg((ct < 128 ? a.c.Ks : a.c.Vs) + at + (ct & 127)) : 0.f;
-    };
     auto convert = [&](uint8_t* to, const uint4 (&x)[kTurns]) {
 #pragma unroll
       for (int u = 0; u < kTurns; ++u) {
@@ -339,61 +328,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
         *reinterpret_cast<uint4*>(to + piece(row, 2 * c + !swap)) = swap ? make_uint4(f[0], f[1], f[2], f[3]) : make_uint4(f[4], f[5], f[6], f[7]);
       }
     };
-    int tile = 0;
-    // bit 2 half + buffer: the parity of the half's steps with the buffer so far; the buffer's tile was a step of the half
-    unsigned uses = 0, theirs = 0;
+    // A buffer's last tile was a step of one half or of both: it is free when that one's scores (its products) have been made.
+    // Bit 2 half + buffer: the parity of the half's steps with the buffer so far; the buffer's tile was a step of the half.
+    struct Buffers {
+      unsigned uses = 0, theirs = 0;
+      int tile = 0;
+      __device__ void given(const Work& w, int i) {
+        const unsigned now = (w.wide ? 5u : 1u << (2 * (i & 1))) << (tile & 1);
+        theirs = (theirs & ~(5u << (tile & 1))) | now;
+        uses ^= now;
+        ++tile;
+      }
+    } of_k, of_v;
+    auto free_again = [&](const Buffers& of, uint64_t (&done)[2][2]) {
+      const int b = of.tile & 1;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (of.theirs >> (2 * s + b) & 1) wait(done[s][b], (of.uses >> (2 * s + b) & 1) ^ 1);
+    };
     for (int r = 0; turn(r) < items; ++r) {
       const Work w(plan, turn(r), G);
-      const int own = w.len - w.n, all_see = own + (w.tree ? 0 : w.q0 / G + 1);   // positions that every row attends to
-      load(w, 0, false);
-      load(w, 0, true);
+      const int all_see = w.len - w.n + (w.tree ? 0 : w.q0 / G + 1);   // positions that every row attends to
+      const size_t at0 = a.c.row(w.slot, w.kh, w.t0 * kTile);
+      auto load = [&](int i, uint4 (&to)[kTurns], const uint8_t* of) {
+        const uint8_t* from = of + (at0 + (size_t)i * kTile) * D + 16 * ct;
+        const int left = w.len - (w.t0 + i) * kTile;
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u)
+          to[u] = u * (kConvert / kLanes) + row0 < left ? ldg_nc_v4(from + u * kConvert * 16) : make_uint4(0, 0, 0, 0);
+      };
+      auto load_k = [&](int i) {
+        load(i, kr, a.c.K);
+        scale = (ct & 127) < w.len - (w.t0 + i) * kTile ? __ldg((ct < 128 ? a.c.Ks : a.c.Vs) + at0 + (size_t)i * kTile + (ct & 127)) : 0.f;
+      };
+      // Some rows may not attend to some of these positions, and 0 * NaN is NaN: NaN codes of V become 0, and their positions' scales NaN.
+      auto partly = [&](int i) { return FMT == BM_KV8_E4M3 && (w.t0 + i + 1) * kTile > all_see; };
+      load_k(0);
+      load(0, vr, a.c.V);
       if (ct == 0) {
         if (r == 0) sm.work[0] = w;
         if (turn(r + 1) < items) sm.work[(r + 1) & 7] = Work(plan, turn(r + 1), G);
       }
-      for (int i = 0; i < w.tiles; ++i, ++tile) {
-        const int b = tile & 1, slot = tile & 3;
-        // the buffer's last tile was a step of one half or of both: its scores (its products) have been made
-        auto free_again = [&](uint64_t (&done)[2][2]) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            if (theirs >> (2 * s + b) & 1) wait(done[s][b], (uses >> (2 * s + b) & 1) ^ 1);
-        };
-        free_again(sm.s_ready);
-        if (ct < 128) {
-          sm.ks[slot][ct] = scale;
-        } else {
-          sm.vs[slot][ct - 128] = scale;
-          sm.lg[slot][ct - 128] = fmaxf(log2_fast(scale), -100.f);
-        }
-        if (FMT == BM_KV8_E4M3 && (w.t0 + i + 1) * kTile > all_see) {
-          // some rows do not attend to some of these positions, and 0 * NaN is NaN: a NaN code becomes 0, and its position's scale NaN
-          sync_some(2, kConvert);
-#pragma unroll
-          for (int u = 0; u < kTurns; ++u) {
-            uint32_t* x = reinterpret_cast<uint32_t*>(&vr[u]);
-            uint32_t any = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t nan = ((x[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-              x[e] &= ~((nan >> 7) * 0xFFu);
-              any |= nan;
-            }
-            if (any) sm.vs[slot][u * (kConvert / kLanes) + row0] = __uint_as_float(0x7FC00000u);
+      // K goes a tile ahead of V, whose buffer comes free later; where V's codes are looked at with K's, it waits until they are here.
+      int ik = 0, iv = 0;
+#pragma unroll 1
+      while (iv < w.tiles) {
+        if (ik < w.tiles && (ik == iv || (ik == iv + 1 && !partly(ik)))) {
+          free_again(of_k, sm.s_ready);
+          const int slot = of_k.tile & 3;
+          if (ct < 128) {
+            sm.ks[slot][ct] = scale;
+          } else {
+            sm.vs[slot][ct - 128] = scale;
+            sm.lg[slot][ct - 128] = fmaxf(log2_fast(scale), -100.f);
           }
+          if (partly(ik)) {
+            sync_some(2, kConvert);                         // the scales are there
+#pragma unroll
+            for (int u = 0; u < kTurns; ++u) {
+              uint32_t* y = reinterpret_cast<uint32_t*>(&vr[u]);
+              uint32_t any = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t nan = ((y[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                y[e] &= ~((nan >> 7) * 0xFFu);
+                any |= nan;
+              }
+              if (any) sm.vs[slot][u * (kConvert / kLanes) + row0] = __uint_as_float(0x7FC00000u);
+            }
+          }
+          convert(sm.k[of_k.tile & 1], kr);
+          tc::fence_proxy_async_smem();
+          arrive(sm.k_full[of_k.tile & 1]);
+          of_k.given(w, ik);
+          if (++ik < w.tiles) load_k(ik);
+        } else {
+          free_again(of_v, sm.o_ready);
+          convert(sm.v[of_v.tile & 1], vr);
+          tc::fence_proxy_async_smem();
+          arrive(sm.v_full[of_v.tile & 1]);
+          of_v.given(w, iv);
+          if (++iv < w.tiles) load(iv, vr, a.c.V);
         }
-        convert(sm.k[b], kr);
-        tc::fence_proxy_async_smem();
-        arrive(sm.k_full[b]);
-        if (i + 1 < w.tiles) load(w, i + 1, false);
-        free_again(sm.o_ready);
-        convert(sm.v[b], vr);
-        tc::fence_proxy_async_smem();
-        arrive(sm.v_full[b]);
-        const unsigned now = (w.wide ? 5u : 1u << (2 * (i & 1))) << b;
-        theirs = (theirs & ~(5u << b)) | now;
-        uses ^= now;
-        if (i + 1 < w.tiles) load(w, i + 1, true);
       }
     }
   } else {
