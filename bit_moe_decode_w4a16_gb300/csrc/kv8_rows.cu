@@ -102,8 +102,7 @@ struct RowsSmem {
   int to[2][kBlockRows], lim[2][kBlockRows];
   unsigned long long bits[2][kBlockRows];
   Work work[8];                                             // by turn: the softmax's, two or three behind the conversion's
-  float m[kSub], l[kSub];                                   // of the second warpgroup, where both have the same rows,
-  float other[kSub / 4 * kSub];                             // and 32 columns of its outputs
+  float m[2][kSub], l[2][kSub];                             // maxima and sums of halves that have the same rows
   uint64_t k_full[2], v_full[2];                            // by the tile's parity
   uint64_t s_ready[2][2], o_ready[2][2];                    // by half and the tile's parity: they also say that K, V may be overwritten
   uint64_t p_ready[2], turn[2];                             // by half
@@ -770,51 +769,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       if (more) ask(sm.work[(turn_no + 1) & 7], first_row(sm.work[(turn_no + 1) & 7]));
       if (steps > 0) products_done();
       tc::fence_after_sync();
-      float f0[4], f1[4];                                   // factors of this warpgroup's sums, and of the other's
+      float f[2][4];                                        // where both halves have the same rows: the factors of their sums
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       }
       if (!w.wide) {
-        if (s == 1 && t == 0) {
+        if (t == 0) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            sm.m[row + 8 * r] = m[r];
-            sm.l[row + 8 * r] = l[r];
+            sm.m[s][row + 8 * r] = m[r];
+            sm.l[s][row + 8 * r] = l[r];
           }
         }
+        tc::fence_before_sync();
         sync_some(1, 256);
-        if (s == 0) {
+        tc::fence_after_sync();
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float om = sm.m[row + 8 * r], mn = fmaxf(m[r], om);
-            f0[r] = exp2_fast(m[r] - mn);
-            f1[r] = exp2_fast(om - mn);
-            l[r] = scaled_down(l[r], m[r] - mn) + scaled_down(sm.l[row + 8 * r], om - mn);
-            m[r] = mn;
-          }
+        for (int r = 0; r < 4; ++r) {
+          const float ma = sm.m[0][row + 8 * r], mb = sm.m[1][row + 8 * r], mn = fmaxf(ma, mb);
+          f[0][r] = exp2_fast(ma - mn);
+          f[1][r] = exp2_fast(mb - mn);
+          l[r] = scaled_down(sm.l[0][row + 8 * r], ma - mn) + scaled_down(sm.l[1][row + 8 * r], mb - mn);
+          m[r] = mn;
         }
       }
-      const bool whole = w.piece == (int)kWhole, mine = w.wide || s == 0;
+      const bool whole = w.piece == (int)kWhole;
       // the records of the warp's rows, 16 by 16: the stream's slabs of a kv head, piece by piece
       const int slabs = (n_rows + 15) >> 4, slab = (w.q0 + sub + 32 * (warp & 3)) >> 4;
       const size_t rec = (size_t)w.rec + ((size_t)w.kh * slabs + slab) * w.most + w.piece;
       float inv[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) inv[r] = l[r] == 0.f ? 0.f : 1.f / l[r];   // nothing to attend to: zeros
-      if (!whole && mine && t == 0) {
+      if (!whole && (w.wide || s == 0) && t == 0) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (slab + (r >> 1) < slabs) a.rec_ml[(rec + (size_t)(r >> 1) * w.most) * 16 + g + 8 * (r & 1)] = make_float2(m[r], l[r]);
       }
+      // 32 elements at a time: o[pair of rows][4 j + 2 (r & 1) + e] is element 8 j + 2 t + e.  Both halves' sums lie in the same lanes of
+      // tensor memory, so either warpgroup can join them, and takes half of the elements.
+      const uint32_t o_first = o_cols + lanes;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {                    // 32 elements: o[pair of rows][4 j + 2 (r & 1) + e] is element 8 j + 2 t + e
+      for (int c = w.wide ? 0 : s * (D / 64); c < (w.wide ? D / 32 : (s + 1) * (D / 64)); ++c) {
         float o[2][16];
         {
           uint32_t x[2][16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) tc::tmem_ld_frag32(o_at + h * half + 32 * c, x[h]);
+          for (int h = 0; h < 2; ++h) tc::tmem_ld_frag32((w.wide ? o_at : o_first) + h * half + 32 * c, x[h]);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -824,31 +826,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
               o[h][e] = __uint_as_float(x[h][e]);
             }
         }
-        if (!w.wide) {                                      // joined with the other half's
-          float4* other = reinterpret_cast<float4*>(sm.other) + wt;
-          if (s == 1) {
+        if (!w.wide && w.tiles > 1) {                       // with one tile, the second half has no sums
+          uint32_t x[2][16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) tc::tmem_ld_frag32(o_first + 128 + h * half + 32 * c, x[h]);
+          tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                other[(4 * h + e) * 128] = steps > 0 ? make_float4(o[h][4 * e], o[h][4 * e + 1], o[h][4 * e + 2], o[h][4 * e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-          sync_some(1, 256);
-          if (s == 0) {
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 x = other[(4 * h + e) * 128];
-                o[h][4 * e] = fmaf(x.x, f1[2 * h], o[h][4 * e] * f0[2 * h]);
-                o[h][4 * e + 1] = fmaf(x.y, f1[2 * h], o[h][4 * e + 1] * f0[2 * h]);
-                o[h][4 * e + 2] = fmaf(x.z, f1[2 * h + 1], o[h][4 * e + 2] * f0[2 * h + 1]);
-                o[h][4 * e + 3] = fmaf(x.w, f1[2 * h + 1], o[h][4 * e + 3] * f0[2 * h + 1]);
-              }
-          }
-          sync_some(1, 256);
+            for (int e = 0; e < 16; ++e) {
+              asm volatile("" : "+r"(x[h][e]));
+              const int r = 2 * h + (e >> 1 & 1);
+              o[h][e] = fmaf(__uint_as_float(x[h][e]), f[1][r], o[h][e] * f[0][r]);
+            }
         }
-        if (!mine) continue;
         if (!whole) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
