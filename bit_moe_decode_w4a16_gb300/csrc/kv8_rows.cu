@@ -128,6 +128,19 @@ template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+// As tc::mbar_wait with kWaitLimit, in a few instructions: what all warps run has to fit the instruction cache.
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "again:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " @p bra over;\n add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra again;\n"
+      "over:\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "n"(kWaitLimit)
+      : "memory");
+  return done;
+}
 __device__ __forceinline__ void sync_some(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -215,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     tc::mbar_init(tc::smem_u32(&sm.q_full), 256);
     tc::mbar_init(tc::smem_u32(&sm.drained), 2);
     tc::fence_mbar_init();
+    sm.work[0] = Work(plan, turn(0), G);
     sm.gave_up = 0;
   }
   tc::fence_before_sync();
@@ -225,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
   // all threads take the same way through the barriers of their warpgroup.
   bool ok = true;
   auto wait = [&](uint64_t& bar, int n) {
-    if (ok) ok = tc::mbar_wait(tc::smem_u32(&bar), n & 1, kWaitLimit);
+    if (ok) ok = bounded_wait(tc::smem_u32(&bar), n & 1);
   };
   auto arrive = [&](uint64_t& bar) {
     if (ok) tc::mbar_arrive(tc::smem_u32(&bar));
@@ -365,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       load_k(0);
       load(0, vr, a.c.V);
       if (ct == 0) {
-        if (r == 0) sm.work[0] = w;
         if (turn(r + 1) < items) sm.work[(r + 1) & 7] = Work(plan, turn(r + 1), G);
       }
       // K goes a tile ahead of V, whose buffer comes free later; where V's codes are looked at with K's, it waits until they are here.
@@ -438,10 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       }
     };
     auto place = [&](const Work& w, int row0, int slot) {
+      static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
       const int c = wt % kPieces, j0 = w.q0 / G, rest = w.q0 - j0 * G, own = w.len - w.n;
+      uint8_t* to = sm.q[row0 >> 7] + piece((row0 & 127) + wt / kPieces, c);
+      float* up_to = sm.up[slot] + row0 + wt / kPieces;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int row = row0 + wt / kPieces + u * kStep;
         const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
         uint32_t mx2 = 0;
 #pragma unroll
@@ -457,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
           const __half2 v = __floats2half2_rn(first(y), second(y));
           f[e] = *reinterpret_cast<const uint32_t*>(&v);
         }
-        *reinterpret_cast<uint4*>(sm.q[row >> 7] + piece(row & 127, c)) = make_uint4(f[0], f[1], f[2], f[3]);
-        if (c == 0) sm.up[slot][row] = up;
+        *reinterpret_cast<uint4*>(to + u * kStep * 128) = make_uint4(f[0], f[1], f[2], f[3]);
+        if (c == 0) up_to[u * kStep] = up;
       }
       // a row to a thread: what else there is to know of it
       if (wt < 64) {
@@ -478,18 +493,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       tc::fence_proxy_async_smem();
       arrive(sm.q_full);
     };
-    {
-      const Work w(plan, turn(0), G);
-      ask(w, first_row(w));
-      place_all(w, 0);
-    }
     const int row = 32 * (warp & 3) + g;                    // this thread's rows of its half: row + 8 r
-    for (int turn_no = 0; turn(turn_no) < items; ++turn_no) {
+#pragma unroll 1
+    for (int turn_no = -1;; ++turn_no) {                    // a piece, and the next one's query rows: -1, the first one's alone
+      const bool more = turn(turn_no + 1) < items;
+      const Work& next = sm.work[(turn_no + 1) & 7];
+      if (turn_no >= 0) {
       // a piece's other fields are read where they are needed rather than held: the tiles' loop needs the registers
       bool wide;
       int tiles, t0, lowest, highest;                       // below `lowest` all of the warp's rows attend to, from `highest` on none does
       {
-        const Work w = turn_no ? sm.work[turn_no & 7] : Work(plan, turn(0), G);
+        const Work w = sm.work[turn_no & 7];
         wide = w.wide;
         tiles = w.tiles;
         t0 = w.t0;
@@ -540,14 +554,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
           }
         }
         // None of them too large, nor a sum by itself (where V is zero the weight is, or NaN, whatever p is): the sums are kept.
-        auto keep = [&](const uint64_t (&sum)[4], __half2 top) {
+        auto keep = [&](const uint64_t (&sum)[4], __half2 top, bool held) {
           float sums[4], most = 0.f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             sums[r] = first(sum[r]) + second(sum[r]);
             most = fmaxf(most, sums[r]);
           }
-          const bool good = __all_sync(0xffffffffu, fmaxf(__low2float(top), __high2float(top)) <= kLargest && most < kLargestSum);
+          const bool good = held || __all_sync(0xffffffffu, fmaxf(__low2float(top), __high2float(top)) <= kLargest && most < kLargestSum);
           if (good) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) l[r] += sums[r];
@@ -555,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
           return good;
         };
         // Weights of 32 positions against the present maxima.
-        auto weights = [&](int c, const uint32_t (&v)[2][16], uint32_t (&out)[2][8]) {
+        auto weights = [&](int c, const uint32_t (&v)[2][16], uint32_t (&out)[2][8], bool held) {
           uint64_t sum[4] = {0, 0, 0, 0};
           __half2 top = __float2half2_rn(0.f);
 #pragma unroll
@@ -565,7 +579,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
             for (int r = 0; r < 4; ++r) {
               const uint32_t* x = &v[r >> 1][4 * jj + 2 * (r & 1)];
               const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
-              uint64_t p = pack2(exp2_fast(first(e)), exp2_fast(second(e))), pv = mul2(p, vs);
+              float e0 = first(e), e1 = second(e);
+              if (held) {
+                const float most0 = 9.f - lg_at[32 * c + 8 * jj], most1 = 9.f - lg_at[32 * c + 8 * jj + 1];   // a maximum may lie 8 below
+                e0 = e0 > most0 ? most0 : e0;               // NaN stays
+                e1 = e1 > most1 ? most1 : e1;
+              }
+              uint64_t p = pack2(exp2_fast(e0), exp2_fast(e1)), pv = mul2(p, vs);
               // both: a scale that is not attended to may be NaN
               const bool s0 = see[r] >> (8 * c + 2 * jj) & 1, s1 = see[r] >> (8 * c + 2 * jj + 1) & 1;
               p = pack2(s0 ? first(p) : 0.f, s1 ? second(p) : 0.f);
@@ -576,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
               top = __hmax2(top, h2);
             }
           }
-          return keep(sum, top);
+          return keep(sum, top, held);
         };
         // Weights go where scores were read: 32 positions' into 16 columns.
         auto put = [&](int c, const uint32_t (&out)[2][8]) {
@@ -655,66 +675,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
           }
           move(c, mx);
         };
-        // Where scores are so large that fp32's steps between them matter, 8 positions at a time: products and differences rounded one
-        // by one, so that a maximum is one of the scores and none lies above it by its product's own rounding.
-        auto exact = [&](int c) {
-          float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
 #pragma unroll 1
-          for (int k = 0; k < 8; ++k) {                     // maxima, then weights
-            if (k == 4) move(c, mx);
-            const int j = 4 * c + (k & 3);
-            uint32_t v[2][4], out[2][2];
-            tc::tmem_ld_frag8(s_at + 8 * j, v[0]);
-            tc::tmem_ld_frag8(s_at + half + 8 * j, v[1]);
-            landed(v);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float z[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const bool here = see[r] >> (2 * j + e) & 1;
-                const float y = __fmul_rn(__fmul_rn(__uint_as_float(v[r >> 1][2 * (r & 1) + e]), ks_at[8 * j + e]), qf[r]), p = exp2_fast(__fadd_rn(y, -m[r]));
-                if (k < 4 && here) mx[r] = fmaxf(mx[r], __fadd_rn(y, lg_at[8 * j + e]));
-                if (k >= 4 && here) l[r] += p;
-                z[e] = here ? p * vs_at[8 * j + e] : 0.f;
-              }
-              const __half2 h2 = __floats2half2_rn(z[0], z[1]);
-              out[r >> 1][r & 1] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
-            if (k >= 4) {
-              tc::tmem_st_pairs4(s_at + 4 * j, out[0]);
-              tc::tmem_st_pairs4(s_at + half + 4 * j, out[1]);
-            }
-          }
-        };
-        int made = 0;                                       // positions, in 32, whose weights are there
-        if (lo >= kTile) {                                  // every row attends to all of the tile: the same way for all of the warp
-          uint32_t v[2][2][8];
-          auto read16 = [&](int c, uint32_t (&to)[2][8]) {
-            tc::tmem_ld_frag16(s_at + 16 * c, to[0]);
-            tc::tmem_ld_frag16(s_at + half + 16 * c, to[1]);
-          };
-          if (it == 0) {                                    // a quarter's maxima will do to begin with
-            uint32_t first32[2][16];
-            read(0, first32);
-            landed(first32);
-            maxima(0, first32);
-          }
-          read16(0, v[0]);
-          landed(v[0]);
-          bool good = true;
-#pragma unroll 1
-          for (int c = 0; c < 4 && good; c += 2) {          // half a tile at a time, read ahead by 16 positions
-            uint32_t out[2][2][8];
+        for (int c2 = 0; c2 < 4; c2 += 2) {                 // half a tile at a time
+          bool good = false;
+          if (it + c2 > 0 && 32 * c2 + 64 <= lo) {          // every row attends to all of it: the same way for all of the warp
+            uint32_t v[2][2][8], out[2][2][8];
             uint64_t sum[4] = {0, 0, 0, 0};
             __half2 top = __float2half2_rn(0.f);
+            auto read16 = [&](int c, uint32_t (&to)[2][8]) {
+              tc::tmem_ld_frag16(s_at + 16 * c, to[0]);
+              tc::tmem_ld_frag16(s_at + half + 16 * c, to[1]);
+            };
+            read16(2 * c2, v[0]);
+            landed(v[0]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (k < 3 || c == 0) read16(2 * c + k + 1, v[(k + 1) & 1]);
+            for (int k = 0; k < 4; ++k) {                   // read ahead by 16 positions
+              if (k < 3) read16(2 * c2 + k + 1, v[(k + 1) & 1]);
 #pragma unroll
               for (int jj = 0; jj < 2; ++jj) {
                 const int j = 2 * k + jj;
-                const uint64_t ks = pair(ks_at + 32 * c, j), vs = pair(vs_at + 32 * c, j);
+                const uint64_t ks = pair(ks_at + 32 * c2, j), vs = pair(vs_at + 32 * c2, j);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                   const uint32_t* x = &v[k & 1][r >> 1][4 * jj + 2 * (r & 1)];
@@ -726,32 +706,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
                   top = __hmax2(top, h2);
                 }
               }
-              if (k < 3 || c == 0) landed(v[(k + 1) & 1]);
+              if (k < 3) landed(v[(k + 1) & 1]);
             }
-            if ((good = keep(sum, top))) {
-              put(c, out[0]);
-              put(c + 1, out[1]);
-              made = c + 2;
+            if ((good = keep(sum, top, false))) {
+              put(c2, out[0]);
+              put(c2 + 1, out[1]);
             }
           }
-        }
+          if (!good) {
 #pragma unroll 1
-        for (int c = made; c < 4; ++c) {                    // 32 positions at a time
-          uint32_t out[2][8] = {};
-          bool good = true;
-          if (32 * c < hi) {
-            uint32_t v[2][16];
-            read(c, v);
-            landed(v);
-            good = false;
+            for (int c = c2; c < c2 + 2; ++c) {             // 32 positions at a time
+              uint32_t out[2][8] = {};
+              if (32 * c < hi) {
+                uint32_t v[2][16];
+                read(c, v);
+                landed(v);
+                // against the present maxima, and against moved ones; where scores are so large that fp32's steps between them
+                // matter, some lie above their maximum by its rounding, and are held there
+                good = false;
 #pragma unroll 1
-            for (int turn = it + c == 0; turn < 2 && !good; ++turn) {
-              if (turn) maxima(c, v);
-              good = weights(c, v, out);
+                for (int turn = it + c == 0; turn < 3 && !good; ++turn) {
+                  if (turn) maxima(c, v);
+                  good = weights(c, v, out, turn == 2);
+                }
+              }
+              put(c, out);
             }
-            if (!good) exact(c);
           }
-          if (good) put(c, out);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -764,9 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
 
       // ---- the rows' outputs, or this piece's records
       const Work& w = sm.work[turn_no & 7];
-      const bool more = turn(turn_no + 1) < items;
       const int n_rows = w.n * G, sub = w.wide ? kSub * s : 0;
-      if (more) ask(sm.work[(turn_no + 1) & 7], first_row(sm.work[(turn_no + 1) & 7]));
       if (steps > 0) products_done();
       tc::fence_after_sync();
       float f[2][4];                                        // where both halves have the same rows: the factors of their sums
@@ -858,10 +837,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
         }
       }
       tc::fence_before_sync();                              // O is read before the next piece's products
-      if (more) {
-        sync_some(1, 256);                                  // both halves' scores are made
-        place_all(sm.work[(turn_no + 1) & 7], (turn_no + 1) & 1);
       }
+      if (!more) break;
+      ask(next, first_row(next));
+      sync_some(1, 256);                                    // both halves' scores are made
+      place_all(next, (turn_no + 1) & 1);
     }
   }
   if (!ok) sm.gave_up = 1;
