@@ -20,9 +20,26 @@
 // on in turn: while one makes weights the other's products run.  A block of up
 // to 128 rows instead gives its even tiles to one warpgroup and the odd ones
 // to the other, each with sums of its own, which are joined at the end.
-// A thread has 4 rows x 32 positions of a tile, so that a load of scales serves
-// 8 scores, and holds the scores in registers between maximum and weights.
-// A warpgroup converts codes, one lane issues the MMAs.
+// fp16, not bf16, because every code of either format is exact in it; a query
+// row is scaled by a power of two to fp16's middle, and a weight loses at most
+// 2^-11 of itself, or what lies 2^-25 below the row's largest.
+// Roles: two warps issue MMAs, two warpgroups convert, K a tile ahead of V, and
+// two make weights.  A thread of these has 4 rows x 32 positions of a tile, so
+// that a load of scales serves 8 scores, and works on half a tile at a time
+// against the maximum as it stands: weights that come out too large are made
+// again with the maximum moved.
+//
+// What bounds it: the chain of a tile of 256 x 128 scores, 4600 clocks: one
+// half's weights (2400; 64 multiplications, exponentials and roundings to a
+// thread, twice as long as the half's MMAs), its product, its next scores.
+// Tensor cores are at work 45% of the time; then the start and end of a piece,
+// 8000 to 10000 clocks of query rows and outputs, which is what short prompts
+// and trees mostly are.  Measured, d = 128, 32 of 8 heads, e4m3: a prompt of 8192
+// rows 562 us (978 TFLOP/s; a warp to a row's head, fp32: 58.7 ms), 1000 rows behind
+// 65536 positions (int8) 1180 us (917), 16 prompts of 1000 rows 121 us, 32 trees of 16
+// rows behind 4096 positions 47 us, one of 13 rows 22 us.  Instructions count: at 147 KB
+// of them, with weights of a whole tile at a time, the same prompts took 127 to
+// 135 us; spills to local memory cost more than a second read of tensor memory.
 //
 // Every wait is bounded.  A CTA in which one gave up leaves NaN in the rows of all
 // of its pieces.
@@ -499,344 +516,344 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       const bool more = turn(turn_no + 1) < items;
       const Work& next = sm.work[(turn_no + 1) & 7];
       if (turn_no >= 0) {
-      // a piece's other fields are read where they are needed rather than held: the tiles' loop needs the registers
-      bool wide;
-      int tiles, t0, lowest, highest;                       // below `lowest` all of the warp's rows attend to, from `highest` on none does
-      {
-        const Work w = sm.work[turn_no & 7];
-        wide = w.wide;
-        tiles = w.tiles;
-        t0 = w.t0;
-        const int own = w.len - w.n, row_a = w.q0 + (wide ? kSub * s : 0) + 32 * (warp & 3), row_z = min(row_a + 31, w.n * G - 1);
-        lowest = own + (w.tree ? 0 : row_a / G + 1);
-        highest = row_z < row_a ? 0 : own + (w.tree ? min(w.n, kDrafts) : row_z / G + 1);
-      }
-      const int info = turn_no & 1, mine_at = (wide ? kSub * s : 0) + row;
-      float qf[4], m[4], l[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        m[r] = -1e30f;
-        l[r] = 0.f;
-      }
-      const int steps = wide ? tiles : (tiles + 1 - s) >> 1;
-      for (int it = 0; it < steps; ++it) {
-        const int i = wide ? it : 2 * it + s, tile = tile0 + i, slot = tile & 3, p0 = (t0 + i) * kTile + 2 * t;   // this thread's first position
-        wait(sm.s_ready[s][tile & 1], uses >> (tile & 1) & 1);
-        tc::fence_after_sync();
-        if (it == 0) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) qf[r] = a.scale_log2 * sm.up[info][mine_at + 8 * r];
+        // a piece's other fields are read where they are needed rather than held: the tiles' loop needs the registers
+        bool wide;
+        int tiles, t0, lowest, highest;                       // below `lowest` all of the warp's rows attend to, from `highest` on none does
+        {
+          const Work w = sm.work[turn_no & 7];
+          wide = w.wide;
+          tiles = w.tiles;
+          t0 = w.t0;
+          const int own = w.len - w.n, row_a = w.q0 + (wide ? kSub * s : 0) + 32 * (warp & 3), row_z = min(row_a + 31, w.n * G - 1);
+          lowest = own + (w.tree ? 0 : row_a / G + 1);
+          highest = row_z < row_a ? 0 : own + (w.tree ? min(w.n, kDrafts) : row_z / G + 1);
         }
-        const float *ks_at = sm.ks[slot] + 2 * t, *vs_at = sm.vs[slot] + 2 * t, *lg_at = sm.lg[slot] + 2 * t;
-        auto pair = [](const float* of, int j) { return *reinterpret_cast<const uint64_t*>(of + 8 * j); };
-        // Scores of 32 positions, rows 2 h and 2 h + 1: v[h][4 j + 2 (r & 1) + e].
-        auto read = [&](int c, uint32_t (&v)[2][16]) {
-          tc::tmem_ld_frag32(s_at + 32 * c, v[0]);
-          tc::tmem_ld_frag32(s_at + half + 32 * c, v[1]);
-        };
-        auto landed = [](auto& v) {                         // nothing that was read is used before
-          tc::tmem_wait_ld();
+        const int info = turn_no & 1, mine_at = (wide ? kSub * s : 0) + row;
+        float qf[4], m[4], l[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (auto& x : v[h]) asm volatile("" : "+r"(x));
-        };
-        // of this tile's positions; a row that ends among them has bits of its own
-        const int lo = lowest - (t0 + i) * kTile, hi = highest - (t0 + i) * kTile;
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};             // bit 2 j + e: position 8 j + e of this thread's is attended to
-        if (lo < kTile) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int lim = sm.lim[info][mine_at + 8 * r];
-            const unsigned long long bits = sm.bits[info][mine_at + 8 * r];
-            see[r] = below(lim - p0);
-            if (bits) see[r] |= among(bits, p0 - lim);      // a tree's rows attend to all before the step's own
-          }
+        for (int r = 0; r < 4; ++r) {
+          m[r] = -1e30f;
+          l[r] = 0.f;
         }
-        // None of them too large, nor a sum by itself (where V is zero the weight is, or NaN, whatever p is): the sums are kept.
-        auto keep = [&](const uint64_t (&sum)[4], __half2 top, bool held) {
-          float sums[4], most = 0.f;
+        const int steps = wide ? tiles : (tiles + 1 - s) >> 1;
+        for (int it = 0; it < steps; ++it) {
+          const int i = wide ? it : 2 * it + s, tile = tile0 + i, slot = tile & 3, p0 = (t0 + i) * kTile + 2 * t;   // this thread's first position
+          wait(sm.s_ready[s][tile & 1], uses >> (tile & 1) & 1);
+          tc::fence_after_sync();
+          if (it == 0) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            sums[r] = first(sum[r]) + second(sum[r]);
-            most = fmaxf(most, sums[r]);
+            for (int r = 0; r < 4; ++r) qf[r] = a.scale_log2 * sm.up[info][mine_at + 8 * r];
           }
-          const bool good = held || __all_sync(0xffffffffu, fmaxf(__low2float(top), __high2float(top)) <= kLargest && most < kLargestSum);
-          if (good) {
+          const float *ks_at = sm.ks[slot] + 2 * t, *vs_at = sm.vs[slot] + 2 * t, *lg_at = sm.lg[slot] + 2 * t;
+          auto pair = [](const float* of, int j) { return *reinterpret_cast<const uint64_t*>(of + 8 * j); };
+          // Scores of 32 positions, rows 2 h and 2 h + 1: v[h][4 j + 2 (r & 1) + e].
+          auto read = [&](int c, uint32_t (&v)[2][16]) {
+            tc::tmem_ld_frag32(s_at + 32 * c, v[0]);
+            tc::tmem_ld_frag32(s_at + half + 32 * c, v[1]);
+          };
+          auto landed = [](auto& v) {                         // nothing that was read is used before
+            tc::tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < 4; ++r) l[r] += sums[r];
-          }
-          return good;
-        };
-        // Weights of 32 positions against the present maxima.
-        auto weights = [&](int c, const uint32_t (&v)[2][16], uint32_t (&out)[2][8], bool held) {
-          uint64_t sum[4] = {0, 0, 0, 0};
-          __half2 top = __float2half2_rn(0.f);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
-            const uint64_t ks = pair(ks_at + 32 * c, jj), vs = pair(vs_at + 32 * c, jj);
+              for (auto& x : v[h]) asm volatile("" : "+r"(x));
+          };
+          // of this tile's positions; a row that ends among them has bits of its own
+          const int lo = lowest - (t0 + i) * kTile, hi = highest - (t0 + i) * kTile;
+          uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};             // bit 2 j + e: position 8 j + e of this thread's is attended to
+          if (lo < kTile) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const uint32_t* x = &v[r >> 1][4 * jj + 2 * (r & 1)];
-              const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
-              float e0 = first(e), e1 = second(e);
-              if (held) {
-                const float most0 = 9.f - lg_at[32 * c + 8 * jj], most1 = 9.f - lg_at[32 * c + 8 * jj + 1];   // a maximum may lie 8 below
-                e0 = e0 > most0 ? most0 : e0;               // NaN stays
-                e1 = e1 > most1 ? most1 : e1;
-              }
-              uint64_t p = pack2(exp2_fast(e0), exp2_fast(e1)), pv = mul2(p, vs);
-              // both: a scale that is not attended to may be NaN
-              const bool s0 = see[r] >> (8 * c + 2 * jj) & 1, s1 = see[r] >> (8 * c + 2 * jj + 1) & 1;
-              p = pack2(s0 ? first(p) : 0.f, s1 ? second(p) : 0.f);
-              pv = pack2(s0 ? first(pv) : 0.f, s1 ? second(pv) : 0.f);
-              sum[r] = add2(sum[r], p);
-              const __half2 h2 = __floats2half2_rn(first(pv), second(pv));
-              out[r >> 1][2 * jj + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
-              top = __hmax2(top, h2);
+              const int lim = sm.lim[info][mine_at + 8 * r];
+              const unsigned long long bits = sm.bits[info][mine_at + 8 * r];
+              see[r] = below(lim - p0);
+              if (bits) see[r] |= among(bits, p0 - lim);      // a tree's rows attend to all before the step's own
             }
           }
-          return keep(sum, top, held);
-        };
-        // Weights go where scores were read: 32 positions' into 16 columns.
-        auto put = [&](int c, const uint32_t (&out)[2][8]) {
-          tc::tmem_st_frag16(s_at + 16 * c, out[0]);
-          tc::tmem_st_frag16(s_at + half + 16 * c, out[1]);
-        };
-        // Maxima that have risen by more than 2^8 are moved there, by whole powers of two once there is one, so that the weights of the
-        // tile's positions before 32 c, which are made already, scale exactly; down to the power of two, so that a row's largest weight
-        // stays at 1 or above, 2^25 times what fp16 drops.
-        auto move = [&](int c, float (&mx)[4]) {
-          float f[4];
-          bool moves = false;
+          // None of them too large, nor a sum by itself (where V is zero the weight is, or NaN, whatever p is): the sums are kept.
+          auto keep = [&](const uint64_t (&sum)[4], __half2 top, bool held) {
+            float sums[4], most = 0.f;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-            f[r] = 1.f;
-            if (mx[r] > m[r] + 8.f) {                       // each row by itself: its neighbours stand elsewhere in another step
-              const float by = m[r] == -1e30f ? 0.f : fminf(floorf(mx[r] - m[r]), 200.f);
-              f[r] = by == 0.f || by > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)by) << 23);
-              const float mn = by == 0.f || by == 200.f ? mx[r] : m[r] + by;
-              l[r] = scaled_down(l[r], m[r] - mn);
-              m[r] = mn;
-              moves = true;
+            for (int r = 0; r < 4; ++r) {
+              sums[r] = first(sum[r]) + second(sum[r]);
+              most = fmaxf(most, sums[r]);
             }
-          }
-          if (!__any_sync(0xffffffffu, moves) || it + c == 0) return;
-          if (it > 0) {                                     // O holds the tiles before
-            products_done();
-            tc::fence_after_sync();
+            const bool good = held || __all_sync(0xffffffffu, fmaxf(__low2float(top), __high2float(top)) <= kLargest && most < kLargestSum);
+            if (good) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) l[r] += sums[r];
+            }
+            return good;
+          };
+          // Weights of 32 positions against the present maxima.
+          auto weights = [&](int c, const uint32_t (&v)[2][16], uint32_t (&out)[2][8], bool held) {
+            uint64_t sum[4] = {0, 0, 0, 0};
+            __half2 top = __float2half2_rn(0.f);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+              const uint64_t ks = pair(ks_at + 32 * c, jj), vs = pair(vs_at + 32 * c, jj);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const uint32_t* x = &v[r >> 1][4 * jj + 2 * (r & 1)];
+                const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
+                float e0 = first(e), e1 = second(e);
+                if (held) {
+                  const float most0 = 9.f - lg_at[32 * c + 8 * jj], most1 = 9.f - lg_at[32 * c + 8 * jj + 1];   // a maximum may lie 8 below
+                  e0 = e0 > most0 ? most0 : e0;               // NaN stays
+                  e1 = e1 > most1 ? most1 : e1;
+                }
+                uint64_t p = pack2(exp2_fast(e0), exp2_fast(e1)), pv = mul2(p, vs);
+                // both: a scale that is not attended to may be NaN
+                const bool s0 = see[r] >> (8 * c + 2 * jj) & 1, s1 = see[r] >> (8 * c + 2 * jj + 1) & 1;
+                p = pack2(s0 ? first(p) : 0.f, s1 ? second(p) : 0.f);
+                pv = pack2(s0 ? first(pv) : 0.f, s1 ? second(pv) : 0.f);
+                sum[r] = add2(sum[r], p);
+                const __half2 h2 = __floats2half2_rn(first(pv), second(pv));
+                out[r >> 1][2 * jj + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
+                top = __hmax2(top, h2);
+              }
+            }
+            return keep(sum, top, held);
+          };
+          // Weights go where scores were read: 32 positions' into 16 columns.
+          auto put = [&](int c, const uint32_t (&out)[2][8]) {
+            tc::tmem_st_frag16(s_at + 16 * c, out[0]);
+            tc::tmem_st_frag16(s_at + half + 16 * c, out[1]);
+          };
+          // Maxima that have risen by more than 2^8 are moved there, by whole powers of two once there is one, so that the weights of the
+          // tile's positions before 32 c, which are made already, scale exactly; down to the power of two, so that a row's largest weight
+          // stays at 1 or above, 2^25 times what fp16 drops.
+          auto move = [&](int c, float (&mx)[4]) {
+            float f[4];
+            bool moves = false;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+              mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+              f[r] = 1.f;
+              if (mx[r] > m[r] + 8.f) {                       // each row by itself: its neighbours stand elsewhere in another step
+                const float by = m[r] == -1e30f ? 0.f : fminf(floorf(mx[r] - m[r]), 200.f);
+                f[r] = by == 0.f || by > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)by) << 23);
+                const float mn = by == 0.f || by == 200.f ? mx[r] : m[r] + by;
+                l[r] = scaled_down(l[r], m[r] - mn);
+                m[r] = mn;
+                moves = true;
+              }
+            }
+            if (!__any_sync(0xffffffffu, moves) || it + c == 0) return;
+            if (it > 0) {                                     // O holds the tiles before
+              products_done();
+              tc::fence_after_sync();
 #pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t at = o_at + (k & 1 ? half : 0) + 32 * (k >> 1);
-              const float fa = k & 1 ? f[2] : f[0], fb = k & 1 ? f[3] : f[1];
-              uint32_t o[16];
-              tc::tmem_ld_frag32(at, o);
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t at = o_at + (k & 1 ? half : 0) + 32 * (k >> 1);
+                const float fa = k & 1 ? f[2] : f[0], fb = k & 1 ? f[3] : f[1];
+                uint32_t o[16];
+                tc::tmem_ld_frag32(at, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[e]));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? fb : fa));
+                tc::tmem_st_frag32(at, o);
+              }
+            }
+            tc::tmem_wait_st();
+#pragma unroll 1
+            for (int k = 0; k < 4 * c; ++k) {
+              const uint32_t at = s_at + (k & 1 ? half : 0) + 8 * (k >> 1);
+              const float fa = k & 1 ? f[2] : f[0], fb = k & 1 ? f[3] : f[1];   // in fp32: weights reach 2^15, and fp16 has no 2^-25
+              uint32_t p[4];
+              tc::tmem_ld_pairs8(at, p);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[e]));
+              for (int e = 0; e < 4; ++e) {
+                asm volatile("" : "+r"(p[e]));
+                const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&p[e]));
+                const __half2 y = __floats2half2_rn(w.x * (e & 1 ? fb : fa), w.y * (e & 1 ? fb : fa));
+                p[e] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              tc::tmem_st_pairs8(at, p);
+            }
+          };
+          // The maxima of score + log2 of V's scale.
+          auto maxima = [&](int c, const uint32_t (&v)[2][16]) {
+            float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? fb : fa));
-              tc::tmem_st_frag32(at, o);
+            for (int jj = 0; jj < 4; ++jj) {
+              const uint64_t ks = pair(ks_at + 32 * c, jj), lg = pair(lg_at + 32 * c, jj);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const uint32_t* x = &v[r >> 1][4 * jj + 2 * (r & 1)];
+                const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), lg);
+                if (see[r] >> (8 * c + 2 * jj) & 1) mx[r] = fmaxf(mx[r], first(e));
+                if (see[r] >> (8 * c + 2 * jj + 1) & 1) mx[r] = fmaxf(mx[r], second(e));
+              }
+            }
+            move(c, mx);
+          };
+#pragma unroll 1
+          for (int c2 = 0; c2 < 4; c2 += 2) {                 // half a tile at a time
+            bool good = false;
+            if (it + c2 > 0 && 32 * c2 + 64 <= lo) {          // every row attends to all of it: the same way for all of the warp
+              uint32_t v[2][2][8], out[2][2][8];
+              uint64_t sum[4] = {0, 0, 0, 0};
+              __half2 top = __float2half2_rn(0.f);
+              auto read16 = [&](int c, uint32_t (&to)[2][8]) {
+                tc::tmem_ld_frag16(s_at + 16 * c, to[0]);
+                tc::tmem_ld_frag16(s_at + half + 16 * c, to[1]);
+              };
+              read16(2 * c2, v[0]);
+              landed(v[0]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {                   // read ahead by 16 positions
+                if (k < 3) read16(2 * c2 + k + 1, v[(k + 1) & 1]);
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                  const int j = 2 * k + jj;
+                  const uint64_t ks = pair(ks_at + 32 * c2, j), vs = pair(vs_at + 32 * c2, j);
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) {
+                    const uint32_t* x = &v[k & 1][r >> 1][4 * jj + 2 * (r & 1)];
+                    const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
+                    const uint64_t p = pack2(exp2_fast(first(e)), exp2_fast(second(e))), pv = mul2(p, vs);
+                    sum[r] = add2(sum[r], p);
+                    const __half2 h2 = __floats2half2_rn(first(pv), second(pv));
+                    out[k >> 1][r >> 1][2 * (j & 3) + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
+                    top = __hmax2(top, h2);
+                  }
+                }
+                if (k < 3) landed(v[(k + 1) & 1]);
+              }
+              if ((good = keep(sum, top, false))) {
+                put(c2, out[0]);
+                put(c2 + 1, out[1]);
+              }
+            }
+            if (!good) {
+#pragma unroll 1
+              for (int c = c2; c < c2 + 2; ++c) {             // 32 positions at a time
+                uint32_t out[2][8] = {};
+                if (32 * c < hi) {
+                  uint32_t v[2][16];
+                  read(c, v);
+                  landed(v);
+                  // against the present maxima, and against moved ones; where scores are so large that fp32's steps between them
+                  // matter, some lie above their maximum by its rounding, and are held there
+                  good = false;
+#pragma unroll 1
+                  for (int turn = it + c == 0; turn < 3 && !good; ++turn) {
+                    if (turn) maxima(c, v);
+                    good = weights(c, v, out, turn == 2);
+                  }
+                }
+                put(c, out);
+              }
             }
           }
           tc::tmem_wait_st();
-#pragma unroll 1
-          for (int k = 0; k < 4 * c; ++k) {
-            const uint32_t at = s_at + (k & 1 ? half : 0) + 8 * (k >> 1);
-            const float fa = k & 1 ? f[2] : f[0], fb = k & 1 ? f[3] : f[1];   // in fp32: weights reach 2^15, and fp16 has no 2^-25
-            uint32_t p[4];
-            tc::tmem_ld_pairs8(at, p);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              asm volatile("" : "+r"(p[e]));
-              const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&p[e]));
-              const __half2 y = __floats2half2_rn(w.x * (e & 1 ? fb : fa), w.y * (e & 1 ? fb : fa));
-              p[e] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            tc::tmem_st_pairs8(at, p);
-          }
-        };
-        // The maxima of score + log2 of V's scale.
-        auto maxima = [&](int c, const uint32_t (&v)[2][16]) {
-          float mx[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
-#pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
-            const uint64_t ks = pair(ks_at + 32 * c, jj), lg = pair(lg_at + 32 * c, jj);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const uint32_t* x = &v[r >> 1][4 * jj + 2 * (r & 1)];
-              const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), lg);
-              if (see[r] >> (8 * c + 2 * jj) & 1) mx[r] = fmaxf(mx[r], first(e));
-              if (see[r] >> (8 * c + 2 * jj + 1) & 1) mx[r] = fmaxf(mx[r], second(e));
-            }
-          }
-          move(c, mx);
-        };
-#pragma unroll 1
-        for (int c2 = 0; c2 < 4; c2 += 2) {                 // half a tile at a time
-          bool good = false;
-          if (it + c2 > 0 && 32 * c2 + 64 <= lo) {          // every row attends to all of it: the same way for all of the warp
-            uint32_t v[2][2][8], out[2][2][8];
-            uint64_t sum[4] = {0, 0, 0, 0};
-            __half2 top = __float2half2_rn(0.f);
-            auto read16 = [&](int c, uint32_t (&to)[2][8]) {
-              tc::tmem_ld_frag16(s_at + 16 * c, to[0]);
-              tc::tmem_ld_frag16(s_at + half + 16 * c, to[1]);
-            };
-            read16(2 * c2, v[0]);
-            landed(v[0]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {                   // read ahead by 16 positions
-              if (k < 3) read16(2 * c2 + k + 1, v[(k + 1) & 1]);
-#pragma unroll
-              for (int jj = 0; jj < 2; ++jj) {
-                const int j = 2 * k + jj;
-                const uint64_t ks = pair(ks_at + 32 * c2, j), vs = pair(vs_at + 32 * c2, j);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  const uint32_t* x = &v[k & 1][r >> 1][4 * jj + 2 * (r & 1)];
-                  const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
-                  const uint64_t p = pack2(exp2_fast(first(e)), exp2_fast(second(e))), pv = mul2(p, vs);
-                  sum[r] = add2(sum[r], p);
-                  const __half2 h2 = __floats2half2_rn(first(pv), second(pv));
-                  out[k >> 1][r >> 1][2 * (j & 3) + (r & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
-                  top = __hmax2(top, h2);
-                }
-              }
-              if (k < 3) landed(v[(k + 1) & 1]);
-            }
-            if ((good = keep(sum, top, false))) {
-              put(c2, out[0]);
-              put(c2 + 1, out[1]);
-            }
-          }
-          if (!good) {
-#pragma unroll 1
-            for (int c = c2; c < c2 + 2; ++c) {             // 32 positions at a time
-              uint32_t out[2][8] = {};
-              if (32 * c < hi) {
-                uint32_t v[2][16];
-                read(c, v);
-                landed(v);
-                // against the present maxima, and against moved ones; where scores are so large that fp32's steps between them
-                // matter, some lie above their maximum by its rounding, and are held there
-                good = false;
-#pragma unroll 1
-                for (int turn = it + c == 0; turn < 3 && !good; ++turn) {
-                  if (turn) maxima(c, v);
-                  good = weights(c, v, out, turn == 2);
-                }
-              }
-              put(c, out);
-            }
-          }
+          tc::fence_before_sync();
+          arrive(sm.p_ready[s]);
+          last = tile & 1;
+          last_use = uses >> last & 1;
+          uses ^= 1u << last;
         }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        arrive(sm.p_ready[s]);
-        last = tile & 1;
-        last_use = uses >> last & 1;
-        uses ^= 1u << last;
-      }
-      tile0 += tiles;
+        tile0 += tiles;
 
-      // ---- the rows' outputs, or this piece's records
-      const Work& w = sm.work[turn_no & 7];
-      const int n_rows = w.n * G, sub = w.wide ? kSub * s : 0;
-      if (steps > 0) products_done();
-      tc::fence_after_sync();
-      float f[2][4];                                        // where both halves have the same rows: the factors of their sums
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      }
-      if (!w.wide) {
-        if (t == 0) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            sm.m[s][row + 8 * r] = m[r];
-            sm.l[s][row + 8 * r] = l[r];
-          }
-        }
-        tc::fence_before_sync();
-        sync_some(1, 256);
+        // ---- the rows' outputs, or this piece's records
+        const Work& w = sm.work[turn_no & 7];
+        const int n_rows = w.n * G, sub = w.wide ? kSub * s : 0;
+        if (steps > 0) products_done();
         tc::fence_after_sync();
+        float f[2][4];                                        // where both halves have the same rows: the factors of their sums
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float ma = sm.m[0][row + 8 * r], mb = sm.m[1][row + 8 * r], mn = fmaxf(ma, mb);
-          f[0][r] = exp2_fast(ma - mn);
-          f[1][r] = exp2_fast(mb - mn);
-          l[r] = scaled_down(sm.l[0][row + 8 * r], ma - mn) + scaled_down(sm.l[1][row + 8 * r], mb - mn);
-          m[r] = mn;
+          l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+          l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         }
-      }
-      const bool whole = w.piece == (int)kWhole;
-      // the records of the warp's rows, 16 by 16: the stream's slabs of a kv head, piece by piece
-      const int slabs = (n_rows + 15) >> 4, slab = (w.q0 + sub + 32 * (warp & 3)) >> 4;
-      const size_t rec = (size_t)w.rec + ((size_t)w.kh * slabs + slab) * w.most + w.piece;
-      float inv[4];
+        if (!w.wide) {
+          if (t == 0) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) inv[r] = l[r] == 0.f ? 0.f : 1.f / l[r];   // nothing to attend to: zeros
-      if (!whole && (w.wide || s == 0) && t == 0) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (slab + (r >> 1) < slabs) a.rec_ml[(rec + (size_t)(r >> 1) * w.most) * 16 + g + 8 * (r & 1)] = make_float2(m[r], l[r]);
-      }
-      // 32 elements at a time: o[pair of rows][4 j + 2 (r & 1) + e] is element 8 j + 2 t + e.  Both halves' sums lie in the same lanes of
-      // tensor memory, so either warpgroup can join them, and takes half of the elements.
-      const uint32_t o_first = o_cols + lanes;
-#pragma unroll 1
-      for (int c = w.wide ? 0 : s * (D / 64); c < (w.wide ? D / 32 : (s + 1) * (D / 64)); ++c) {
-        float o[2][16];
-        {
-          uint32_t x[2][16];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) tc::tmem_ld_frag32((w.wide ? o_at : o_first) + h * half + 32 * c, x[h]);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              asm volatile("" : "+r"(x[h][e]));
-              o[h][e] = __uint_as_float(x[h][e]);
+            for (int r = 0; r < 4; ++r) {
+              sm.m[s][row + 8 * r] = m[r];
+              sm.l[s][row + 8 * r] = l[r];
             }
-        }
-        if (!w.wide && w.tiles > 1) {                       // with one tile, the second half has no sums
-          uint32_t x[2][16];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) tc::tmem_ld_frag32(o_first + 128 + h * half + 32 * c, x[h]);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              asm volatile("" : "+r"(x[h][e]));
-              const int r = 2 * h + (e >> 1 & 1);
-              o[h][e] = fmaf(__uint_as_float(x[h][e]), f[1][r], o[h][e] * f[0][r]);
-            }
-        }
-        if (!whole) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (slab + h < slabs) {
-              float4* at = a.rec_o + ((rec + (size_t)h * w.most) * (D / 32) + c) * 128 + lane;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) at[32 * e] = make_float4(o[h][4 * e], o[h][4 * e + 1], o[h][4 * e + 2], o[h][4 * e + 3]);
-            }
-        } else {
+          }
+          tc::fence_before_sync();
+          sync_some(1, 256);
+          tc::fence_after_sync();
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const uint4 p = rounded_row(o[r >> 1] + 2 * (r & 1), inv[r], t);
-            const int to = sm.to[info][mine_at + 8 * r];
-            if (to >= 0) *reinterpret_cast<uint4*>(a.O + (size_t)to * D + 32 * c + 8 * t) = p;
+            const float ma = sm.m[0][row + 8 * r], mb = sm.m[1][row + 8 * r], mn = fmaxf(ma, mb);
+            f[0][r] = exp2_fast(ma - mn);
+            f[1][r] = exp2_fast(mb - mn);
+            l[r] = scaled_down(sm.l[0][row + 8 * r], ma - mn) + scaled_down(sm.l[1][row + 8 * r], mb - mn);
+            m[r] = mn;
           }
         }
-      }
-      tc::fence_before_sync();                              // O is read before the next piece's products
+        const bool whole = w.piece == (int)kWhole;
+        // the records of the warp's rows, 16 by 16: the stream's slabs of a kv head, piece by piece
+        const int slabs = (n_rows + 15) >> 4, slab = (w.q0 + sub + 32 * (warp & 3)) >> 4;
+        const size_t rec = (size_t)w.rec + ((size_t)w.kh * slabs + slab) * w.most + w.piece;
+        float inv[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) inv[r] = l[r] == 0.f ? 0.f : 1.f / l[r];   // nothing to attend to: zeros
+        if (!whole && (w.wide || s == 0) && t == 0) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (slab + (r >> 1) < slabs) a.rec_ml[(rec + (size_t)(r >> 1) * w.most) * 16 + g + 8 * (r & 1)] = make_float2(m[r], l[r]);
+        }
+        // 32 elements at a time: o[pair of rows][4 j + 2 (r & 1) + e] is element 8 j + 2 t + e.  Both halves' sums lie in the same lanes of
+        // tensor memory, so either warpgroup can join them, and takes half of the elements.
+        const uint32_t o_first = o_cols + lanes;
+#pragma unroll 1
+        for (int c = w.wide ? 0 : s * (D / 64); c < (w.wide ? D / 32 : (s + 1) * (D / 64)); ++c) {
+          float o[2][16];
+          {
+            uint32_t x[2][16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) tc::tmem_ld_frag32((w.wide ? o_at : o_first) + h * half + 32 * c, x[h]);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                asm volatile("" : "+r"(x[h][e]));
+                o[h][e] = __uint_as_float(x[h][e]);
+              }
+          }
+          if (!w.wide && w.tiles > 1) {                       // with one tile, the second half has no sums
+            uint32_t x[2][16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) tc::tmem_ld_frag32(o_first + 128 + h * half + 32 * c, x[h]);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                asm volatile("" : "+r"(x[h][e]));
+                const int r = 2 * h + (e >> 1 & 1);
+                o[h][e] = fmaf(__uint_as_float(x[h][e]), f[1][r], o[h][e] * f[0][r]);
+              }
+          }
+          if (!whole) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (slab + h < slabs) {
+                float4* at = a.rec_o + ((rec + (size_t)h * w.most) * (D / 32) + c) * 128 + lane;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) at[32 * e] = make_float4(o[h][4 * e], o[h][4 * e + 1], o[h][4 * e + 2], o[h][4 * e + 3]);
+              }
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint4 p = rounded_row(o[r >> 1] + 2 * (r & 1), inv[r], t);
+              const int to = sm.to[info][mine_at + 8 * r];
+              if (to >= 0) *reinterpret_cast<uint4*>(a.O + (size_t)to * D + 32 * c + 8 * t) = p;
+            }
+          }
+        }
+        tc::fence_before_sync();                              // O is read before the next piece's products
       }
       if (!more) break;
       ask(next, first_row(next));
@@ -876,7 +893,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_rows_merge(RowsArgs a)
   const int units = mine ? plan.head->units * (D / 32) : 0, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = a.qh / a.c.kvh;
   for (int b = threadIdx.x; b < a.B && mine; b += kMergeWarps * 32) unit[b] = plan.streams[b].unit;
   __syncthreads();
-  pdl_wait();
+  bool waited = false;
   for (int u = blockIdx.x * kMergeWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kMergeWarps) {
     const int slab_no = u / (D / 32), c = u % (D / 32);
     int lo = 0, hi = a.B;                                   // the last stream whose units begin at or before this one
@@ -890,6 +907,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_rows_merge(RowsArgs a)
     const int block = slab / (kBlockRows / 16);
     const int n = Pieces(block * a.c.kvh + kh, Cut{st.cut, st.pitch}, extent_of(block, st.n, st.len, G, st.tree)).count;
     if (n == 1) continue;                                   // the block is whole: its outputs are there
+    if (!waited) pdl_wait();                                // the plan was there before; the records are now
+    waited = true;
     const size_t rec = (size_t)st.rec + (size_t)local * st.most;
     const float4* o = a.rec_o + (rec * (D / 32) + c) * 128 + lane;
     const float2* ml = a.rec_ml + rec * 16 + g;
@@ -935,6 +954,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_rows_merge(RowsArgs a)
       if (q < n_rows) *reinterpret_cast<uint4*>(a.O + ((size_t)(st.start + j) * a.qh + kh * G + q - j * G) * D + 32 * c + 8 * t) = p;
     }
   }
+  if (!waited) pdl_wait();                                  // done means done: the kernel before is
 }
 
 template <int D, int FMT>

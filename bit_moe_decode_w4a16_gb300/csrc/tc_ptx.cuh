@@ -141,11 +141,6 @@ __device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t (&v)[8])
                : "r"(taddr)
                : "memory");
 }
-// As tmem_st_frag16, 4 columns.
-__device__ __forceinline__ void tmem_st_pairs4(uint32_t taddr, const uint32_t (&v)[2]) {
-  __syncwarp();
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(v[0]), "r"(v[1]) : "memory");
-}
 // As tmem_st_frag16, 8 columns.
 __device__ __forceinline__ void tmem_st_pairs8(uint32_t taddr, const uint32_t (&v)[4]) {
   __syncwarp();
@@ -218,9 +213,6 @@ __device__ __forceinline__ void warp_mma_commit(uint32_t mbar_smem, uint32_t on)
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(mbar_smem),
       "r"(on)
       : "memory");
-}
-__device__ __forceinline__ void warp_mbar_arrive(uint32_t mbar_smem, uint32_t on) {
-  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(mbar_smem), "r"(on) : "memory");
 }
 
 // Arrive once on the mbarrier when all earlier tcgen05 ops of this thread complete.
