@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
         scale = (ct & 127) < w.len - (w.t0 + i) * kTile ? __ldg((ct < 128 ? a.c.Ks : a.c.Vs) + at0 + (size_t)i * kTile + (ct & 127)) : 0.f;
       };
       // Some rows may not attend to some of these positions, and 0 * NaN is NaN: NaN codes of V become 0, and their positions' scales NaN.
-      auto partly = [&](int i) { return FMT == BM_KV8_E4M3 && (w.t0 + i + 1) * kTile > all_see; };
+      auto partly = [&](int i) { return FMT == BM_KV8_E4M3 && (w.t0 + i) * kTile > all_see - kTile; };
       load_k(0);
       load(0, vr, a.c.V);
       if (ct == 0) {

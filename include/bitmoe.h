@@ -567,6 +567,8 @@ size_t kv8_plan_bytes(int B, int T, int q_heads, int kv_heads);
  * refused by itself: after[b] = -1, its rows and those behind the last
  * stream's get row_slot -1 (padding for kv8_append), index and pos 0, and the
  * other calls leave their outputs for it alone where they say so.
+ * Streams that name one slot share its positions; where two rows of a step go to
+ * the same position of it, what is left there is undefined, as in kv8_append.
  * `plan` also holds how the attention splits the step, for caches of c's
  * slots, ctx_cap and kv_heads and these q_heads (of c, K, V and their scales
  * are not touched).  The calls below take it as it is; while they run it may

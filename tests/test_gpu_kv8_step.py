@@ -338,6 +338,32 @@ def test_nan_stays_with_the_rows_that_attend_to_it(bm):
     assert O[bad].isnan().all() and O[~bad].isfinite().all()
 
 
+@pytest.mark.parametrize("fmt,qh,kvh,d,n,base", [(E4M3, 16, 2, 128, 40, 700), (INT8, 8, 1, 64, 33, 0), (E4M3, 32, 4, 128, 700, 100)])
+def test_spoilt_query_rows_leave_their_neighbours(bm, fmt, qh, kvh, d, n, base):
+    """NaN and infinities in a few heads of a few rows: the same warps' other rows are as near as ever."""
+    cache = _filled(fmt, [base], [n], kvh, d, 28)
+    s = Step(bm, cache, qh, [0], [base], [n], n)
+    Q = _rows(n, qh, d)
+    bad = torch.zeros(n, qh, dtype=torch.bool, device="cuda")
+    for j, h, x in ((3, 2, "nan"), (4, 3, "inf"), (5, 0, "-inf"), (n - 1, qh - 1, "inf"), (n // 2, 1, "nan")):
+        bad[j, h] = True
+        Q[j, h, (5 * j + h) % d] = float(x)
+    O = s.attend(Q)
+    assert O[bad].isnan().all()
+    Q[bad] = 0
+    O[bad] = s.attend(Q)[bad]
+    s.check(Q, O)
+
+
+def test_streams_of_one_slot(bm):
+    """A slot that several streams of a step read, their rows at positions of their own; one stream's rows lie among another's past."""
+    lens, counts = [0, 300, 100, 300, 700], [100, 40, 200, 1, 64]
+    cache = ref.random_cache(E4M3, 1, 800, 2, 128, 30)
+    s = Step(bm, cache, 16, [0] * 5, lens, counts, sum(counts))
+    Q = _rows(sum(counts), 16, 128)
+    s.check(Q, s.attend(Q))
+
+
 # ---------------------------------------------------------------- magnitudes
 
 @pytest.mark.parametrize("seed", [0, 1, 47, 51, 89, 99, 114, 148, 179, 181, 205, 241, 259, 297])
