@@ -321,6 +321,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
         my_turn();
         if (s < steps) scores(s);
         pass();
+        // the next piece's query rows into L2; its fields came with this piece's first codes
+        if (s < steps && turn(r + 1) < items) {
+          const Work& next = sm.work[(r + 1) & 7];
+          const int q0 = next.q0 + s * kSub + lane, end = min(next.n * G, next.q0 + kBlockRows);
+          const bf16* from = a.Q + ((size_t)next.start * a.qh + next.kh * G) * D;
+          for (int q = q0; q < min(end, q0 - lane + kSub); q += 32) {
+            const bf16* at = from + ((size_t)(q / G) * a.qh + q % G) * D;
+#pragma unroll
+            for (int e = 0; e < D; e += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + e));
+          }
+        }
         for (int k = s; k < steps; k += 2) {
           if (k + 2 < steps) wait(sm.k_full[tile_of(k + 2) & 1], tile_of(k + 2) >> 1);
           product(k);
