@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, half = 16u << 16;
     const uint32_t s_at = s_cols + s * kTile + lanes, o_at = o_cols + s * 128 + lanes;
     int tile0 = 0;                                          // the CTA's tiles so far
-    unsigned uses = 0, last = 0, last_use = 0;              // bit b: the parity of this half's steps with buffer b; the latest step's buffer, and that parity before it
-    auto products_done = [&]() { wait(sm.o_ready[s][last], last_use); };
+    unsigned uses = 0, last = 0;                            // bit b: the parity of this half's steps with buffer b; the latest step's buffer
+    auto products_done = [&]() { wait(sm.o_ready[s][last], (uses >> last & 1) ^ 1); };
     // ---- a block's query rows as fp16 of about their own magnitude, d / 8 lanes to a row, asked for while the piece before ends.  All rows
     // of the halves in use are written, whatever the block's own: 128 of this half's, or 64 of the half that both share.
     auto first_row = [&](const Work& w) { return w.wide ? kSub * s : 64 * s; };
@@ -526,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     for (int turn_no = -1;; ++turn_no) {                    // a piece, and the next one's query rows: -1, the first one's alone
       const bool more = turn(turn_no + 1) < items;
       const Work& next = sm.work[(turn_no + 1) & 7];
+      float m[4], l[4];
       if (turn_no >= 0) {
         // a piece's other fields are read where they are needed rather than held: the tiles' loop needs the registers
         bool wide;
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
           highest = row_z < row_a ? 0 : own + (w.tree ? min(w.n, kDrafts) : row_z / G + 1);
         }
         const int info = turn_no & 1, mine_at = (wide ? kSub * s : 0) + row;
-        float qf[4], m[4], l[4];
+        float qf[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           m[r] = -1e30f;
@@ -766,15 +767,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
           tc::fence_before_sync();
           arrive(sm.p_ready[s]);
           last = tile & 1;
-          last_use = uses >> last & 1;
           uses ^= 1u << last;
         }
         tile0 += tiles;
-
+      }
+      // ---- the next piece's query rows go first, so that its first scores are made while this one's outputs are written
+      if (more) {
+        ask(next, first_row(next));
+        sync_some(1, 256);                                  // both halves' scores are made
+        place_all(next, (turn_no + 1) & 1);
+      }
+      if (turn_no >= 0) {
         // ---- the rows' outputs, or this piece's records
         const Work& w = sm.work[turn_no & 7];
-        const int n_rows = w.n * G, sub = w.wide ? kSub * s : 0;
-        if (steps > 0) products_done();
+        const int n_rows = w.n * G, sub = w.wide ? kSub * s : 0, mine_at = sub + row, info = turn_no & 1;
+        if (w.wide || w.tiles > s) products_done();           // this half has had steps
         tc::fence_after_sync();
         float f[2][4];                                        // where both halves have the same rows: the factors of their sums
 #pragma unroll
@@ -864,12 +871,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
             }
           }
         }
-        tc::fence_before_sync();                              // O is read before the next piece's products
+        tc::fence_before_sync();                            // O is read before the next piece's products
+        if (!w.wide) sync_some(1, 256);                     // by both halves
       }
       if (!more) break;
-      ask(next, first_row(next));
-      sync_some(1, 256);                                    // both halves' scores are made
-      place_all(next, (turn_no + 1) & 1);
     }
   }
   if (!ok) sm.gave_up = 1;
