@@ -85,7 +85,7 @@ struct Work {
   long long rec;                        // its first record
   int most, tree;
   int kh, q0, rows, wide;               // kv head; first of the block's query rows and their number; both halves have some
-  int t0, tiles, piece, pad;            // tiles from t0 on; 65535: the whole block
+  int t0, tiles, piece, j0;             // tiles from t0 on; 65535: the whole block; the stream's row of the first query row
   Work() = default;
   __device__ Work(const Plan& plan, int i, int G) {
     const PlanItem it = plan.items[i];
@@ -101,6 +101,7 @@ struct Work {
     q0 = (it.what & 65535) * kBlockRows;
     rows = min(kBlockRows, n * G - q0);
     wide = rows > kSub;
+    j0 = q0 / G;
     t0 = it.t0;
     tiles = it.t1 - it.t0;
     piece = it.what >> 16;
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
         if (s < steps) scores(s);
         pass();
         // the next piece's query rows into L2; its fields came with this piece's first codes
-        if (s < steps && turn(r + 1) < items) {
+        if (ok && s < steps && turn(r + 1) < items) {
           const Work& next = sm.work[(r + 1) & 7];
           const int q0 = next.q0 + s * kSub + lane, end = min(next.n * G, next.q0 + kBlockRows);
           const bf16* from = a.Q + ((size_t)next.start * a.qh + next.kh * G) * D;
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     };
     for (int r = 0; turn(r) < items; ++r) {
       const Work w(plan, turn(r), G);
-      const int all_see = w.len - w.n + (w.tree ? 0 : w.q0 / G + 1);   // positions that every row attends to
+      const int all_see = w.len - w.n + (w.tree ? 0 : w.j0 + 1);   // positions that every row attends to
       const size_t at0 = a.c.row(w.slot, w.kh, w.t0 * kTile);
       auto load = [&](int i, uint4 (&to)[kTurns], const uint8_t* of) {
         const uint8_t* from = of + (at0 + (size_t)i * kTile) * D + 16 * ct;
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       load_k(0);
       load(0, vr, a.c.V);
       if (ct == 0) {
-        if (turn(r + 1) < items) sm.work[(r + 1) & 7] = Work(plan, turn(r + 1), G);
+        if (ok && turn(r + 1) < items) sm.work[(r + 1) & 7] = Work(plan, turn(r + 1), G);   // not by one that waits for nothing any more
       }
       // K goes a tile ahead of V, whose buffer comes free later; where V's codes are looked at with K's, it waits until they are here.
       int ik = 0, iv = 0;
@@ -466,21 +467,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     // of the halves in use are written, whatever the block's own: 128 of this half's, or 64 of the half that both share.
     auto first_row = [&](const Work& w) { return w.wide ? kSub * s : 64 * s; };
     constexpr int kPieces = D / 8, kStep = 128 / kPieces, kBatch = 64 / kStep;
-    const float inv_g = 1.f / G;
-    uint4 x[kBatch];
-    auto ask = [&](const Work& w, int row0) {
-      const int c = wt % kPieces, j0 = w.q0 / G, rest = w.q0 - j0 * G;
+    auto of_group = [&](int x) { return (int)__fdividef(x + 0.5f, (float)G); };   // x / G, x below 2^9: off by a few 2^-24 of it, and at least 2^-4 from a border
+    auto ask = [&](const Work& w, int row0, uint4 (&x)[kBatch]) {
+      const int c = wt % kPieces, j0 = w.j0, rest = w.q0 - j0 * G;
       const bf16* from = a.Q + ((size_t)w.start * a.qh + w.kh * G) * D + 8 * c;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int row = row0 + wt / kPieces + u * kStep, q = w.q0 + row, j = j0 + (int)((rest + row + 0.5f) * inv_g);   // q / G: the quotient's argument is below 2^9
+        const int row = row0 + wt / kPieces + u * kStep, q = w.q0 + row, j = j0 + of_group(rest + row);
         x[u] = make_uint4(0, 0, 0, 0);
         if (q < w.n * G) x[u] = *reinterpret_cast<const uint4*>(from + ((size_t)j * a.qh + q - j * G) * D);
       }
     };
-    auto place = [&](const Work& w, int row0, int slot) {
+    auto place = [&](const Work& w, int row0, int slot, const uint4 (&x)[kBatch]) {
       static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
-      const int c = wt % kPieces, j0 = w.q0 / G, rest = w.q0 - j0 * G, own = w.len - w.n;
+      const int c = wt % kPieces, j0 = w.j0, rest = w.q0 - j0 * G, own = w.len - w.n;
       uint8_t* to = sm.q[row0 >> 7] + piece((row0 & 127) + wt / kPieces, c);
       float* up_to = sm.up[slot] + row0 + wt / kPieces;
 #pragma unroll
@@ -505,18 +505,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       }
       // a row to a thread: what else there is to know of it
       if (wt < 64) {
-        const int row = row0 + wt, q = w.q0 + row, j = j0 + (int)((rest + row + 0.5f) * inv_g);
+        const int row = row0 + wt, q = w.q0 + row, j = j0 + of_group(rest + row);
         const bool live = q < w.n * G;
         sm.to[slot][row] = live ? (w.start + j) * a.qh + w.kh * G + q - j * G : -1;
         sm.lim[slot][row] = w.tree ? own : own + j + 1;
         sm.bits[slot][row] = live && w.tree ? plan.masks[w.start + j] : 0;
       }
     };
-    auto place_all = [&](const Work& w, int slot) {
+    auto place_all = [&](const Work& w, int slot, uint4 (&x)[kBatch]) {
 #pragma unroll 1
       for (int k = 0; k <= w.wide; ++k) {
-        if (k) ask(w, first_row(w) + 64);
-        place(w, first_row(w) + 64 * k, slot);
+        if (k) ask(w, first_row(w) + 64, x);
+        place(w, first_row(w) + 64 * k, slot, x);
       }
       tc::fence_proxy_async_smem();
       arrive(sm.q_full);
@@ -536,9 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
           wide = w.wide;
           tiles = w.tiles;
           t0 = w.t0;
-          const int own = w.len - w.n, row_a = w.q0 + (wide ? kSub * s : 0) + 32 * (warp & 3), row_z = min(row_a + 31, w.n * G - 1);
-          lowest = own + (w.tree ? 0 : row_a / G + 1);
-          highest = row_z < row_a ? 0 : own + (w.tree ? min(w.n, kDrafts) : row_z / G + 1);
+          const int own = w.len - w.n, rest = w.q0 - w.j0 * G, a_at = (wide ? kSub * s : 0) + 32 * (warp & 3), z_at = min(a_at + 31, w.rows - 1);
+          lowest = own + (w.tree ? 0 : w.j0 + of_group(rest + a_at) + 1);
+          highest = z_at < a_at ? 0 : own + (w.tree ? min(w.n, kDrafts) : w.j0 + of_group(rest + z_at) + 1);
         }
         const int info = turn_no & 1, mine_at = (wide ? kSub * s : 0) + row;
         float qf[4];
@@ -773,9 +773,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       }
       // ---- the next piece's query rows go first, so that its first scores are made while this one's outputs are written
       if (more) {
-        ask(next, first_row(next));
-        sync_some(1, 256);                                  // both halves' scores are made
-        place_all(next, (turn_no + 1) & 1);
+        if (!ok) sm.work[(turn_no + 1) & 7] = Work(plan, turn(turn_no + 1), G);   // whoever gave up may be ahead of the conversion
+        // A half without a step in this piece has waited for nothing: what the conversion left of the next one is there when
+        // the other half, which had the step, has come here.
+        const bool idle = turn_no >= 0 && !sm.work[turn_no & 7].wide && sm.work[turn_no & 7].tiles == 1;
+        if (idle) sync_some(1, 256);
+        uint4 x[kBatch];
+        ask(next, first_row(next), x);
+        if (!idle) sync_some(1, 256);                       // both halves' scores are made
+        place_all(next, (turn_no + 1) & 1, x);
       }
       if (turn_no >= 0) {
         // ---- the rows' outputs, or this piece's records

@@ -573,6 +573,21 @@ def test_offsets_past_32_bits(bm):
     assert torch.equal(got[:, 21], before[:, 27]) and torch.equal(got[:, 22], before[:, 39]) and torch.equal(got[:, 23:], before[:, 23:])
 
 
+@pytest.mark.parametrize("fmt,qh,kvh,d,most", [(E4M3, 32, 8, 128, 128), (INT8, 8, 8, 64, 128), (E4M3, 16, 4, 64, 300)])
+def test_many_short_streams(bm, fmt, qh, kvh, d, most):
+    """More pieces of one tile than the GPU has SMs, many times over, some of two or three tiles among them: a CTA goes from one to the next."""
+    rs = random.Random(most + d)
+    lens = [rs.randrange(most) for _ in range(700)]
+    counts = [min(rs.choice([1, 1, 2, 7, 16]), most - n) for n in lens]
+    cache = _filled(fmt, lens, counts, kvh, d, 40)
+    s = Step(bm, cache, qh, list(range(700)), lens, counts, sum(counts) + 3)
+    Q = _rows(sum(counts) + 3, qh, d)
+    O = s.attend(Q)
+    s.check(Q, O)
+    for _ in range(10):
+        assert torch.equal(s.attend(Q), O)
+
+
 def test_largest_step(bm):
     """1024 streams, some of them on one slot."""
     rs = random.Random(8)
