@@ -33,11 +33,12 @@
 // half's weights (2400; 64 multiplications, exponentials and roundings to a
 // thread, twice as long as the half's MMAs), its product, its next scores.
 // Tensor cores are at work 45% of the time; then the start and end of a piece,
-// 8000 to 10000 clocks of query rows and outputs, which is what short prompts
-// and trees mostly are.  Measured, d = 128, 32 of 8 heads, e4m3: a prompt of 8192
-// rows 562 us (978 TFLOP/s; a warp to a row's head, fp32: 58.7 ms), 1000 rows behind
-// 65536 positions (int8) 1180 us (917), 16 prompts of 1000 rows 121 us, 32 trees of 16
-// rows behind 4096 positions 47 us, one of 13 rows 22 us.  Instructions count: at 147 KB
+// 5000 to 7000 clocks of query rows, whose place comes free with the last scores,
+// 5000 of outputs beside the next scores, and a first and a masked tile of
+// twice the work: what short prompts and trees mostly are.  Measured, d = 128, 32 query and 4 kv heads, e4m3: a prompt of 8192
+// rows 556 us (988 TFLOP/s; a warp to a row's head, fp32: 58.7 ms), 1000 rows behind
+// 65536 positions (int8) 1180 us (917), 16 prompts of up to 1000 rows 116 to 120 us, 32 trees
+// of 16 rows behind 4096 positions 46 us, one of 13 rows 23 us.  Instructions count: at 147 KB
 // of them, with weights of a whole tile at a time, the same prompts took 127 to
 // 135 us; spills to local memory cost more than a second read of tensor memory.
 //
@@ -119,14 +120,14 @@ struct RowsSmem {
   float up[2][kBlockRows];
   int to[2][kBlockRows], lim[2][kBlockRows];
   unsigned long long bits[2][kBlockRows];
-  Work work[8];                                             // by turn: the softmax's, two or three behind the conversion's
+  Work work[8];                                             // by turn: written two ahead of the conversion's, which is up to four ahead of the softmax's
   float m[2][kSub], l[2][kSub];                             // maxima and sums of halves that have the same rows
   uint64_t k_full[2], v_full[2];                            // by the tile's parity
   uint64_t s_ready[2][2], o_ready[2][2];                    // by half and the tile's parity: they also say that K, V may be overwritten
   uint64_t p_ready[2], turn[2];                             // by half
   uint64_t q_full, drained;
   uint32_t tmem;
-  int gave_up;
+  int gave_up, stop[2];                                     // a wait gave up; one of the softmax's, by the turn's parity
 };
 
 // 16-byte piece c of row r: 128-byte rows of 64 fp16, pieces swizzled by the row.
@@ -247,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     tc::mbar_init(tc::smem_u32(&sm.drained), 2);
     tc::fence_mbar_init();
     sm.work[0] = Work(plan, turn(0), G);
-    sm.gave_up = 0;
+    if (turn(1) < items) sm.work[1] = Work(plan, turn(1), G);
+    sm.gave_up = sm.stop[0] = sm.stop[1] = 0;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
         my_turn();
         if (s < steps) scores(s);
         pass();
-        // the next piece's query rows into L2; its fields came with this piece's first codes
+        // the next piece's query rows into L2; its fields were there before this piece's first codes
         if (ok && s < steps && turn(r + 1) < items) {
           const Work& next = sm.work[(r + 1) & 7];
           const int q0 = next.q0 + s * kSub + lane, end = min(next.n * G, next.q0 + kBlockRows);
@@ -407,8 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       auto partly = [&](int i) { return FMT == BM_KV8_E4M3 && (w.t0 + i) * kTile > all_see - kTile; };
       load_k(0);
       load(0, vr, a.c.V);
+      // two pieces ahead: a half without steps in a piece waits for nothing there, and has seen only what was written before the piece
+      // before; not by a thread that waits for nothing any more
       if (ct == 0) {
-        if (ok && turn(r + 1) < items) sm.work[(r + 1) & 7] = Work(plan, turn(r + 1), G);   // not by one that waits for nothing any more
+        if (ok && turn(r + 2) < items) sm.work[(r + 2) & 7] = Work(plan, turn(r + 2), G);
       }
       // K goes a tile ahead of V, whose buffer comes free later; where V's codes are looked at with K's, it waits until they are here.
       int ik = 0, iv = 0;
@@ -467,7 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     // of the halves in use are written, whatever the block's own: 128 of this half's, or 64 of the half that both share.
     auto first_row = [&](const Work& w) { return w.wide ? kSub * s : 64 * s; };
     constexpr int kPieces = D / 8, kStep = 128 / kPieces, kBatch = 64 / kStep;
-    auto of_group = [&](int x) { return (int)__fdividef(x + 0.5f, (float)G); };   // x / G, x below 2^9: off by a few 2^-24 of it, and at least 2^-4 from a border
+    // x / G, x below 2^9: the quotient is off by a few 2^-24 of itself, and at least 2^-4 from a border
+    auto of_group = [&](int x) { return (int)__fdividef(x + 0.5f, (float)G); };
     auto ask = [&](const Work& w, int row0, uint4 (&x)[kBatch]) {
       const int c = wt % kPieces, j0 = w.j0, rest = w.q0 - j0 * G;
       const bf16* from = a.Q + ((size_t)w.start * a.qh + w.kh * G) * D + 8 * c;
@@ -773,14 +778,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       }
       // ---- the next piece's query rows go first, so that its first scores are made while this one's outputs are written
       if (more) {
-        if (!ok) sm.work[(turn_no + 1) & 7] = Work(plan, turn(turn_no + 1), G);   // whoever gave up may be ahead of the conversion
-        // A half without a step in this piece has waited for nothing: what the conversion left of the next one is there when
-        // the other half, which had the step, has come here.
-        const bool idle = turn_no >= 0 && !sm.work[turn_no & 7].wide && sm.work[turn_no & 7].tiles == 1;
-        if (idle) sync_some(1, 256);
+        if (!ok) sm.stop[turn_no & 1] = 1;
         uint4 x[kBatch];
         ask(next, first_row(next), x);
-        if (!idle) sync_some(1, 256);                       // both halves' scores are made
+        sync_some(1, 256);                                  // both halves' scores are made
+        if (sm.stop[turn_no & 1]) break;                    // both halves or none: the flag is next written behind another such barrier
         place_all(next, (turn_no + 1) & 1, x);
       }
       if (turn_no >= 0) {
