@@ -12,7 +12,7 @@
 // tensor memory):
 //   S[row][position] = Q K^T, MMAs of 128 x 128 x 16, both in shared memory;
 //   weights 2^(S ks qf - m) vs, as fp16, over S's place in tensor memory; m is
-//     the running maximum of x + log2 vs, moved only when it rises by 2^8;
+//     a reference at or below the running maximum of x + log2 vs, moved only when a weight passes 2^15;
 //   O[row][element] += P V, MMAs of 128 x d x 16, A in tensor memory, B the
 //     tile's V as it lies (positions down, elements along: N-major).
 // K and V are converted to fp16 with the same layout (128-byte swizzle), once
@@ -22,12 +22,19 @@
 // to the other, each with sums of its own, which are joined at the end.
 // fp16, not bf16, because every code of either format is exact in it; a query
 // row is scaled by a power of two to fp16's middle, and a weight loses at most
-// 2^-11 of itself, or what lies 2^-25 below the row's largest.
+// 2^-11 of itself, or half of fp16's last step, 2^-25.  The largest weight of a row is 1 or
+// more, in long pieces 2^4 or 2^8: what many light weights lose together is then at most
+// 2^-12 of it in a piece of up to 2^21 positions (with 1 throughout, 2^19 positions of
+// 2^-25.1 each were lost, 1.5% of it, also for elements to which the large one gives nothing).
+// A reference that begins lower has less room before it is moved: 4% of the time of 1000
+// rows behind 65536 positions.  Beside a large sum the tensor cores themselves cut products off
+// at 2^-25 of its binary order, and sums of 16 of them at 2^-23: pieces of more than 2^17
+// positions can lose more than the output's rounding to that.
 // Roles: two warps issue MMAs, two warpgroups convert, K a tile ahead of V, and
 // two make weights.  A thread of these has 4 rows x 32 positions of a tile, so
 // that a load of scales serves 8 scores, and works on half a tile at a time
-// against the maximum as it stands: weights that come out too large are made
-// again with the maximum moved.
+// against the reference as it stands: weights that come out too large are made
+// again with the reference moved.
 //
 // What bounds it: the chain of a tile of 256 x 128 scores, 4600 clocks: one
 // half's weights (2400; 64 multiplications, exponentials and roundings to a
@@ -76,8 +83,12 @@ constexpr int kConvert = 256, kThreads = 128 + kConvert + 256;   // a warpgroup 
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 160, kConvertRegs = 64, kIssueRegs = 32;
 static_assert(2 * kSoftmaxRegs + 2 * kConvertRegs + kIssueRegs <= 5 * kLaunchRegs, "warpgroups share what the launch has");
 constexpr uint32_t kTmemCols = 512;                         // S of both halves (later P), O of both halves
-constexpr float kLargest = 32768.f;                         // a weight above it moves its row's maximum; fp16 ends at 65504
-constexpr float kLargestSum = 2.028240960365167e31f;        // 2^104: V scales below 2^-100 count as that in a maximum
+constexpr float kLargest = 32768.f;                         // a weight above it moves its row's reference; fp16 ends at 65504
+// Binary orders by which references lie below their maxima, in pieces of up to 2^13, 2^17 and more positions.
+__device__ __forceinline__ float lowered(int tiles) { return tiles <= 64 ? 0.f : tiles <= 1024 ? 4.f : 8.f; }
+// V scales below it count as it in a maximum: weights of positions without V are below 2^102, whatever the reference.
+__device__ __forceinline__ float least_scale_log(int tiles) { return lowered(tiles) - 100.f; }
+constexpr float kLargestSum = 4.056481920730334e31f;        // 2^105, of 16 positions
 constexpr uint32_t kWaitLimit = 1u << 18;                   // polls of ~3.7 us: a wait gives up after about a second
 
 // A piece as all roles see it.
@@ -425,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
             sm.ks[slot][ct] = scale;
           } else {
             sm.vs[slot][ct - 128] = scale;
-            sm.lg[slot][ct - 128] = fmaxf(log2_fast(scale), -100.f);
+            sm.lg[slot][ct - 128] = fmaxf(log2_fast(scale), least_scale_log(w.tiles));
           }
           if (partly(ik)) {
             sync_some(2, kConvert);                         // the scales are there
@@ -602,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
             }
             return good;
           };
-          // Weights of 32 positions against the present maxima.
+          // Weights of 32 positions against the present references.
           auto weights = [&](int c, const uint32_t (&v)[2][16], uint32_t (&out)[2][8], bool held) {
             uint64_t sum[4] = {0, 0, 0, 0};
             __half2 top = __float2half2_rn(0.f);
@@ -615,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
                 const uint64_t e = fma2(mul2(join(x[0], x[1]), ks), pack2(qf[r], qf[r]), pack2(-m[r], -m[r]));
                 float e0 = first(e), e1 = second(e);
                 if (held) {
-                  const float most0 = 9.f - lg_at[32 * c + 8 * jj], most1 = 9.f - lg_at[32 * c + 8 * jj + 1];   // a maximum may lie 8 below
+                  // a maximum is less than low + 1 above its reference
+                  const float low = lowered(tiles), most0 = low + 2.f - lg_at[32 * c + 8 * jj], most1 = low + 2.f - lg_at[32 * c + 8 * jj + 1];
                   e0 = e0 > most0 ? most0 : e0;               // NaN stays
                   e1 = e1 > most1 ? most1 : e1;
                 }
@@ -637,22 +649,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
             tc::tmem_st_frag16(s_at + 16 * c, out[0]);
             tc::tmem_st_frag16(s_at + half + 16 * c, out[1]);
           };
-          // Maxima that have risen by more than 2^8 are moved there, by whole powers of two once there is one, so that the weights of the
-          // tile's positions before 32 c, which are made already, scale exactly; down to the power of two, so that a row's largest weight
-          // stays at 1 or above, 2^25 times what fp16 drops.
+          // References of rows whose maxima have risen follow them, in whole numbers: the weights of the tile's positions before 32 c,
+          // which are made already, scale exactly.  (Where maxima are so large that fp32 has no such numbers, they are the references.)
           auto move = [&](int c, float (&mx)[4]) {
             float f[4];
             bool moves = false;
+            const float low = lowered(tiles);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
               mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
               f[r] = 1.f;
-              if (mx[r] > m[r] + 8.f) {                       // each row by itself: its neighbours stand elsewhere in another step
-                const float by = m[r] == -1e30f ? 0.f : fminf(floorf(mx[r] - m[r]), 200.f);
-                f[r] = by == 0.f || by > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)by) << 23);
-                const float mn = by == 0.f || by == 200.f ? mx[r] : m[r] + by;
-                l[r] = scaled_down(l[r], m[r] - mn);
+              if (mx[r] > m[r] + low + 1.f) {                 // each row by itself: its neighbours stand elsewhere in another step
+                float mn = floorf(mx[r]) - low;
+                if (!(mx[r] - mn <= 9.f)) mn = mx[r];
+                const float by = mn - m[r];                   // the first time 2^99 and more
+                f[r] = by <= 126.f ? __uint_as_float((uint32_t)(127 - (int)by) << 23) : 0.f;
+                l[r] = scaled_down(l[r], -by);
                 m[r] = mn;
                 moves = true;
               }
@@ -755,8 +768,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
                   uint32_t v[2][16];
                   read(c, v);
                   landed(v);
-                  // against the present maxima, and against moved ones; where scores are so large that fp32's steps between them
-                  // matter, some lie above their maximum by its rounding, and are held there
+                  // against the present references, and against moved ones; where scores are so large that fp32's steps between them
+                  // matter, some lie above their maximum by its rounding, and are held
                   good = false;
 #pragma unroll 1
                   for (int turn = it + c == 0; turn < 3 && !good; ++turn) {

@@ -600,7 +600,11 @@ size_t kv8_rows_workspace_bytes(int B, int T, int q_heads, int kv_heads, int hea
  * it, whatever it is.  A row's bytes depend on its own stream's rows and
  * length, not on the rest of the step.  A position whose V holds a NaN code
  * may make all of an attending row's output NaN.  Ranges of scales and scores as for
- * kv8_attend.
+ * kv8_attend.  Weights are rounded to 16 bits; what those too light for it lose
+ * is together at most 2^-12 of the row's largest term.  The fp32 sums are the
+ * tensor cores', which cut products off at 2^-25 of the sum they are added to:
+ * where more than 2^17 positions are summed in one piece, many light ones may
+ * lose more to that than the output's rounding does (at most 2^-24.6 of the output each).
  * Q, O: DEVICE bf16 [T][q_heads][head_dim], 16-byte aligned; ws: DEVICE, 16-byte
  * aligned, kv8_rows_workspace_bytes(...) bytes, caller-owned, contents
  * irrelevant before and after; calls that may overlap on the GPU need
