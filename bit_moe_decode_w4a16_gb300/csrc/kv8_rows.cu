@@ -8,20 +8,21 @@
 // A stream's rows are gathered per kv head (row r is head r % G of row r / G),
 // 256 to a block; a CTA takes pieces of blocks from the plan's list (longest
 // first, dealt out back and forth) and walks over a piece's tiles of 128
-// positions on the 5th-generation tensor cores (fp16 operands, fp32 sums in
-// tensor memory):
-//   S[row][position] = Q K^T, MMAs of 128 x 128 x 16, both in shared memory;
+// positions on the 5th-generation tensor cores (fp32 sums in tensor memory):
+//   S[row][position] = Q K^T, bf16 MMAs of 128 x 128 x 16, both in shared memory;
 //   weights 2^(S ks qf - m) vs, as fp16, over S's place in tensor memory; m is
 //     a reference at or below the running maximum of x + log2 vs, moved only when a weight passes 2^15;
 //   O[row][element] += P V, MMAs of 128 x d x 16, A in tensor memory, B the
 //     tile's V as it lies (positions down, elements along: N-major).
-// K and V are converted to fp16 with the same layout (128-byte swizzle), once
+// K is converted to bf16 and V to fp16, in the same layout (128-byte swizzle), once
 // for the block's two halves of 128 rows, which two warpgroups of softmax work
 // on in turn: while one makes weights the other's products run.  A block of up
 // to 128 rows instead gives its even tiles to one warpgroup and the odd ones
 // to the other, each with sums of its own, which are joined at the end.
-// fp16, not bf16, because every code of either format is exact in it; a query
-// row is scaled by a power of two to fp16's middle, and a weight loses at most
+// Every code of either format is exact in both types.  Queries are bf16, scaled by
+// a power of two so that no score overflows: exact down to 2^-126 of the row's
+// largest element (in fp16 what lay 2^-17 below it lost bits, and 2^-25 all).
+// Weights are fp16, which has three bits more: one loses at most
 // 2^-11 of itself, or half of fp16's last step, 2^-25.  The largest weight of a row is 1 or
 // more, in long pieces 2^4 or 2^8: what many light weights lose together is then at most
 // 2^-12 of it in a piece of up to 2^21 positions (with 1 throughout, 2^19 positions of
@@ -122,8 +123,8 @@ struct Work {
 
 template <int D>
 struct RowsSmem {
-  uint8_t q[2][kSub * D * 2];                               // [d / 64][row][64] fp16, swizzled
-  uint8_t k[2][kTile * D * 2], v[2][kTile * D * 2];         // [d / 64][position][64]
+  uint8_t q[2][kSub * D * 2];                               // [d / 64][row][64] bf16, swizzled
+  uint8_t k[2][kTile * D * 2], v[2][kTile * D * 2];         // [d / 64][position][64], bf16 and fp16
   // scales and log2 of V's, of four tiles: they are written with a tile's K, when the softmax may be two tiles back
   float ks[4][kTile], vs[4][kTile], lg[4][kTile];
   // of the query rows of this piece and of the next: the factor that its scores are short of, its place among all heads of all rows
@@ -141,7 +142,7 @@ struct RowsSmem {
   int gave_up, stop[2];                                     // a wait gave up; one of the softmax's, by the turn's parity
 };
 
-// 16-byte piece c of row r: 128-byte rows of 64 fp16, pieces swizzled by the row.
+// 16-byte piece c of row r: 128-byte rows of 64 elements, pieces swizzled by the row.
 __device__ __forceinline__ uint32_t piece(int r, int c) { return (c >> 3) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
 // Descriptors with the 128-byte swizzle (layout type 2), 8-row atoms of 1024 bytes: the low word, to which a start 16 bytes further on
 // adds 1, and the whole.  Rows of K and Q: the start moves by 32 bytes per 16 elements.  V, N-major: by 16 rows per 16
@@ -149,6 +150,30 @@ __device__ __forceinline__ uint32_t piece(int r, int c) { return (c >> 3) * kTil
 __device__ __forceinline__ uint32_t k_major(uint32_t at) { return at >> 4 | 1u << 16; }
 __device__ __forceinline__ uint32_t n_major(uint32_t at) { return at >> 4 | (uint32_t)(kTile * 128 >> 4) << 16; }
 __device__ __forceinline__ uint64_t operand(uint32_t low) { return (uint64_t)low | (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32; }
+
+// Four codes -> two bf16 pairs (exact).
+template <int FMT>
+__device__ __forceinline__ void codes4_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == BM_KV8_E4M3) {
+    codes4<FMT>(w, lo, hi);
+    auto again = [](uint32_t& x) {
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x));
+      const __nv_bfloat162 z = __floats2bfloat162_rn(y.x, y.y);
+      x = *reinterpret_cast<const uint32_t*>(&z);
+    };
+    again(lo);
+    again(hi);
+  } else {
+    // a code is its low seven bits less 128 if its sign is set: 0x43 in front of u < 128 is the bf16 128 + u, in front of 128 it is 256
+    auto pair = [](uint32_t x) {
+      const uint32_t a = x & 0xFF7FFF7Fu, b = x & 0xFF80FF80u;
+      const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&y);
+    };
+    lo = pair(__byte_perm(w, 0x43434343u, 0x4140));
+    hi = pair(__byte_perm(w, 0x43434343u, 0x4342));
+  }
+}
 
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -284,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     regs_down<kIssueRegs>();
     if (warp < 2) {
       const int s = warp;
-      constexpr uint32_t qk = tc::idesc_f16_f32(kSub, kTile), pv = tc::idesc_f16_f32(kSub, D) | tc::kIdescBMajorN;
+      constexpr uint32_t qk = tc::idesc_bf16_f32(kSub, kTile), pv = tc::idesc_f16_f32(kSub, D) | tc::kIdescBMajorN;
       constexpr uint32_t kBuffer = kTile * D * 2 >> 4, kBlock = kTile * 128 >> 4;
       const uint32_t k_at = k_major(tc::smem_u32(sm.k[0])), v_at = n_major(tc::smem_u32(sm.v[0])), q_at = k_major(tc::smem_u32(sm.q[0]));
       const uint32_t leader = tc::elect_one();
@@ -370,15 +395,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     const bool swap = c & 4;                                // the second half's pieces in the other order: no bank conflict
     uint4 kr[kTurns], vr[kTurns];
     float scale = 0.f;                                      // of position ct % 128: K's in the first warpgroup, V's in the other
-    auto convert = [&](uint8_t* to, const uint4 (&x)[kTurns]) {
+    auto convert = [&](uint8_t* to, const uint4 (&x)[kTurns], bool to_bf16) {
 #pragma unroll
       for (int u = 0; u < kTurns; ++u) {
         const int row = u * (kConvert / kLanes) + row0;
+        const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
         uint32_t f[8];
-        codes4<FMT>(x[u].x, f[0], f[1]);
-        codes4<FMT>(x[u].y, f[2], f[3]);
-        codes4<FMT>(x[u].z, f[4], f[5]);
-        codes4<FMT>(x[u].w, f[6], f[7]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (to_bf16) codes4_bf16<FMT>(in[e], f[2 * e], f[2 * e + 1]);
+          else codes4<FMT>(in[e], f[2 * e], f[2 * e + 1]);
+        }
         *reinterpret_cast<uint4*>(to + piece(row, 2 * c + swap)) = swap ? make_uint4(f[4], f[5], f[6], f[7]) : make_uint4(f[0], f[1], f[2], f[3]);
         *reinterpret_cast<uint4*>(to + piece(row, 2 * c + !swap)) = swap ? make_uint4(f[0], f[1], f[2], f[3]) : make_uint4(f[4], f[5], f[6], f[7]);
       }
@@ -453,14 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
               if (any) sm.vs[slot][u * (kConvert / kLanes) + row0] = __uint_as_float(0x7FC00000u);
             }
           }
-          convert(sm.k[of_k.tile & 1], kr);
+          convert(sm.k[of_k.tile & 1], kr, true);
           tc::fence_proxy_async_smem();
           arrive(sm.k_full[of_k.tile & 1]);
           of_k.given(w, ik);
           if (++ik < w.tiles) load_k(ik);
         } else {
           free_again(of_v, sm.o_ready);
-          convert(sm.v[of_v.tile & 1], vr);
+          convert(sm.v[of_v.tile & 1], vr, false);
           tc::fence_proxy_async_smem();
           arrive(sm.v_full[of_v.tile & 1]);
           of_v.given(w, iv);
@@ -478,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
     int tile0 = 0;                                          // the CTA's tiles so far
     unsigned uses = 0, last = 0;                            // bit b: the parity of this half's steps with buffer b; the latest step's buffer
     auto products_done = [&]() { wait(sm.o_ready[s][last], (uses >> last & 1) ^ 1); };
-    // ---- a block's query rows as fp16 of about their own magnitude, d / 8 lanes to a row, asked for while the piece before ends.  All rows
+    // ---- a block's query rows, brought to a magnitude of about 1, d / 8 lanes to a row, asked for while the piece before ends.  All rows
     // of the halves in use are written, whatever the block's own: 128 of this half's, or 64 of the half that both share.
     auto first_row = [&](const Work& w) { return w.wide ? kSub * s : 64 * s; };
     constexpr int kPieces = D / 8, kStep = 128 / kPieces, kBatch = 64 / kStep;
@@ -513,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint64_t y = mul2(pack2(bf_lo(in[e]), bf_hi(in[e])), pack2(down, down));
-          const __half2 v = __floats2half2_rn(first(y), second(y));
+          const __nv_bfloat162 v = __floats2bfloat162_rn(first(y), second(y));
           f[e] = *reinterpret_cast<const uint32_t*>(&v);
         }
         *reinterpret_cast<uint4*>(to + u * kStep * 128) = make_uint4(f[0], f[1], f[2], f[3]);

@@ -1,5 +1,5 @@
 """Attention of ragged steps where the 16-bit operands could lose something:
-weights far below the row's largest."""
+weights far below the row's largest, and query elements far below theirs."""
 
 import math
 
@@ -8,7 +8,7 @@ import torch
 
 import kv8_ref as ref
 from kv8_ref import E4M3, INT8
-from test_gpu_kv8_step import BF16_HALF, Step
+from test_gpu_kv8_step import BF16_HALF, FORMATS, Step, _rows
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,17 @@ def test_light_weights_keep_their_share(bm, fmt, d, n, base, piece, at, depth):
     err = (O.double() - o[:, None]).abs()
     tol = (BF16_HALF * o + bound * (1 + BF16_HALF))[:, None]
     assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("qh,kvh,d,n,base", [(8, 2, 64, 50, 150), (32, 4, 128, 300, 40)])
+@pytest.mark.parametrize("exp", [10, 18, 24, 30, 90])
+def test_query_elements_far_below_their_rows_largest(bm, fmt, qh, kvh, d, n, base, exp):
+    """An element that all keys answer with zero says nothing about the others, however large it is."""
+    cache = ref.random_cache(fmt, 1, base + n, kvh, d, 41)
+    at = 5
+    cache["K"][..., at] = 0
+    Q = _rows(n, qh, d)
+    Q[:, :, at] = 2.0 ** exp
+    s = Step(bm, cache, qh, [0], [base], [n], n)
+    s.check(Q, s.attend(Q))
