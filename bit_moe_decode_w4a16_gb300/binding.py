@@ -123,6 +123,8 @@ def lib():
             "kv8_plan": ([V, I, V, V, V, V, V, V, V, V, V, I, I, V, SZ, V], S),
             "kv8_rows_workspace_bytes": ([I, I, I, I, I, I], SZ),
             "kv8_attend_rows": ([V, V, SZ, V, I, ctypes.c_float, V, I, I, V, SZ, V], S),
+            "kv8_rows_status": ([V], S),
+            "bm_test_kv8_rows_hold": ([I, I, I], S),
             "kv8_tree_accept": ([V, SZ, V, V, V, V, V, V, V, I, I, V], S),
             "kv8_tree_keep": ([V, V, SZ, V, V, I, V], S),
             "bm_sample": ([V, I, ctypes.c_int64, I, I, V, V, V, V, V, V, V, V], S),
@@ -572,6 +574,15 @@ def kv8_attend_rows(cache, plan, Q, O, B, ws, scale=None, stream=None):
                                  _tensor(Q, w, "Q", t.bfloat16, None, dev), qh, d ** -0.5 if scale is None else scale,
                                  _tensor(O, w, "O", t.bfloat16, shape, dev), B, T, _tensor(ws, w, "ws", t.uint8, None, dev),
                                  ws.numel(), _stream(stream, dev)))
+
+
+def kv8_rows_status(stream=None):
+    """Waits for the stream; raises if a wait inside kv8_attend_rows gave up on this device since the last call."""
+    _check(lib().kv8_rows_status(_stream(stream, _here())))
+
+
+def bm_test_kv8_rows_hold(what, cta=0, at=0):
+    _check(lib().bm_test_kv8_rows_hold(int(what), int(cta), int(at)))
 
 
 def kv8_tree_accept(plan, tokens, ids, path, kept, fresh, n_fresh, lens, stream=None):

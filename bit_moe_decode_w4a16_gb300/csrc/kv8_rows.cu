@@ -51,7 +51,7 @@
 // 135 us; spills to local memory cost more than a second read of tensor memory.
 //
 // Every wait is bounded.  A CTA in which one gave up leaves NaN in the rows of all
-// of its pieces.
+// of its pieces and counts itself, for kv8_rows_status.
 #include <type_traits>
 
 #include "kv8_attend.cuh"
@@ -63,6 +63,9 @@ namespace {
 
 using namespace kv8;
 
+// What a CTA holds back, so that waits run out: failure-detection tests only.
+enum Hold { kHoldNone, kHoldKeys, kHoldValues, kHoldQueries, kHoldWeights };
+
 struct RowsArgs {
   Cache c;
   const void* plan;
@@ -72,7 +75,10 @@ struct RowsArgs {
   float2* rec_ml;      // [16] their maxima and sums
   int B, T, qh;
   float scale_log2;
+  int hold, hold_cta, hold_at;   // a Hold; of this CTA; which of its tiles (queries: pieces; weights: the first half's steps)
 };
+
+__device__ unsigned gave_up_count;   // CTAs in which a wait gave up, ever
 
 // The plan is for these sizes.
 __device__ __forceinline__ bool fits(const PlanHead& h, const RowsArgs& a) {
@@ -386,6 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
       // nothing of this CTA's is in flight when it ends
       tc::warp_mma_commit(tc::smem_u32(&sm.drained), leader);
       if (!tc::mbar_wait(tc::smem_u32(&sm.drained), 0, kWaitLimit)) ok = false;
+    } else if (warp == 2 && lane == 0 && a.hold != kHoldNone && a.hold_cta == (int)blockIdx.x) {
+      // A warp without work, so that the others' code is what always runs: bytes are awaited on the barrier's phase that never come.
+      const bool by_tile = a.hold == kHoldKeys || a.hold == kHoldValues;
+      uint64_t& bar = a.hold == kHoldKeys ? sm.k_full[a.hold_at & 1] : a.hold == kHoldValues ? sm.v_full[a.hold_at & 1]
+                      : a.hold == kHoldQueries ? sm.q_full : sm.p_ready[0];
+      bool there = true;
+      for (int n = 0; n < (by_tile ? a.hold_at >> 1 : a.hold_at) && there; ++n) there = bounded_wait(tc::smem_u32(&bar), n & 1);
+      if (there) tc::mbar_expect_tx(tc::smem_u32(&bar), 16);
     }
   } else if (warp < 4 + kConvert / 32) {
     // ---------------- conversion: 16 codes to a thread and turn
@@ -931,6 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_rows(RowsArgs a) {
   tc::fence_after_sync();
   if (warp == 0) tc::tmem_dealloc(s_cols, kTmemCols);
   if (sm.gave_up) {                                         // NaN in all rows of this CTA's pieces
+    if (tid == 0) atomicAdd(&gave_up_count, 1u);
     for (int r = 0; turn(r) < items; ++r) {
       const Work w(plan, turn(r), G);
       const int slabs = (w.n * G + 15) >> 4;
@@ -1021,6 +1036,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_rows_merge(RowsArgs a)
   if (!waited) pdl_wait();                                  // done means done: the kernel before is
 }
 
+std::atomic<int> test_hold{kHoldNone}, test_hold_cta{0}, test_hold_at{0};
+
 template <int D, int FMT>
 cudaError_t launch_rows(const RowsArgs& a, int64_t records, cudaStream_t s) {
   const size_t smem = sizeof(RowsSmem<D>) + 1024;
@@ -1076,11 +1093,45 @@ bm_status kv8_attend_rows(const bm_kv8_cache* c, const void* plan, size_t plan_b
   a.T = T;
   a.qh = q_heads;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.hold = test_hold;
+  a.hold_cta = test_hold_cta;
+  a.hold_at = test_hold_at;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4 = c->format == BM_KV8_E4M3, d128 = c->head_dim == 128;
   const cudaError_t e = d128 ? (e4 ? launch_rows<128, BM_KV8_E4M3>(a, records, s) : launch_rows<128, BM_KV8_INT8>(a, records, s))
                              : (e4 ? launch_rows<64, BM_KV8_E4M3>(a, records, s) : launch_rows<64, BM_KV8_INT8>(a, records, s));
   if (e != cudaSuccess) return set_error(BM_ERR_CUDA, std::string("kv8_attend_rows: ") + cudaGetErrorString(e));
+  return ok();
+}
+
+bm_status kv8_rows_status(void* stream) {
+  using namespace bm;
+  auto fail = [](cudaError_t e) { return set_error(BM_ERR_CUDA, std::string("kv8_rows_status: ") + cudaGetErrorString(e)); };
+  static std::atomic<unsigned> told[64] = {};               // per device, of what was counted on it
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(s, &capture);
+  if (e != cudaSuccess) return fail(e);
+  if (capture != cudaStreamCaptureStatusNone) return set_error(BM_ERR_INVALID_ARG, "kv8_rows_status: the stream is being captured");
+  int dev = 0;
+  unsigned count = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return fail(e);
+  if (dev >= 64) return set_error(BM_ERR_UNSUPPORTED, "kv8_rows_status: more than 64 devices");
+  if ((e = cudaMemcpyFromSymbolAsync(&count, gave_up_count, sizeof(count), 0, cudaMemcpyDeviceToHost, s)) != cudaSuccess) return fail(e);
+  if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return fail(e);
+  const unsigned before = told[dev].exchange(count);
+  if (count == before) return ok();
+  return set_error(BM_ERR_DEVICE_CHECK, "kv8_attend_rows: a bounded wait gave up in " + std::to_string(count - before) +
+                                            " CTAs; the rows that they had are NaN");
+}
+
+bm_status bm_test_kv8_rows_hold(int what, int cta, int at) {
+  using namespace bm;
+  if (what < kHoldNone || what > kHoldWeights || cta < 0 || at < 0)
+    return set_error(BM_ERR_INVALID_ARG, "bm_test_kv8_rows_hold: need 0 <= what <= 4, cta >= 0, at >= 0");
+  test_hold = what;
+  test_hold_cta = cta;
+  test_hold_at = at;
   return ok();
 }
 

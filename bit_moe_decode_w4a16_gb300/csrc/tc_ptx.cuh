@@ -256,6 +256,10 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void mbar_arrive(uint32_t mbar_smem) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mbar_smem) : "memory");
 }
+// The present phase completes only when this many bytes have arrived, too.
+__device__ __forceinline__ void mbar_expect_tx(uint32_t mbar_smem, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(mbar_smem), "r"(bytes) : "memory");
+}
 // Wait until the phase with the given parity has completed; gives up after
 // `limit` polls (each poll may suspend the thread for a bounded time) and
 // returns false.

@@ -614,6 +614,21 @@ size_t kv8_rows_workspace_bytes(int B, int T, int q_heads, int kv_heads, int hea
 bm_status kv8_attend_rows(const bm_kv8_cache* c, const void* plan, size_t plan_bytes, const uint16_t* Q, int q_heads,
                           float scale, uint16_t* O, int B, int T, void* ws, size_t ws_bytes, void* stream);
 
+/* Waits inside kv8_attend_rows are bounded.  One that gives up after about a
+ * second leaves NaN in the rows of its CTA, and is told here: waits for
+ * `stream`, then BM_ERR_DEVICE_CHECK if, on the current device, a wait of any
+ * such call that has ended gave up since this was last asked, with the number of
+ * CTAs in the message.  The calls after it are as good as ever.  Errors:
+ * BM_ERR_INVALID_ARG (the stream is being captured), BM_ERR_CUDA. */
+bm_status kv8_rows_status(void* stream);
+
+/* Failure-detection tests only: in the kv8_attend_rows calls made from now on (what
+ * = 0: none, the default) a part of what CTA `cta` makes is held back from
+ * who waits for it: 1 the keys of its tile `at`, 2 the values, 3 the query rows of its
+ * piece `at`, 4 the weights of step `at` of its first half; counts from 0.  The waits run
+ * out; nothing faults.  Errors: BM_ERR_INVALID_ARG. */
+bm_status bm_test_kv8_rows_hold(int what, int cta, int at);
+
 /* Walk down a planned step's trees: from a stream's first row on, to the first
  * child whose token is what the model chose behind its parent, until none is.
  * tokens: DEVICE int32 [T], the rows' own tokens (the first row's, the stream's

@@ -133,3 +133,9 @@ def test_wrong_tensors_are_refused():
         with pytest.raises(bm.BitMoeError) as e:
             call()
         assert "kv8_" in str(e.value), n
+
+
+def test_hold_refusals():
+    for args in ((-1, 0, 0), (5, 0, 0), (1, -1, 0), (1, 0, -1)):
+        assert bm.lib().bm_test_kv8_rows_hold(*args) == 1 and bm.last_error().startswith("bm_test_kv8_rows_hold: ")
+    assert bm.lib().bm_test_kv8_rows_hold(0, 0, 0) == 0
