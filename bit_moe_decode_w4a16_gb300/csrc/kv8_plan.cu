@@ -415,8 +415,11 @@ bm_status kv8_plan(const bm_kv8_cache* c, int q_heads, const int32_t* slots, con
   const size_t need = kv8::plan_bytes(B, T, q_heads, c->kv_heads);
   if (plan_bytes < need) return refuse("plan of " + std::to_string(plan_bytes) + " bytes, " + std::to_string(need) + " needed");
   const PlanArgs a{plan, slots, lens, counts, parents, row_start, after, row_slot, row_index, row_pos, B, T, q_heads, c->kv_heads, c->slots, c->ctx_cap};
-  // A CTA alone has less to wait for: 8 trees of 17 rows 9.6 us with eight, 8.3 with one; 512 streams of up to 128 rows 20.8 with eight.
-  const int ctas = T <= 2048 && B <= 64 ? 1 : kPlanCtas;
+  // A CTA alone has less to wait for, eight share the pieces, whose number grows with the streams' blocks.  One and eight, us, 32 / 4 heads:
+  // 8 trees of 17 rows behind 4000 positions (128 pieces) 8.0 and 9.2; 32 single rows behind 4096 (640) 8.8 and 10.0; 32 trees of 16 behind 32768
+  // (1152) 13.2 and 13.3; 64 single rows behind 4096 (1280) 12.0 and 11.6; 64 trees of 32 behind 131072 (4352) 25.1 and 13.7; 512 single
+  // rows 44.5 and 17.9.  Prompts of 2048, 4096 and 8192 rows: 7.4 and 8.2, 8.3 and 8.6, 10.6 and 9.9.
+  const int ctas = T <= 2048 && B * c->kv_heads <= 128 ? 1 : kPlanCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
