@@ -67,6 +67,25 @@ def test_streams_of_many_blocks(bm, fmt, qh, kvh, d, n, base):
     _check_rows(cache, 1, base, Q, O, _borders(n, base, qh // kvh, n), {0, qh // kvh - 1, qh // 2, qh - 1})
 
 
+# in long pieces references lie 2^4 and 2^8 below their maxima, weights accordingly higher
+@pytest.mark.parametrize("exp,dead", [(-91, 0.0), (-91, 0.9), (0, 0.999), (0, 1.0), (100, 0.0), (100, 0.9)])
+@pytest.mark.parametrize("fmt,n,base", [(E4M3, 2600, 70000), (INT8, 19500, 131072)])
+def test_long_pieces_at_the_ends_of_the_scales(bm, fmt, n, base, exp, dead):
+    """V scales from 2^-100 to 2^100, and positions without V, which weigh in the sum alone."""
+    cache = ref.random_cache(fmt, 1, base + n, 1, 64, 63)
+    cache["Vs"] *= 2.0 ** exp
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    off = torch.rand(base + n, generator=g, device="cuda") < dead
+    cache["V"][0, 0, off] = 0
+    cache["Vs"][0, 0, off] = 0
+    s = Step(bm, cache, 8, [0], [base], [n], n)
+    Q = _rows(n, 8, 64)
+    O = s.attend(Q)
+    assert O.isfinite().all()
+    _check_rows(cache, 0, base, Q, O, [0, 1, 31, 32, 33, n // 2, n - 2, n - 1] + list(range(100, 116)), range(8))
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("qh,kvh,d,counts,lens", [(16, 16, 128, [1, 40, 300, 1, 7], [5000, 0, 100, 127, 4096]), (32, 16, 64, [64, 1, 200], [2048, 9000, 0]),
                                                   (77, 77, 64, [1, 33, 260, 5], [4500, 10, 0, 4200]), (154, 77, 64, [3, 140], [6000, 128]),
