@@ -37,18 +37,20 @@
 // against the reference as it stands: weights that come out too large are made
 // again with the reference moved.
 //
-// What bounds it: the chain of a tile of 256 x 128 scores, 4600 clocks: one
+// What bounds it: the chain of a tile of 256 x 128 scores, about 4750 clocks: one
 // half's weights (2400; 64 multiplications, exponentials and roundings to a
 // thread, twice as long as the half's MMAs), its product, its next scores.
-// Tensor cores are at work 45% of the time; then the start and end of a piece,
+// Tensor cores are at work 42% of the time; then the start and end of a piece,
 // 5000 to 7000 clocks of query rows, whose place comes free with the last scores,
 // 5000 of outputs beside the next scores, and a first and a masked tile of
 // twice the work: what short prompts and trees mostly are.  Measured, d = 128, 32 query and 4 kv heads, e4m3: a prompt of 8192
-// rows 556 us (988 TFLOP/s; a warp to a row's head, fp32: 58.7 ms), 1000 rows behind
-// 65536 positions (int8) 1180 us (917), 16 prompts of up to 1000 rows 116 to 120 us, 32 trees
-// of 16 rows behind 4096 positions 46 us, one of 13 rows 23 us.  Instructions count: at 147 KB
+// rows 577 us (953 TFLOP/s; a warp to a row's head, fp32: 58.7 ms), 1000 rows behind
+// 65536 positions (int8) 1287 us (841), 16 prompts of up to 1000 rows 118 to 123 us, 32 trees
+// of up to 16 rows behind 4096 positions 47 us, one of 13 rows 23.7 us, 32 single rows
+// behind 4096 75 us (they fill 8 of a half's 128 rows; kv8_attend 33).  Instructions count: at 147 KB
 // of them, with weights of a whole tile at a time, the same prompts took 127 to
-// 135 us; spills to local memory cost more than a second read of tensor memory.
+// 135 us; spills inside the tiles' loop cost more than a second read of tensor memory (for d = 128
+// ptxas spills four bytes outside it, read once a piece).
 //
 // Every wait is bounded.  A CTA in which one gave up leaves NaN in the rows of all
 // of its pieces and counts itself, for kv8_rows_status.

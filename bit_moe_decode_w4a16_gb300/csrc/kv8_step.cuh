@@ -62,9 +62,10 @@ __host__ __device__ inline int blocks_of(int n, int G) { return (n * G + kBlockR
 __host__ __device__ inline int tiles_of(int len) { return (int)(((long long)len + kTile - 1) / kTile); }
 
 // Tiles to a piece (0: blocks stay whole), and tiles from one block's begin to the next's on the line.
-// A piece has a fixed cost (its query rows, its records to write and to merge), so it is at least 4 tiles
-// long, twice that for each fourfold length beyond 2048.  A stream alone should fill the GPU: up to half as many
-// blocks as SMs are each cut evenly; more of them, up to four for each SM, where the line of
+// A piece has a fixed cost (its query rows, its records to write and to merge), so cuts are at least 4 tiles
+// apart, twice that for each fourfold length beyond 2048; what is left behind a block's last cut is a piece of its
+// own, shorter than that (33 tiles are cut 8 8 8 8 1), and so are pieces at both ends of a block on the line.  A stream
+// alone should fill the GPU: up to half as many blocks as SMs are each cut evenly; more of them, up to four for each SM, where the line of
 // all blocks passes a multiple of an SM's share, so that the SMs end together (rows that
 // mostly attend to each other have blocks of many sizes, which do without).
 struct Cut {

@@ -586,7 +586,10 @@ bm_status kv8_plan(const bm_kv8_cache* c, int q_heads, const int32_t* slots, con
                    int32_t* row_pos, int B, int T, void* plan, size_t plan_bytes, void* stream);
 
 /* Bytes of DEVICE workspace kv8_attend_rows needs; 0 for sizes it rejects.  It
- * does not fall with B, T or ctx_cap. */
+ * does not fall with B, T or ctx_cap.  It holds fp32 records of all rows that
+ * may be cut, as a row's cut may not depend on the others: gigabytes for large steps over
+ * long caches (32 / 4 heads of 128, 256 streams, 8192 rows: 2.3 GB at a capacity
+ * of 32768, 4.6 GB at 131072). */
 size_t kv8_rows_workspace_bytes(int B, int T, int q_heads, int kv_heads, int head_dim, int ctx_cap);
 
 /* Attention of a planned step's rows over the cache, in which they have been
