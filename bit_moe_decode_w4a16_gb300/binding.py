@@ -578,7 +578,8 @@ def kv8_attend_rows(cache, plan, Q, O, B, ws, scale=None, stream=None):
 
 def kv8_rows_status(stream=None):
     """Waits for the stream; raises if a wait inside kv8_attend_rows gave up on this device since the last call."""
-    _check(lib().kv8_rows_status(_stream(stream, _here())))
+    dev = _here()
+    _check(lib().kv8_rows_status(_stream(stream, dev) if dev >= 0 else None))   # without a device: BM_ERR_CUDA
 
 
 def bm_test_kv8_rows_hold(what, cta=0, at=0):

@@ -139,3 +139,12 @@ def test_hold_refusals():
     for args in ((-1, 0, 0), (5, 0, 0), (1, -1, 0), (1, 0, -1)):
         assert bm.lib().bm_test_kv8_rows_hold(*args) == 1 and bm.last_error().startswith("bm_test_kv8_rows_hold: ")
     assert bm.lib().bm_test_kv8_rows_hold(0, 0, 0) == 0
+
+
+def test_status_without_a_device():
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("needs a machine without a GPU")
+    with pytest.raises(bm.BitMoeError) as e:
+        bm.kv8_rows_status()
+    assert e.value.status == 5 and "kv8_rows_status" in e.value.message
