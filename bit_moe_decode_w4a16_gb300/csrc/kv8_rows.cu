@@ -1121,8 +1121,9 @@ bm_status kv8_rows_status(void* stream) {
   if (dev >= 64) return set_error(BM_ERR_UNSUPPORTED, "kv8_rows_status: more than 64 devices");
   if ((e = cudaMemcpyFromSymbolAsync(&count, gave_up_count, sizeof(count), 0, cudaMemcpyDeviceToHost, s)) != cudaSuccess) return fail(e);
   if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return fail(e);
-  const unsigned before = told[dev].exchange(count);
-  if (count == before) return ok();
+  unsigned before = told[dev];                              // two threads that ask at once tell each CTA once
+  while ((int)(count - before) > 0 && !told[dev].compare_exchange_weak(before, count)) {}
+  if ((int)(count - before) <= 0) return ok();
   return set_error(BM_ERR_DEVICE_CHECK, "kv8_attend_rows: a bounded wait gave up in " + std::to_string(count - before) +
                                             " CTAs; the rows that they had are NaN");
 }

@@ -604,7 +604,7 @@ size_t kv8_rows_workspace_bytes(int B, int T, int q_heads, int kv_heads, int hea
  * length, not on the rest of the step.  A position whose V holds a NaN code
  * may make all of an attending row's output NaN.  Ranges of scales and scores as for
  * kv8_attend.  Weights are rounded to 16 bits; what those too light for it lose
- * is together at most 2^-12 of the row's largest term.  The fp32 sums are the
+ * is together at most 2^-12 of the row's largest term (up to 2^21 positions).  The fp32 sums are the
  * tensor cores', which cut products off at 2^-25 of the sum they are added to:
  * where more than 2^17 positions are summed in one piece, many light ones may
  * lose more to that than the output's rounding does (at most 2^-24.6 of the output each).

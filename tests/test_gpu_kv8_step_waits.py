@@ -129,3 +129,31 @@ def test_status_refuses_a_captured_stream(bm):
     g.replay()
     bm.kv8_rows_status()
     assert torch.equal(O, want)
+
+
+def test_threads_that_ask_at_once(bm):
+    """Each CTA is told of once, to one of them."""
+    import re
+    import threading
+    s = _case("wide", bm)
+    Q = _rows(s.T, s.qh, 128)
+    for cta in (0, 3, 9):
+        bm.bm_test_kv8_rows_hold(KEYS, cta, 0)
+        s.attend(Q)
+    bm.bm_test_kv8_rows_hold(0)
+    told, others = [], []
+    stream = torch.cuda.current_stream()
+
+    def ask():
+        for _ in range(20):
+            try:
+                bm.kv8_rows_status(stream)
+            except bm.BitMoeError as e:
+                (told if e.status == 8 else others).append(int(re.search(r"in (\d+) CTAs", e.message).group(1)))
+
+    threads = [threading.Thread(target=ask) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert sum(told) == 3 and not others
